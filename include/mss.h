@@ -18,7 +18,9 @@
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers to dense, row-major fp32 arrays
- *     on the current HIP device, allocated and owned by the caller.  The
+ *     (the activations of the gated recurrence and the block norms below may
+ *     be bf16 or fp16) on the current HIP device, allocated and owned by the
+ *     caller.  The
  *     library allocates nothing and never frees a caller buffer; the backward
  *     passes take a caller workspace.  Its only device state is the static
  *     scratch array of mss_selective_scan_backward_noalloc.
@@ -48,7 +50,7 @@
 extern "C" {
 #endif
 
-#define MSS_VERSION 2
+#define MSS_VERSION 3
 
 /* Status codes. */
 #define MSS_OK 0
@@ -341,6 +343,188 @@ int mss_time_split(const mss_dims* dims, int op, int64_t* segment_steps);
 /* The same for mss_ssd_scan: every (batch row, head) sequence is cut into
  * segments of *segment_steps steps starting at t = 0.                       */
 int mss_ssd_time_split(const mss_ssd_dims* dims, int64_t* segment_steps);
+
+/* ---- Gated linear recurrence ---------------------------------------------------
+ * One state per channel instead of d_state of them, with gates that every
+ * token brings along.  Per batch row b and channel d:
+ *   h_t = v_t + (reset_t ? 0 : a_t h_{t-1})        (h_{-1} = h0, or 0)
+ *   y_t = h_t SiLU(z_t)                             (h_t when z is NULL)
+ * with the carry factor a and the input term v by `gate`:
+ *   MSS_GATE_SIGMOID  a = sigma(r),                   v = (1 - a) x
+ *   MSS_GATE_DECAY    a = exp(-c softplus(decay[d]) sigma(r)),
+ *                     v = sqrt(1 - a^2) sigma(i) x    (c = gate_scale)
+ *   MSS_GATE_LOG      a = exp(r),                     v = x
+ * r = -inf is valid: it means a = 0 (a = 1 for MSS_GATE_DECAY).  reset_t != 0 drops the state carried into step
+ * t (the start of another document packed into the same row, or the end of a
+ * row's left padding).
+ * The activations x, r, i, z, y and their gradients are of type dims->dtype;
+ * the states, decay and its gradient are fp32.  States are carried in fp32
+ * and results are rounded once, to the nearest even.                       */
+#define MSS_F32 0
+#define MSS_BF16 1
+#define MSS_F16 2
+#define MSS_GATE_SIGMOID 0
+#define MSS_GATE_DECAY 1
+#define MSS_GATE_LOG 2
+/* h_ckpt holds the state entering steps 0, 64, 128, ... */
+#define MSS_GATED_CKPT_STEPS 64
+typedef struct mss_gated_dims {
+    int32_t struct_size;    /* sizeof(mss_gated_dims) */
+    int32_t flags;          /* must be 0 */
+    int32_t dtype;          /* MSS_F32, MSS_BF16 or MSS_F16 */
+    int32_t gate;           /* MSS_GATE_*; no default */
+    int64_t batch;          /* B */
+    int64_t seq_len;        /* L (ignored by mss_gated_step) */
+    int64_t d_inner;        /* D */
+    float gate_scale;       /* c of MSS_GATE_DECAY: finite, > 0 (ignored otherwise) */
+    int32_t reserved;       /* must be 0 */
+} mss_gated_dims;
+
+/* Row strides in elements, each at least D; NULL in a call means dense rows
+ * (stride D).  With strides given the activation tensors need only their
+ * element's alignment (x and z as the two halves of a projection's output,
+ * dx and dz as the halves of its gradient); outputs may then interleave with
+ * each other inside one buffer as long as no element is shared.  Fields of
+ * tensors that a call does not take are ignored. */
+typedef struct mss_gated_strides {
+    int32_t struct_size;    /* sizeof(mss_gated_strides) */
+    int32_t reserved;       /* must be 0 */
+    int64_t x, r, i, z;
+    int64_t y;              /* y (forward, step) or dout (backward) */
+    int64_t dx, dr, di, dz;
+} mss_gated_strides;
+
+#define MSS_OP_GATED_SCAN 4
+#define MSS_OP_GATED_SCAN_BACKWARD 5
+/* Workspace size in bytes of mss_gated_scan / mss_gated_scan_backward: a
+ * function of the sizes alone, 0 for empty problems and for calls that need
+ * none.  256-byte aligned; its contents on entry do not matter; it may be
+ * reused, by a captured graph's replay too, once the call's work has
+ * finished (calls that overlap in time need one each). */
+int mss_gated_workspace_bytes(const mss_gated_dims* dims, int op, size_t* bytes);
+
+/* The recurrence over a sequence.
+ *   x, r, y (M, D);  i (M, D) and decay (D): required for MSS_GATE_DECAY,
+ *   NULL otherwise;  z (M, D), h0 (B, D), reset (M) bytes: may be NULL;
+ *   h_ckpt (B, ceil(L/64), D), h_last (B, D): outputs, may be NULL.
+ * Deterministic: the output bits are a function of the inputs and sizes.
+ * A sequence of length 0 still defines h_last (= h0, or zeros).            */
+int mss_gated_scan(const mss_gated_dims* dims, const mss_gated_strides* strides, const void* x,
+                   const void* r, const void* i, const float* decay, const void* z,
+                   const float* h0, const uint8_t* reset, void* y, float* h_ckpt, float* h_last,
+                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Its gradients, against dout (M, D), the gradient of y, and dh_last (B, D),
+ * the gradient of h_last (NULL = 0).  h_ckpt: the forward's, from a call with
+ * the same inputs.  With dy = dout SiLU(z), G_t = dy_t + (reset_{t+1} ? 0 :
+ * a_{t+1} G_{t+1}) and p_t = (reset_t ? 0 : h_{t-1}):
+ *   SIGMOID  dx = G (1 - a),  dr = G (p - x) a (1 - a)
+ *   DECAY    dx = G m s,  di = G m x s (1 - s)     (s = sigma(i), m = sqrt(1 - a^2))
+ *            w = G (a p - x s a^2 / m),  dr = -w c softplus(decay) q (1 - q),
+ *            ddecay = -c sigma(decay) sum_{b,t} w q     (q = sigma(r); the
+ *            terms over m take their limit, 0, where m = 0)
+ *   LOG      dx = G,  dr = G a p
+ *   dz = dout h SiLU'(z);  dh0 (B, D) = (reset_0 ? 0 : a_0 G_0)
+ * Required: dx, dr; di and ddecay for MSS_GATE_DECAY (NULL otherwise); dz iff
+ * z is given; dh0 may be NULL.  For L = 0 dh0 is dh_last (or zeros) and
+ * ddecay zeros.  Gradients are written, not accumulated; deterministic.    */
+int mss_gated_scan_backward(const mss_gated_dims* dims, const mss_gated_strides* strides,
+                            const void* x, const void* r, const void* i, const float* decay,
+                            const void* z, const uint8_t* reset, const float* h_ckpt,
+                            const void* dout, const float* dh_last, void* dx, void* dr, void* di,
+                            float* ddecay, void* dz, float* dh0, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/* One token per sequence: x, r, i, z, y (B, D), h (B, D) updated in place. */
+int mss_gated_step(const mss_gated_dims* dims, const mss_gated_strides* strides, const void* x,
+                   const void* r, const void* i, const float* decay, const void* z, float* h,
+                   void* y, hipStream_t stream);
+
+/* ---- Norms before and after a block ---------------------------------------------
+ * norm(v) over `width` channels in `groups` equal contiguous groups:
+ *   MSS_NORM_RMS    v / sqrt(mean(v^2) + eps)
+ *   MSS_NORM_LAYER  (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps)
+ * (RMSNorm with eps 1e-6 is the pages' pre-block norm: cpu_ops.ts
+ * rmsNormForward, RMSNORM_EPS.)  Activations are of type dims->dtype, the
+ * residual stream of res_dtype (dtype, or fp32); w, b, scale and their
+ * gradients fp32; statistics and sums fp32.                                */
+#define MSS_NORM_RMS 0
+#define MSS_NORM_LAYER 1
+#define MSS_GATE_BEFORE_NORM 0
+#define MSS_GATE_AFTER_NORM 1
+typedef struct mss_norm_dims {
+    int32_t struct_size;    /* sizeof(mss_norm_dims) */
+    int32_t flags;          /* must be 0 */
+    int32_t dtype;          /* MSS_F32, MSS_BF16 or MSS_F16 */
+    int32_t res_dtype;      /* add_norm: dtype or MSS_F32; gated_norm: dtype */
+    int32_t kind;           /* MSS_NORM_*; no default */
+    int32_t order;          /* gated_norm: MSS_GATE_*_NORM; add_norm: 0 */
+    int64_t rows;           /* M */
+    int64_t width;          /* D */
+    int64_t groups;         /* divides D (add_norm: 1) */
+    float eps;              /* finite, > 0 */
+    float alpha;            /* scalar factor of the residual scale, finite */
+} mss_norm_dims;
+
+/* Row strides in elements, as in mss_gated_strides (NULL: dense rows). */
+typedef struct mss_norm_strides {
+    int32_t struct_size;    /* sizeof(mss_norm_strides) */
+    int32_t reserved;       /* must be 0 */
+    int64_t x, z, residual;
+    int64_t s;              /* add_norm: the new residual stream */
+    int64_t y;              /* y (forward) or dy / dout (backward) */
+    int64_t ds;             /* add_norm backward: gradient of s */
+    int64_t dx, dz, dresidual;
+} mss_norm_strides;
+
+#define MSS_OP_ADD_NORM_BACKWARD 6
+#define MSS_OP_GATED_NORM_BACKWARD 7
+/* Workspace size in bytes of the norm backward passes (partial sums of the
+ * parameter gradients), under the rules of mss_gated_workspace_bytes. */
+int mss_norm_workspace_bytes(const mss_norm_dims* dims, int op, size_t* bytes);
+
+/* Before a block: s = residual + alpha scale[d] x, rounded to res_dtype, and
+ * y = norm(s) w + b of the rounded s (so that the backward, which reads s,
+ * differentiates the same numbers).
+ *   x, y (M, D) dtype;  residual, s (M, D) res_dtype;  w, b, scale (D).
+ *   Optional: residual (= 0), b (= 0), scale (= 1).  s may be residual itself
+ *   (same pointer and stride): the stream is then updated in place.         */
+int mss_add_norm(const mss_norm_dims* dims, const mss_norm_strides* strides, const void* x,
+                 const void* residual, const float* w, const float* b, const float* scale, void* s,
+                 void* y, hipStream_t stream);
+
+/* Its gradients against dy (M, D) dtype and ds (M, D) res_dtype, what else
+ * reaches the stream (NULL = 0):
+ *   dresidual = ds + (norm backward of dy w at s)   res_dtype
+ *   dx        = alpha scale[d] dresidual            dtype
+ *   dw, db, dscale (D) = sum dy n,  sum dy,  alpha sum dresidual x
+ * Required: s, w, dy, dresidual; x when dscale is wanted; dx, dw, db, dscale
+ * are computed where given.                                                */
+int mss_add_norm_backward(const mss_norm_dims* dims, const mss_norm_strides* strides,
+                          const void* s, const float* w, const void* dy, const void* ds,
+                          const void* x, const float* scale, void* dx, void* dresidual, float* dw,
+                          float* db, float* dscale, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
+/* After a block: with the gate SiLU(z) (1 when z is NULL),
+ *   MSS_GATE_BEFORE_NORM  n = norm(x SiLU(z)) w + b
+ *   MSS_GATE_AFTER_NORM   n = (norm(x) w + b) SiLU(z)
+ *   y = alpha scale[d] n, plus residual when given.
+ *   x, z, residual, y (M, D) dtype;  w, b, scale (D).
+ *   Optional: z, b (= 0), residual (= 0), scale (= 1).                     */
+int mss_gated_norm(const mss_norm_dims* dims, const mss_norm_strides* strides, const void* x,
+                   const void* z, const float* w, const float* b, const void* residual,
+                   const float* scale, void* y, hipStream_t stream);
+
+/* Its gradients against dout (M, D) (the residual's is dout itself):
+ *   dx, dz (M, D) dtype;  dw, db, dscale (D) where given (b: the forward's;
+ *   it enters dz of MSS_GATE_AFTER_NORM and dscale).
+ * Required: x, w, dout, dx; dz iff z is given.                             */
+int mss_gated_norm_backward(const mss_norm_dims* dims, const mss_norm_strides* strides,
+                            const void* x, const void* z, const float* w, const float* b,
+                            const float* scale, const void* dout, void* dx, void* dz, float* dw,
+                            float* db, float* dscale, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
 
 /* Human-readable text for a status code (static storage). */
 const char* mss_strerror(int status);

@@ -11,10 +11,16 @@ Layouts (fp32, contiguous, on the current CUDA/HIP device):
   h0, h_last : (batch, D, N)   h_cache : (batch, seq_len, D, N)
 Single-token step: x, z, delta, y : (batch, D); B, C : (batch, N);
   conv_state : (batch, K-1, D) oldest first; h : (batch, D, N).
+
+The gated linear recurrence (``gated_scan``, ``gated_scan_backward``,
+``gated_step``) and the norms before and after a block (``add_norm``,
+``gated_norm`` and their backward passes) take activations in float32,
+bfloat16 or float16, row-strided where that is handy; see each function.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import inputs  # noqa: F401  (seeded synthetic inputs; no method arithmetic)
@@ -75,16 +81,51 @@ def make_ssd_dims(batch, seq_len, n_heads, head_dim, d_state, n_groups=1, exact=
                    head_dim, d_state, n_groups)
 
 
+class GatedDims(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("batch", ctypes.c_int64), ("seq_len", ctypes.c_int64),
+                ("d_inner", ctypes.c_int64), ("gate_scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class GatedStrides(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                *((n, ctypes.c_int64) for n in ("x", "r", "i", "z", "y", "dx", "dr", "di", "dz"))]
+
+
+class NormDims(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("kind", ctypes.c_int32), ("order", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("width", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("alpha", ctypes.c_float)]
+
+
+class NormStrides(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                *((n, ctypes.c_int64) for n in ("x", "z", "residual", "s", "y", "ds", "dx", "dz",
+                                                "dresidual"))]
+
+
 EXPORTS = ("mss_conv1d_silu", "mss_selective_scan", "mss_mamba1_core", "mss_selective_step",
            "mss_selective_scan_strided", "mss_mamba1_core_strided",
            "mss_workspace_bytes", "mss_selective_scan_backward", "mss_conv1d_silu_backward",
            "mss_ssd_scan", "mss_time_split", "mss_ssd_time_split",
            "mss_selective_scan_backward_noalloc",
+           "mss_gated_workspace_bytes", "mss_gated_scan", "mss_gated_scan_backward",
+           "mss_gated_step", "mss_norm_workspace_bytes", "mss_add_norm", "mss_add_norm_backward",
+           "mss_gated_norm", "mss_gated_norm_backward",
            "mss_strerror", "mss_version", "mss_last_hip_error")
 
 OP_SELECTIVE_SCAN_BACKWARD = 1
 OP_CONV1D_SILU_BACKWARD = 2
 OP_SELECTIVE_SCAN = 3
+OP_GATED_SCAN = 4
+OP_GATED_SCAN_BACKWARD = 5
+OP_ADD_NORM_BACKWARD = 6
+OP_GATED_NORM_BACKWARD = 7
+GATED_CKPT_STEPS = 64                 # MSS_GATED_CKPT_STEPS
 NOALLOC_SCRATCH_BYTES = 256 << 20     # MSS_NOALLOC_SCRATCH_BYTES
 MSS_ESCRATCH = -6
 
@@ -121,6 +162,21 @@ def lib():
         L.mss_ssd_scan.argtypes = [ctypes.POINTER(SsdDims), i] + [p] * 11
         L.mss_time_split.argtypes = [dp, i, ctypes.POINTER(ctypes.c_int64)]
         L.mss_ssd_time_split.argtypes = [ctypes.POINTER(SsdDims), ctypes.POINTER(ctypes.c_int64)]
+        gd, gs = ctypes.POINTER(GatedDims), ctypes.POINTER(GatedStrides)
+        nd, ns = ctypes.POINTER(NormDims), ctypes.POINTER(NormStrides)
+        L.mss_gated_workspace_bytes.argtypes = [gd, i, ctypes.POINTER(sz)]
+        L.mss_gated_scan.argtypes = [gd, gs] + [p] * 11 + [sz, p]
+        L.mss_gated_scan_backward.argtypes = [gd, gs] + [p] * 16 + [sz, p]
+        L.mss_gated_step.argtypes = [gd, gs] + [p] * 8
+        L.mss_norm_workspace_bytes.argtypes = [nd, i, ctypes.POINTER(sz)]
+        L.mss_add_norm.argtypes = [nd, ns] + [p] * 8
+        L.mss_add_norm_backward.argtypes = [nd, ns] + [p] * 12 + [sz, p]
+        L.mss_gated_norm.argtypes = [nd, ns] + [p] * 8
+        L.mss_gated_norm_backward.argtypes = [nd, ns] + [p] * 12 + [sz, p]
+        for f in ("mss_gated_workspace_bytes", "mss_gated_scan", "mss_gated_scan_backward",
+                  "mss_gated_step", "mss_norm_workspace_bytes", "mss_add_norm",
+                  "mss_add_norm_backward", "mss_gated_norm", "mss_gated_norm_backward"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("mss_conv1d_silu", "mss_selective_scan", "mss_mamba1_core",
                   "mss_selective_step", "mss_selective_scan_strided", "mss_mamba1_core_strided",
                   "mss_workspace_bytes", "mss_selective_scan_backward",
@@ -497,3 +553,401 @@ def ssd_scan(x, dt, A_log, B, C, D_vec=None, dt_bias=None, h0=None, *, batch, se
         _ptr(h0, "h0", (batch, H, P, N), False), _ptr(y, "y", (M, H * P)),
         _ptr(hl, "h_last", (batch, H, P, N), False), _stream(stream)))
     return y, hl
+
+
+# ---- gated linear recurrence and block norms ---------------------------------
+
+GATES = {"sigmoid": 0, "decay": 1, "log": 2}      # MSS_GATE_*
+NORM_KINDS = {"rms": 0, "layer": 1}               # MSS_NORM_*
+GATE_ORDERS = {"before": 0, "after": 1}           # MSS_GATE_*_NORM
+
+
+def _choice(table, value, name):
+    try:
+        return table[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be one of {', '.join(map(repr, table))}") from None
+
+
+@functools.lru_cache(maxsize=None)
+def _dtype_codes():
+    torch = _torch()
+    return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}     # MSS_F32, ...
+
+
+@functools.lru_cache(maxsize=1024)
+def make_gated_dims(batch, seq_len, d_inner, dtype, gate, gate_scale=8.0) -> GatedDims:
+    """Parameter block of the mss_gated_* calls (dtype, gate: MSS_* codes)."""
+    return GatedDims(ctypes.sizeof(GatedDims), 0, dtype, gate, batch, seq_len, d_inner,
+                     gate_scale, 0)
+
+
+@functools.lru_cache(maxsize=1024)
+def make_gated_strides(*strides) -> GatedStrides:
+    """Row strides x, r, i, z, y, dx, dr, di, dz (trailing ones may be left out)."""
+    return GatedStrides(ctypes.sizeof(GatedStrides), 0, *strides)
+
+
+@functools.lru_cache(maxsize=1024)
+def make_norm_dims(rows, width, dtype, res_dtype, kind, order=0, groups=1, eps=1e-6,
+                   alpha=1.0) -> NormDims:
+    """Parameter block of the norm calls (dtype, res_dtype, kind, order: MSS_* codes)."""
+    return NormDims(ctypes.sizeof(NormDims), 0, dtype, res_dtype, kind, order, rows, width, groups,
+                    eps, alpha)
+
+
+@functools.lru_cache(maxsize=1024)
+def make_norm_strides(*strides) -> NormStrides:
+    """Row strides x, z, residual, s, y, ds, dx, dz, dresidual (trailing ones may be left out)."""
+    return NormStrides(ctypes.sizeof(NormStrides), 0, *strides)
+
+
+class _Call:
+    """Argument checks of one call: the current device and the activation type."""
+
+    def __init__(self, like, name):
+        torch = _torch()
+        if not isinstance(like, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not like.is_cuda:
+            raise ValueError(f"{name} must be on the GPU")
+        if like.dtype not in _dtype_codes():
+            raise TypeError(f"{name} must be float32, bfloat16 or float16, got {like.dtype}")
+        self.tensor, self.f32 = torch.Tensor, torch.float32
+        self.dev = torch.cuda.current_device()
+        self.like, self.dtype = like, like.dtype
+        self.code = _dtype_codes()[like.dtype]
+
+    def _basic(self, t, name, dtype, shape):
+        if not isinstance(t, self.tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != self.dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{self.dev}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+    def rows(self, t, name, rows, cols, dtype=None, required=True):
+        """(pointer, row stride) of a (rows, cols) activation whose rows may be strided."""
+        if t is None:
+            if required:
+                raise ValueError(f"{name} is required")
+            return None, cols
+        self._basic(t, name, dtype or self.dtype, (rows, cols))
+        row, col = t.stride()
+        if cols > 1 and rows > 0 and col != 1:
+            raise ValueError(f"{name}: columns must be contiguous")
+        return t.data_ptr() or None, row if rows > 1 else cols
+
+    def dense(self, t, name, shape, dtype=None, required=False):
+        """Pointer of a contiguous tensor (float32 unless said otherwise)."""
+        if t is None:
+            if required:
+                raise ValueError(f"{name} is required")
+            return None
+        self._basic(t, name, dtype or self.f32, shape)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr() or None
+
+    def empty(self, shape, dtype=None):
+        return _torch().empty(shape, dtype=dtype or self.dtype, device=self.like.device)
+
+    def workspace(self, need, workspace, stream):
+        """(pointer, bytes, tensor) of the caller's workspace, or of a fresh one."""
+        if workspace is None:
+            if need == 0:
+                return None, 0, None
+            workspace = self.empty((need + 256,), _torch().uint8)
+            if stream is not None:
+                workspace.record_stream(stream)
+        elif (not isinstance(workspace, self.tensor) or workspace.dtype != _torch().uint8
+              or workspace.get_device() != self.dev or not workspace.is_contiguous()):
+            raise TypeError("workspace must be a contiguous uint8 tensor on the current GPU")
+        base = workspace.data_ptr()
+        pad = (-base) % 256
+        return base + pad, max(0, workspace.numel() - pad), workspace
+
+
+@functools.lru_cache(maxsize=1024)
+def gated_workspace_bytes(op, *, batch, seq_len, d_inner, gate) -> int:
+    """Workspace bytes of ``gated_scan`` (OP_GATED_SCAN) or ``gated_scan_backward``
+    (OP_GATED_SCAN_BACKWARD)."""
+    dims = make_gated_dims(batch, seq_len, d_inner, 0, _choice(GATES, gate, "gate"))
+    n = ctypes.c_size_t(0)
+    _check("mss_gated_workspace_bytes",
+           lib().mss_gated_workspace_bytes(ctypes.byref(dims), op, ctypes.byref(n)))
+    return int(n.value)
+
+
+@functools.lru_cache(maxsize=1024)
+def norm_workspace_bytes(op, *, rows, width, groups=1) -> int:
+    """Workspace bytes of ``add_norm_backward`` (OP_ADD_NORM_BACKWARD) or
+    ``gated_norm_backward`` (OP_GATED_NORM_BACKWARD)."""
+    dims = make_norm_dims(rows, width, 0, 0, 0, 0, groups)
+    n = ctypes.c_size_t(0)
+    _check("mss_norm_workspace_bytes",
+           lib().mss_norm_workspace_bytes(ctypes.byref(dims), op, ctypes.byref(n)))
+    return int(n.value)
+
+
+def _ref(block):
+    return ctypes.byref(block)
+
+
+def _flag(t, shape, call, dtype=None):
+    """An optional output given as False / True (allocate) or a tensor."""
+    if isinstance(t, bool):
+        return call.empty(shape, dtype or call.f32) if t else None
+    return t
+
+
+def _gated_inputs(c, x, r, i, decay, z, rows, D, gate):
+    if gate != "decay" and (i is not None or decay is not None):
+        raise ValueError(f"i and decay belong to gate='decay', not {gate!r}")
+    return (c.rows(x, "x", rows, D), c.rows(r, "r", rows, D),
+            c.rows(i, "i", rows, D, required=gate == "decay"),
+            c.dense(decay, "decay", (D,), required=gate == "decay"),
+            c.rows(z, "z", rows, D, required=False))
+
+
+def _reset(c, reset, rows):
+    if reset is not None and reset.dtype == _torch().bool:
+        reset = reset.view(_torch().uint8)
+    return c.dense(reset, "reset", (rows,), _torch().uint8)
+
+
+def gated_ckpt_steps(seq_len) -> int:
+    """Rows of gated_scan's checkpoints: ceil(seq_len / 64)."""
+    return -(-seq_len // GATED_CKPT_STEPS)
+
+
+def gated_scan(x, r, i=None, decay=None, z=None, h0=None, reset=None, *, batch, seq_len, gate,
+               gate_scale=8.0, h_ckpt=False, h_last=False, out=None, workspace=None, stream=None):
+    """Gated linear recurrence h_t = v_t + a_t h_{t-1}, y_t = h_t SiLU(z_t) (h_t without z).
+    Returns (y, h_ckpt, h_last).
+
+    ``gate``: "sigmoid" (a = sigma(r), v = (1 - a) x), "decay" (a = exp(-gate_scale
+    softplus(decay) sigma(r)), v = sqrt(1 - a^2) sigma(i) x) or "log" (a = exp(r), v = x).
+    x, r, i, z, out: (batch*seq_len, D) float32, bfloat16 or float16, all the same, rows may
+    be strided; decay (D,), h0 (batch, D) float32; reset (batch*seq_len,) uint8 or bool: where
+    set, the state carried into that step is dropped.
+    ``h_ckpt`` / ``h_last``: False (skip), True (allocate) or an output tensor: the state
+    entering every 64th step (batch, ceil(seq_len/64), D), which the backward pass takes, and
+    the final state (batch, D), both float32.
+    ``workspace``: uint8 GPU tensor of at least ``gated_workspace_bytes(OP_GATED_SCAN, ...)``
+    + 256 bytes (allocated here when omitted)."""
+    D, M = x.shape[-1], batch * seq_len
+    c = _Call(x, "x")
+    code = _choice(GATES, gate, "gate")
+    (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, M, D, gate)
+    y = out if out is not None else c.empty((M, D))
+    py, ly = c.rows(y, "out", M, D)
+    ck = _flag(h_ckpt, (batch, gated_ckpt_steps(seq_len), D), c)
+    hl = _flag(h_last, (batch, D), c)
+    need = gated_workspace_bytes(OP_GATED_SCAN, batch=batch, seq_len=seq_len, d_inner=D, gate=gate)
+    wp, wn, _keep = c.workspace(need, workspace, stream)
+    _check("mss_gated_scan", lib().mss_gated_scan(
+        _ref(make_gated_dims(batch, seq_len, D, c.code, code, gate_scale)),
+        _ref(make_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
+        c.dense(h0, "h0", (batch, D)), _reset(c, reset, M), py,
+        c.dense(ck, "h_ckpt", (batch, gated_ckpt_steps(seq_len), D)),
+        c.dense(hl, "h_last", (batch, D)), wp, wn, _stream(stream)))
+    return y, ck, hl
+
+
+def gated_scan_backward(x, r, i, decay, z, reset, h_ckpt, dout, *, batch, seq_len, gate,
+                        gate_scale=8.0, dh_last=None, need_dh0=False, out=None, workspace=None,
+                        stream=None):
+    """Gradients of ``gated_scan`` against ``dout`` (batch*seq_len, D), the gradient of y, and
+    ``dh_last`` (batch, D), that of h_last (0 when None).
+
+    ``h_ckpt``: the forward's checkpoints (a call with the same inputs and ``h_ckpt=True``).
+    Returns a dict: dx, dr, di, dz (M, D) in x's type, ddecay (D,) and dh0 (batch, D) float32;
+    di and ddecay are None unless gate is "decay", dz is None when z is, dh0 unless
+    ``need_dh0``.  ``out``: optional dict of output tensors for some of them (dx, dr, di, dz
+    may be row-strided).  ``workspace`` as in gated_scan, with OP_GATED_SCAN_BACKWARD."""
+    D, M = x.shape[-1], batch * seq_len
+    c = _Call(x, "x")
+    code = _choice(GATES, gate, "gate")
+    (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, M, D, gate)
+    want = {"dx": True, "dr": True, "di": gate == "decay", "ddecay": gate == "decay",
+            "dz": z is not None, "dh0": need_dh0}
+    g = _outputs(c, want, out, {"ddecay": (D,), "dh0": (batch, D)}, (M, D))
+    (pdx, ldx), (pdr, ldr), (pdi, ldi), (pdz, ldz) = (
+        c.rows(g[k], k, M, D, required=False) for k in ("dx", "dr", "di", "dz"))
+    po, lo = c.rows(dout, "dout", M, D)
+    need = gated_workspace_bytes(OP_GATED_SCAN_BACKWARD, batch=batch, seq_len=seq_len, d_inner=D,
+                                 gate=gate)
+    wp, wn, _keep = c.workspace(need, workspace, stream)
+    _check("mss_gated_scan_backward", lib().mss_gated_scan_backward(
+        _ref(make_gated_dims(batch, seq_len, D, c.code, code, gate_scale)),
+        _ref(make_gated_strides(lx, lr, li, lz, lo, ldx, ldr, ldi, ldz)), px, pr, pi, pdec, pz,
+        _reset(c, reset, M),
+        c.dense(h_ckpt, "h_ckpt", (batch, gated_ckpt_steps(seq_len), D), required=True), po,
+        c.dense(dh_last, "dh_last", (batch, D)), pdx, pdr, pdi,
+        c.dense(g["ddecay"], "ddecay", (D,)), pdz, c.dense(g["dh0"], "dh0", (batch, D)),
+        wp, wn, _stream(stream)))
+    return g
+
+
+def _outputs(c, want, out, f32_shapes, shape, types=None):
+    """The dict of results: the caller's tensors, fresh ones, or None where not wanted."""
+    out = out or {}
+    unknown = [k for k in out if k not in want]
+    if unknown:
+        raise ValueError(f"out has no place for {', '.join(unknown)}")
+    g = {}
+    for k, w in want.items():
+        if not w:
+            g[k] = None
+        elif out.get(k) is not None:
+            g[k] = out[k]
+        elif k in f32_shapes:
+            g[k] = c.empty(f32_shapes[k], c.f32)
+        else:
+            g[k] = c.empty(shape, (types or {}).get(k))
+    return g
+
+
+def gated_step(x, r, i, decay, z, h, *, gate, gate_scale=8.0, out=None, stream=None):
+    """One token per sequence of ``gated_scan``: x, r, i, z (batch, D); updates ``h``
+    (batch, D) float32 in place.  Returns y (batch, D)."""
+    batch, D = x.shape
+    c = _Call(x, "x")
+    code = _choice(GATES, gate, "gate")
+    (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, batch, D,
+                                                                 gate)
+    y = out if out is not None else c.empty((batch, D))
+    py, ly = c.rows(y, "out", batch, D)
+    _check("mss_gated_step", lib().mss_gated_step(
+        _ref(make_gated_dims(batch, 1, D, c.code, code, gate_scale)),
+        _ref(make_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
+        c.dense(h, "h", (batch, D), required=True), py, _stream(stream)))
+    return y
+
+
+def _res_code(c, t, name):
+    code = _dtype_codes().get(t.dtype)
+    if code is None or (code != c.code and t.dtype != c.f32):
+        raise TypeError(f"{name} must be {c.dtype} or float32, got {t.dtype}")
+    return code
+
+
+def add_norm(x, residual, weight, bias=None, scale=None, *, kind="rms", eps=1e-6, alpha=1.0,
+             res_dtype=None, out=None, residual_out=None, stream=None):
+    """Before a block: s = residual + alpha scale x, y = norm(s) weight + bias.  Returns (y, s).
+
+    x (M, D) float32, bfloat16 or float16; residual (M, D) of x's type or float32, or None (0);
+    weight, bias, scale (D,) float32; ``kind``: "rms" or "layer".  s has the residual's type
+    (``res_dtype``, x's by default, where residual is None) and the norm reads s as that type
+    holds it.  ``residual_out`` may be ``residual`` itself: updated in place.  Rows of x,
+    residual and the outputs may be strided."""
+    M, D = x.shape
+    c = _Call(x, "x")
+    rt = (residual.dtype if residual is not None else
+          residual_out.dtype if residual_out is not None else res_dtype or c.dtype)
+    s = residual_out if residual_out is not None else c.empty((M, D), rt)
+    rc = _res_code(c, s, "the residual stream")
+    y = out if out is not None else c.empty((M, D))
+    px, lx = c.rows(x, "x", M, D)
+    pr, lr = c.rows(residual, "residual", M, D, s.dtype, False)
+    ps, ls = c.rows(s, "residual_out", M, D, s.dtype)
+    py, ly = c.rows(y, "out", M, D)
+    _check("mss_add_norm", lib().mss_add_norm(
+        _ref(make_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
+        _ref(make_norm_strides(lx, 0, lr, ls, ly)), px, pr,
+        c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)),
+        c.dense(scale, "scale", (D,)), ps, py, _stream(stream)))
+    return y, s
+
+
+def add_norm_backward(s, weight, dy, ds=None, x=None, scale=None, *, bias=False, kind="rms",
+                      eps=1e-6, alpha=1.0, need_dx=True, out=None, workspace=None, stream=None):
+    """Gradients of ``add_norm`` against ``dy`` (M, D), the gradient of y, and ``ds`` (M, D),
+    what else reaches s (0 when None).
+
+    ``s``: the forward's residual stream; ``x``: the forward's x, needed with ``scale``.
+    Returns a dict: dx in dy's type (None unless ``need_dx``), dresidual in s's, dweight,
+    dbias (with ``bias``) and dscale (with ``scale``) float32.  ``out`` and ``workspace`` as in
+    gated_scan_backward (``norm_workspace_bytes(OP_ADD_NORM_BACKWARD, ...)``)."""
+    M, D = dy.shape
+    c = _Call(dy, "dy")
+    rc = _res_code(c, s, "s")
+    want = {"dx": need_dx, "dresidual": True, "dweight": True, "dbias": bool(bias),
+            "dscale": scale is not None}
+    f32 = {k: (D,) for k in ("dweight", "dbias", "dscale")}
+    g = _outputs(c, want, out, f32, (M, D), {"dresidual": s.dtype})
+    ps, ls = c.rows(s, "s", M, D, s.dtype)
+    po, lo = c.rows(dy, "dy", M, D)
+    pds, lds = c.rows(ds, "ds", M, D, s.dtype, False)
+    px, lx = c.rows(x, "x", M, D, required=scale is not None)
+    pdx, ldx = c.rows(g["dx"], "dx", M, D, required=False)
+    pdr, ldr = c.rows(g["dresidual"], "dresidual", M, D, s.dtype)
+    wp, wn, _keep = c.workspace(norm_workspace_bytes(OP_ADD_NORM_BACKWARD, rows=M, width=D),
+                                workspace, stream)
+    _check("mss_add_norm_backward", lib().mss_add_norm_backward(
+        _ref(make_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
+        _ref(make_norm_strides(lx, 0, 0, ls, lo, lds, ldx, 0, ldr)), ps,
+        c.dense(weight, "weight", (D,), required=True), po, pds, px,
+        c.dense(scale, "scale", (D,)), pdx, pdr, c.dense(g["dweight"], "dweight", (D,)),
+        c.dense(g["dbias"], "dbias", (D,)), c.dense(g["dscale"], "dscale", (D,)), wp, wn,
+        _stream(stream)))
+    return g
+
+
+def gated_norm(x, z, weight, bias=None, residual=None, scale=None, *, groups=1, order="before",
+               kind="rms", eps=1e-6, alpha=1.0, out=None, stream=None):
+    """After a block: n = norm(x SiLU(z)) weight + bias (``order="before"``) or
+    n = (norm(x) weight + bias) SiLU(z) (``order="after"``); y = alpha scale n, plus residual
+    when given.  Returns y.
+
+    x, z, residual, y (M, D) float32, bfloat16 or float16, all the same, rows may be strided;
+    z, residual may be None; weight, bias, scale (D,) float32; the norm runs over each of
+    ``groups`` equal groups of channels."""
+    M, D = x.shape
+    c = _Call(x, "x")
+    y = out if out is not None else c.empty((M, D))
+    px, lx = c.rows(x, "x", M, D)
+    pz, lz = c.rows(z, "z", M, D, required=False)
+    pr, lr = c.rows(residual, "residual", M, D, required=False)
+    py, ly = c.rows(y, "out", M, D)
+    _check("mss_gated_norm", lib().mss_gated_norm(
+        _ref(make_norm_dims(M, D, c.code, c.code, _choice(NORM_KINDS, kind, "kind"),
+                            _choice(GATE_ORDERS, order, "order"), groups, eps, alpha)),
+        _ref(make_norm_strides(lx, lz, lr, 0, ly)), px, pz,
+        c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)), pr,
+        c.dense(scale, "scale", (D,)), py, _stream(stream)))
+    return y
+
+
+def gated_norm_backward(x, z, weight, bias, scale, dout, *, groups=1, order="before", kind="rms",
+                        eps=1e-6, alpha=1.0, out=None, workspace=None, stream=None):
+    """Gradients of ``gated_norm`` against ``dout`` (M, D) (the residual's is dout itself).
+
+    Returns a dict: dx, dz in x's type (dz None when z is), dweight, dbias (with ``bias``) and
+    dscale (with ``scale``) float32.  ``out`` and ``workspace`` as in gated_scan_backward
+    (``norm_workspace_bytes(OP_GATED_NORM_BACKWARD, ...)``)."""
+    M, D = x.shape
+    c = _Call(x, "x")
+    want = {"dx": True, "dz": z is not None, "dweight": True, "dbias": bias is not None,
+            "dscale": scale is not None}
+    g = _outputs(c, want, out, {k: (D,) for k in ("dweight", "dbias", "dscale")}, (M, D))
+    px, lx = c.rows(x, "x", M, D)
+    pz, lz = c.rows(z, "z", M, D, required=False)
+    po, lo = c.rows(dout, "dout", M, D)
+    pdx, ldx = c.rows(g["dx"], "dx", M, D)
+    pdz, ldz = c.rows(g["dz"], "dz", M, D, required=False)
+    wp, wn, _keep = c.workspace(
+        norm_workspace_bytes(OP_GATED_NORM_BACKWARD, rows=M, width=D, groups=groups), workspace,
+        stream)
+    _check("mss_gated_norm_backward", lib().mss_gated_norm_backward(
+        _ref(make_norm_dims(M, D, c.code, c.code, _choice(NORM_KINDS, kind, "kind"),
+                            _choice(GATE_ORDERS, order, "order"), groups, eps, alpha)),
+        _ref(make_norm_strides(lx, lz, 0, 0, lo, 0, ldx, ldz)), px, pz,
+        c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)),
+        c.dense(scale, "scale", (D,)), po, pdx, pdz, c.dense(g["dweight"], "dweight", (D,)),
+        c.dense(g["dbias"], "dbias", (D,)), c.dense(g["dscale"], "dscale", (D,)), wp, wn,
+        _stream(stream)))
+    return g

@@ -1,0 +1,49 @@
+// block_math.h -- element types and gate functions of the gated recurrence and
+// the block norms (gated_kernel.hip, norm_kernel.hip).
+#pragma once
+
+#include "device_math.h"
+
+namespace mss {
+
+using bf16 = __bf16;
+using f16 = _Float16;
+
+// sigma(v) and 1 - sigma(v), each to a few ulp of itself: the exponential of
+// -|v| never overflows and neither result is formed by a subtraction.
+// v = +-inf gives exactly 0 and 1.
+__device__ __forceinline__ void sigmoid2(float v, float& s, float& c) {
+    const float e = ex2(-kLog2e * __builtin_fabsf(v));
+    const float big = rcp(1.0f + e);
+    const float small = e * big;
+    s = v >= 0.0f ? big : small;
+    c = v >= 0.0f ? small : big;
+}
+
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + ex2(-kLog2e * v)); }
+
+// SiLU(v) = v sigma(v) and its slope sigma(v) (1 + v (1 - sigma(v))).
+__device__ __forceinline__ void silu2(float v, float& f, float& slope) {
+    float s, c;
+    sigmoid2(v, s, c);
+    f = v * s;
+    slope = s * __builtin_fmaf(v, c, 1.0f);
+}
+
+// sqrt(1 - a^2) for a = 2^l2, l2 <= 0: -expm1(q) with q = 2 ln(2) l2, by its
+// series for |q| < 1/4 (seven terms, the first left out is below 6e-9
+// relative), where 1 - a^2 would cancel.
+__device__ __forceinline__ float decay_input_scale(float l2, float a) {
+    const float q = (2.0f * kLn2) * l2;
+    float p = __builtin_fmaf(q, 1.0f / 5040.0f, 1.0f / 720.0f);
+    p = __builtin_fmaf(q, p, 1.0f / 120.0f);
+    p = __builtin_fmaf(q, p, 1.0f / 24.0f);
+    p = __builtin_fmaf(q, p, 1.0f / 6.0f);
+    p = __builtin_fmaf(q, p, 0.5f);
+    p = __builtin_fmaf(q, p, 1.0f);
+    const float near0 = -q * p;
+    const float far0 = __builtin_fmaf(-a, a, 1.0f);
+    return __builtin_amdgcn_sqrtf(q > -0.25f ? near0 : far0);
+}
+
+}  // namespace mss
