@@ -222,7 +222,7 @@ int zero_params(const mss::NormArgs& a, hipStream_t stream) {
 // Bytes of the norm backward's workspace for these sizes.
 bool norm_need(const mss::NormArgs& a, int64_t& need) {
     need = 0;
-    return a.M == 0 || a.D == 0 || mss::norm_bwd_workspace(a.M, a.D, need);
+    return a.M == 0 || a.D == 0 || mss::norm_bwd_workspace(a.M, a.D, a.G, need);
 }
 
 }  // namespace

@@ -73,7 +73,7 @@ struct NormArgs {
     void* ws;
 };
 
-bool norm_bwd_workspace(int64_t M, int64_t D, int64_t& bytes);
+bool norm_bwd_workspace(int64_t M, int64_t D, int64_t G, int64_t& bytes);
 hipError_t launch_add_norm(const NormArgs& a, hipStream_t st);
 hipError_t launch_add_norm_bwd(const NormArgs& a, hipStream_t st);
 hipError_t launch_gated_norm(const NormArgs& a, hipStream_t st);

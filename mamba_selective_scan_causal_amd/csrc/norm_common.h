@@ -1,0 +1,249 @@
+// norm_common.h -- what the add_norm and gated_norm kernels share: rows held
+// in registers by a team of lanes, and the team's sums.
+//
+// A team holds one group of n channels of one row: 16 lanes, a wave, or (TEAM
+// = kGroup) a workgroup of as many waves as the row needs.  Lane l keeps the
+// NC vectors of V channels that start at V (l + j lanes).  Every input is read
+// once, in 16-byte pieces (2-byte types 8 channels, fp32 4) that stay in
+// registers as they were read, the moments come from there, and one or two
+// rounds of sums per row (RMS: one; LAYER: the mean first, so that the
+// variance is that of the centred values) are all the lanes exchange.
+// Vectors are read and written with the element's alignment (global memory
+// takes unaligned vector accesses), so strided rows and odd widths run the
+// same code and give the same bits; only a row's last, partial vector goes
+// element by element.  A team walks several rows, reading the next one while
+// it works on this one; the per-channel parameters are read once, and the
+// backward keeps its sums of the parameter gradients in registers.
+#pragma once
+
+#include <type_traits>
+
+#include "block_math.h"
+#include "launch_block.h"
+
+namespace mss {
+
+constexpr int kGroup = 0;   // TEAM: the workgroup
+
+template <typename T>
+constexpr int kVec = sizeof(T) == 4 ? 4 : 8;
+
+// V channels as memory holds them.
+template <typename T, int V>
+struct RowVec {
+    typedef T type __attribute__((ext_vector_type(V), aligned(alignof(T))));
+    type t;
+
+    // Channels c .. c + V - 1 of a row (group) of n; zeros past its end.
+    __device__ __forceinline__ void load(const T* p, int c, int n) {
+        if (c + V <= n) {
+            t = *reinterpret_cast<const type*>(p + c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; e++) t[e] = c + e < n ? p[c + e] : static_cast<T>(0.0f);
+        }
+    }
+    __device__ __forceinline__ void store(T* p, int c, int n) const {
+        if (c + V <= n) {
+            *reinterpret_cast<type*>(p + c) = t;
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; e++)
+                if (c + e < n) p[c + e] = t[e];
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < V; e++) t[e] = static_cast<T>(0.0f);
+    }
+    // Tells the compiler nothing it computed from the vector still holds, so
+    // that it keeps the 2-byte values across a round of sums and widens them
+    // again afterwards, not their fp32 copies (twice the registers).
+    __device__ __forceinline__ void narrow() {
+        typedef unsigned int words __attribute__((ext_vector_type(V * sizeof(T) / 4)));
+        words u = __builtin_bit_cast(words, t);
+        asm volatile("" : "+v"(u));
+        t = __builtin_bit_cast(type, u);
+    }
+    __device__ __forceinline__ float operator[](int e) const { return static_cast<float>(t[e]); }
+    __device__ __forceinline__ void set(int e, float v) { t[e] = static_cast<T>(v); }
+};
+
+// A per-channel parameter, or `otherwise` where it is not given; 0 past the end.
+template <int V>
+__device__ __forceinline__ void load_param(const float* p, int c, int n, float otherwise,
+                                           float (&v)[V]) {
+    RowVec<float, V> t;
+    t.zero();
+    if (p && c < n) t.load(p, c, n);
+#pragma unroll
+    for (int e = 0; e < V; e++) v[e] = p ? t[e] : c + e < n ? otherwise : 0.0f;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL,
+                                                                  0xf, 0xf, true));
+}
+
+__device__ __forceinline__ float read_lane(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+template <int TEAM>
+__device__ __forceinline__ int team_lanes() {
+    return TEAM == kGroup ? blockDim.x : TEAM;
+}
+template <int TEAM>
+__device__ __forceinline__ int team_lane() {
+    return TEAM == kGroup ? threadIdx.x : threadIdx.x % (TEAM ? TEAM : 1);
+}
+
+// The team's number in its workgroup, known to be the same for all lanes of a
+// wave where it is, so that row addresses stay in scalar registers.
+template <int TEAM>
+__device__ __forceinline__ int team_of() {
+    const int team = TEAM == kGroup ? 0 : threadIdx.x / (TEAM ? TEAM : 1);
+    return TEAM == 64 ? __builtin_amdgcn_readfirstlane(team) : team;
+}
+
+// LDS floats of team_sum for K sums at once.
+template <int TEAM, int K>
+constexpr int kSumLds = TEAM == kGroup ? 2 * K * 16 : 1;
+
+// The sum over the team in each of its lanes, K sums at once, always in the
+// same order.  The two halves of `lds` take turns from call to call, so that
+// a wave that is a round ahead never writes what another still reads, with
+// one barrier a round.
+template <int TEAM, int K>
+__device__ __forceinline__ void team_sum(float (&v)[K], float* lds, int& turn) {
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+        v[k] = dpp_add<0x128>(v[k]);   // rotations inside 16 lanes, by 8, 4, 2, 1
+        v[k] = dpp_add<0x124>(v[k]);
+        v[k] = dpp_add<0x122>(v[k]);
+        v[k] = dpp_add<0x121>(v[k]);
+        if constexpr (TEAM != 16)
+            v[k] = (read_lane(v[k], 0) + read_lane(v[k], 16)) +
+                   (read_lane(v[k], 32) + read_lane(v[k], 48));
+    }
+    if constexpr (TEAM == kGroup) {
+        const int waves = blockDim.x / 64;
+        float* at = lds + turn * (K * 16);
+        turn ^= 1;
+        if (threadIdx.x % 64 == 0) {
+#pragma unroll
+            for (int k = 0; k < K; k++) at[k * 16 + threadIdx.x / 64] = v[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; k++) v[k] = 0.0f;
+        for (int w = 0; w < waves; w++)
+#pragma unroll
+            for (int k = 0; k < K; k++) v[k] += at[k * 16 + w];
+    }
+}
+
+// The workgroup's share of K sums per channel, in the row of the workspace
+// that is its own: acc[k] of its teams added in order through `lds`.  Every
+// thread of the workgroup calls it.
+template <int TEAM, int NC, int V, int K>
+__device__ __forceinline__ void write_part(float (&acc)[K][NC][V], float* lds, float* part,
+                                           int64_t D, int64_t g0, int n) {
+    const int lane = team_lane<TEAM>();
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+        float* out = part + k * D + g0;
+        if constexpr (TEAM == kGroup) {
+#pragma unroll
+            for (int j = 0; j < NC; j++) {
+                const int c = V * (lane + j * blockDim.x);
+                RowVec<float, V> t;
+#pragma unroll
+                for (int e = 0; e < V; e++) t.set(e, acc[k][j][e]);
+                if (c < n) t.store(out, c, n);
+            }
+        } else {
+            constexpr int slots = TEAM * NC * V, teams = 256 / (TEAM ? TEAM : 1);
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < NC; j++)
+#pragma unroll
+                for (int e = 0; e < V; e++)
+                    lds[team_of<TEAM>() * slots + V * (lane + j * TEAM) + e] = acc[k][j][e];
+            __syncthreads();
+            for (int c = threadIdx.x; c < n; c += 256) {
+                float s = 0.0f;
+#pragma unroll
+                for (int t = 0; t < teams; t++) s += lds[t * slots + c];
+                out[c] = s;
+            }
+        }
+    }
+}
+
+template <int TEAM, int NC, int V>
+constexpr int kPartLds = TEAM == kGroup ? 1 : 256 * NC * V;
+
+template <typename T>
+__device__ __forceinline__ T* row_of(const void* p, int64_t row, int64_t ld, int64_t col = 0) {
+    return p ? const_cast<T*>(static_cast<const T*>(p)) + row * ld + col : nullptr;
+}
+
+// dw, db and dscale from `rows` rows of K sums per channel in the workspace:
+//   add_norm    S[0] = sum dy n, S[1] = sum dy, S[2] = sum dresidual x
+//   gated_norm  S[0] = sum d n, S[1] = sum d, with d = dout (times the gate
+//               where it comes after the norm): dw = k S[0], db = k S[1],
+//               dscale = alpha (w S[0] + b S[1]), k = alpha scale
+hipError_t launch_norm_params(const NormArgs& a, bool gated, int64_t rows, int K, hipStream_t st);
+
+// ---- sizes -------------------------------------------------------------------
+
+// A launch: the team, its workgroup's threads, and the rows that a workgroup
+// takes at a time.
+template <int TEAM_, int NC_>
+struct Shape {
+    static constexpr int TEAM = TEAM_, NC = NC_;
+    int threads, rows;
+};
+
+// Workgroups per group of channels: two thousand lanes for each of 256 CUs
+// over all groups (a CU's waves, or twice what its registers hold: the next
+// ones start as others end), none without a row of its own.  `most` bounds
+// the backward's, whose workgroups each write a row of partial sums.
+inline int64_t row_groups(int64_t M, int64_t G, int threads, int rows, int64_t most) {
+    int64_t p = 256 * 2048 / threads;
+    if (p > most) p = most;
+    p = (p + G - 1) / G;
+    const int64_t all = (M + rows - 1) / rows;
+    return p < all ? p : all;
+}
+constexpr int64_t kPartRows = 1024;   // backward
+constexpr int64_t kRowGroups = 1 << 20;
+
+// f(Shape) for groups of n channels, V to a vector: a quarter of a wave or a
+// wave where one vector a lane is enough, else a workgroup with one (two past
+// 1024 lanes).  One vector a lane keeps the backward passes at four waves or
+// more on a SIMD (the backward of gated_norm in bf16 takes about 100 registers
+// with one vector and over 200 with two).  False for wider groups.
+template <int V, typename F>
+bool by_width(int64_t n, F f) {
+    const int64_t nv = (n + V - 1) / V;
+    if (nv <= 16)
+        f(Shape<16, 1>{256, 16});
+    else if (nv <= 64)
+        f(Shape<64, 1>{256, 4});
+    else if (nv <= 1024)
+        f(Shape<kGroup, 1>{static_cast<int>((nv + 63) / 64 * 64), 1});
+    else if (nv <= 1536)
+        f(Shape<kGroup, 2>{static_cast<int>((nv + 127) / 128 * 64), 1});
+    else
+        return false;
+    return true;
+}
+
+// Threads of a kernel's largest workgroup.
+template <int TEAM, int NC>
+constexpr int kMaxThreads = TEAM != kGroup ? 256 : NC == 1 ? 1024 : 768;
+
+}  // namespace mss

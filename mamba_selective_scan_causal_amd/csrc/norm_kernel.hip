@@ -1,292 +1,409 @@
-// norm_kernel.hip -- the norms before and after a block (mss_add_norm,
-// mss_gated_norm) and their backward passes.
+// norm_kernel.hip -- the norm before a block: s = residual + alpha scale x,
+// y = norm(s) w + b, and its backward pass (mss_add_norm,
+// mss_add_norm_backward); the sum of the parameter gradients' parts that
+// gated_norm shares.
 //
-// One workgroup per row: the row's groups are normalised one after the other,
-// each in a pass for its moments and one that writes.  The backward adds its
-// rows' shares of the parameter gradients to a row of the workspace that is
-// its own, and a second kernel sums those rows in order.
-#include "block_math.h"
-#include "launch_block.h"
+// Bound by HBM: the forward reads x and the residual and writes s and y, the
+// backward reads s, dy, ds (and x) and writes dresidual and dx, each once.
+#include "norm_common.h"
 
 namespace mss {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int64_t kPartRows = 512;
+// s of one channel.  The product is rounded before the sum, as where the two
+// are separate operations: with a half-precision stream and a scale like 0.7
+// many sums lie next to the middle of two representable values, and a fused
+// product would round them the other way.
+__device__ __forceinline__ float scaled_sum(float res, float k, float x) {
+    return __fadd_rn(res, __fmul_rn(k, x));
+}
 
-// Sum of `v` over the workgroup, in every thread (two values at once).
-__device__ __forceinline__ void block_sum2(float& a, float& b, float* lds) {
+// A row as it was read: x and the residual, or s, dy, ds and x.
+template <typename T, typename R, int NC>
+struct AddRow {
+    static constexpr int V = kVec<T>;
+    RowVec<R, V> r[NC], ds[NC];
+    RowVec<T, V> x[NC], dy[NC];
+};
+
+template <typename T, typename R, int TEAM, int NC>
+__global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormArgs q) {
+    constexpr int V = kVec<T>;
+    __shared__ float lds[kSumLds<TEAM, 1>];
+    const int n = static_cast<int>(q.D), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
+    const bool layer = q.kind == MSS_NORM_LAYER;
+    const float inv_n = 1.0f / static_cast<float>(n);
+    const int rows = TEAM == kGroup ? 1 : 256 / lanes;
+    const int64_t step = gridDim.x * static_cast<int64_t>(rows);
+    float w[NC][V], b[NC][V], k[NC][V];
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) {
-        a += __shfl_xor(a, m, 64);
-        b += __shfl_xor(b, m, 64);
+    for (int j = 0; j < NC; j++) {
+        const int c = V * (lane + j * lanes);
+        load_param<V>(q.w, c, n, 1.0f, w[j]);
+        load_param<V>(q.b, c, n, 0.0f, b[j]);
+        load_param<V>(q.scale, c, n, 1.0f, k[j]);
+#pragma unroll
+        for (int e = 0; e < V; e++) k[j][e] *= q.alpha;
     }
-    const int wave = threadIdx.x / 64;
-    __syncthreads();
-    if (threadIdx.x % 64 == 0) {
-        lds[2 * wave] = a;
-        lds[2 * wave + 1] = b;
-    }
-    __syncthreads();
-    a = b = 0.0f;
-    for (int w = 0; w < kThreads / 64; w++) {
-        a += lds[2 * w];
-        b += lds[2 * w + 1];
+    auto read = [&](int64_t m, RowVec<R, V>(&res)[NC], RowVec<T, V>(&x)[NC]) {
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            const int c = V * (lane + j * lanes);
+            res[j].zero();
+            x[j].zero();
+            if (c < n && m < q.M) {
+                if (q.res) res[j].load(row_of<R>(q.res, m, q.ld_res), c, n);
+                x[j].load(row_of<T>(q.x, m, q.ld_x), c, n);
+            }
+        }
+    };
+    int turn = 0;
+    int64_t m = blockIdx.x * static_cast<int64_t>(rows) + team_of<TEAM>();
+    RowVec<R, V> res[NC];
+    RowVec<T, V> x[NC];
+    read(m, res, x);
+    for (; m < q.M; m += step) {
+        RowVec<R, V> s[NC];
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            const int c = V * (lane + j * lanes);
+#pragma unroll
+            for (int e = 0; e < V; e++) s[j].set(e, scaled_sum(res[j][e], k[j][e], x[j][e]));
+            if (c < n) s[j].store(row_of<R>(q.s, m, q.ld_s), c, n);
+        }
+        // the next row; this one has been read, so s may be the residual
+        read(m + step, res, x);
+        float mean = 0.0f;
+        float sum[1] = {0.0f};
+        if (layer) {
+#pragma unroll
+            for (int j = 0; j < NC; j++)
+#pragma unroll
+                for (int e = 0; e < V; e++) sum[0] += s[j][e];
+            team_sum<TEAM>(sum, lds, turn);
+            mean = sum[0] * inv_n;
+            sum[0] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < NC; j++)
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+                const float v = V * (lane + j * lanes) + e < n ? s[j][e] - mean : 0.0f;
+                sum[0] = __builtin_fmaf(v, v, sum[0]);
+            }
+        team_sum<TEAM>(sum, lds, turn);
+        const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], inv_n, q.eps));
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            const int c = V * (lane + j * lanes);
+            RowVec<T, V> y;
+#pragma unroll
+            for (int e = 0; e < V; e++)
+                y.set(e, __builtin_fmaf((s[j][e] - mean) * rstd, w[j][e], b[j][e]));
+            if (c < n) y.store(row_of<T>(q.y, m, q.ld_y), c, n);
+        }
     }
 }
 
-// Mean (0 for RMS) and 1 / deviation of load(c), c in [0, n).
-template <typename F>
-__device__ __forceinline__ void moments(F load, int64_t n, int kind, float eps, float* lds,
-                                        float& mean, float& rstd) {
-    float sum = 0.0f, none = 0.0f;
-    mean = 0.0f;
-    if (kind == MSS_NORM_LAYER) {
-        for (int64_t c = threadIdx.x; c < n; c += kThreads) sum += load(c);
-        block_sum2(sum, none, lds);
-        mean = sum / static_cast<float>(n);
+// EXTRA: db or dscale is wanted besides dw.
+template <typename T, typename R, int TEAM, int NC, bool EXTRA>
+__global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(NormArgs q) {
+    constexpr int V = kVec<T>, K = EXTRA ? 3 : 1;
+    __shared__ float lds[kSumLds<TEAM, 3>];
+    __shared__ float part_lds[kPartLds<TEAM, NC, V>];
+    const int n = static_cast<int>(q.D), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
+    const bool layer = q.kind == MSS_NORM_LAYER;
+    const float inv_n = 1.0f / static_cast<float>(n);
+    const int rows = TEAM == kGroup ? 1 : 256 / lanes;
+    const int64_t step = gridDim.x * static_cast<int64_t>(rows);
+    float w[NC][V], k[NC][V], acc[K][NC][V];
+#pragma unroll
+    for (int j = 0; j < NC; j++) {
+        const int c = V * (lane + j * lanes);
+        load_param<V>(q.w, c, n, 1.0f, w[j]);
+        load_param<V>(q.scale, c, n, 1.0f, k[j]);
+#pragma unroll
+        for (int e = 0; e < V; e++) {
+            k[j][e] *= q.alpha;
+#pragma unroll
+            for (int a = 0; a < K; a++) acc[a][j][e] = 0.0f;
+        }
     }
-    float sq = 0.0f;
-    for (int64_t c = threadIdx.x; c < n; c += kThreads) {
-        const float v = load(c) - mean;
-        sq = __builtin_fmaf(v, v, sq);
+    using Row = AddRow<T, R, NC>;
+    auto read = [&](int64_t m, Row& r) {
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            const int c = V * (lane + j * lanes);
+            r.r[j].zero();
+            r.dy[j].zero();
+            r.ds[j].zero();
+            r.x[j].zero();
+            if (c < n && m < q.M) {
+                r.r[j].load(row_of<R>(q.s, m, q.ld_s), c, n);
+                r.dy[j].load(row_of<T>(q.dy, m, q.ld_y), c, n);
+                if (q.ds) r.ds[j].load(row_of<R>(q.ds, m, q.ld_ds), c, n);
+                if (EXTRA && q.x) r.x[j].load(row_of<T>(q.x, m, q.ld_x), c, n);
+            }
+        }
+    };
+    int turn = 0;
+    int64_t m = blockIdx.x * static_cast<int64_t>(rows) + team_of<TEAM>();
+    Row next;
+    read(m, next);
+    for (; m < q.M; m += step) {
+        Row r = next;
+        read(m + step, next);
+        float mean = 0.0f;
+        if (layer) {
+            float sum[1] = {0.0f};
+#pragma unroll
+            for (int j = 0; j < NC; j++)
+#pragma unroll
+                for (int e = 0; e < V; e++) sum[0] += r.r[j][e];
+            team_sum<TEAM>(sum, lds, turn);
+            mean = sum[0] * inv_n;
+        }
+        // sums of (s - mean)^2, dy w (s - mean) and dy w (dy is 0 past the end)
+        float sums[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < NC; j++)
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+                const float v = V * (lane + j * lanes) + e < n ? r.r[j][e] - mean : 0.0f;
+                const float gw = r.dy[j][e] * w[j][e];
+                sums[0] = __builtin_fmaf(v, v, sums[0]);
+                sums[1] = __builtin_fmaf(gw, v, sums[1]);
+                sums[2] += gw;
+            }
+        team_sum<TEAM>(sums, lds, turn);
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            r.r[j].narrow();
+            r.dy[j].narrow();
+        }
+        const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(sums[0], inv_n, q.eps));
+        const float c1 = sums[1] * inv_n * rstd;
+        const float c2 = layer ? sums[2] * inv_n : 0.0f;
+#pragma unroll
+        for (int j = 0; j < NC; j++) {
+            const int c = V * (lane + j * lanes);
+            RowVec<R, V> dres;
+            RowVec<T, V> dx;
+#pragma unroll
+            for (int e = 0; e < V; e++) {
+                const float nv = (r.r[j][e] - mean) * rstd, g = r.dy[j][e];
+                acc[0][j][e] = __builtin_fmaf(g, nv, acc[0][j][e]);
+                const float t = __builtin_fmaf(g, w[j][e], -__builtin_fmaf(nv, c1, c2));
+                const float d = __builtin_fmaf(rstd, t, r.ds[j][e]);
+                if constexpr (EXTRA) {
+                    acc[1][j][e] += g;
+                    acc[2][j][e] = __builtin_fmaf(d, r.x[j][e], acc[2][j][e]);
+                }
+                dres.set(e, d);
+                dx.set(e, d * k[j][e]);
+            }
+            if (c < n) {
+                dres.store(row_of<R>(q.dres, m, q.ld_dres), c, n);
+                if (q.dx) dx.store(row_of<T>(q.dx, m, q.ld_dx), c, n);
+            }
+        }
     }
-    block_sum2(sq, none, lds);
-    rstd = 1.0f / __builtin_sqrtf(sq / static_cast<float>(n) + eps);
+    write_part<TEAM, NC, V, K>(acc, part_lds, static_cast<float*>(q.ws) + blockIdx.x * K * q.D,
+                               q.D, 0, n);
 }
 
-template <typename T>
-__device__ __forceinline__ T* row_of(const void* p, int64_t row, int64_t ld) {
-    return const_cast<T*>(static_cast<const T*>(p)) + row * ld;
-}
+// ---- rows too wide for the registers -------------------------------------------
+
+constexpr int kWide = 1024;
 
 template <typename T, typename R>
-__global__ __launch_bounds__(kThreads) void add_norm_kernel(NormArgs q) {
-    __shared__ float lds[2 * kThreads / 64];
+__global__ __launch_bounds__(kWide) void add_norm_wide_kernel(NormArgs q) {
+    __shared__ float lds[kSumLds<kGroup, 1>];
+    int turn = 0;
     for (int64_t m = blockIdx.x; m < q.M; m += gridDim.x) {
         const T* x = row_of<T>(q.x, m, q.ld_x);
         const R* res = row_of<R>(q.res, m, q.ld_res);
         R* s = row_of<R>(q.s, m, q.ld_s);
         T* y = row_of<T>(q.y, m, q.ld_y);
-        for (int64_t c = threadIdx.x; c < q.D; c += kThreads) {
-            const float k = q.alpha * (q.scale ? q.scale[c] : 1.0f);
-            const float base = q.res ? static_cast<float>(res[c]) : 0.0f;
-            s[c] = static_cast<R>(__builtin_fmaf(k, static_cast<float>(x[c]), base));
+        float sum[1] = {0.0f};
+        for (int64_t c = threadIdx.x; c < q.D; c += kWide) {
+            const float k = q.scale ? q.alpha * q.scale[c] : q.alpha;
+            const float base = res ? static_cast<float>(res[c]) : 0.0f;
+            s[c] = static_cast<R>(scaled_sum(base, k, static_cast<float>(x[c])));
+            sum[0] += static_cast<float>(s[c]);
         }
-        float mean, rstd;
-        moments([&](int64_t c) { return static_cast<float>(s[c]); }, q.D, q.kind, q.eps, lds, mean,
-                rstd);
-        for (int64_t c = threadIdx.x; c < q.D; c += kThreads) {
-            const float n = (static_cast<float>(s[c]) - mean) * rstd;
-            y[c] = static_cast<T>(__builtin_fmaf(n, q.w[c], q.b ? q.b[c] : 0.0f));
+        float mean = 0.0f;
+        if (q.kind == MSS_NORM_LAYER) {
+            team_sum<kGroup>(sum, lds, turn);
+            mean = sum[0] / static_cast<float>(q.D);
+        }
+        sum[0] = 0.0f;
+        for (int64_t c = threadIdx.x; c < q.D; c += kWide) {
+            const float v = static_cast<float>(s[c]) - mean;
+            sum[0] = __builtin_fmaf(v, v, sum[0]);
+        }
+        team_sum<kGroup>(sum, lds, turn);
+        const float rstd = __builtin_amdgcn_rsqf(sum[0] / static_cast<float>(q.D) + q.eps);
+        for (int64_t c = threadIdx.x; c < q.D; c += kWide) {
+            const float nv = (static_cast<float>(s[c]) - mean) * rstd;
+            y[c] = static_cast<T>(__builtin_fmaf(nv, q.w[c], q.b ? q.b[c] : 0.0f));
         }
     }
 }
 
 template <typename T, typename R>
-__global__ __launch_bounds__(kThreads) void add_norm_bwd_kernel(NormArgs q) {
-    __shared__ float lds[2 * kThreads / 64];
+__global__ __launch_bounds__(kWide) void add_norm_bwd_wide_kernel(NormArgs q) {
+    __shared__ float lds[kSumLds<kGroup, 3>];
+    int turn = 0;
     float* part = static_cast<float*>(q.ws) + blockIdx.x * 3 * q.D;
-    for (int64_t c = threadIdx.x; c < q.D; c += kThreads)
+    for (int64_t c = threadIdx.x; c < q.D; c += kWide)
         part[c] = part[q.D + c] = part[2 * q.D + c] = 0.0f;
     for (int64_t m = blockIdx.x; m < q.M; m += gridDim.x) {
         const R* s = row_of<R>(q.s, m, q.ld_s);
         const T* dy = row_of<T>(q.dy, m, q.ld_y);
         const R* ds = row_of<R>(q.ds, m, q.ld_ds);
         const T* x = row_of<T>(q.x, m, q.ld_x);
-        float mean, rstd, c1 = 0.0f, c2 = 0.0f;
-        moments([&](int64_t c) { return static_cast<float>(s[c]); }, q.D, q.kind, q.eps, lds, mean,
-                rstd);
-        for (int64_t c = threadIdx.x; c < q.D; c += kThreads) {
-            const float g = static_cast<float>(dy[c]) * q.w[c];
-            const float n = (static_cast<float>(s[c]) - mean) * rstd;
-            c1 = __builtin_fmaf(g, n, c1);
-            c2 += g;
+        R* dres = row_of<R>(q.dres, m, q.ld_dres);
+        T* dx = row_of<T>(q.dx, m, q.ld_dx);
+        float mean = 0.0f;
+        if (q.kind == MSS_NORM_LAYER) {
+            float sum[1] = {0.0f};
+            for (int64_t c = threadIdx.x; c < q.D; c += kWide) sum[0] += static_cast<float>(s[c]);
+            team_sum<kGroup>(sum, lds, turn);
+            mean = sum[0] / static_cast<float>(q.D);
         }
-        block_sum2(c1, c2, lds);
-        c1 /= static_cast<float>(q.D);
-        c2 = q.kind == MSS_NORM_LAYER ? c2 / static_cast<float>(q.D) : 0.0f;
-        for (int64_t c = threadIdx.x; c < q.D; c += kThreads) {
-            const float gy = static_cast<float>(dy[c]);
-            const float n = (static_cast<float>(s[c]) - mean) * rstd;
-            float dres = rstd * (gy * q.w[c] - n * c1 - c2);
-            if (q.ds) dres += static_cast<float>(ds[c]);
-            const float k = q.alpha * (q.scale ? q.scale[c] : 1.0f);
-            row_of<R>(q.dres, m, q.ld_dres)[c] = static_cast<R>(dres);
-            if (q.dx) row_of<T>(q.dx, m, q.ld_dx)[c] = static_cast<T>(k * dres);
-            part[c] += gy * n;
-            part[q.D + c] += gy;
-            if (q.x) part[2 * q.D + c] += dres * static_cast<float>(x[c]);
+        float sums[3] = {0.0f, 0.0f, 0.0f};
+        for (int64_t c = threadIdx.x; c < q.D; c += kWide) {
+            const float v = static_cast<float>(s[c]) - mean;
+            const float gw = static_cast<float>(dy[c]) * q.w[c];
+            sums[0] = __builtin_fmaf(v, v, sums[0]);
+            sums[1] = __builtin_fmaf(gw, v, sums[1]);
+            sums[2] += gw;
         }
-    }
-}
-
-template <typename T>
-__global__ __launch_bounds__(kThreads) void gated_norm_kernel(NormArgs q) {
-    __shared__ float lds[2 * kThreads / 64];
-    const int64_t n = q.D / q.G;
-    const bool before = q.order == MSS_GATE_BEFORE_NORM;
-    for (int64_t m = blockIdx.x; m < q.M; m += gridDim.x) {
-        for (int64_t g0 = 0; g0 < q.D; g0 += n) {
-            const T* x = row_of<T>(q.x, m, q.ld_x) + g0;
-            const T* z = row_of<T>(q.z, m, q.ld_z) + g0;
-            const T* res = row_of<T>(q.res, m, q.ld_res) + g0;
-            T* y = row_of<T>(q.y, m, q.ld_y) + g0;
-            auto gate = [&](int64_t c) { return q.z ? silu(static_cast<float>(z[c])) : 1.0f; };
-            auto v = [&](int64_t c) {
-                return before ? static_cast<float>(x[c]) * gate(c) : static_cast<float>(x[c]);
-            };
-            float mean, rstd;
-            moments(v, n, q.kind, q.eps, lds, mean, rstd);
-            for (int64_t c = threadIdx.x; c < n; c += kThreads) {
-                float o = __builtin_fmaf((v(c) - mean) * rstd, q.w[g0 + c], q.b ? q.b[g0 + c] : 0.0f);
-                if (!before) o *= gate(c);
-                o *= q.alpha * (q.scale ? q.scale[g0 + c] : 1.0f);
-                if (q.res) o += static_cast<float>(res[c]);
-                y[c] = static_cast<T>(o);
-            }
+        team_sum<kGroup>(sums, lds, turn);
+        const float inv_n = 1.0f / static_cast<float>(q.D);
+        const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(sums[0], inv_n, q.eps));
+        const float c1 = sums[1] * inv_n * rstd;
+        const float c2 = q.kind == MSS_NORM_LAYER ? sums[2] * inv_n : 0.0f;
+        for (int64_t c = threadIdx.x; c < q.D; c += kWide) {
+            const float nv = (static_cast<float>(s[c]) - mean) * rstd;
+            const float g = static_cast<float>(dy[c]);
+            float d = ds ? static_cast<float>(ds[c]) : 0.0f;
+            d = __builtin_fmaf(rstd, __builtin_fmaf(g, q.w[c], -__builtin_fmaf(nv, c1, c2)), d);
+            part[c] = __builtin_fmaf(g, nv, part[c]);
+            part[q.D + c] += g;
+            if (x) part[2 * q.D + c] = __builtin_fmaf(d, static_cast<float>(x[c]), part[2 * q.D + c]);
+            dres[c] = static_cast<R>(d);
+            if (dx) dx[c] = static_cast<T>((q.scale ? q.alpha * q.scale[c] : q.alpha) * d);
         }
     }
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void gated_norm_bwd_kernel(NormArgs q) {
-    __shared__ float lds[2 * kThreads / 64];
-    const int64_t n = q.D / q.G;
-    const bool before = q.order == MSS_GATE_BEFORE_NORM;
-    float* part = static_cast<float*>(q.ws) + blockIdx.x * 3 * q.D;
-    for (int64_t c = threadIdx.x; c < q.D; c += kThreads)
-        part[c] = part[q.D + c] = part[2 * q.D + c] = 0.0f;
-    __syncthreads();
-    for (int64_t m = blockIdx.x; m < q.M; m += gridDim.x) {
-        for (int64_t g0 = 0; g0 < q.D; g0 += n) {
-            const T* x = row_of<T>(q.x, m, q.ld_x) + g0;
-            const T* z = row_of<T>(q.z, m, q.ld_z) + g0;
-            const T* dout = row_of<T>(q.dy, m, q.ld_y) + g0;
-            T* dx = row_of<T>(q.dx, m, q.ld_dx) + g0;
-            T* dz = row_of<T>(q.dz, m, q.ld_dz) + g0;
-            auto gate = [&](int64_t c) { return q.z ? silu(static_cast<float>(z[c])) : 1.0f; };
-            auto v = [&](int64_t c) {
-                return before ? static_cast<float>(x[c]) * gate(c) : static_cast<float>(x[c]);
-            };
-            // gradient of the normed row times w plus b
-            auto dp = [&](int64_t c) {
-                const float k = q.alpha * (q.scale ? q.scale[g0 + c] : 1.0f);
-                const float dq = k * static_cast<float>(dout[c]);
-                return before ? dq : dq * gate(c);
-            };
-            float mean, rstd, c1 = 0.0f, c2 = 0.0f;
-            moments(v, n, q.kind, q.eps, lds, mean, rstd);
-            for (int64_t c = threadIdx.x; c < n; c += kThreads) {
-                const float g = dp(c) * q.w[g0 + c];
-                c1 = __builtin_fmaf(g, (v(c) - mean) * rstd, c1);
-                c2 += g;
-            }
-            block_sum2(c1, c2, lds);
-            c1 /= static_cast<float>(n);
-            c2 = q.kind == MSS_NORM_LAYER ? c2 / static_cast<float>(n) : 0.0f;
-            for (int64_t c = threadIdx.x; c < n; c += kThreads) {
-                const float nv = (v(c) - mean) * rstd;
-                const float g = dp(c);
-                const float p = __builtin_fmaf(nv, q.w[g0 + c], q.b ? q.b[g0 + c] : 0.0f);
-                const float dv = rstd * (g * q.w[g0 + c] - nv * c1 - c2);
-                const float k = q.alpha * (q.scale ? q.scale[g0 + c] : 1.0f);
-                const float go = static_cast<float>(dout[c]);
-                float f = 1.0f, slope = 0.0f;
-                if (q.z) silu2(static_cast<float>(z[c]), f, slope);
-                dx[c] = static_cast<T>(before ? dv * f : dv);
-                if (q.z)
-                    dz[c] = static_cast<T>(before ? dv * static_cast<float>(x[c]) * slope
-                                                  : k * go * p * slope);
-                part[g0 + c] += g * nv;
-                part[q.D + g0 + c] += g;
-                part[2 * q.D + g0 + c] += go * (before ? p : p * f);
-            }
-        }
-    }
-}
-
-// dw, db and dscale from the workgroups' rows of partial sums.
-__global__ __launch_bounds__(64) void norm_params_kernel(NormArgs q, int64_t rows) {
-    const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-    if (d >= q.D) return;
+// One workgroup sums 32 channels: 32 lanes side by side, 32 rows at a time.
+__global__ __launch_bounds__(1024) void norm_params_kernel(NormArgs q, bool gated, int64_t rows,
+                                                           int K) {
+    __shared__ float lds[32][33];
+    const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
+    const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     const float* part = static_cast<const float*>(q.ws);
-    float w = 0.0f, b = 0.0f, s = 0.0f;
-    for (int64_t p = 0; p < rows; p++) {
-        w += part[(3 * p) * q.D + d];
-        b += part[(3 * p + 1) * q.D + d];
-        s += part[(3 * p + 2) * q.D + d];
+    float S[3] = {0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < K; k++) {
+        float s = 0.0f;
+        if (d < q.D) {
+#pragma unroll 8
+            for (int64_t p = group; p < rows; p += 32) s += part[(p * K + k) * q.D + d];
+        }
+        __syncthreads();
+        lds[group][lane] = s;
+        __syncthreads();
+        if (group == 0) {
+            s = 0.0f;
+#pragma unroll
+            for (int g = 0; g < 32; g++) s += lds[g][lane];
+        }
+        S[0] = k == 0 ? s : S[0];
+        S[1] = k == 1 ? s : S[1];
+        S[2] = k == 2 ? s : S[2];
     }
-    if (q.dw) q.dw[d] = w;
-    if (q.db) q.db[d] = b;
-    if (q.dscale) q.dscale[d] = q.alpha * s;
+    if (group != 0 || d >= q.D) return;
+    if (gated) {
+        const float k = q.scale ? q.alpha * q.scale[d] : q.alpha;
+        const float b = q.b ? q.b[d] : 0.0f;
+        if (q.dw) q.dw[d] = k * S[0];
+        if (q.db) q.db[d] = k * S[1];
+        if (q.dscale) q.dscale[d] = q.alpha * __builtin_fmaf(q.w[d], S[0], b * S[1]);
+    } else {
+        if (q.dw) q.dw[d] = S[0];
+        if (q.db) q.db[d] = S[1];
+        if (q.dscale) q.dscale[d] = q.alpha * S[2];
+    }
 }
 
-int64_t part_rows(int64_t M) { return M < kPartRows ? M : kPartRows; }
-unsigned row_grid(int64_t M) { return static_cast<unsigned>(M < (1 << 20) ? M : (1 << 20)); }
-
-hipError_t launch_params(const NormArgs& a, hipStream_t st) {
-    if (!a.dw && !a.db && !a.dscale) return hipGetLastError();
-    norm_params_kernel<<<static_cast<unsigned>((a.D + 63) / 64), 64, 0, st>>>(a, part_rows(a.M));
-    return hipGetLastError();
-}
-
+// f(activation, residual) for the call's types.
 template <typename F>
-hipError_t dispatch(int dtype, F f) {
-    switch (dtype) {
-        case MSS_F32: f(float{}); break;
-        case MSS_BF16: f(bf16{}); break;
-        case MSS_F16: f(f16{}); break;
+hipError_t dispatch(const NormArgs& a, F f) {
+    const bool wide = a.res_dtype == MSS_F32;
+    switch (a.dtype) {
+        case MSS_F32: f(float{}, float{}); break;
+        case MSS_BF16: wide ? f(bf16{}, float{}) : f(bf16{}, bf16{}); break;
+        case MSS_F16: wide ? f(f16{}, float{}) : f(f16{}, f16{}); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }
 
-// f(activation, residual) for the call's types.
-template <typename F>
-hipError_t dispatch2(const NormArgs& a, F f) {
-    return dispatch(a.dtype, [&](auto t) {
-        if (a.res_dtype == MSS_F32)
-            f(t, float{});
-        else
-            f(t, t);
-    });
-}
-
 }  // namespace
 
-bool norm_bwd_workspace(int64_t M, int64_t D, int64_t& bytes) {
-    if (D > INT32_MAX) return false;
-    bytes = (part_rows(M) * 3 * D * 4 + 255) / 256 * 256;
+bool norm_bwd_workspace(int64_t M, int64_t D, int64_t G, int64_t& bytes) {
+    if (D > INT32_MAX / 2 || G > INT32_MAX / 1024) return false;
+    bytes = (row_groups(M, G, 64, 1, kPartRows) * 3 * D * 4 + 255) / 256 * 256;
     return true;
 }
 
+hipError_t launch_norm_params(const NormArgs& a, bool gated, int64_t rows, int K, hipStream_t st) {
+    if (!a.dw && !a.db && !a.dscale) return hipGetLastError();
+    norm_params_kernel<<<static_cast<unsigned>((a.D + 31) / 32), 1024, 0, st>>>(a, gated, rows, K);
+    return hipGetLastError();
+}
+
 hipError_t launch_add_norm(const NormArgs& a, hipStream_t st) {
-    return dispatch2(a, [&](auto t, auto r) {
-        add_norm_kernel<decltype(t), decltype(r)><<<row_grid(a.M), kThreads, 0, st>>>(a);
+    return dispatch(a, [&](auto t, auto r) {
+        using T = decltype(t);
+        using R = decltype(r);
+        const bool held = by_width<kVec<T>>(a.D, [&](auto s) {
+            const auto grid = row_groups(a.M, 1, s.threads, s.rows, kRowGroups);
+            add_norm_kernel<T, R, s.TEAM, s.NC>
+                <<<static_cast<unsigned>(grid), s.threads, 0, st>>>(a);
+        });
+        if (!held) {
+            const auto grid = row_groups(a.M, 1, kWide, 1, kRowGroups);
+            add_norm_wide_kernel<T, R><<<static_cast<unsigned>(grid), kWide, 0, st>>>(a);
+        }
     });
 }
 
 hipError_t launch_add_norm_bwd(const NormArgs& a, hipStream_t st) {
-    const hipError_t e = dispatch2(a, [&](auto t, auto r) {
-        add_norm_bwd_kernel<decltype(t), decltype(r)>
-            <<<static_cast<unsigned>(part_rows(a.M)), kThreads, 0, st>>>(a);
+    const bool extra = a.db || a.dscale;
+    int64_t rows = 0;
+    int K = extra ? 3 : 1;
+    const hipError_t e = dispatch(a, [&](auto t, auto r) {
+        using T = decltype(t);
+        using R = decltype(r);
+        const bool held = by_width<kVec<T>>(a.D, [&](auto s) {
+            rows = row_groups(a.M, 1, s.threads, s.rows, kPartRows);
+            const unsigned grid = static_cast<unsigned>(rows);
+            if (extra)
+                add_norm_bwd_kernel<T, R, s.TEAM, s.NC, true><<<grid, s.threads, 0, st>>>(a);
+            else
+                add_norm_bwd_kernel<T, R, s.TEAM, s.NC, false><<<grid, s.threads, 0, st>>>(a);
+        });
+        if (!held) {
+            rows = row_groups(a.M, 1, kWide, 1, kPartRows);
+            K = 3;
+            add_norm_bwd_wide_kernel<T, R><<<static_cast<unsigned>(rows), kWide, 0, st>>>(a);
+        }
     });
-    return e == hipSuccess ? launch_params(a, st) : e;
-}
-
-hipError_t launch_gated_norm(const NormArgs& a, hipStream_t st) {
-    return dispatch(a.dtype, [&](auto t) {
-        gated_norm_kernel<decltype(t)><<<row_grid(a.M), kThreads, 0, st>>>(a);
-    });
-}
-
-hipError_t launch_gated_norm_bwd(const NormArgs& a, hipStream_t st) {
-    const hipError_t e = dispatch(a.dtype, [&](auto t) {
-        gated_norm_bwd_kernel<decltype(t)>
-            <<<static_cast<unsigned>(part_rows(a.M)), kThreads, 0, st>>>(a);
-    });
-    return e == hipSuccess ? launch_params(a, st) : e;
+    return e == hipSuccess ? launch_norm_params(a, false, rows, K, st) : e;
 }
 
 }  // namespace mss
