@@ -239,7 +239,7 @@ int mss_gated_workspace_bytes(const mss_gated_dims* dims, int op, size_t* bytes)
     if (n == 0) return MSS_OK;
     const bool ok = op == MSS_OP_GATED_SCAN
                         ? mss::gated_scan_workspace(dims->batch, dims->seq_len, dims->d_inner,
-                                                    dims->gate, need)
+                                                    need)
                         : mss::gated_scan_bwd_workspace(dims->batch, dims->seq_len, dims->d_inner,
                                                         dims->gate, need);
     if (!ok) return MSS_EINVAL;
@@ -268,7 +268,7 @@ int mss_gated_scan(const mss_gated_dims* dims, const mss_gated_strides* strides,
     if (!count(M, {a.B, a.L}) || !count(MD, {M, a.D, 4}) || !count(BD, {a.B, a.D}) ||
         !count(BKD, {a.B, ckpt_rows(a.L), a.D, 4}))
         return MSS_EINVAL;
-    if (MD > 0 && !mss::gated_scan_workspace(a.B, a.L, a.D, a.gate, need)) return MSS_EINVAL;
+    if (MD > 0 && !mss::gated_scan_workspace(a.B, a.L, a.D, need)) return MSS_EINVAL;
     Checks ck(strides != nullptr);
     gated_inputs(ck, a, M);
     ck.in(h0, BD, 4, false);
@@ -354,7 +354,7 @@ int mss_gated_step(const mss_gated_dims* dims, const mss_gated_strides* strides,
     a.h = h;
     a.y = y;
     int64_t BD;
-    if (!count(BD, {a.B, a.D, 4})) return MSS_EINVAL;
+    if (!count(BD, {a.B, a.D, 4}) || !mss::gated_step_fits(a.B, a.D)) return MSS_EINVAL;
     BD /= 4;
     Checks ck(strides != nullptr);
     gated_inputs(ck, a, a.B);

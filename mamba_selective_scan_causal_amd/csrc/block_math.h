@@ -9,6 +9,47 @@ namespace mss {
 using bf16 = __bf16;
 using f16 = _Float16;
 
+// V channels as memory holds them.
+template <typename T, int V>
+struct RowVec {
+    typedef T type __attribute__((ext_vector_type(V), aligned(alignof(T))));
+    type t;
+
+    // Channels c .. c + V - 1 of a row (group) of n; zeros past its end.
+    __device__ __forceinline__ void load(const T* p, int c, int n) {
+        if (c + V <= n) {
+            t = *reinterpret_cast<const type*>(p + c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; e++) t[e] = c + e < n ? p[c + e] : static_cast<T>(0.0f);
+        }
+    }
+    __device__ __forceinline__ void store(T* p, int c, int n) const {
+        if (c + V <= n) {
+            *reinterpret_cast<type*>(p + c) = t;
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; e++)
+                if (c + e < n) p[c + e] = t[e];
+        }
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int e = 0; e < V; e++) t[e] = static_cast<T>(0.0f);
+    }
+    // Tells the compiler nothing it computed from the vector still holds, so
+    // that it keeps the 2-byte values across a round of sums and widens them
+    // again afterwards, not their fp32 copies (twice the registers).
+    __device__ __forceinline__ void narrow() {
+        typedef unsigned int words __attribute__((ext_vector_type(V * sizeof(T) / 4)));
+        words u = __builtin_bit_cast(words, t);
+        asm volatile("" : "+v"(u));
+        t = __builtin_bit_cast(type, u);
+    }
+    __device__ __forceinline__ float operator[](int e) const { return static_cast<float>(t[e]); }
+    __device__ __forceinline__ void set(int e, float v) { t[e] = static_cast<T>(v); }
+};
+
 // sigma(v) and 1 - sigma(v), each to a few ulp of itself: the exponential of
 // -|v| never overflows and neither result is formed by a subtraction.
 // v = +-inf gives exactly 0 and 1.

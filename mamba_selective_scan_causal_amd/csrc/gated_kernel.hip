@@ -1,8 +1,35 @@
 // gated_kernel.hip -- the gated linear recurrence h_t = v_t + a_t h_{t-1} of
 // mss.h, its backward pass and its single-token step.
 //
-// One lane per (batch row, channel) walks the sequence; neighbouring lanes
-// hold neighbouring channels, so every time row is read in whole lines.
+// Bound by HBM: per channel and step the forward reads x, r (i, z) and writes
+// y, the backward reads those and dout and writes their gradients, and every
+// tensor is read once.  One state per channel leaves too few channels to fill
+// the chip, so time is cut into chunks that different workgroups hold at the
+// same time:
+//
+//   A lane holds V neighbouring channels (2-byte types two, fp32 one, so that
+//   a wave reads 256 bytes of a row) and S consecutive steps of them in
+//   registers; the kWaves waves of a workgroup hold consecutive pieces of S
+//   steps.  A piece is an affine map of the state that enters it, (A, H):
+//   h -> A h + H, and so is a chunk, the pieces' composition.
+//   A workgroup publishes its chunk's map as soon as its inputs are in, then
+//   waits for the state entering its chunk, and only then steps through its
+//   registers a second time, now with the true state, and writes the outputs.
+//
+// The state entering chunk c is formed from the state entering the group of
+// kWaves chunks that c lies in, published by the last chunk of the group
+// before, and the maps of the group's chunks before c, in that order: a
+// serial chain of one handover per kWaves chunks, and results that do not
+// depend on which workgroup runs when.
+//
+// Workgroups take their chunk from a counter, time first, so a workgroup waits
+// only for ones that have taken a lower number, and the lowest number that is
+// not done never waits: every wait ends.  (The wait is bounded besides; past
+// the bound, seconds, the outputs become NaN.)  What is handed over are
+// 8-byte words that are written and read by single relaxed atomics of agent
+// scope; all ones means not written yet, so that the words need no flags and
+// no fences.  A first small kernel sets them, and the counter, in the
+// workspace.
 #include "block_math.h"
 #include "launch_block.h"
 
@@ -56,177 +83,632 @@ struct Gates {
     }
 };
 
-constexpr int kSeg = MSS_GATED_CKPT_STEPS;
+constexpr int kWaves = 8;                        // waves of a workgroup, chunks of a group
+constexpr int kSteps = 16;                       // S of the forward
+constexpr int kChunk = kWaves * kSteps;
+constexpr int kBwdSteps = 8;                     // S of the backward: twice the inputs per step
+constexpr int kBwdChunk = kWaves * kBwdSteps;
+static_assert(kBwdChunk == MSS_GATED_CKPT_STEPS, "a backward chunk starts from a checkpoint");
+static_assert(kChunk % MSS_GATED_CKPT_STEPS == 0, "checkpoints lie between a chunk's waves");
 
-template <typename T, int GATE>
-__global__ __launch_bounds__(64) void gated_scan_kernel(GatedArgs q) {
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-    if (j >= q.B * q.D) return;
-    const int64_t b = j / q.D, d = j % q.D;
-    const T* x = static_cast<const T*>(q.x) + b * q.L * q.ld_x + d;
-    const T* r = static_cast<const T*>(q.r) + b * q.L * q.ld_r + d;
-    const T* in = static_cast<const T*>(q.i) + b * q.L * q.ld_i + d;
-    const T* z = static_cast<const T*>(q.z) + b * q.L * q.ld_z + d;
-    T* y = static_cast<T*>(q.y) + b * q.L * q.ld_y + d;
-    const float k = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(q.decay[d]) : 0.0f;
-    const int64_t nck = (q.L + kSeg - 1) / kSeg;
-    float h = q.h0 ? q.h0[j] : 0.0f;
-    for (int64_t t = 0; t < q.L; t++) {
-        if (q.h_ckpt && t % kSeg == 0) q.h_ckpt[(b * nck + t / kSeg) * q.D + d] = h;
-        Gates<GATE> g;
-        const float iv = GATE == MSS_GATE_DECAY ? static_cast<float>(in[t * q.ld_i]) : 0.0f;
-        g.set(static_cast<float>(x[t * q.ld_x]), static_cast<float>(r[t * q.ld_r]), iv, k);
-        h = q.reset && q.reset[b * q.L + t] ? g.v : __builtin_fmaf(g.a, h, g.v);
-        const float out = q.z ? h * silu(static_cast<float>(z[t * q.ld_z])) : h;
-        y[t * q.ld_y] = static_cast<T>(out);
+typedef unsigned long long Word;
+constexpr Word kUnset = ~0ull;
+
+// What a launch's workgroups share (chain: chunks > 1).
+struct Chain {
+    unsigned tiles, ctiles;    // B * ctiles tiles of 64 V channels
+    int64_t chunks, groups;
+    unsigned* ticket;
+    Word* maps;                // [tile][chunk][V][64]: (A, H)
+    Word* states;              // [tile][group][V][64]: the state entering a group
+};
+
+// The affine map h -> A h + H.  A = 0 drops what was carried whatever it is.
+struct Map {
+    float A, H;
+    __device__ __forceinline__ float operator()(float h) const {
+        return A != 0.0f ? __builtin_fmaf(A, h, H) : H;
     }
-    if (q.h_last) q.h_last[j] = h;
+    // this after first
+    __device__ __forceinline__ Map after(const Map& first) const { return {A * first.A, (*this)(first.H)}; }
+};
+
+__device__ __forceinline__ void put(Word* p, float lo, float hi) {
+    Word w = static_cast<Word>(__builtin_bit_cast(unsigned, lo)) |
+             static_cast<Word>(__builtin_bit_cast(unsigned, hi)) << 32;
+    if (w == kUnset) w = 0x7fc000007fc00000ull;   // two NaNs, but not the mark
+    __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <typename T, int GATE>
-__global__ __launch_bounds__(64) void gated_scan_bwd_kernel(GatedArgs q) {
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-    if (j >= q.B * q.D) return;
-    const int64_t b = j / q.D, d = j % q.D;
-    const T* x = static_cast<const T*>(q.x) + b * q.L * q.ld_x + d;
-    const T* r = static_cast<const T*>(q.r) + b * q.L * q.ld_r + d;
-    const T* in = static_cast<const T*>(q.i) + b * q.L * q.ld_i + d;
-    const T* z = static_cast<const T*>(q.z) + b * q.L * q.ld_z + d;
-    const T* dout = static_cast<const T*>(q.dout) + b * q.L * q.ld_y + d;
-    T* dx = static_cast<T*>(q.dx) + b * q.L * q.ld_dx + d;
-    T* dr = static_cast<T*>(q.dr) + b * q.L * q.ld_dr + d;
-    T* di = static_cast<T*>(q.di) + b * q.L * q.ld_di + d;
-    T* dz = static_cast<T*>(q.dz) + b * q.L * q.ld_dz + d;
-    const float k = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(q.decay[d]) : 0.0f;
-    const int64_t nck = (q.L + kSeg - 1) / kSeg;
-    float Q = q.dh_last ? q.dh_last[j] : 0.0f;   // what the step after passes to h_t
-    float sum = 0.0f;
-    for (int64_t s = nck - 1; s >= 0; s--) {
-        const int64_t t0 = s * kSeg;
-        const int n = static_cast<int>(q.L - t0 < kSeg ? q.L - t0 : kSeg);
-        float before[kSeg];
-        float h = q.h_ckpt[(b * nck + s) * q.D + d];
-        for (int u = 0; u < n; u++) {
-            const int64_t t = t0 + u;
-            Gates<GATE> g;
-            const float iv = GATE == MSS_GATE_DECAY ? static_cast<float>(in[t * q.ld_i]) : 0.0f;
-            g.set(static_cast<float>(x[t * q.ld_x]), static_cast<float>(r[t * q.ld_r]), iv, k);
-            before[u] = q.reset && q.reset[b * q.L + t] ? 0.0f : h;
-            h = __builtin_fmaf(g.a, before[u], g.v);
+// Each lane's V words at p (64 words apart), once all of the wave's are there.
+template <int V>
+__device__ __forceinline__ void wait_for(Word* p, Map (&m)[V]) {
+    Word w[V];
+    for (int tries = 0;; tries++) {
+        bool unset = false;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            w[v] = __hip_atomic_load(p + 64 * v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            unset |= w[v] == kUnset;
         }
-        for (int u = n - 1; u >= 0; u--) {
-            const int64_t t = t0 + u;
-            Gates<GATE> g;
-            const float xv = static_cast<float>(x[t * q.ld_x]);
-            const float iv = GATE == MSS_GATE_DECAY ? static_cast<float>(in[t * q.ld_i]) : 0.0f;
-            g.set(xv, static_cast<float>(r[t * q.ld_r]), iv, k);
-            float dy = static_cast<float>(dout[t * q.ld_y]);
-            if (q.z) {
-                float f, slope;
-                silu2(static_cast<float>(z[t * q.ld_z]), f, slope);
-                dz[t * q.ld_dz] = static_cast<T>(dy * __builtin_fmaf(g.a, before[u], g.v) * slope);
-                dy *= f;
+        if (!wave_any(unset)) break;
+        if (tries > (1 << 22)) {
+#pragma unroll
+            for (int v = 0; v < V; v++) w[v] = 0x7fc000007fc00000ull;
+            break;
+        }
+        __builtin_amdgcn_s_sleep(1);
+    }
+#pragma unroll
+    for (int v = 0; v < V; v++)
+        m[v] = {__builtin_bit_cast(float, static_cast<unsigned>(w[v])),
+                __builtin_bit_cast(float, static_cast<unsigned>(w[v] >> 32))};
+}
+
+__global__ __launch_bounds__(256) void gated_unset_kernel(Word* ws, int64_t n) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * 256)
+        ws[i] = i < 32 ? 0 : kUnset;
+}
+
+// The number of this workgroup's piece of work.
+__device__ __forceinline__ unsigned take(const Chain& g, unsigned* lds) {
+    if (g.chunks == 1) return blockIdx.x;
+    if (threadIdx.x == 0) *lds = atomicAdd(g.ticket, 1u);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*lds);
+}
+
+// V channels of one row; an odd row's last lane takes the last V channels, so
+// its first is its neighbour's too, computed twice to the same bits.
+template <typename T, int V>
+struct Piece {
+    typename std::conditional<V == 1, T, typename RowVec<T, V == 1 ? 2 : V>::type>::type t;
+    __device__ __forceinline__ void load(const T* row, unsigned c) {
+        t = *reinterpret_cast<const decltype(t)*>(row + c);
+    }
+    __device__ __forceinline__ void store(T* row, unsigned c) const {
+        *reinterpret_cast<decltype(t)*>(row + c) = t;
+    }
+    __device__ __forceinline__ float get(int v) const {
+        if constexpr (V == 1)
+            return static_cast<float>(t);
+        else
+            return static_cast<float>(t[v]);
+    }
+    __device__ __forceinline__ void set(int v, float f) {
+        if constexpr (V == 1)
+            t = static_cast<T>(f);
+        else
+            t[v] = static_cast<T>(f);
+    }
+    // The compiler keeps the value as it was read, not what it made of it.
+    __device__ __forceinline__ void keep() {
+        typename std::conditional<sizeof(t) == 2, unsigned short, unsigned>::type u;
+        __builtin_memcpy(&u, &t, sizeof(t));
+        asm volatile("" : "+v"(u));
+        __builtin_memcpy(&t, &u, sizeof(t));
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ T* at_row(const void* p, int64_t row, int64_t ld) {
+    return const_cast<T*>(static_cast<const T*>(p)) + row * ld;
+}
+
+// Bit s: step t0 + s (of S) drops what is carried into it.
+template <int S>
+__device__ __forceinline__ unsigned reset_bits(const uint8_t* reset, int64_t row0, int64_t t0, int64_t L,
+                                               int lane) {
+    if (!reset) return 0;
+    const int64_t t = t0 + lane;
+    return static_cast<unsigned>(
+        __builtin_amdgcn_ballot_w64(lane < S && t < L && reset[row0 + t] != 0));
+}
+
+template <typename T, int V, int GATE, bool Z>
+__global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Chain g) {
+    constexpr int S = kSteps;
+    __shared__ Map own[kWaves][V][64], mates[kWaves][V][64];
+    __shared__ float entering[V][64];
+    __shared__ unsigned ticket;
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const unsigned id = take(g, &ticket);
+    const unsigned tile = id % g.tiles;
+    const int64_t chunk = id / g.tiles;
+    const unsigned b = tile / g.ctiles;
+    unsigned c = tile % g.ctiles * (64 * V) + lane * V;
+    const bool live = c < q.D;
+    c = live && c + V <= q.D ? c : static_cast<unsigned>(q.D - V);
+    const int64_t t0 = chunk * kChunk + wave * S, row0 = int64_t{b} * q.L;
+    const int n = t0 >= q.L ? 0 : q.L - t0 < S ? static_cast<int>(q.L - t0) : S;
+
+    Piece<T, V> x[S], r[S], in[S], z[S];
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+        const int64_t row = row0 + (t0 + s < q.L ? t0 + s : q.L - 1);
+        x[s].load(at_row<T>(q.x, row, q.ld_x), c);
+        r[s].load(at_row<T>(q.r, row, q.ld_r), c);
+        if constexpr (GATE == MSS_GATE_DECAY) in[s].load(at_row<T>(q.i, row, q.ld_i), c);
+    }
+    if constexpr (Z) {
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            const int64_t row = row0 + (t0 + s < q.L ? t0 + s : q.L - 1);
+            z[s].load(at_row<T>(q.z, row, q.ld_z), c);
+        }
+    }
+    const unsigned resets = reset_bits<S>(q.reset, row0, t0, q.L, lane);
+    float k[V];
+#pragma unroll
+    for (int v = 0; v < V; v++)
+        k[v] = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(q.decay[c + v]) : 0.0f;
+
+    float a[S][V], u[S][V];
+    Map m[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) m[v] = {1.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            Gates<GATE> e;
+            e.set(x[s].get(v), r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
+            a[s][v] = s < n ? e.a : 1.0f;
+            u[s][v] = s < n ? e.v : 0.0f;
+            const bool drop = resets >> s & 1;
+            m[v].A = drop ? 0.0f : m[v].A * a[s][v];
+            m[v].H = drop ? u[s][v] : __builtin_fmaf(a[s][v], m[v].H, u[s][v]);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; v++) own[wave][v][lane] = m[v];
+    __syncthreads();
+
+    float h[V];
+    const int mate = static_cast<int>(chunk % kWaves);
+    if (g.chunks > 1) {
+        const int64_t first = chunk - mate, words = 64 * V;
+        if (wave == 0 && mate != kWaves - 1 && chunk + 1 < g.chunks) {
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                Map all = own[0][v][lane];
+#pragma unroll
+                for (int w = 1; w < kWaves; w++) all = own[w][v][lane].after(all);
+                put(g.maps + (int64_t{tile} * g.chunks + chunk) * words + 64 * v + lane, all.A, all.H);
             }
-            const float G = dy + Q;
-            float gx, gr, gi = 0.0f, ws = 0.0f;
-            g.grads(G, before[u], xv, k, gx, gr, gi, ws);
-            dx[t * q.ld_dx] = static_cast<T>(gx);
-            dr[t * q.ld_dr] = static_cast<T>(gr);
-            if constexpr (GATE == MSS_GATE_DECAY) di[t * q.ld_di] = static_cast<T>(gi);
-            sum += ws;
-            Q = q.reset && q.reset[b * q.L + t] ? 0.0f : g.a * G;
         }
+        if (wave < mate) {
+            Map e[V];
+            wait_for<V>(g.maps + (int64_t{tile} * g.chunks + first + wave) * words + lane, e);
+#pragma unroll
+            for (int v = 0; v < V; v++) mates[wave][v][lane] = e[v];
+        }
+        if (wave == kWaves - 1) {
+            Map e[V];
+            if (first > 0)
+                wait_for<V>(g.states + (int64_t{tile} * g.groups + first / kWaves) * words + lane, e);
+            else
+#pragma unroll
+                for (int v = 0; v < V; v++) e[v].H = q.h0 ? q.h0[int64_t{b} * q.D + c + v] : 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; v++) entering[v][lane] = e[v].H;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; v++) h[v] = entering[v][lane];
+        for (int w = 0; w < mate; w++)
+#pragma unroll
+            for (int v = 0; v < V; v++) h[v] = mates[w][v][lane](h[v]);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; v++) h[v] = q.h0 ? q.h0[int64_t{b} * q.D + c + v] : 0.0f;
     }
-    if (q.dh0) q.dh0[j] = Q;
-    if constexpr (GATE == MSS_GATE_DECAY) static_cast<float*>(q.ws)[j] = sum;
+    for (int w = 0; w < wave; w++)
+#pragma unroll
+        for (int v = 0; v < V; v++) h[v] = own[w][v][lane](h[v]);
+    if (wave == kWaves - 1 && mate == kWaves - 1 && chunk + 1 < g.chunks) {
+#pragma unroll
+        for (int v = 0; v < V; v++)
+            put(g.states + (int64_t{tile} * g.groups + chunk / kWaves + 1) * (64 * V) + 64 * v + lane, 0.0f,
+                m[v](h[v]));
+    }
+    if (q.h_ckpt && t0 % MSS_GATED_CKPT_STEPS == 0 && n > 0 && live) {
+        const int64_t per = (q.L + MSS_GATED_CKPT_STEPS - 1) / MSS_GATED_CKPT_STEPS;
+        float* out = q.h_ckpt + (int64_t{b} * per + t0 / MSS_GATED_CKPT_STEPS) * q.D;
+#pragma unroll
+        for (int v = 0; v < V; v++) out[c + v] = h[v];
+    }
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+        if (s >= n) continue;
+        Piece<T, V> y;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            h[v] = resets >> s & 1 ? u[s][v] : __builtin_fmaf(a[s][v], h[v], u[s][v]);
+            if constexpr (Z)
+                y.set(v, h[v] * silu(z[s].get(v)));
+            else
+                y.set(v, h[v]);
+        }
+        if (live) y.store(at_row<T>(q.y, row0 + t0 + s, q.ld_y), c);
+    }
+    if (q.h_last && n > 0 && t0 + n == q.L && live) {
+#pragma unroll
+        for (int v = 0; v < V; v++) q.h_last[int64_t{b} * q.D + c + v] = h[v];
+    }
 }
 
-// ddecay[d] = -c sigma(decay[d]) sum over the partial rows.
-__global__ __launch_bounds__(64) void gated_ddecay_kernel(const float* __restrict__ part,
-                                                          const float* __restrict__ decay,
-                                                          float* __restrict__ ddecay, int64_t rows,
-                                                          int64_t D, float scale) {
-    const int64_t d = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-    if (d >= D) return;
+// The adjoint runs through the chunks from the last to the first: a piece maps
+// what the steps after it pass to its last state, Q, to A Q + R, with the same
+// A as the forward's map.  The states inside a chunk come from its checkpoint
+// and the pieces' forward maps.
+template <typename T, int V, int GATE, bool Z>
+__global__ __launch_bounds__(64 * kWaves) void gated_scan_bwd_kernel(GatedArgs q, Chain g,
+                                                                     float* part) {
+    constexpr int S = kBwdSteps;
+    __shared__ Map fwd[kWaves][V][64], rev[kWaves][V][64], mates[kWaves][V][64];
+    __shared__ float entering[V][64];
+    __shared__ unsigned ticket;
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const unsigned id = take(g, &ticket);
+    const unsigned tile = id % g.tiles;
+    const int64_t turn = id / g.tiles;   // turn 0: the last chunk
+    const int64_t chunk = g.chunks - 1 - turn;
+    const unsigned b = tile / g.ctiles;
+    unsigned c = tile % g.ctiles * (64 * V) + lane * V;
+    const bool live = c < q.D;
+    c = live && c + V <= q.D ? c : static_cast<unsigned>(q.D - V);
+    const int64_t t0 = chunk * kBwdChunk + wave * S, row0 = int64_t{b} * q.L;
+    const int n = t0 >= q.L ? 0 : q.L - t0 < S ? static_cast<int>(q.L - t0) : S;
+
+    Piece<T, V> x[S], r[S], in[S], z[S], dout[S];
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+        const int64_t row = row0 + (t0 + s < q.L ? t0 + s : q.L - 1);
+        x[s].load(at_row<T>(q.x, row, q.ld_x), c);
+        r[s].load(at_row<T>(q.r, row, q.ld_r), c);
+        if constexpr (GATE == MSS_GATE_DECAY) in[s].load(at_row<T>(q.i, row, q.ld_i), c);
+        if constexpr (Z) z[s].load(at_row<T>(q.z, row, q.ld_z), c);
+        dout[s].load(at_row<T>(q.dout, row, q.ld_y), c);
+    }
+    const unsigned resets = reset_bits<S>(q.reset, row0, t0, q.L, lane);
+    float k[V], h[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        k[v] = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(q.decay[c + v]) : 0.0f;
+        h[v] = q.h_ckpt[(int64_t{b} * g.chunks + chunk) * q.D + c + v];
+    }
+
+    float a[S][V], u[S][V];   // u: the input term, later the state
+    Map f[V], w[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        f[v] = {1.0f, 0.0f};
+        w[v].H = 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            Gates<GATE> e;
+            e.set(x[s].get(v), r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
+            float dy = s < n ? dout[s].get(v) : 0.0f;
+            if constexpr (Z) dy *= silu(z[s].get(v));
+            a[s][v] = s < n ? e.a : 1.0f;
+            u[s][v] = s < n ? e.v : 0.0f;
+            const bool drop = resets >> s & 1;
+            f[v].H = drop ? u[s][v] : __builtin_fmaf(a[s][v], f[v].H, u[s][v]);
+            f[v].A = drop ? 0.0f : f[v].A * a[s][v];
+            w[v].H = __builtin_fmaf(f[v].A, dy, w[v].H);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        w[v].A = f[v].A;
+        fwd[wave][v][lane] = f[v];
+        rev[wave][v][lane] = w[v];
+    }
+    __syncthreads();
+
+    float Q[V];
+    const int mate = static_cast<int>(turn % kWaves);
+    const int64_t first = turn - mate, words = 64 * V;
+    if (wave == 0 && mate != kWaves - 1 && turn + 1 < g.chunks) {
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            Map all = rev[kWaves - 1][v][lane];
+#pragma unroll
+            for (int p = kWaves - 2; p >= 0; p--) all = rev[p][v][lane].after(all);
+            put(g.maps + (int64_t{tile} * g.chunks + turn) * words + 64 * v + lane, all.A, all.H);
+        }
+    }
+    if (wave < mate) {
+        Map e[V];
+        wait_for<V>(g.maps + (int64_t{tile} * g.chunks + first + wave) * words + lane, e);
+#pragma unroll
+        for (int v = 0; v < V; v++) mates[wave][v][lane] = e[v];
+    }
+    if (wave == kWaves - 1) {
+        Map e[V];
+        if (first > 0)
+            wait_for<V>(g.states + (int64_t{tile} * g.groups + first / kWaves) * words + lane, e);
+        else
+#pragma unroll
+            for (int v = 0; v < V; v++) e[v].H = q.dh_last ? q.dh_last[int64_t{b} * q.D + c + v] : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; v++) entering[v][lane] = e[v].H;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; v++) Q[v] = entering[v][lane];
+    for (int p = 0; p < mate; p++)
+#pragma unroll
+        for (int v = 0; v < V; v++) Q[v] = mates[p][v][lane](Q[v]);
+    for (int p = kWaves - 1; p > wave; p--)
+#pragma unroll
+        for (int v = 0; v < V; v++) Q[v] = rev[p][v][lane](Q[v]);
+    if (wave == 0 && mate == kWaves - 1 && turn + 1 < g.chunks) {
+#pragma unroll
+        for (int v = 0; v < V; v++)
+            put(g.states + (int64_t{tile} * g.groups + turn / kWaves + 1) * words + 64 * v + lane, 0.0f,
+                w[v](Q[v]));
+    }
+    for (int p = 0; p < wave; p++)
+#pragma unroll
+        for (int v = 0; v < V; v++) h[v] = fwd[p][v][lane](h[v]);
+
+    float before[V];   // the state entering the piece
+#pragma unroll
+    for (int v = 0; v < V; v++) before[v] = h[v];
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+        x[s].keep();
+        r[s].keep();
+        if constexpr (GATE == MSS_GATE_DECAY) in[s].keep();
+        if constexpr (Z) z[s].keep();
+#pragma unroll
+        for (int v = 0; v < V; v++)
+            h[v] = u[s][v] = resets >> s & 1 ? u[s][v] : __builtin_fmaf(a[s][v], h[v], u[s][v]);
+    }
+    float sum[V];
+#pragma unroll
+    for (int v = 0; v < V; v++) sum[v] = 0.0f;
+#pragma unroll
+    for (int s = S - 1; s >= 0; s--) {
+        if (s >= n) continue;
+        Piece<T, V> dx, dr, di, dz;
+        const bool drop = resets >> s & 1;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            Gates<GATE> e;
+            const float xv = x[s].get(v);
+            e.set(xv, r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
+            const float p = drop ? 0.0f : s > 0 ? u[s > 0 ? s - 1 : 0][v] : before[v];
+            float dy = dout[s].get(v);
+            if constexpr (Z) {
+                float gate, slope;
+                silu2(z[s].get(v), gate, slope);
+                dz.set(v, dy * u[s][v] * slope);
+                dy *= gate;
+            }
+            const float G = dy + Q[v];
+            float gx, gr, gi = 0.0f, ws = 0.0f;
+            e.grads(G, p, xv, k[v], gx, gr, gi, ws);
+            Q[v] = drop ? 0.0f : a[s][v] * G;
+            sum[v] += ws;
+            dx.set(v, gx);
+            dr.set(v, gr);
+            di.set(v, gi);
+        }
+        if (live) {
+            const int64_t row = row0 + t0 + s;
+            dx.store(at_row<T>(q.dx, row, q.ld_dx), c);
+            dr.store(at_row<T>(q.dr, row, q.ld_dr), c);
+            if constexpr (GATE == MSS_GATE_DECAY) di.store(at_row<T>(q.di, row, q.ld_di), c);
+            if constexpr (Z) dz.store(at_row<T>(q.dz, row, q.ld_dz), c);
+        }
+    }
+    if (q.dh0 && t0 == 0 && live) {
+#pragma unroll
+        for (int v = 0; v < V; v++) q.dh0[int64_t{b} * q.D + c + v] = Q[v];
+    }
+    if constexpr (GATE == MSS_GATE_DECAY) {
+        // the chunk's share of sum w sigma(r), its waves in order
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; v++) fwd[wave][v][lane].A = sum[v];
+        __syncthreads();
+        if (wave == 0 && live) {
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                float all = 0.0f;
+#pragma unroll
+                for (int p = 0; p < kWaves; p++) all += fwd[p][v][lane].A;
+                part[(int64_t{b} * g.chunks + chunk) * q.D + c + v] = all;
+            }
+        }
+    }
+}
+
+// ddecay[d] = -c sigma(decay[d]) sum over the partial rows: 32 channels a
+// workgroup, 32 rows at a time.
+__global__ __launch_bounds__(1024) void gated_ddecay_kernel(const float* __restrict__ part,
+                                                            const float* __restrict__ decay,
+                                                            float* __restrict__ ddecay,
+                                                            int64_t rows, int64_t D, float scale) {
+    __shared__ float lds[32][33];
+    const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
+    const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float sum = 0.0f;
-    for (int64_t p = 0; p < rows; p++) sum += part[p * D + d];
+    if (d < D) {
+#pragma unroll 8
+        for (int64_t p = group; p < rows; p += 32) sum += part[p * D + d];
+    }
+    lds[group][lane] = sum;
+    __syncthreads();
+    if (group != 0 || d >= D) return;
+    sum = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 32; p++) sum += lds[p][lane];
     ddecay[d] = -scale * sigmoid(decay[d]) * sum;
 }
 
+// One token: lanes side by side over (sequence, vector of 4 channels).
+constexpr int kStepVec = 4;
 template <typename T, int GATE>
-__global__ __launch_bounds__(64) void gated_step_kernel(GatedArgs q) {
+__global__ __launch_bounds__(64) void gated_step_kernel(GatedArgs q, unsigned per) {
+    constexpr int V = kStepVec;
     const int64_t j = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-    if (j >= q.B * q.D) return;
-    const int64_t b = j / q.D, d = j % q.D;
-    const float k = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(q.decay[d]) : 0.0f;
-    const float iv = GATE == MSS_GATE_DECAY
-                         ? static_cast<float>(static_cast<const T*>(q.i)[b * q.ld_i + d])
-                         : 0.0f;
-    Gates<GATE> g;
-    g.set(static_cast<float>(static_cast<const T*>(q.x)[b * q.ld_x + d]),
-          static_cast<float>(static_cast<const T*>(q.r)[b * q.ld_r + d]), iv, k);
-    const float h = __builtin_fmaf(g.a, q.h[j], g.v);
-    q.h[j] = h;
-    const float out =
-        q.z ? h * silu(static_cast<float>(static_cast<const T*>(q.z)[b * q.ld_z + d])) : h;
-    static_cast<T*>(q.y)[b * q.ld_y + d] = static_cast<T>(out);
+    const int64_t b = j / per;
+    if (b >= q.B) return;
+    const int c = V * static_cast<int>(j - b * per), n = static_cast<int>(q.D);
+    RowVec<T, V> x, r, in, z, y;
+    RowVec<float, V> h, decay;
+    x.load(at_row<T>(q.x, b, q.ld_x), c, n);
+    r.load(at_row<T>(q.r, b, q.ld_r), c, n);
+    h.load(q.h + b * q.D, c, n);
+    if constexpr (GATE == MSS_GATE_DECAY) {
+        in.load(at_row<T>(q.i, b, q.ld_i), c, n);
+        decay.load(q.decay, c, n);
+    }
+    if (q.z) z.load(at_row<T>(q.z, b, q.ld_z), c, n);
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        Gates<GATE> e;
+        const float k = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(decay[v]) : 0.0f;
+        e.set(x[v], r[v], GATE == MSS_GATE_DECAY ? in[v] : 0.0f, k);
+        h.set(v, __builtin_fmaf(e.a, h[v], e.v));
+        y.set(v, q.z ? h[v] * silu(z[v]) : h[v]);
+    }
+    h.store(q.h + b * q.D, c, n);
+    y.store(at_row<T>(q.y, b, q.ld_y), c, n);
 }
 
-template <typename T, typename F>
+template <typename T, int V, typename F>
 hipError_t by_gate(int gate, F f) {
+    constexpr std::integral_constant<int, V> v{};
     switch (gate) {
-        case MSS_GATE_SIGMOID: f(T{}, std::integral_constant<int, MSS_GATE_SIGMOID>{}); break;
-        case MSS_GATE_DECAY: f(T{}, std::integral_constant<int, MSS_GATE_DECAY>{}); break;
-        case MSS_GATE_LOG: f(T{}, std::integral_constant<int, MSS_GATE_LOG>{}); break;
+        case MSS_GATE_SIGMOID: f(T{}, v, std::integral_constant<int, MSS_GATE_SIGMOID>{}); break;
+        case MSS_GATE_DECAY: f(T{}, v, std::integral_constant<int, MSS_GATE_DECAY>{}); break;
+        case MSS_GATE_LOG: f(T{}, v, std::integral_constant<int, MSS_GATE_LOG>{}); break;
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }
 
-// f(element, gate) for the call's types.
+// f(element, channels per lane, gate) for the call's types.  A single channel
+// is no pair.
 template <typename F>
 hipError_t dispatch(const GatedArgs& a, F f) {
     switch (a.dtype) {
-        case MSS_F32: return by_gate<float>(a.gate, f);
-        case MSS_BF16: return by_gate<bf16>(a.gate, f);
-        case MSS_F16: return by_gate<f16>(a.gate, f);
+        case MSS_F32: return by_gate<float, 1>(a.gate, f);
+        case MSS_BF16: return a.D > 1 ? by_gate<bf16, 2>(a.gate, f) : by_gate<bf16, 1>(a.gate, f);
+        case MSS_F16: return a.D > 1 ? by_gate<f16, 2>(a.gate, f) : by_gate<f16, 1>(a.gate, f);
         default: return hipErrorInvalidValue;
     }
 }
 
-unsigned blocks(int64_t n) { return static_cast<unsigned>((n + 63) / 64); }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// Words handed over for chunks of `len` steps, over tiles of whole pairs of
+// waves' channels (what either V needs).
+int64_t chain_words(int64_t B, int64_t L, int64_t D, int64_t len) {
+    const int64_t chunks = cdiv(L, len);
+    return chunks <= 1 ? 0 : B * cdiv(D, 128) * 128 * (chunks + cdiv(chunks, kWaves));
+}
+
+bool chain_bytes(int64_t B, int64_t L, int64_t D, int64_t len, int64_t& bytes) {
+    // a workgroup per chunk and tile; the word counts stay far below 2^63
+    // (8 bytes for every `len` steps of a channel whose elements were counted)
+    if (D > INT32_MAX - 128 || cdiv(L, len) > INT32_MAX / (B * cdiv(D, 64))) return false;
+    const int64_t words = chain_words(B, L, D, len);
+    bytes = words == 0 ? 0 : align256(256 + 8 * words);
+    return true;
+}
+
+Chain chain_of(const GatedArgs& a, int V, int64_t len) {
+    Chain g;
+    g.ctiles = static_cast<unsigned>(cdiv(a.D, 64 * V));
+    g.tiles = static_cast<unsigned>(a.B * g.ctiles);
+    g.chunks = cdiv(a.L, len);
+    g.groups = cdiv(g.chunks, kWaves);
+    g.ticket = static_cast<unsigned*>(a.ws);
+    g.maps = static_cast<Word*>(a.ws) + 32;
+    g.states = g.maps + int64_t{g.tiles} * g.chunks * 64 * V;
+    return g;
+}
+
+// Marks the words of a chain as not written and zeroes its counter.
+hipError_t unset(const Chain& g, int V, hipStream_t st) {
+    if (g.chunks == 1) return hipSuccess;
+    const int64_t n = 32 + g.tiles * (g.chunks + g.groups) * 64 * V;
+    const int64_t blocks = cdiv(n, 1024);
+    gated_unset_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, st>>>(
+        static_cast<Word*>(static_cast<void*>(g.ticket)), n);
+    return hipGetLastError();
+}
 
 }  // namespace
 
-bool gated_scan_workspace(int64_t B, int64_t L, int64_t D, int gate, int64_t& bytes) {
-    bytes = 0;
-    return B * D <= (int64_t{INT32_MAX} - 1) * 64;
+bool gated_step_fits(int64_t B, int64_t D) {
+    return D <= INT32_MAX - 64 && (B == 0 || cdiv(D, kStepVec) <= (int64_t{INT32_MAX} - 1) * 64 / B);
+}
+
+bool gated_scan_workspace(int64_t B, int64_t L, int64_t D, int64_t& bytes) {
+    return chain_bytes(B, L, D, kChunk, bytes);
 }
 
 bool gated_scan_bwd_workspace(int64_t B, int64_t L, int64_t D, int gate, int64_t& bytes) {
-    bytes = gate == MSS_GATE_DECAY ? (B * D * 4 + 255) / 256 * 256 : 0;
-    return B * D <= (int64_t{INT32_MAX} - 1) * 64;
+    if (!chain_bytes(B, L, D, kBwdChunk, bytes)) return false;
+    if (gate == MSS_GATE_DECAY) bytes += align256(B * cdiv(L, kBwdChunk) * D * 4);
+    return true;
 }
 
 hipError_t launch_gated_scan(const GatedArgs& a, hipStream_t st) {
-    return dispatch(a, [&](auto t, auto gate) {
-        gated_scan_kernel<decltype(t), gate.value><<<blocks(a.B * a.D), 64, 0, st>>>(a);
+    return dispatch(a, [&](auto t, auto v, auto gate) {
+        using T = decltype(t);
+        const Chain g = chain_of(a, v.value, kChunk);
+        if (unset(g, v.value, st) != hipSuccess) return;
+        const unsigned grid = g.tiles * static_cast<unsigned>(g.chunks);
+        if (a.z)
+            gated_scan_kernel<T, v.value, gate.value, true><<<grid, 64 * kWaves, 0, st>>>(a, g);
+        else
+            gated_scan_kernel<T, v.value, gate.value, false><<<grid, 64 * kWaves, 0, st>>>(a, g);
     });
 }
 
 hipError_t launch_gated_scan_bwd(const GatedArgs& a, hipStream_t st) {
-    const hipError_t e = dispatch(a, [&](auto t, auto gate) {
-        gated_scan_bwd_kernel<decltype(t), gate.value><<<blocks(a.B * a.D), 64, 0, st>>>(a);
+    const int64_t rows = a.B * cdiv(a.L, kBwdChunk);
+    int64_t bytes = 0;
+    chain_bytes(a.B, a.L, a.D, kBwdChunk, bytes);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + bytes);
+    const hipError_t e = dispatch(a, [&](auto t, auto v, auto gate) {
+        using T = decltype(t);
+        const Chain g = chain_of(a, v.value, kBwdChunk);
+        if (unset(g, v.value, st) != hipSuccess) return;
+        const unsigned grid = g.tiles * static_cast<unsigned>(g.chunks);
+        if (a.z)
+            gated_scan_bwd_kernel<T, v.value, gate.value, true>
+                <<<grid, 64 * kWaves, 0, st>>>(a, g, part);
+        else
+            gated_scan_bwd_kernel<T, v.value, gate.value, false>
+                <<<grid, 64 * kWaves, 0, st>>>(a, g, part);
     });
     if (e != hipSuccess || a.gate != MSS_GATE_DECAY) return e;
-    gated_ddecay_kernel<<<blocks(a.D), 64, 0, st>>>(static_cast<const float*>(a.ws), a.decay,
-                                                    a.ddecay, a.B, a.D, a.gate_scale);
+    gated_ddecay_kernel<<<static_cast<unsigned>(cdiv(a.D, 32)), 1024, 0, st>>>(
+        part, a.decay, a.ddecay, rows, a.D, a.gate_scale);
     return hipGetLastError();
 }
 
 hipError_t launch_gated_step(const GatedArgs& a, hipStream_t st) {
-    return dispatch(a, [&](auto t, auto gate) {
-        gated_step_kernel<decltype(t), gate.value><<<blocks(a.B * a.D), 64, 0, st>>>(a);
+    return dispatch(a, [&](auto t, auto, auto gate) {
+        const int64_t per = cdiv(a.D, kStepVec);
+        gated_step_kernel<decltype(t), gate.value>
+            <<<static_cast<unsigned>(cdiv(a.B * per, 64)), 64, 0, st>>>(a, static_cast<unsigned>(per));
     });
 }
 

@@ -42,8 +42,9 @@ struct GatedArgs {
 
 // Workspace bytes (sizes and gate only; never the pointers or strides).
 // False when a size overflows or the launch would not fit a grid.
-bool gated_scan_workspace(int64_t B, int64_t L, int64_t D, int gate, int64_t& bytes);
+bool gated_scan_workspace(int64_t B, int64_t L, int64_t D, int64_t& bytes);
 bool gated_scan_bwd_workspace(int64_t B, int64_t L, int64_t D, int gate, int64_t& bytes);
+bool gated_step_fits(int64_t B, int64_t D);
 hipError_t launch_gated_scan(const GatedArgs& a, hipStream_t st);
 hipError_t launch_gated_scan_bwd(const GatedArgs& a, hipStream_t st);
 hipError_t launch_gated_step(const GatedArgs& a, hipStream_t st);
