@@ -605,23 +605,24 @@ def make_norm_strides(*strides) -> NormStrides:
 class _Call:
     """Argument checks of one call: the current device and the activation type."""
 
+    __slots__ = ("torch", "dev", "like", "dtype", "code")
+
     def __init__(self, like, name):
-        torch = _torch()
+        self.torch = torch = _torch()
         if not isinstance(like, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if not like.is_cuda:
             raise ValueError(f"{name} must be on the GPU")
-        if like.dtype not in _dtype_codes():
-            raise TypeError(f"{name} must be float32, bfloat16 or float16, got {like.dtype}")
-        self.tensor, self.f32 = torch.Tensor, torch.float32
-        self.dev = torch.cuda.current_device()
         self.like, self.dtype = like, like.dtype
-        self.code = _dtype_codes()[like.dtype]
+        self.code = _dtype_codes().get(self.dtype)
+        if self.code is None:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16, got {like.dtype}")
+        self.dev = torch.cuda.current_device()
 
     def _basic(self, t, name, dtype, shape):
-        if not isinstance(t, self.tensor):
+        if not isinstance(t, self.torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.get_device() != self.dev:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{self.dev}")
@@ -636,7 +637,7 @@ class _Call:
             return None, cols
         self._basic(t, name, dtype or self.dtype, (rows, cols))
         row, col = t.stride()
-        if cols > 1 and rows > 0 and col != 1:
+        if col != 1 and cols > 1 and rows > 0:
             raise ValueError(f"{name}: columns must be contiguous")
         return t.data_ptr() or None, row if rows > 1 else cols
 
@@ -646,24 +647,34 @@ class _Call:
             if required:
                 raise ValueError(f"{name} is required")
             return None
-        self._basic(t, name, dtype or self.f32, shape)
+        self._basic(t, name, dtype or self.torch.float32, shape)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr() or None
 
     def empty(self, shape, dtype=None):
-        return _torch().empty(shape, dtype=dtype or self.dtype, device=self.like.device)
+        like = self.like
+        if (dtype is None or dtype is self.dtype) and shape == like.shape and like.is_contiguous():
+            return self.torch.empty_like(like)
+        return self.torch.empty(shape, dtype=dtype or self.dtype, device=like.device)
+
+    def stream(self, stream):
+        """The stream's handle (the current stream's without a stream)."""
+        if stream is None:
+            return self.torch.cuda.current_stream(self.dev).cuda_stream
+        return _stream(stream)
 
     def workspace(self, need, workspace, stream):
         """(pointer, bytes, tensor) of the caller's workspace, or of a fresh one."""
         if workspace is None:
             if need == 0:
                 return None, 0, None
-            workspace = self.empty((need + 256,), _torch().uint8)
+            workspace = self.empty((need + 256,), self.torch.uint8)
             if stream is not None:
                 workspace.record_stream(stream)
-        elif (not isinstance(workspace, self.tensor) or workspace.dtype != _torch().uint8
-              or workspace.get_device() != self.dev or not workspace.is_contiguous()):
+        elif (not isinstance(workspace, self.torch.Tensor)
+              or workspace.dtype != self.torch.uint8 or workspace.get_device() != self.dev
+              or not workspace.is_contiguous()):
             raise TypeError("workspace must be a contiguous uint8 tensor on the current GPU")
         base = workspace.data_ptr()
         pad = (-base) % 256
@@ -699,7 +710,7 @@ def _ref(block):
 def _flag(t, shape, call, dtype=None):
     """An optional output given as False / True (allocate) or a tensor."""
     if isinstance(t, bool):
-        return call.empty(shape, dtype or call.f32) if t else None
+        return call.empty(shape, dtype or call.torch.float32) if t else None
     return t
 
 
@@ -753,7 +764,7 @@ def gated_scan(x, r, i=None, decay=None, z=None, h0=None, reset=None, *, batch, 
         _ref(make_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
         c.dense(h0, "h0", (batch, D)), _reset(c, reset, M), py,
         c.dense(ck, "h_ckpt", (batch, gated_ckpt_steps(seq_len), D)),
-        c.dense(hl, "h_last", (batch, D)), wp, wn, _stream(stream)))
+        c.dense(hl, "h_last", (batch, D)), wp, wn, c.stream(stream)))
     return y, ck, hl
 
 
@@ -788,7 +799,7 @@ def gated_scan_backward(x, r, i, decay, z, reset, h_ckpt, dout, *, batch, seq_le
         c.dense(h_ckpt, "h_ckpt", (batch, gated_ckpt_steps(seq_len), D), required=True), po,
         c.dense(dh_last, "dh_last", (batch, D)), pdx, pdr, pdi,
         c.dense(g["ddecay"], "ddecay", (D,)), pdz, c.dense(g["dh0"], "dh0", (batch, D)),
-        wp, wn, _stream(stream)))
+        wp, wn, c.stream(stream)))
     return g
 
 
@@ -805,7 +816,7 @@ def _outputs(c, want, out, f32_shapes, shape, types=None):
         elif out.get(k) is not None:
             g[k] = out[k]
         elif k in f32_shapes:
-            g[k] = c.empty(f32_shapes[k], c.f32)
+            g[k] = c.empty(f32_shapes[k], c.torch.float32)
         else:
             g[k] = c.empty(shape, (types or {}).get(k))
     return g
@@ -824,13 +835,13 @@ def gated_step(x, r, i, decay, z, h, *, gate, gate_scale=8.0, out=None, stream=N
     _check("mss_gated_step", lib().mss_gated_step(
         _ref(make_gated_dims(batch, 1, D, c.code, code, gate_scale)),
         _ref(make_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
-        c.dense(h, "h", (batch, D), required=True), py, _stream(stream)))
+        c.dense(h, "h", (batch, D), required=True), py, c.stream(stream)))
     return y
 
 
 def _res_code(c, t, name):
     code = _dtype_codes().get(t.dtype)
-    if code is None or (code != c.code and t.dtype != c.f32):
+    if code is None or (code != c.code and t.dtype != c.torch.float32):
         raise TypeError(f"{name} must be {c.dtype} or float32, got {t.dtype}")
     return code
 
@@ -859,7 +870,7 @@ def add_norm(x, residual, weight, bias=None, scale=None, *, kind="rms", eps=1e-6
         _ref(make_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
         _ref(make_norm_strides(lx, 0, lr, ls, ly)), px, pr,
         c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)),
-        c.dense(scale, "scale", (D,)), ps, py, _stream(stream)))
+        c.dense(scale, "scale", (D,)), ps, py, c.stream(stream)))
     return y, s
 
 
@@ -893,7 +904,7 @@ def add_norm_backward(s, weight, dy, ds=None, x=None, scale=None, *, bias=False,
         c.dense(weight, "weight", (D,), required=True), po, pds, px,
         c.dense(scale, "scale", (D,)), pdx, pdr, c.dense(g["dweight"], "dweight", (D,)),
         c.dense(g["dbias"], "dbias", (D,)), c.dense(g["dscale"], "dscale", (D,)), wp, wn,
-        _stream(stream)))
+        c.stream(stream)))
     return g
 
 
@@ -918,7 +929,7 @@ def gated_norm(x, z, weight, bias=None, residual=None, scale=None, *, groups=1, 
                             _choice(GATE_ORDERS, order, "order"), groups, eps, alpha)),
         _ref(make_norm_strides(lx, lz, lr, 0, ly)), px, pz,
         c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)), pr,
-        c.dense(scale, "scale", (D,)), py, _stream(stream)))
+        c.dense(scale, "scale", (D,)), py, c.stream(stream)))
     return y
 
 
@@ -949,5 +960,5 @@ def gated_norm_backward(x, z, weight, bias, scale, dout, *, groups=1, order="bef
         c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)),
         c.dense(scale, "scale", (D,)), po, pdx, pdz, c.dense(g["dweight"], "dweight", (D,)),
         c.dense(g["dbias"], "dbias", (D,)), c.dense(g["dscale"], "dscale", (D,)), wp, wn,
-        _stream(stream)))
+        c.stream(stream)))
     return g

@@ -44,20 +44,20 @@ class Checks {
     // A row-strided activation tensor: the element's alignment when the call
     // gives strides, 16 bytes otherwise.
     void in(const void* p, int64_t rows, int64_t width, int64_t ld, int64_t elem, bool required) {
-        add(ins_, p, rows, width, ld, elem, required, strided_ ? elem : 16);
+        add(ins_, n_ins_, p, rows, width, ld, elem, required, strided_ ? elem : 16);
     }
     void out(void* p, int64_t rows, int64_t width, int64_t ld, int64_t elem, bool required) {
-        add(outs_, p, rows, width, ld, elem, required, strided_ ? elem : 16);
+        add(outs_, n_outs_, p, rows, width, ld, elem, required, strided_ ? elem : 16);
     }
     // A dense tensor (16-byte aligned).
     void in(const void* p, int64_t elems, int64_t elem, bool required) {
-        add(ins_, p, elems > 0 ? 1 : 0, elems, elems, elem, required, 16);
+        add(ins_, n_ins_, p, elems > 0 ? 1 : 0, elems, elems, elem, required, 16);
     }
     void out(void* p, int64_t elems, int64_t elem, bool required) {
-        add(outs_, p, elems > 0 ? 1 : 0, elems, elems, elem, required, 16);
+        add(outs_, n_outs_, p, elems > 0 ? 1 : 0, elems, elems, elem, required, 16);
     }
     // Bytes of any alignment (the reset flags).
-    void in_bytes(const void* p, int64_t n) { add(ins_, p, n > 0 ? 1 : 0, n, n, 1, false, 1); }
+    void in_bytes(const void* p, int64_t n) { add(ins_, n_ins_, p, n > 0 ? 1 : 0, n, n, 1, false, 1); }
     void must(bool ok) {
         if (!ok && status_ == MSS_OK) status_ = MSS_EINVAL;
     }
@@ -67,26 +67,27 @@ class Checks {
         ws_status_ = !p || bytes < static_cast<uint64_t>(need) ? MSS_EWORKSPACE
                      : reinterpret_cast<uintptr_t>(p) % 256    ? MSS_EALIGN
                                                                : MSS_OK;
-        if (p) outs_.push_back({p, 1, need, need});
+        if (p) outs_[n_outs_++] = {p, 1, need, need};
     }
     // `out` may be exactly `in` (same pointer and stride), updated in place.
     int finish(const void* in_place = nullptr) {
         if (status_ != MSS_OK) return status_;
-        for (size_t i = 0; i < outs_.size(); i++) {
-            for (const Rows& s : ins_) {
+        for (int i = 0; i < n_outs_; i++) {
+            for (int j = 0; j < n_ins_; j++) {
+                const Rows& s = ins_[j];
                 if (in_place && outs_[i].p == in_place && s.p == in_place &&
                     outs_[i].stride == s.stride)
                     continue;
                 if (overlap(outs_[i], s)) return MSS_EALIAS;
             }
-            for (size_t j = i + 1; j < outs_.size(); j++)
+            for (int j = i + 1; j < n_outs_; j++)
                 if (overlap(outs_[i], outs_[j])) return MSS_EALIAS;
         }
         return ws_status_;
     }
 
   private:
-    void add(std::vector<Rows>& v, const void* p, int64_t rows, int64_t width, int64_t ld,
+    void add(Rows* v, int& used, const void* p, int64_t rows, int64_t width, int64_t ld,
              int64_t elem, bool required, int64_t align) {
         if (status_ != MSS_OK) return;
         int64_t all;
@@ -102,12 +103,14 @@ class Checks {
             status_ = MSS_EALIGN;
             return;
         }
-        if (rows > 0 && width > 0) v.push_back({p, rows, width * elem, ld * elem});
+        if (rows > 0 && width > 0) v[used++] = {p, rows, width * elem, ld * elem};
     }
 
     bool strided_;
     int status_ = MSS_OK, ws_status_ = MSS_OK;
-    std::vector<Rows> ins_, outs_;
+    // the longest argument list has ten inputs and seven outputs
+    Rows ins_[16], outs_[16];
+    int n_ins_ = 0, n_outs_ = 0;
 };
 
 int launched(hipError_t e) { return e == hipSuccess ? MSS_OK : hip_fail(e); }

@@ -44,14 +44,20 @@ struct Gates {
     float s, m, g;    // DECAY: sigma(r), sqrt(1 - a^2), sigma(i)
     float gc;         // DECAY: 1 - sigma(i)
 
-    // k = c softplus(decay) (DECAY)
+    // a and v alone, or (FULL) all of them; k = c softplus(decay) (DECAY).
+    template <bool FULL>
     __device__ __forceinline__ void set(float x, float r, float i, float k) {
         if constexpr (GATE == MSS_GATE_SIGMOID) {
             sigmoid2(r, a, c);
             v = c * x;
         } else if constexpr (GATE == MSS_GATE_DECAY) {
-            sigmoid2(r, s, c);
-            sigmoid2(i, g, gc);
+            if constexpr (FULL) {
+                sigmoid2(r, s, c);
+                sigmoid2(i, g, gc);
+            } else {
+                s = sigmoid(r);
+                g = sigmoid(i);
+            }
             const float l2 = -kLog2e * k * s;
             a = ex2(l2);
             m = decay_input_scale(l2, a);
@@ -84,12 +90,20 @@ struct Gates {
 };
 
 constexpr int kWaves = 8;                        // waves of a workgroup, chunks of a group
-constexpr int kSteps = 16;                       // S of the forward
-constexpr int kChunk = kWaves * kSteps;
+#ifndef KS2
+#define KS2 16
+#endif
+#ifndef KS4
+#define KS4 16
+#endif
+template <typename T>                            // S of the forward
+constexpr int kSteps = sizeof(T) == 2 ? KS2 : KS4;
+template <typename T>
+constexpr int kChunk = kWaves * kSteps<T>;
+constexpr int kMinChunk = 64;
 constexpr int kBwdSteps = 8;                     // S of the backward: twice the inputs per step
 constexpr int kBwdChunk = kWaves * kBwdSteps;
 static_assert(kBwdChunk == MSS_GATED_CKPT_STEPS, "a backward chunk starts from a checkpoint");
-static_assert(kChunk % MSS_GATED_CKPT_STEPS == 0, "checkpoints lie between a chunk's waves");
 
 typedef unsigned long long Word;
 constexpr Word kUnset = ~0ull;
@@ -206,9 +220,51 @@ __device__ __forceinline__ unsigned reset_bits(const uint8_t* reset, int64_t row
         __builtin_amdgcn_ballot_w64(lane < S && t < L && reset[row0 + t] != 0));
 }
 
+// Steps past the end of the sequence carry the state as it is; a reset's
+// carry factor is 0.  Both are rare, and the same for all lanes.
+template <int S, int V>
+__device__ __forceinline__ void mend(float (&a)[S][V], float (&u)[S][V], int n, unsigned resets) {
+    if (n < S) {
+#pragma unroll
+        for (int s = 0; s < S; s++)
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                a[s][v] = s < n ? a[s][v] : 1.0f;
+                u[s][v] = s < n ? u[s][v] : 0.0f;
+            }
+    }
+    if (resets) {
+#pragma unroll
+        for (int s = 0; s < S; s++)
+#pragma unroll
+            for (int v = 0; v < V; v++) a[s][v] = resets >> s & 1 ? 0.0f : a[s][v];
+    }
+}
+
+// The states after each step in the place of the input terms, from the state
+// h that enters; h: the last.  Where a step resets, an infinite state goes no
+// further (0 times it would be NaN).
+template <int S, int V>
+__device__ __forceinline__ void states(const float (&a)[S][V], float (&u)[S][V], float (&h)[V],
+                                       unsigned resets) {
+    if (resets) {
+#pragma unroll
+        for (int s = 0; s < S; s++)
+#pragma unroll
+            for (int v = 0; v < V; v++)
+                h[v] = u[s][v] = resets >> s & 1 ? u[s][v] : __builtin_fmaf(a[s][v], h[v], u[s][v]);
+    } else {
+#pragma unroll
+        for (int s = 0; s < S; s++)
+#pragma unroll
+            for (int v = 0; v < V; v++) h[v] = u[s][v] = __builtin_fmaf(a[s][v], h[v], u[s][v]);
+    }
+}
+
 template <typename T, int V, int GATE, bool Z>
 __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Chain g) {
-    constexpr int S = kSteps;
+    constexpr int S = kSteps<T>;
+    static_assert(kChunk<T> % MSS_GATED_CKPT_STEPS == 0, "checkpoints lie between a chunk's waves");
     __shared__ Map own[kWaves][V][64], mates[kWaves][V][64];
     __shared__ float entering[V][64];
     __shared__ unsigned ticket;
@@ -221,7 +277,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
     unsigned c = tile % g.ctiles * (64 * V) + lane * V;
     const bool live = c < q.D;
     c = live && c + V <= q.D ? c : static_cast<unsigned>(q.D - V);
-    const int64_t t0 = chunk * kChunk + wave * S, row0 = int64_t{b} * q.L;
+    const int64_t t0 = chunk * kChunk<T> + wave * S, row0 = int64_t{b} * q.L;
     const int n = t0 >= q.L ? 0 : q.L - t0 < S ? static_cast<int>(q.L - t0) : S;
 
     Piece<T, V> x[S], r[S], in[S], z[S];
@@ -248,18 +304,24 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
     float a[S][V], u[S][V];
     Map m[V];
 #pragma unroll
-    for (int v = 0; v < V; v++) m[v] = {1.0f, 0.0f};
-#pragma unroll
     for (int s = 0; s < S; s++) {
 #pragma unroll
         for (int v = 0; v < V; v++) {
             Gates<GATE> e;
-            e.set(x[s].get(v), r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
-            a[s][v] = s < n ? e.a : 1.0f;
-            u[s][v] = s < n ? e.v : 0.0f;
-            const bool drop = resets >> s & 1;
-            m[v].A = drop ? 0.0f : m[v].A * a[s][v];
-            m[v].H = drop ? u[s][v] : __builtin_fmaf(a[s][v], m[v].H, u[s][v]);
+            e.template set<false>(x[s].get(v), r[s].get(v),
+                                  GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
+            a[s][v] = e.a;
+            u[s][v] = e.v;
+        }
+    }
+    mend<S, V>(a, u, n, resets);
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        m[v] = {1.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            m[v].A *= a[s][v];
+            m[v].H = __builtin_fmaf(a[s][v], m[v].H, u[s][v]);
         }
     }
 #pragma unroll
@@ -320,17 +382,17 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
 #pragma unroll
         for (int v = 0; v < V; v++) out[c + v] = h[v];
     }
+    states<S, V>(a, u, h, resets);
 #pragma unroll
     for (int s = 0; s < S; s++) {
         if (s >= n) continue;
         Piece<T, V> y;
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            h[v] = resets >> s & 1 ? u[s][v] : __builtin_fmaf(a[s][v], h[v], u[s][v]);
             if constexpr (Z)
-                y.set(v, h[v] * silu(z[s].get(v)));
+                y.set(v, u[s][v] * silu(z[s].get(v)));
             else
-                y.set(v, h[v]);
+                y.set(v, u[s][v]);
         }
         if (live) y.store(at_row<T>(q.y, row0 + t0 + s, q.ld_y), c);
     }
@@ -385,23 +447,34 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_bwd_kernel(GatedArgs q
     float a[S][V], u[S][V];   // u: the input term, later the state
     Map f[V], w[V];
 #pragma unroll
-    for (int v = 0; v < V; v++) {
-        f[v] = {1.0f, 0.0f};
-        w[v].H = 0.0f;
-    }
-#pragma unroll
     for (int s = 0; s < S; s++) {
 #pragma unroll
         for (int v = 0; v < V; v++) {
             Gates<GATE> e;
-            e.set(x[s].get(v), r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
-            float dy = s < n ? dout[s].get(v) : 0.0f;
+            e.template set<false>(x[s].get(v), r[s].get(v),
+                                  GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
+            a[s][v] = e.a;
+            u[s][v] = e.v;
+        }
+    }
+    mend<S, V>(a, u, n, resets);
+    if (n < S) {
+#pragma unroll
+        for (int s = 0; s < S; s++)
+#pragma unroll
+            for (int v = 0; v < V; v++)
+                if (s >= n) dout[s].set(v, 0.0f);
+    }
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        f[v] = {1.0f, 0.0f};
+        w[v].H = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            float dy = dout[s].get(v);
             if constexpr (Z) dy *= silu(z[s].get(v));
-            a[s][v] = s < n ? e.a : 1.0f;
-            u[s][v] = s < n ? e.v : 0.0f;
-            const bool drop = resets >> s & 1;
-            f[v].H = drop ? u[s][v] : __builtin_fmaf(a[s][v], f[v].H, u[s][v]);
-            f[v].A = drop ? 0.0f : f[v].A * a[s][v];
+            f[v].A *= a[s][v];
+            f[v].H = __builtin_fmaf(a[s][v], f[v].H, u[s][v]);
             w[v].H = __builtin_fmaf(f[v].A, dy, w[v].H);
         }
     }
@@ -469,10 +542,8 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_bwd_kernel(GatedArgs q
         r[s].keep();
         if constexpr (GATE == MSS_GATE_DECAY) in[s].keep();
         if constexpr (Z) z[s].keep();
-#pragma unroll
-        for (int v = 0; v < V; v++)
-            h[v] = u[s][v] = resets >> s & 1 ? u[s][v] : __builtin_fmaf(a[s][v], h[v], u[s][v]);
     }
+    states<S, V>(a, u, h, resets);
     float sum[V];
 #pragma unroll
     for (int v = 0; v < V; v++) sum[v] = 0.0f;
@@ -485,7 +556,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_bwd_kernel(GatedArgs q
         for (int v = 0; v < V; v++) {
             Gates<GATE> e;
             const float xv = x[s].get(v);
-            e.set(xv, r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
+            e.template set<true>(xv, r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
             const float p = drop ? 0.0f : s > 0 ? u[s > 0 ? s - 1 : 0][v] : before[v];
             float dy = dout[s].get(v);
             if constexpr (Z) {
@@ -497,7 +568,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_bwd_kernel(GatedArgs q
             const float G = dy + Q[v];
             float gx, gr, gi = 0.0f, ws = 0.0f;
             e.grads(G, p, xv, k[v], gx, gr, gi, ws);
-            Q[v] = drop ? 0.0f : a[s][v] * G;
+            Q[v] = a[s][v] * G;
             sum[v] += ws;
             dx.set(v, gx);
             dr.set(v, gr);
@@ -579,7 +650,7 @@ __global__ __launch_bounds__(64) void gated_step_kernel(GatedArgs q, unsigned pe
     for (int v = 0; v < V; v++) {
         Gates<GATE> e;
         const float k = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(decay[v]) : 0.0f;
-        e.set(x[v], r[v], GATE == MSS_GATE_DECAY ? in[v] : 0.0f, k);
+        e.template set<false>(x[v], r[v], GATE == MSS_GATE_DECAY ? in[v] : 0.0f, k);
         h.set(v, __builtin_fmaf(e.a, h[v], e.v));
         y.set(v, q.z ? h[v] * silu(z[v]) : h[v]);
     }
@@ -659,7 +730,7 @@ bool gated_step_fits(int64_t B, int64_t D) {
 }
 
 bool gated_scan_workspace(int64_t B, int64_t L, int64_t D, int64_t& bytes) {
-    return chain_bytes(B, L, D, kChunk, bytes);
+    return chain_bytes(B, L, D, kMinChunk, bytes);
 }
 
 bool gated_scan_bwd_workspace(int64_t B, int64_t L, int64_t D, int gate, int64_t& bytes) {
@@ -671,7 +742,7 @@ bool gated_scan_bwd_workspace(int64_t B, int64_t L, int64_t D, int gate, int64_t
 hipError_t launch_gated_scan(const GatedArgs& a, hipStream_t st) {
     return dispatch(a, [&](auto t, auto v, auto gate) {
         using T = decltype(t);
-        const Chain g = chain_of(a, v.value, kChunk);
+        const Chain g = chain_of(a, v.value, kChunk<T>);
         if (unset(g, v.value, st) != hipSuccess) return;
         const unsigned grid = g.tiles * static_cast<unsigned>(g.chunks);
         if (a.z)

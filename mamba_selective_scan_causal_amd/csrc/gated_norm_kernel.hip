@@ -363,7 +363,7 @@ hipError_t launch_gated_norm(const NormArgs& a, hipStream_t st) {
     return dispatch(a, [&](auto t) {
         using T = decltype(t);
         const bool held = by_width<kVec<T>>(a.D / a.G, [&](auto s) {
-            const auto grid = a.G * row_groups(a.M, a.G, s.threads, s.rows, kRowGroups);
+            const auto grid = a.G * row_groups(a.M, a.G, s.threads, s.rows);
             auto go = [&](auto before) {
                 gated_norm_kernel<T, s.TEAM, s.NC, before.value>
                     <<<static_cast<unsigned>(grid), s.threads, 0, st>>>(a);
@@ -374,7 +374,7 @@ hipError_t launch_gated_norm(const NormArgs& a, hipStream_t st) {
                 go(std::false_type{});
         });
         if (!held) {
-            const auto grid = a.G * row_groups(a.M, a.G, kWide, 1, kRowGroups);
+            const auto grid = a.G * row_groups(a.M, a.G, kWide, 1);
             gated_norm_wide_kernel<T><<<static_cast<unsigned>(grid), kWide, 0, st>>>(a);
         }
     });
@@ -387,7 +387,7 @@ hipError_t launch_gated_norm_bwd(const NormArgs& a, hipStream_t st) {
     const hipError_t e = dispatch(a, [&](auto t) {
         using T = decltype(t);
         const bool held = by_width<kVec<T>>(a.D / a.G, [&](auto s) {
-            rows = row_groups(a.M, a.G, s.threads, s.rows, kPartRows);
+            rows = part_groups(a.M, a.G, s.threads, s.rows);
             const unsigned grid = static_cast<unsigned>(rows * a.G);
             auto go = [&](auto before, auto more) {
                 gated_norm_bwd_kernel<T, s.TEAM, s.NC, before.value, more.value>
@@ -400,7 +400,7 @@ hipError_t launch_gated_norm_bwd(const NormArgs& a, hipStream_t st) {
                       : go(std::false_type{}, std::false_type{});
         });
         if (!held) {
-            rows = row_groups(a.M, a.G, kWide, 1, kPartRows);
+            rows = part_groups(a.M, a.G, kWide, 1);
             K = 2;
             gated_norm_bwd_wide_kernel<T>
                 <<<static_cast<unsigned>(rows * a.G), kWide, 0, st>>>(a);

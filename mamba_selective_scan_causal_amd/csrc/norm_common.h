@@ -168,17 +168,21 @@ struct Shape {
 
 // Workgroups per group of channels: two thousand lanes for each of 256 CUs
 // over all groups (a CU's waves, or twice what its registers hold: the next
-// ones start as others end), none without a row of its own.  `most` bounds
-// the backward's, whose workgroups each write a row of partial sums.
-inline int64_t row_groups(int64_t M, int64_t G, int threads, int rows, int64_t most) {
+// ones start as others end), none without a row of its own.
+inline int64_t row_groups(int64_t M, int64_t G, int threads, int rows, int64_t most = 1 << 20) {
     int64_t p = 256 * 2048 / threads;
     if (p > most) p = most;
     p = (p + G - 1) / G;
     const int64_t all = (M + rows - 1) / rows;
     return p < all ? p : all;
 }
-constexpr int64_t kPartRows = 1024;   // backward
-constexpr int64_t kRowGroups = 1 << 20;
+
+// The same for the backward passes, whose workgroups each write a row of
+// partial sums: eight rows of input to each, between 256 and 1024 workgroups.
+inline int64_t part_groups(int64_t M, int64_t G, int threads, int rows) {
+    const int64_t most = M / 8 < 256 ? 256 : M / 8 < 1024 ? M / 8 : 1024;
+    return row_groups(M, G, threads, rows, most);
+}
 
 // f(Shape) for groups of n channels, V to a vector: a quarter of a wave or a
 // wave where one vector a lane is enough, else a workgroup with one (two past

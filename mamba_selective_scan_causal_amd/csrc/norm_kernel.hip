@@ -356,7 +356,7 @@ hipError_t dispatch(const NormArgs& a, F f) {
 
 bool norm_bwd_workspace(int64_t M, int64_t D, int64_t G, int64_t& bytes) {
     if (D > INT32_MAX / 2 || G > INT32_MAX / 1024) return false;
-    bytes = (row_groups(M, G, 64, 1, kPartRows) * 3 * D * 4 + 255) / 256 * 256;
+    bytes = (part_groups(M, G, 64, 1) * 3 * D * 4 + 255) / 256 * 256;
     return true;
 }
 
@@ -371,12 +371,12 @@ hipError_t launch_add_norm(const NormArgs& a, hipStream_t st) {
         using T = decltype(t);
         using R = decltype(r);
         const bool held = by_width<kVec<T>>(a.D, [&](auto s) {
-            const auto grid = row_groups(a.M, 1, s.threads, s.rows, kRowGroups);
+            const auto grid = row_groups(a.M, 1, s.threads, s.rows);
             add_norm_kernel<T, R, s.TEAM, s.NC>
                 <<<static_cast<unsigned>(grid), s.threads, 0, st>>>(a);
         });
         if (!held) {
-            const auto grid = row_groups(a.M, 1, kWide, 1, kRowGroups);
+            const auto grid = row_groups(a.M, 1, kWide, 1);
             add_norm_wide_kernel<T, R><<<static_cast<unsigned>(grid), kWide, 0, st>>>(a);
         }
     });
@@ -390,7 +390,7 @@ hipError_t launch_add_norm_bwd(const NormArgs& a, hipStream_t st) {
         using T = decltype(t);
         using R = decltype(r);
         const bool held = by_width<kVec<T>>(a.D, [&](auto s) {
-            rows = row_groups(a.M, 1, s.threads, s.rows, kPartRows);
+            rows = part_groups(a.M, 1, s.threads, s.rows);
             const unsigned grid = static_cast<unsigned>(rows);
             if (extra)
                 add_norm_bwd_kernel<T, R, s.TEAM, s.NC, true><<<grid, s.threads, 0, st>>>(a);
@@ -398,7 +398,7 @@ hipError_t launch_add_norm_bwd(const NormArgs& a, hipStream_t st) {
                 add_norm_bwd_kernel<T, R, s.TEAM, s.NC, false><<<grid, s.threads, 0, st>>>(a);
         });
         if (!held) {
-            rows = row_groups(a.M, 1, kWide, 1, kPartRows);
+            rows = part_groups(a.M, 1, kWide, 1);
             K = 3;
             add_norm_bwd_wide_kernel<T, R><<<static_cast<unsigned>(rows), kWide, 0, st>>>(a);
         }
