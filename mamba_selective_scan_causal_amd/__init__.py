@@ -605,10 +605,11 @@ def make_norm_strides(*strides) -> NormStrides:
 class _Call:
     """Argument checks of one call: the current device and the activation type."""
 
-    __slots__ = ("torch", "dev", "like", "dtype", "code")
+    __slots__ = ("torch", "Tensor", "f32", "dev", "like", "dtype", "code")
 
     def __init__(self, like, name):
         self.torch = torch = _torch()
+        self.Tensor, self.f32 = torch.Tensor, torch.float32
         if not isinstance(like, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if not like.is_cuda:
@@ -619,15 +620,14 @@ class _Call:
             raise TypeError(f"{name} must be float32, bfloat16 or float16, got {like.dtype}")
         self.dev = torch.cuda.current_device()
 
-    def _basic(self, t, name, dtype, shape):
+    def _refuse(self, t, name, dtype, shape):
         if not isinstance(t, self.torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.get_device() != self.dev:
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{self.dev}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
     def rows(self, t, name, rows, cols, dtype=None, required=True):
         """(pointer, row stride) of a (rows, cols) activation whose rows may be strided."""
@@ -635,7 +635,10 @@ class _Call:
             if required:
                 raise ValueError(f"{name} is required")
             return None, cols
-        self._basic(t, name, dtype or self.dtype, (rows, cols))
+        dtype = dtype or self.dtype
+        if (not isinstance(t, self.Tensor) or t.dtype is not dtype or t.get_device() != self.dev
+                or t.shape != (rows, cols)):
+            self._refuse(t, name, dtype, (rows, cols))
         row, col = t.stride()
         if col != 1 and cols > 1 and rows > 0:
             raise ValueError(f"{name}: columns must be contiguous")
@@ -647,7 +650,10 @@ class _Call:
             if required:
                 raise ValueError(f"{name} is required")
             return None
-        self._basic(t, name, dtype or self.torch.float32, shape)
+        dtype = dtype or self.f32
+        if (not isinstance(t, self.Tensor) or t.dtype is not dtype or t.get_device() != self.dev
+                or t.shape != shape):
+            self._refuse(t, name, dtype, shape)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr() or None

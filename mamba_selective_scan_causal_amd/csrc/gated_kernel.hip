@@ -36,73 +36,77 @@
 namespace mss {
 namespace {
 
-// The gates of one token and channel: a, v and what the backward pass needs.
+// The gates of one token and channel: a and v.  The backward works in two
+// halves, with `er` and `ei` kept in between in the place of r and i.
 template <int GATE>
 struct Gates {
     float a, v;
-    float c;          // SIGMOID: 1 - a;  DECAY: 1 - sigma(r)
-    float s, m, g;    // DECAY: sigma(r), sqrt(1 - a^2), sigma(i)
-    float gc;         // DECAY: 1 - sigma(i)
+    float er, ei;     // DECAY: e^-r, e^-i, at most 2^126 so that their sigmoids stay normal
+                      // numbers (what that adds to a closed gate is below 2^-60);
+                      // SIGMOID: r itself;  LOG: a
+    static constexpr float kMost = 8.507059173023462e37f;   // 2^126
 
-    // a and v alone, or (FULL) all of them; k = c softplus(decay) (DECAY).
-    template <bool FULL>
+    // k = c softplus(decay) (DECAY)
     __device__ __forceinline__ void set(float x, float r, float i, float k) {
         if constexpr (GATE == MSS_GATE_SIGMOID) {
+            float c;
             sigmoid2(r, a, c);
             v = c * x;
+            er = r;
         } else if constexpr (GATE == MSS_GATE_DECAY) {
-            if constexpr (FULL) {
-                sigmoid2(r, s, c);
-                sigmoid2(i, g, gc);
-            } else {
-                s = sigmoid(r);
-                g = sigmoid(i);
-            }
-            const float l2 = -kLog2e * k * s;
+            er = __builtin_fminf(ex2(-kLog2e * r), kMost);
+            ei = __builtin_fminf(ex2(-kLog2e * i), kMost);
+            const float l2 = -kLog2e * k * rcp(1.0f + er);
             a = ex2(l2);
-            m = decay_input_scale(l2, a);
-            v = m * g * x;
+            v = __builtin_amdgcn_sqrtf(one_minus_square(l2, a)) * rcp(1.0f + ei) * x;
         } else {
             a = ex2(kLog2e * r);
             v = x;
+            er = a;
         }
     }
 
-    // Gradients for G = dL/dh_t and p = the state carried into the step.
-    // `ws` is w sigma(r), whose sum gives ddecay: sigma(r) goes into the
-    // term over m first, so that it has its limit where both vanish.
-    __device__ __forceinline__ void grads(float G, float p, float x, float k, float& dx, float& dr,
-                                          float& di, float& ws) const {
+    // Gradients for G = dL/dh_t and p = the state carried into the step, from
+    // the kept er and ei.  `ws` is w sigma(r), whose sum gives ddecay.
+    static __device__ __forceinline__ void grads(float er, float ei, float G, float p, float x,
+                                                 float k, float& dx, float& dr, float& di,
+                                                 float& ws) {
         if constexpr (GATE == MSS_GATE_SIGMOID) {
+            float a, c;
+            sigmoid2(er, a, c);
             dx = G * c;
             dr = G * (p - x) * (a * c);
         } else if constexpr (GATE == MSS_GATE_DECAY) {
-            dx = G * (m * g);
+            const float s = rcp(1.0f + er), c = er * s;   // sigma(r), 1 - sigma(r)
+            const float g = rcp(1.0f + ei), gc = ei * g;
+            const float l2 = -kLog2e * k * s;
+            const float a = ex2(l2);
+            // m = sqrt(1 - a^2) and 1 / m; where m vanishes, so do sigma(r) or
+            // k, and k sigma(r) / m (all that 1 / m enters) is below 2^-60
+            // with the bound on 1 / m
+            const float mm = one_minus_square(l2, a);
+            const float rm = __builtin_amdgcn_rsqf(__builtin_fmaxf(mm, 0x1p-126f));
+            const float as = a * s;
+            dx = G * (mm * rm * g);
             di = dx * x * gc;
-            const float q = m > 0.0f ? g * a * a * (s * rcp(m)) : 0.0f;
-            ws = G * __builtin_fmaf(a * s, p, -x * q);
+            ws = G * __builtin_fmaf(-x, (g * a) * (as * rm), as * p);
             dr = -k * ws * c;
         } else {
             dx = G;
-            dr = G * a * p;
+            dr = G * er * p;
         }
     }
 };
 
 constexpr int kWaves = 8;                        // waves of a workgroup, chunks of a group
-#ifndef KS2
-#define KS2 16
-#endif
-#ifndef KS4
-#define KS4 16
-#endif
-template <typename T>                            // S of the forward
-constexpr int kSteps = sizeof(T) == 2 ? KS2 : KS4;
-template <typename T>
-constexpr int kChunk = kWaves * kSteps<T>;
-constexpr int kMinChunk = 64;
+// S of the forward.  Half of it leaves room for three workgroups on a CU
+// instead of two, and measures slower for the handovers it adds: 480 -> 568 us
+// on B4 L8192 D5120 fp32 with a gate, 59 -> 60 us on B8 L2048 D1536 bf16.
+constexpr int kSteps = 16;
+constexpr int kChunk = kWaves * kSteps;
 constexpr int kBwdSteps = 8;                     // S of the backward: twice the inputs per step
 constexpr int kBwdChunk = kWaves * kBwdSteps;
+static_assert(kChunk % MSS_GATED_CKPT_STEPS == 0, "checkpoints lie between a chunk's waves");
 static_assert(kBwdChunk == MSS_GATED_CKPT_STEPS, "a backward chunk starts from a checkpoint");
 
 typedef unsigned long long Word;
@@ -263,8 +267,7 @@ __device__ __forceinline__ void states(const float (&a)[S][V], float (&u)[S][V],
 
 template <typename T, int V, int GATE, bool Z>
 __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Chain g) {
-    constexpr int S = kSteps<T>;
-    static_assert(kChunk<T> % MSS_GATED_CKPT_STEPS == 0, "checkpoints lie between a chunk's waves");
+    constexpr int S = kSteps;
     __shared__ Map own[kWaves][V][64], mates[kWaves][V][64];
     __shared__ float entering[V][64];
     __shared__ unsigned ticket;
@@ -277,7 +280,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
     unsigned c = tile % g.ctiles * (64 * V) + lane * V;
     const bool live = c < q.D;
     c = live && c + V <= q.D ? c : static_cast<unsigned>(q.D - V);
-    const int64_t t0 = chunk * kChunk<T> + wave * S, row0 = int64_t{b} * q.L;
+    const int64_t t0 = chunk * kChunk + wave * S, row0 = int64_t{b} * q.L;
     const int n = t0 >= q.L ? 0 : q.L - t0 < S ? static_cast<int>(q.L - t0) : S;
 
     Piece<T, V> x[S], r[S], in[S], z[S];
@@ -308,8 +311,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
 #pragma unroll
         for (int v = 0; v < V; v++) {
             Gates<GATE> e;
-            e.template set<false>(x[s].get(v), r[s].get(v),
-                                  GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
+            e.set(x[s].get(v), r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
             a[s][v] = e.a;
             u[s][v] = e.v;
         }
@@ -407,7 +409,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
 // A as the forward's map.  The states inside a chunk come from its checkpoint
 // and the pieces' forward maps.
 template <typename T, int V, int GATE, bool Z>
-__global__ __launch_bounds__(64 * kWaves) void gated_scan_bwd_kernel(GatedArgs q, Chain g,
+__global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArgs q, Chain g,
                                                                      float* part) {
     constexpr int S = kBwdSteps;
     __shared__ Map fwd[kWaves][V][64], rev[kWaves][V][64], mates[kWaves][V][64];
@@ -444,17 +446,19 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_bwd_kernel(GatedArgs q
         h[v] = q.h_ckpt[(int64_t{b} * g.chunks + chunk) * q.D + c + v];
     }
 
-    float a[S][V], u[S][V];   // u: the input term, later the state
+    float a[S][V], u[S][V];     // u: the input term, later the state
+    float er[S][V], ei[S][V];   // what the gradients take of r and i
     Map f[V], w[V];
 #pragma unroll
     for (int s = 0; s < S; s++) {
 #pragma unroll
         for (int v = 0; v < V; v++) {
             Gates<GATE> e;
-            e.template set<false>(x[s].get(v), r[s].get(v),
-                                  GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
+            e.set(x[s].get(v), r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
             a[s][v] = e.a;
             u[s][v] = e.v;
+            er[s][v] = e.er;
+            if constexpr (GATE == MSS_GATE_DECAY) ei[s][v] = e.ei;
         }
     }
     mend<S, V>(a, u, n, resets);
@@ -539,9 +543,14 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_bwd_kernel(GatedArgs q
 #pragma unroll
     for (int s = 0; s < S; s++) {
         x[s].keep();
-        r[s].keep();
-        if constexpr (GATE == MSS_GATE_DECAY) in[s].keep();
+        dout[s].keep();
         if constexpr (Z) z[s].keep();
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            // nothing but these is kept of the gates
+            asm volatile("" : "+v"(er[s][v]));
+            if constexpr (GATE == MSS_GATE_DECAY) asm volatile("" : "+v"(ei[s][v]));
+        }
     }
     states<S, V>(a, u, h, resets);
     float sum[V];
@@ -554,9 +563,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_bwd_kernel(GatedArgs q
         const bool drop = resets >> s & 1;
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            Gates<GATE> e;
             const float xv = x[s].get(v);
-            e.template set<true>(xv, r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
             const float p = drop ? 0.0f : s > 0 ? u[s > 0 ? s - 1 : 0][v] : before[v];
             float dy = dout[s].get(v);
             if constexpr (Z) {
@@ -567,7 +574,8 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_bwd_kernel(GatedArgs q
             }
             const float G = dy + Q[v];
             float gx, gr, gi = 0.0f, ws = 0.0f;
-            e.grads(G, p, xv, k[v], gx, gr, gi, ws);
+            Gates<GATE>::grads(er[s][v], GATE == MSS_GATE_DECAY ? ei[s][v] : 0.0f, G, p, xv, k[v], gx,
+                               gr, gi, ws);
             Q[v] = a[s][v] * G;
             sum[v] += ws;
             dx.set(v, gx);
@@ -650,7 +658,7 @@ __global__ __launch_bounds__(64) void gated_step_kernel(GatedArgs q, unsigned pe
     for (int v = 0; v < V; v++) {
         Gates<GATE> e;
         const float k = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(decay[v]) : 0.0f;
-        e.template set<false>(x[v], r[v], GATE == MSS_GATE_DECAY ? in[v] : 0.0f, k);
+        e.set(x[v], r[v], GATE == MSS_GATE_DECAY ? in[v] : 0.0f, k);
         h.set(v, __builtin_fmaf(e.a, h[v], e.v));
         y.set(v, q.z ? h[v] * silu(z[v]) : h[v]);
     }
@@ -730,7 +738,7 @@ bool gated_step_fits(int64_t B, int64_t D) {
 }
 
 bool gated_scan_workspace(int64_t B, int64_t L, int64_t D, int64_t& bytes) {
-    return chain_bytes(B, L, D, kMinChunk, bytes);
+    return chain_bytes(B, L, D, kChunk, bytes);
 }
 
 bool gated_scan_bwd_workspace(int64_t B, int64_t L, int64_t D, int gate, int64_t& bytes) {
@@ -742,7 +750,7 @@ bool gated_scan_bwd_workspace(int64_t B, int64_t L, int64_t D, int gate, int64_t
 hipError_t launch_gated_scan(const GatedArgs& a, hipStream_t st) {
     return dispatch(a, [&](auto t, auto v, auto gate) {
         using T = decltype(t);
-        const Chain g = chain_of(a, v.value, kChunk<T>);
+        const Chain g = chain_of(a, v.value, kChunk);
         if (unset(g, v.value, st) != hipSuccess) return;
         const unsigned grid = g.tiles * static_cast<unsigned>(g.chunks);
         if (a.z)

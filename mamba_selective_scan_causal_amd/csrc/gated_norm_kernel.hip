@@ -21,12 +21,11 @@ __device__ __forceinline__ Place place(const NormArgs& q) {
     return {g * (q.D / q.G), p * rows + team, gridDim.x / q.G * rows};
 }
 
-template <typename T, int TEAM, int NC, bool before>
+template <typename T, int TEAM, int NC, bool before, bool layer>
 __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(NormArgs q) {
     constexpr int V = kVec<T>;
     __shared__ float lds[kSumLds<TEAM, 1>];
     const int n = static_cast<int>(q.D / q.G), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
-    const bool layer = q.kind == MSS_NORM_LAYER;
     const float inv_n = 1.0f / static_cast<float>(n);
     const Place at = place<TEAM>(q);
     // k (norm w + b) with k = alpha scale folded into w and b
@@ -77,18 +76,20 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
             for (int e = 0; e < V; e++) {
                 v[j][e] = r.x[j][e];
                 if (before && q.z) v[j][e] *= silu(r.z[j][e]);
-                sum[0] += v[j][e];
+                if constexpr (layer) sum[0] += v[j][e];
             }
-        if (layer) {
+        if constexpr (layer) {
             team_sum<TEAM>(sum, lds, turn);
             mean = sum[0] * inv_n;
+            sum[0] = 0.0f;
         }
-        sum[0] = 0.0f;
 #pragma unroll
         for (int j = 0; j < NC; j++)
 #pragma unroll
             for (int e = 0; e < V; e++) {
-                v[j][e] = V * (lane + j * lanes) + e < n ? v[j][e] - mean : 0.0f;
+                // (past the end an RMS norm's v is 0 already)
+                if constexpr (layer)
+                    v[j][e] = V * (lane + j * lanes) + e < n ? v[j][e] - mean : 0.0f;
                 sum[0] = __builtin_fmaf(v[j][e], v[j][e], sum[0]);
             }
         team_sum<TEAM>(sum, lds, turn);
@@ -99,10 +100,15 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
             RowVec<T, V> y;
 #pragma unroll
             for (int e = 0; e < V; e++) {
-                float o = __builtin_fmaf(v[j][e] * rstd, w[j][e], b[j][e]);
-                if (!before && q.z) o *= silu(r.z[j][e]);
-                y.set(e, o + r.res[j][e]);
+                v[j][e] = __builtin_fmaf(v[j][e] * rstd, w[j][e], b[j][e]);
+                if (!before && q.z) v[j][e] *= silu(r.z[j][e]);
             }
+            if (q.res) {
+#pragma unroll
+                for (int e = 0; e < V; e++) v[j][e] += r.res[j][e];
+            }
+#pragma unroll
+            for (int e = 0; e < V; e++) y.set(e, v[j][e]);
             if (c < n) y.store(row_of<T>(q.y, m, q.ld_y, at.g0), c, n);
         }
     }
@@ -110,13 +116,12 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
 
 // EXTRA: the sum of the gradients alone is wanted too (for db, and for dscale
 // where there is a bias).
-template <typename T, int TEAM, int NC, bool before, bool EXTRA>
+template <typename T, int TEAM, int NC, bool before, bool layer, bool EXTRA>
 __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel(NormArgs q) {
     constexpr int V = kVec<T>, K = EXTRA ? 2 : 1;
     __shared__ float lds[kSumLds<TEAM, 3>];
     __shared__ float part_lds[kPartLds<TEAM, NC, V>];
     const int n = static_cast<int>(q.D / q.G), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
-    const bool layer = q.kind == MSS_NORM_LAYER;
     const float inv_n = 1.0f / static_cast<float>(n);
     const Place at = place<TEAM>(q);
     float w[NC][V], acc[K][NC][V];   // w: k w, k = alpha scale
@@ -167,7 +172,7 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
         auto normed = [&](int j, int e) { return before ? r.x[j][e] * gate(j, e) : r.x[j][e]; };
         auto grad = [&](int j, int e) { return before ? r.d[j][e] : r.d[j][e] * gate(j, e); };
         float mean = 0.0f;
-        if (layer) {
+        if constexpr (layer) {
             float sum[1] = {0.0f};
 #pragma unroll
             for (int j = 0; j < NC; j++)
@@ -182,16 +187,20 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
             r.z[j].narrow();
             r.d[j].narrow();
         }
-        float sums[3] = {0.0f, 0.0f, 0.0f};
+        constexpr int S = layer ? 3 : 2;
+        float sums[S];
+#pragma unroll
+        for (int a = 0; a < S; a++) sums[a] = 0.0f;
 #pragma unroll
         for (int j = 0; j < NC; j++)
 #pragma unroll
             for (int e = 0; e < V; e++) {
-                const float v = V * (lane + j * lanes) + e < n ? normed(j, e) - mean : 0.0f;
+                float v = normed(j, e);
+                if constexpr (layer) v = V * (lane + j * lanes) + e < n ? v - mean : 0.0f;
                 const float gw = grad(j, e) * w[j][e];
                 sums[0] = __builtin_fmaf(v, v, sums[0]);
                 sums[1] = __builtin_fmaf(gw, v, sums[1]);
-                sums[2] += gw;
+                if constexpr (layer) sums[S - 1] += gw;
             }
         team_sum<TEAM>(sums, lds, turn);
 #pragma unroll
@@ -202,7 +211,7 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
         }
         const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(sums[0], inv_n, q.eps));
         const float c1 = sums[1] * inv_n * rstd;
-        const float c2 = layer ? sums[2] * inv_n : 0.0f;
+        const float c2 = layer ? sums[S - 1] * inv_n : 0.0f;
 #pragma unroll
         for (int j = 0; j < NC; j++) {
             const int c = V * (lane + j * lanes);
@@ -217,7 +226,8 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
                 const float nv = (normed(j, e) - mean) * rstd, d = grad(j, e);
                 acc[0][j][e] = __builtin_fmaf(d, nv, acc[0][j][e]);
                 if constexpr (EXTRA) acc[1][j][e] += d;
-                const float t = __builtin_fmaf(d, w[j][e], -__builtin_fmaf(nv, c1, c2)) * rstd;
+                const float t =
+                    __builtin_fmaf(d, w[j][e], -(layer ? __builtin_fmaf(nv, c1, c2) : nv * c1)) * rstd;
                 dx.set(e, before ? t * gate(j, e) : t);
                 if (q.z) {
                     // SiLU'(z) = sigma (1 + z (1 - sigma)); far below 0,
@@ -357,6 +367,16 @@ hipError_t dispatch(const NormArgs& a, F f) {
     return hipGetLastError();
 }
 
+// f(gate before norm, layer norm) for the call.
+template <typename F>
+void by_kind(const NormArgs& a, F f) {
+    const bool layer = a.kind == MSS_NORM_LAYER;
+    if (a.order == MSS_GATE_BEFORE_NORM)
+        layer ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+    else
+        layer ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
+}
+
 }  // namespace
 
 hipError_t launch_gated_norm(const NormArgs& a, hipStream_t st) {
@@ -364,14 +384,10 @@ hipError_t launch_gated_norm(const NormArgs& a, hipStream_t st) {
         using T = decltype(t);
         const bool held = by_width<kVec<T>>(a.D / a.G, [&](auto s) {
             const auto grid = a.G * row_groups(a.M, a.G, s.threads, s.rows);
-            auto go = [&](auto before) {
-                gated_norm_kernel<T, s.TEAM, s.NC, before.value>
+            by_kind(a, [&](auto before, auto layer) {
+                gated_norm_kernel<T, s.TEAM, s.NC, before.value, layer.value>
                     <<<static_cast<unsigned>(grid), s.threads, 0, st>>>(a);
-            };
-            if (a.order == MSS_GATE_BEFORE_NORM)
-                go(std::true_type{});
-            else
-                go(std::false_type{});
+            });
         });
         if (!held) {
             const auto grid = a.G * row_groups(a.M, a.G, kWide, 1);
@@ -389,15 +405,14 @@ hipError_t launch_gated_norm_bwd(const NormArgs& a, hipStream_t st) {
         const bool held = by_width<kVec<T>>(a.D / a.G, [&](auto s) {
             rows = part_groups(a.M, a.G, s.threads, s.rows);
             const unsigned grid = static_cast<unsigned>(rows * a.G);
-            auto go = [&](auto before, auto more) {
-                gated_norm_bwd_kernel<T, s.TEAM, s.NC, before.value, more.value>
-                    <<<grid, s.threads, 0, st>>>(a);
-            };
-            if (a.order == MSS_GATE_BEFORE_NORM)
-                extra ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
-            else
-                extra ? go(std::false_type{}, std::true_type{})
-                      : go(std::false_type{}, std::false_type{});
+            by_kind(a, [&](auto before, auto layer) {
+                if (extra)
+                    gated_norm_bwd_kernel<T, s.TEAM, s.NC, before.value, layer.value, true>
+                        <<<grid, s.threads, 0, st>>>(a);
+                else
+                    gated_norm_bwd_kernel<T, s.TEAM, s.NC, before.value, layer.value, false>
+                        <<<grid, s.threads, 0, st>>>(a);
+            });
         });
         if (!held) {
             rows = part_groups(a.M, a.G, kWide, 1);
