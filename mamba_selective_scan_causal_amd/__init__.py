@@ -658,16 +658,17 @@ class _Call:
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr() or None
 
-    def empty(self, shape, dtype=None):
-        like = self.like
-        if (dtype is None or dtype is self.dtype) and shape == like.shape and like.is_contiguous():
+    def empty(self, shape, dtype=None, like=None):
+        """An uninitialised tensor; ``like``: one that may be of its shape and type (cheaper)."""
+        dtype, like = dtype or self.dtype, self.like if like is None else like
+        if like.shape == shape and like.dtype is dtype and like.is_contiguous():
             return self.torch.empty_like(like)
-        return self.torch.empty(shape, dtype=dtype or self.dtype, device=like.device)
+        return self.torch.empty(shape, dtype=dtype, device=like.device)
 
     def stream(self, stream):
         """The stream's handle (the current stream's without a stream)."""
         if stream is None:
-            return self.torch.cuda.current_stream(self.dev).cuda_stream
+            return self.torch._C._cuda_getCurrentRawStream(self.dev)
         return _stream(stream)
 
     def workspace(self, need, workspace, stream):
@@ -716,7 +717,7 @@ def _ref(block):
 def _flag(t, shape, call, dtype=None):
     """An optional output given as False / True (allocate) or a tensor."""
     if isinstance(t, bool):
-        return call.empty(shape, dtype or call.torch.float32) if t else None
+        return call.empty(shape, dtype or call.f32) if t else None
     return t
 
 
@@ -789,9 +790,11 @@ def gated_scan_backward(x, r, i, decay, z, reset, h_ckpt, dout, *, batch, seq_le
     c = _Call(x, "x")
     code = _choice(GATES, gate, "gate")
     (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, M, D, gate)
-    want = {"dx": True, "dr": True, "di": gate == "decay", "ddecay": gate == "decay",
-            "dz": z is not None, "dh0": need_dh0}
-    g = _outputs(c, want, out, {"ddecay": (D,), "dh0": (batch, D)}, (M, D))
+    has_decay, MD, f32 = gate == "decay", (M, D), c.f32
+    g = _outputs(c, out, {
+        "dx": (True, MD, None, x), "dr": (True, MD, None, r), "di": (has_decay, MD, None, i),
+        "ddecay": (has_decay, (D,), f32, decay), "dz": (z is not None, MD, None, z),
+        "dh0": (need_dh0, (batch, D), f32, dh_last)})
     (pdx, ldx), (pdr, ldr), (pdi, ldi), (pdz, ldz) = (
         c.rows(g[k], k, M, D, required=False) for k in ("dx", "dr", "di", "dz"))
     po, lo = c.rows(dout, "dout", M, D)
@@ -809,23 +812,15 @@ def gated_scan_backward(x, r, i, decay, z, reset, h_ckpt, dout, *, batch, seq_le
     return g
 
 
-def _outputs(c, want, out, f32_shapes, shape, types=None):
-    """The dict of results: the caller's tensors, fresh ones, or None where not wanted."""
+def _outputs(c, out, results):
+    """The dict of results, each given as (wanted, shape, dtype, a tensor like it): the
+    caller's tensors, fresh ones, or None where not wanted."""
     out = out or {}
-    unknown = [k for k in out if k not in want]
+    unknown = [k for k in out if k not in results]
     if unknown:
         raise ValueError(f"out has no place for {', '.join(unknown)}")
-    g = {}
-    for k, w in want.items():
-        if not w:
-            g[k] = None
-        elif out.get(k) is not None:
-            g[k] = out[k]
-        elif k in f32_shapes:
-            g[k] = c.empty(f32_shapes[k], c.torch.float32)
-        else:
-            g[k] = c.empty(shape, (types or {}).get(k))
-    return g
+    return {k: None if not w else out[k] if out.get(k) is not None else c.empty(shape, dtype, like)
+            for k, (w, shape, dtype, like) in results.items()}
 
 
 def gated_step(x, r, i, decay, z, h, *, gate, gate_scale=8.0, out=None, stream=None):
@@ -847,7 +842,7 @@ def gated_step(x, r, i, decay, z, h, *, gate, gate_scale=8.0, out=None, stream=N
 
 def _res_code(c, t, name):
     code = _dtype_codes().get(t.dtype)
-    if code is None or (code != c.code and t.dtype != c.torch.float32):
+    if code is None or (code != c.code and t.dtype != c.f32):
         raise TypeError(f"{name} must be {c.dtype} or float32, got {t.dtype}")
     return code
 
@@ -865,7 +860,7 @@ def add_norm(x, residual, weight, bias=None, scale=None, *, kind="rms", eps=1e-6
     c = _Call(x, "x")
     rt = (residual.dtype if residual is not None else
           residual_out.dtype if residual_out is not None else res_dtype or c.dtype)
-    s = residual_out if residual_out is not None else c.empty((M, D), rt)
+    s = residual_out if residual_out is not None else c.empty((M, D), rt, residual)
     rc = _res_code(c, s, "the residual stream")
     y = out if out is not None else c.empty((M, D))
     px, lx = c.rows(x, "x", M, D)
@@ -892,10 +887,10 @@ def add_norm_backward(s, weight, dy, ds=None, x=None, scale=None, *, bias=False,
     M, D = dy.shape
     c = _Call(dy, "dy")
     rc = _res_code(c, s, "s")
-    want = {"dx": need_dx, "dresidual": True, "dweight": True, "dbias": bool(bias),
-            "dscale": scale is not None}
-    f32 = {k: (D,) for k in ("dweight", "dbias", "dscale")}
-    g = _outputs(c, want, out, f32, (M, D), {"dresidual": s.dtype})
+    g = _outputs(c, out, {
+        "dx": (need_dx, (M, D), None, dy), "dresidual": (True, (M, D), s.dtype, s),
+        "dweight": (True, (D,), c.f32, weight), "dbias": (bool(bias), (D,), c.f32, weight),
+        "dscale": (scale is not None, (D,), c.f32, scale)})
     ps, ls = c.rows(s, "s", M, D, s.dtype)
     po, lo = c.rows(dy, "dy", M, D)
     pds, lds = c.rows(ds, "ds", M, D, s.dtype, False)
@@ -948,9 +943,10 @@ def gated_norm_backward(x, z, weight, bias, scale, dout, *, groups=1, order="bef
     (``norm_workspace_bytes(OP_GATED_NORM_BACKWARD, ...)``)."""
     M, D = x.shape
     c = _Call(x, "x")
-    want = {"dx": True, "dz": z is not None, "dweight": True, "dbias": bias is not None,
-            "dscale": scale is not None}
-    g = _outputs(c, want, out, {k: (D,) for k in ("dweight", "dbias", "dscale")}, (M, D))
+    g = _outputs(c, out, {
+        "dx": (True, (M, D), None, x), "dz": (z is not None, (M, D), None, z),
+        "dweight": (True, (D,), c.f32, weight), "dbias": (bias is not None, (D,), c.f32, bias),
+        "dscale": (scale is not None, (D,), c.f32, scale)})
     px, lx = c.rows(x, "x", M, D)
     pz, lz = c.rows(z, "z", M, D, required=False)
     po, lo = c.rows(dout, "dout", M, D)

@@ -24,9 +24,14 @@ struct RowVec {
             for (int e = 0; e < V; e++) t[e] = c + e < n ? p[c + e] : static_cast<T>(0.0f);
         }
     }
+    // STREAM: with the nontemporal hint, for what is not read again here.
+    template <bool STREAM>
     __device__ __forceinline__ void store(T* p, int c, int n) const {
         if (c + V <= n) {
-            *reinterpret_cast<type*>(p + c) = t;
+            if constexpr (STREAM)
+                __builtin_nontemporal_store(t, reinterpret_cast<type*>(p + c));
+            else
+                *reinterpret_cast<type*>(p + c) = t;
         } else {
 #pragma unroll
             for (int e = 0; e < V; e++)

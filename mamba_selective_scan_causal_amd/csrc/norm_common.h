@@ -120,7 +120,7 @@ __device__ __forceinline__ void write_part(float (&acc)[K][NC][V], float* lds, f
                 RowVec<float, V> t;
 #pragma unroll
                 for (int e = 0; e < V; e++) t.set(e, acc[k][j][e]);
-                if (c < n) t.store(out, c, n);
+                if (c < n) t.template store<false>(out, c, n);
             }
         } else {
             constexpr int slots = TEAM * NC * V, teams = 256 / (TEAM ? TEAM : 1);
@@ -178,10 +178,12 @@ inline int64_t row_groups(int64_t M, int64_t G, int threads, int rows, int64_t m
 }
 
 // The same for the backward passes, whose workgroups each write a row of
-// partial sums: eight rows of input to each, between 256 and 1024 workgroups.
+// partial sums: eight rows of input to each, but four waves for each CU at
+// least, and 1024 workgroups at most.
 inline int64_t part_groups(int64_t M, int64_t G, int threads, int rows) {
-    const int64_t most = M / 8 < 256 ? 256 : M / 8 < 1024 ? M / 8 : 1024;
-    return row_groups(M, G, threads, rows, most);
+    int64_t most = 256 * 4 * 64 / threads;
+    if (most < M / 8) most = M / 8;
+    return row_groups(M, G, threads, rows, most < 1024 ? most : 1024);
 }
 
 // f(Shape) for groups of n channels, V to a vector: a quarter of a wave or a

@@ -5,6 +5,8 @@
 //
 // Bound by HBM: the forward reads x and the residual and writes s and y, the
 // backward reads s, dy, ds (and x) and writes dresidual and dx, each once.
+// The outputs go through the cache: with the nontemporal hint the forward and
+// backward of M 32768 D 2560 in turn take 561 us, without it 538.
 #include "norm_common.h"
 
 namespace mss {
@@ -69,7 +71,7 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormA
             const int c = V * (lane + j * lanes);
 #pragma unroll
             for (int e = 0; e < V; e++) s[j].set(e, scaled_sum(res[j][e], k[j][e], x[j][e]));
-            if (c < n) s[j].store(row_of<R>(q.s, m, q.ld_s), c, n);
+            if (c < n) s[j].template store<false>(row_of<R>(q.s, m, q.ld_s), c, n);
         }
         // the next row; this one has been read, so s may be the residual
         read(m + step, res, x);
@@ -100,7 +102,7 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormA
 #pragma unroll
             for (int e = 0; e < V; e++)
                 y.set(e, __builtin_fmaf((s[j][e] - mean) * rstd, w[j][e], b[j][e]));
-            if (c < n) y.store(row_of<T>(q.y, m, q.ld_y), c, n);
+            if (c < n) y.template store<false>(row_of<T>(q.y, m, q.ld_y), c, n);
         }
     }
 }
@@ -203,8 +205,8 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(N
                 dx.set(e, d * k[j][e]);
             }
             if (c < n) {
-                dres.store(row_of<R>(q.dres, m, q.ld_dres), c, n);
-                if (q.dx) dx.store(row_of<T>(q.dx, m, q.ld_dx), c, n);
+                dres.template store<false>(row_of<R>(q.dres, m, q.ld_dres), c, n);
+                if (q.dx) dx.template store<false>(row_of<T>(q.dx, m, q.ld_dx), c, n);
             }
         }
     }
