@@ -17,7 +17,9 @@ namespace {
 // many sums lie next to the middle of two representable values, and a fused
 // product would round them the other way.
 __device__ __forceinline__ float scaled_sum(float res, float k, float x) {
-    return __fadd_rn(res, __fmul_rn(k, x));
+#pragma clang fp contract(off)
+    const float p = k * x;
+    return res + p;
 }
 
 // A row as it was read: x and the residual, or s, dy, ds and x.

@@ -120,6 +120,22 @@ def test_gated_norm_groups(D, groups, order):
     gated_case(6, D, "f32", "layer" if D > groups else "rms", order, groups)
 
 
+@pytest.mark.parametrize("res", ("f32", "f16"))
+@pytest.mark.parametrize("D", (1001, 17000))
+def test_stream_rounds_as_scale_and_add_do(res, D):
+    """s is the product's rounding added and rounded, bit for bit: in a half-precision stream with
+    a scale of 0.7 one sum in sixty lies next to a tie, which a fused product breaks otherwise."""
+    import torch
+    rng = np.random.default_rng(8)
+    x, old, w = put(rng.normal(size=(40, D)), "f16"), put(2 * rng.normal(size=(40, D)), res), put(np.ones(D))
+    sc = put(1 + 0.2 * rng.normal(size=D))
+    for scale, k in ((None, 0.7), (sc, 0.7 * sc)):
+        _, s = mss.add_norm(x, old, w, scale=scale, alpha=0.7)
+        want = (old.float() + k * x.float()).to(old.dtype)
+        torch.cuda.synchronize()
+        assert torch.equal(s, want)
+
+
 def test_many_rows():
     add_case(5001, 96, "bf16", "f32", "rms")
     gated_case(5001, 96, "bf16", "rms", "before", 2)
