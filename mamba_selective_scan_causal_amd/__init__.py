@@ -665,6 +665,13 @@ class _Call:
             return self.torch.empty_like(like)
         return self.torch.empty(shape, dtype=dtype, device=like.device)
 
+    def output(self, t, name, rows, cols, dtype=None, like=None):
+        """(tensor, pointer, row stride) of an output: the caller's, or a fresh one."""
+        if t is None:
+            t = self.empty((rows, cols), dtype, like)
+            return t, t.data_ptr() or None, cols
+        return (t, *self.rows(t, name, rows, cols, dtype))
+
     def stream(self, stream):
         """The stream's handle (the current stream's without a stream)."""
         if stream is None:
@@ -760,8 +767,7 @@ def gated_scan(x, r, i=None, decay=None, z=None, h0=None, reset=None, *, batch, 
     c = _Call(x, "x")
     code = _choice(GATES, gate, "gate")
     (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, M, D, gate)
-    y = out if out is not None else c.empty((M, D))
-    py, ly = c.rows(y, "out", M, D)
+    y, py, ly = c.output(out, "out", M, D)
     ck = _flag(h_ckpt, (batch, gated_ckpt_steps(seq_len), D), c)
     hl = _flag(h_last, (batch, D), c)
     need = gated_workspace_bytes(OP_GATED_SCAN, batch=batch, seq_len=seq_len, d_inner=D, gate=gate)
@@ -791,12 +797,12 @@ def gated_scan_backward(x, r, i, decay, z, reset, h_ckpt, dout, *, batch, seq_le
     code = _choice(GATES, gate, "gate")
     (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, M, D, gate)
     has_decay, MD, f32 = gate == "decay", (M, D), c.f32
-    g = _outputs(c, out, {
-        "dx": (True, MD, None, x), "dr": (True, MD, None, r), "di": (has_decay, MD, None, i),
-        "ddecay": (has_decay, (D,), f32, decay), "dz": (z is not None, MD, None, z),
-        "dh0": (need_dh0, (batch, D), f32, dh_last)})
-    (pdx, ldx), (pdr, ldr), (pdi, ldi), (pdz, ldz) = (
-        c.rows(g[k], k, M, D, required=False) for k in ("dx", "dr", "di", "dz"))
+    g, at = _outputs(c, out, {
+        "dx": (True, MD, None, x, True), "dr": (True, MD, None, r, True),
+        "di": (has_decay, MD, None, i, True), "ddecay": (has_decay, (D,), f32, decay, False),
+        "dz": (z is not None, MD, None, z, True),
+        "dh0": (need_dh0, (batch, D), f32, dh_last, False)})
+    (pdx, ldx), (pdr, ldr), (pdi, ldi), (pdz, ldz) = at["dx"], at["dr"], at["di"], at["dz"]
     po, lo = c.rows(dout, "dout", M, D)
     need = gated_workspace_bytes(OP_GATED_SCAN_BACKWARD, batch=batch, seq_len=seq_len, d_inner=D,
                                  gate=gate)
@@ -807,20 +813,31 @@ def gated_scan_backward(x, r, i, decay, z, reset, h_ckpt, dout, *, batch, seq_le
         _reset(c, reset, M),
         c.dense(h_ckpt, "h_ckpt", (batch, gated_ckpt_steps(seq_len), D), required=True), po,
         c.dense(dh_last, "dh_last", (batch, D)), pdx, pdr, pdi,
-        c.dense(g["ddecay"], "ddecay", (D,)), pdz, c.dense(g["dh0"], "dh0", (batch, D)),
-        wp, wn, c.stream(stream)))
+        at["ddecay"][0], pdz, at["dh0"][0], wp, wn, c.stream(stream)))
     return g
 
 
 def _outputs(c, out, results):
-    """The dict of results, each given as (wanted, shape, dtype, a tensor like it): the
-    caller's tensors, fresh ones, or None where not wanted."""
-    out = out or {}
-    unknown = [k for k in out if k not in results]
-    if unknown:
-        raise ValueError(f"out has no place for {', '.join(unknown)}")
-    return {k: None if not w else out[k] if out.get(k) is not None else c.empty(shape, dtype, like)
-            for k, (w, shape, dtype, like) in results.items()}
+    """Results, each given as (wanted, shape, dtype, a tensor like it, rows may be strided):
+    the caller's tensors, fresh ones, or None where not wanted; and their (pointer, row
+    stride)."""
+    if out:
+        unknown = [k for k in out if k not in results]
+        if unknown:
+            raise ValueError(f"out has no place for {', '.join(unknown)}")
+    g, at = {}, {}
+    for k, (wanted, shape, dtype, like, strided) in results.items():
+        given = out.get(k) if out and wanted else None
+        if not wanted:
+            g[k], at[k] = None, (None, shape[-1])
+        elif given is None:
+            g[k] = t = c.empty(shape, dtype, like)
+            at[k] = t.data_ptr() or None, shape[-1]
+        else:
+            g[k] = given
+            at[k] = (c.rows(given, k, *shape, dtype) if strided else
+                     (c.dense(given, k, shape, dtype), shape[-1]))
+    return g, at
 
 
 def gated_step(x, r, i, decay, z, h, *, gate, gate_scale=8.0, out=None, stream=None):
@@ -831,8 +848,7 @@ def gated_step(x, r, i, decay, z, h, *, gate, gate_scale=8.0, out=None, stream=N
     code = _choice(GATES, gate, "gate")
     (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, batch, D,
                                                                  gate)
-    y = out if out is not None else c.empty((batch, D))
-    py, ly = c.rows(y, "out", batch, D)
+    y, py, ly = c.output(out, "out", batch, D)
     _check("mss_gated_step", lib().mss_gated_step(
         _ref(make_gated_dims(batch, 1, D, c.code, code, gate_scale)),
         _ref(make_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
@@ -840,11 +856,10 @@ def gated_step(x, r, i, decay, z, h, *, gate, gate_scale=8.0, out=None, stream=N
     return y
 
 
-def _res_code(c, t, name):
-    code = _dtype_codes().get(t.dtype)
-    if code is None or (code != c.code and t.dtype != c.f32):
-        raise TypeError(f"{name} must be {c.dtype} or float32, got {t.dtype}")
-    return code
+def _res_code(c, dtype, name):
+    if dtype is not c.dtype and dtype is not c.f32:
+        raise TypeError(f"{name} must be {c.dtype} or float32, got {dtype}")
+    return _dtype_codes()[dtype]
 
 
 def add_norm(x, residual, weight, bias=None, scale=None, *, kind="rms", eps=1e-6, alpha=1.0,
@@ -860,13 +875,11 @@ def add_norm(x, residual, weight, bias=None, scale=None, *, kind="rms", eps=1e-6
     c = _Call(x, "x")
     rt = (residual.dtype if residual is not None else
           residual_out.dtype if residual_out is not None else res_dtype or c.dtype)
-    s = residual_out if residual_out is not None else c.empty((M, D), rt, residual)
-    rc = _res_code(c, s, "the residual stream")
-    y = out if out is not None else c.empty((M, D))
+    rc = _res_code(c, rt, "the residual stream")
+    s, ps, ls = c.output(residual_out, "residual_out", M, D, rt, residual)
     px, lx = c.rows(x, "x", M, D)
-    pr, lr = c.rows(residual, "residual", M, D, s.dtype, False)
-    ps, ls = c.rows(s, "residual_out", M, D, s.dtype)
-    py, ly = c.rows(y, "out", M, D)
+    pr, lr = c.rows(residual, "residual", M, D, rt, False)
+    y, py, ly = c.output(out, "out", M, D)
     _check("mss_add_norm", lib().mss_add_norm(
         _ref(make_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
         _ref(make_norm_strides(lx, 0, lr, ls, ly)), px, pr,
@@ -886,26 +899,25 @@ def add_norm_backward(s, weight, dy, ds=None, x=None, scale=None, *, bias=False,
     gated_scan_backward (``norm_workspace_bytes(OP_ADD_NORM_BACKWARD, ...)``)."""
     M, D = dy.shape
     c = _Call(dy, "dy")
-    rc = _res_code(c, s, "s")
-    g = _outputs(c, out, {
-        "dx": (need_dx, (M, D), None, dy), "dresidual": (True, (M, D), s.dtype, s),
-        "dweight": (True, (D,), c.f32, weight), "dbias": (bool(bias), (D,), c.f32, weight),
-        "dscale": (scale is not None, (D,), c.f32, scale)})
+    rc = _res_code(c, s.dtype, "s")
+    g, at = _outputs(c, out, {
+        "dx": (need_dx, (M, D), None, dy, True), "dresidual": (True, (M, D), s.dtype, s, True),
+        "dweight": (True, (D,), c.f32, weight, False),
+        "dbias": (bool(bias), (D,), c.f32, weight, False),
+        "dscale": (scale is not None, (D,), c.f32, scale, False)})
     ps, ls = c.rows(s, "s", M, D, s.dtype)
     po, lo = c.rows(dy, "dy", M, D)
     pds, lds = c.rows(ds, "ds", M, D, s.dtype, False)
     px, lx = c.rows(x, "x", M, D, required=scale is not None)
-    pdx, ldx = c.rows(g["dx"], "dx", M, D, required=False)
-    pdr, ldr = c.rows(g["dresidual"], "dresidual", M, D, s.dtype)
+    (pdx, ldx), (pdr, ldr) = at["dx"], at["dresidual"]
     wp, wn, _keep = c.workspace(norm_workspace_bytes(OP_ADD_NORM_BACKWARD, rows=M, width=D),
                                 workspace, stream)
     _check("mss_add_norm_backward", lib().mss_add_norm_backward(
         _ref(make_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
         _ref(make_norm_strides(lx, 0, 0, ls, lo, lds, ldx, 0, ldr)), ps,
         c.dense(weight, "weight", (D,), required=True), po, pds, px,
-        c.dense(scale, "scale", (D,)), pdx, pdr, c.dense(g["dweight"], "dweight", (D,)),
-        c.dense(g["dbias"], "dbias", (D,)), c.dense(g["dscale"], "dscale", (D,)), wp, wn,
-        c.stream(stream)))
+        c.dense(scale, "scale", (D,)), pdx, pdr, at["dweight"][0], at["dbias"][0], at["dscale"][0],
+        wp, wn, c.stream(stream)))
     return g
 
 
@@ -920,11 +932,10 @@ def gated_norm(x, z, weight, bias=None, residual=None, scale=None, *, groups=1, 
     ``groups`` equal groups of channels."""
     M, D = x.shape
     c = _Call(x, "x")
-    y = out if out is not None else c.empty((M, D))
     px, lx = c.rows(x, "x", M, D)
     pz, lz = c.rows(z, "z", M, D, required=False)
     pr, lr = c.rows(residual, "residual", M, D, required=False)
-    py, ly = c.rows(y, "out", M, D)
+    y, py, ly = c.output(out, "out", M, D)
     _check("mss_gated_norm", lib().mss_gated_norm(
         _ref(make_norm_dims(M, D, c.code, c.code, _choice(NORM_KINDS, kind, "kind"),
                             _choice(GATE_ORDERS, order, "order"), groups, eps, alpha)),
@@ -943,15 +954,15 @@ def gated_norm_backward(x, z, weight, bias, scale, dout, *, groups=1, order="bef
     (``norm_workspace_bytes(OP_GATED_NORM_BACKWARD, ...)``)."""
     M, D = x.shape
     c = _Call(x, "x")
-    g = _outputs(c, out, {
-        "dx": (True, (M, D), None, x), "dz": (z is not None, (M, D), None, z),
-        "dweight": (True, (D,), c.f32, weight), "dbias": (bias is not None, (D,), c.f32, bias),
-        "dscale": (scale is not None, (D,), c.f32, scale)})
+    g, at = _outputs(c, out, {
+        "dx": (True, (M, D), None, x, True), "dz": (z is not None, (M, D), None, z, True),
+        "dweight": (True, (D,), c.f32, weight, False),
+        "dbias": (bias is not None, (D,), c.f32, bias, False),
+        "dscale": (scale is not None, (D,), c.f32, scale, False)})
     px, lx = c.rows(x, "x", M, D)
     pz, lz = c.rows(z, "z", M, D, required=False)
     po, lo = c.rows(dout, "dout", M, D)
-    pdx, ldx = c.rows(g["dx"], "dx", M, D)
-    pdz, ldz = c.rows(g["dz"], "dz", M, D, required=False)
+    (pdx, ldx), (pdz, ldz) = at["dx"], at["dz"]
     wp, wn, _keep = c.workspace(
         norm_workspace_bytes(OP_GATED_NORM_BACKWARD, rows=M, width=D, groups=groups), workspace,
         stream)
@@ -960,7 +971,6 @@ def gated_norm_backward(x, z, weight, bias, scale, dout, *, groups=1, order="bef
                             _choice(GATE_ORDERS, order, "order"), groups, eps, alpha)),
         _ref(make_norm_strides(lx, lz, 0, 0, lo, 0, ldx, ldz)), px, pz,
         c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)),
-        c.dense(scale, "scale", (D,)), po, pdx, pdz, c.dense(g["dweight"], "dweight", (D,)),
-        c.dense(g["dbias"], "dbias", (D,)), c.dense(g["dscale"], "dscale", (D,)), wp, wn,
-        c.stream(stream)))
+        c.dense(scale, "scale", (D,)), po, pdx, pdz, at["dweight"][0], at["dbias"][0], at["dscale"][0],
+        wp, wn, c.stream(stream)))
     return g
