@@ -36,6 +36,11 @@
 namespace mss {
 namespace {
 
+// k of Gates: log2 of a where sigma(r) = 1.
+__device__ __forceinline__ float decay_rate(float scale, float decay) {
+    return -kLog2e * (scale * softplus(decay));
+}
+
 // The gates of one token and channel: a and v.  The backward works in two
 // halves, with `er` and `ei` kept in between in the place of r and i.
 template <int GATE>
@@ -46,7 +51,8 @@ struct Gates {
                       // SIGMOID: r itself;  LOG: a
     static constexpr float kMost = 8.507059173023462e37f;   // 2^126
 
-    // k = c softplus(decay) (DECAY)
+    // k = -log2(e) c softplus(decay) (DECAY);  KEEP: er and ei are used later
+    template <bool KEEP>
     __device__ __forceinline__ void set(float x, float r, float i, float k) {
         if constexpr (GATE == MSS_GATE_SIGMOID) {
             float c;
@@ -54,9 +60,13 @@ struct Gates {
             v = c * x;
             er = r;
         } else if constexpr (GATE == MSS_GATE_DECAY) {
-            er = __builtin_fminf(ex2(-kLog2e * r), kMost);
-            ei = __builtin_fminf(ex2(-kLog2e * i), kMost);
-            const float l2 = -kLog2e * k * rcp(1.0f + er);
+            er = ex2(-kLog2e * r);
+            ei = ex2(-kLog2e * i);
+            if constexpr (KEEP) {
+                er = __builtin_fminf(er, kMost);
+                ei = __builtin_fminf(ei, kMost);
+            }
+            const float l2 = k * rcp(1.0f + er);
             a = ex2(l2);
             v = __builtin_amdgcn_sqrtf(one_minus_square(l2, a)) * rcp(1.0f + ei) * x;
         } else {
@@ -79,7 +89,7 @@ struct Gates {
         } else if constexpr (GATE == MSS_GATE_DECAY) {
             const float s = rcp(1.0f + er), c = er * s;   // sigma(r), 1 - sigma(r)
             const float g = rcp(1.0f + ei), gc = ei * g;
-            const float l2 = -kLog2e * k * s;
+            const float l2 = k * s;
             const float a = ex2(l2);
             // m = sqrt(1 - a^2) and 1 / m; where m vanishes, so do sigma(r) or
             // k, and k sigma(r) / m (all that 1 / m enters) is below 2^-60
@@ -90,7 +100,7 @@ struct Gates {
             dx = G * (mm * rm * g);
             di = dx * x * gc;
             ws = G * __builtin_fmaf(-x, (g * a) * (as * rm), as * p);
-            dr = -k * ws * c;
+            dr = kLn2 * k * ws * c;
         } else {
             dx = G;
             dr = G * er * p;
@@ -182,14 +192,16 @@ __device__ __forceinline__ unsigned take(const Chain& g, unsigned* lds) {
 template <typename T, int V>
 struct Piece {
     typename std::conditional<V == 1, T, typename RowVec<T, V == 1 ? 2 : V>::type>::type t;
-    __device__ __forceinline__ void load(const T* row, unsigned c) {
-        t = *reinterpret_cast<const decltype(t)*>(row + c);
+    // `row` is the same for all lanes and `at` the lane's byte offset in it,
+    // below 2^31: one register pair and one register of address.
+    __device__ __forceinline__ void load(const T* row, unsigned at) {
+        t = *reinterpret_cast<const decltype(t)*>(reinterpret_cast<const char*>(row) + at);
     }
     // Outputs carry the nontemporal hint: B4 L8192 D5120 fp32 with a gate,
     // forward 469 -> 441 us, backward 832 -> 813; B8 L2048 D1536 bf16 decay,
     // forward 60 -> 54 us, backward 98 -> 87.
-    __device__ __forceinline__ void store(T* row, unsigned c) const {
-        __builtin_nontemporal_store(t, reinterpret_cast<decltype(t)*>(row + c));
+    __device__ __forceinline__ void store(T* row, unsigned at) const {
+        __builtin_nontemporal_store(t, reinterpret_cast<decltype(t)*>(reinterpret_cast<char*>(row) + at));
     }
     __device__ __forceinline__ float get(int v) const {
         if constexpr (V == 1)
@@ -215,6 +227,24 @@ struct Piece {
 template <typename T>
 __device__ __forceinline__ T* at_row(const void* p, int64_t row, int64_t ld) {
     return const_cast<T*>(static_cast<const T*>(p)) + row * ld;
+}
+
+// A piece's S rows from `row` on, of which n are there (the others read the
+// last one again, or the row given when none is).
+template <int S, typename T, int V>
+__device__ __forceinline__ void load_rows(Piece<T, V> (&p)[S], const void* base, int64_t row, int64_t ld,
+                                          int n, unsigned at) {
+    const T* from = at_row<T>(base, row, ld);
+    if (n == S) {
+#pragma unroll
+        for (int s = 0; s < S; s++, from += ld) p[s].load(from, at);
+    } else {
+#pragma unroll
+        for (int s = 0; s < S; s++) {
+            p[s].load(from, at);
+            from += s + 1 < n ? ld : 0;
+        }
+    }
 }
 
 // Bit s: step t0 + s (of S) drops what is carried into it.
@@ -286,26 +316,19 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
     const int64_t t0 = chunk * kChunk + wave * S, row0 = int64_t{b} * q.L;
     const int n = t0 >= q.L ? 0 : q.L - t0 < S ? static_cast<int>(q.L - t0) : S;
 
+    const int64_t row = row0 + (n > 0 ? t0 : q.L - 1);
+    const unsigned at = c * sizeof(T);
+
     Piece<T, V> x[S], r[S], in[S], z[S];
-#pragma unroll
-    for (int s = 0; s < S; s++) {
-        const int64_t row = row0 + (t0 + s < q.L ? t0 + s : q.L - 1);
-        x[s].load(at_row<T>(q.x, row, q.ld_x), c);
-        r[s].load(at_row<T>(q.r, row, q.ld_r), c);
-        if constexpr (GATE == MSS_GATE_DECAY) in[s].load(at_row<T>(q.i, row, q.ld_i), c);
-    }
-    if constexpr (Z) {
-#pragma unroll
-        for (int s = 0; s < S; s++) {
-            const int64_t row = row0 + (t0 + s < q.L ? t0 + s : q.L - 1);
-            z[s].load(at_row<T>(q.z, row, q.ld_z), c);
-        }
-    }
+    load_rows<S>(r, q.r, row, q.ld_r, n, at);
+    if constexpr (GATE == MSS_GATE_DECAY) load_rows<S>(in, q.i, row, q.ld_i, n, at);
+    load_rows<S>(x, q.x, row, q.ld_x, n, at);
+    if constexpr (Z) load_rows<S>(z, q.z, row, q.ld_z, n, at);
     const unsigned resets = reset_bits<S>(q.reset, row0, t0, q.L, lane);
     float k[V];
 #pragma unroll
     for (int v = 0; v < V; v++)
-        k[v] = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(q.decay[c + v]) : 0.0f;
+        k[v] = GATE == MSS_GATE_DECAY ? decay_rate(q.gate_scale, q.decay[c + v]) : 0.0f;
 
     float a[S][V], u[S][V];
     Map m[V];
@@ -314,7 +337,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
 #pragma unroll
         for (int v = 0; v < V; v++) {
             Gates<GATE> e;
-            e.set(x[s].get(v), r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
+            e.template set<false>(x[s].get(v), r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
             a[s][v] = e.a;
             u[s][v] = e.v;
         }
@@ -388,8 +411,9 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
         for (int v = 0; v < V; v++) out[c + v] = h[v];
     }
     states<S, V>(a, u, h, resets);
+    T* y_row = at_row<T>(q.y, row, q.ld_y);
 #pragma unroll
-    for (int s = 0; s < S; s++) {
+    for (int s = 0; s < S; s++, y_row += q.ld_y) {
         if (s >= n) continue;
         Piece<T, V> y;
 #pragma unroll
@@ -399,7 +423,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
             else
                 y.set(v, u[s][v]);
         }
-        if (live) y.store(at_row<T>(q.y, row0 + t0 + s, q.ld_y), c);
+        if (live) y.store(y_row, at);
     }
     if (q.h_last && n > 0 && t0 + n == q.L && live) {
 #pragma unroll
@@ -431,21 +455,20 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
     const int64_t t0 = chunk * kBwdChunk + wave * S, row0 = int64_t{b} * q.L;
     const int n = t0 >= q.L ? 0 : q.L - t0 < S ? static_cast<int>(q.L - t0) : S;
 
+    const int64_t row = row0 + (n > 0 ? t0 : q.L - 1);
+    const unsigned at = c * sizeof(T);
+
     Piece<T, V> x[S], r[S], in[S], z[S], dout[S];
-#pragma unroll
-    for (int s = 0; s < S; s++) {
-        const int64_t row = row0 + (t0 + s < q.L ? t0 + s : q.L - 1);
-        x[s].load(at_row<T>(q.x, row, q.ld_x), c);
-        r[s].load(at_row<T>(q.r, row, q.ld_r), c);
-        if constexpr (GATE == MSS_GATE_DECAY) in[s].load(at_row<T>(q.i, row, q.ld_i), c);
-        if constexpr (Z) z[s].load(at_row<T>(q.z, row, q.ld_z), c);
-        dout[s].load(at_row<T>(q.dout, row, q.ld_y), c);
-    }
+    load_rows<S>(r, q.r, row, q.ld_r, n, at);
+    if constexpr (GATE == MSS_GATE_DECAY) load_rows<S>(in, q.i, row, q.ld_i, n, at);
+    load_rows<S>(x, q.x, row, q.ld_x, n, at);
+    if constexpr (Z) load_rows<S>(z, q.z, row, q.ld_z, n, at);
+    load_rows<S>(dout, q.dout, row, q.ld_y, n, at);
     const unsigned resets = reset_bits<S>(q.reset, row0, t0, q.L, lane);
     float k[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; v++) {
-        k[v] = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(q.decay[c + v]) : 0.0f;
+        k[v] = GATE == MSS_GATE_DECAY ? decay_rate(q.gate_scale, q.decay[c + v]) : 0.0f;
         h[v] = q.h_ckpt[(int64_t{b} * g.chunks + chunk) * q.D + c + v];
     }
 
@@ -457,7 +480,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
 #pragma unroll
         for (int v = 0; v < V; v++) {
             Gates<GATE> e;
-            e.set(x[s].get(v), r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
+            e.template set<true>(x[s].get(v), r[s].get(v), GATE == MSS_GATE_DECAY ? in[s].get(v) : 0.0f, k[v]);
             a[s][v] = e.a;
             u[s][v] = e.v;
             er[s][v] = e.er;
@@ -559,9 +582,17 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
     float sum[V];
 #pragma unroll
     for (int v = 0; v < V; v++) sum[v] = 0.0f;
+    T* dx_row = at_row<T>(q.dx, row + n, q.ld_dx);
+    T* dr_row = at_row<T>(q.dr, row + n, q.ld_dr);
+    T* di_row = at_row<T>(q.di, row + n, q.ld_di);
+    T* dz_row = at_row<T>(q.dz, row + n, q.ld_dz);
 #pragma unroll
     for (int s = S - 1; s >= 0; s--) {
         if (s >= n) continue;
+        dx_row -= q.ld_dx;
+        dr_row -= q.ld_dr;
+        di_row -= q.ld_di;
+        dz_row -= q.ld_dz;
         Piece<T, V> dx, dr, di, dz;
         const bool drop = resets >> s & 1;
 #pragma unroll
@@ -586,11 +617,10 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
             di.set(v, gi);
         }
         if (live) {
-            const int64_t row = row0 + t0 + s;
-            dx.store(at_row<T>(q.dx, row, q.ld_dx), c);
-            dr.store(at_row<T>(q.dr, row, q.ld_dr), c);
-            if constexpr (GATE == MSS_GATE_DECAY) di.store(at_row<T>(q.di, row, q.ld_di), c);
-            if constexpr (Z) dz.store(at_row<T>(q.dz, row, q.ld_dz), c);
+            dx.store(dx_row, at);
+            dr.store(dr_row, at);
+            if constexpr (GATE == MSS_GATE_DECAY) di.store(di_row, at);
+            if constexpr (Z) dz.store(dz_row, at);
         }
     }
     if (q.dh0 && t0 == 0 && live) {
@@ -660,8 +690,8 @@ __global__ __launch_bounds__(64) void gated_step_kernel(GatedArgs q, unsigned pe
 #pragma unroll
     for (int v = 0; v < V; v++) {
         Gates<GATE> e;
-        const float k = GATE == MSS_GATE_DECAY ? q.gate_scale * softplus(decay[v]) : 0.0f;
-        e.set(x[v], r[v], GATE == MSS_GATE_DECAY ? in[v] : 0.0f, k);
+        const float k = GATE == MSS_GATE_DECAY ? decay_rate(q.gate_scale, decay[v]) : 0.0f;
+        e.template set<false>(x[v], r[v], GATE == MSS_GATE_DECAY ? in[v] : 0.0f, k);
         h.set(v, __builtin_fmaf(e.a, h[v], e.v));
         y.set(v, q.z ? h[v] * silu(z[v]) : h[v]);
     }
@@ -706,7 +736,8 @@ int64_t chain_words(int64_t B, int64_t L, int64_t D, int64_t len) {
 bool chain_bytes(int64_t B, int64_t L, int64_t D, int64_t len, int64_t& bytes) {
     // a workgroup per chunk and tile; the word counts stay far below 2^63
     // (8 bytes for every `len` steps of a channel whose elements were counted)
-    if (D > INT32_MAX - 128 || cdiv(L, len) > INT32_MAX / (B * cdiv(D, 64))) return false;
+    // byte offsets in a row stay below 2^31
+    if (D > (1 << 29) - 128 || cdiv(L, len) > INT32_MAX / (B * cdiv(D, 64))) return false;
     const int64_t words = chain_words(B, L, D, len);
     bytes = words == 0 ? 0 : align256(256 + 8 * words);
     return true;

@@ -26,7 +26,7 @@ __device__ __forceinline__ Place place(const NormArgs& q) {
 template <typename T, int TEAM, int NC, bool before, bool layer>
 __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(NormArgs q) {
     constexpr int V = kVec<T>;
-    __shared__ float lds[kSumLds<TEAM, 1>];
+    __shared__ float lds[kSumLds<TEAM>];
     const int n = static_cast<int>(q.D / q.G), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
     const float inv_n = 1.0f / static_cast<float>(n);
     const Place at = place<TEAM>(q);
@@ -52,9 +52,6 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
 #pragma unroll
         for (int j = 0; j < NC; j++) {
             const int c = V * (lane + j * lanes);
-            r.x[j].zero();
-            r.z[j].zero();
-            r.res[j].zero();
             if (c < n && m < q.M) {
                 r.x[j].load(row_of<T>(q.x, m, q.ld_x, at.g0), c, n);
                 if (q.z) r.z[j].load(row_of<T>(q.z, m, q.ld_z, at.g0), c, n);
@@ -64,7 +61,14 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
     };
     int turn = 0;
     int64_t m = at.first;
-    Row next;
+    Row next;   // what lies past a row's end, or is not given, stays 0
+#pragma unroll
+    for (int j = 0; j < NC; j++) {
+        next.x[j].zero();
+        next.z[j].zero();
+        next.res[j].zero();
+    }
+    clear_sums<TEAM>(lds);
     read(m, next);
     for (; m < q.M; m += at.step) {
         const Row r = next;
@@ -121,7 +125,7 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
 template <typename T, int TEAM, int NC, bool before, bool layer, bool EXTRA>
 __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel(NormArgs q) {
     constexpr int V = kVec<T>, K = EXTRA ? 2 : 1;
-    __shared__ float lds[kSumLds<TEAM, 3>];
+    __shared__ float lds[kSumLds<TEAM>];
     __shared__ float part_lds[kPartLds<TEAM, NC, V>];
     const int n = static_cast<int>(q.D / q.G), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
     const float inv_n = 1.0f / static_cast<float>(n);
@@ -147,9 +151,6 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
 #pragma unroll
         for (int j = 0; j < NC; j++) {
             const int c = V * (lane + j * lanes);
-            r.x[j].zero();
-            r.z[j].zero();
-            r.d[j].zero();
             if (c < n && m < q.M) {
                 r.x[j].load(row_of<T>(q.x, m, q.ld_x, at.g0), c, n);
                 if (q.z) r.z[j].load(row_of<T>(q.z, m, q.ld_z, at.g0), c, n);
@@ -159,7 +160,14 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
     };
     int turn = 0;
     int64_t m = at.first;
-    Row next;
+    Row next;   // what lies past a row's end, or is not given, stays 0
+#pragma unroll
+    for (int j = 0; j < NC; j++) {
+        next.x[j].zero();
+        next.z[j].zero();
+        next.d[j].zero();
+    }
+    clear_sums<TEAM>(lds);
     read(m, next);
     for (; m < q.M; m += at.step) {
         Row r = next;
@@ -281,7 +289,7 @@ __device__ __forceinline__ float wide_mean(const WideRow<T>& r, int64_t n, int k
 
 template <typename T>
 __global__ __launch_bounds__(kWide) void gated_norm_wide_kernel(NormArgs q) {
-    __shared__ float lds[kSumLds<kGroup, 1>];
+    __shared__ float lds[kSumLds<kGroup>];
     const int64_t n = q.D / q.G;
     const float inv_n = 1.0f / static_cast<float>(n);
     const Place at = place<kGroup>(q);
@@ -311,7 +319,7 @@ __global__ __launch_bounds__(kWide) void gated_norm_wide_kernel(NormArgs q) {
 
 template <typename T>
 __global__ __launch_bounds__(kWide) void gated_norm_bwd_wide_kernel(NormArgs q) {
-    __shared__ float lds[kSumLds<kGroup, 3>];
+    __shared__ float lds[kSumLds<kGroup>];
     const int64_t n = q.D / q.G;
     const float inv_n = 1.0f / static_cast<float>(n);
     const Place at = place<kGroup>(q);

@@ -66,9 +66,10 @@ __device__ __forceinline__ int team_of() {
     return TEAM == 64 ? __builtin_amdgcn_readfirstlane(team) : team;
 }
 
-// LDS floats of team_sum for K sums at once.
-template <int TEAM, int K>
-constexpr int kSumLds = TEAM == kGroup ? 2 * K * 16 : 1;
+// LDS floats of team_sum: twice up to three sums of sixteen waves.
+constexpr int kSumHalf = 3 * 16;
+template <int TEAM>
+constexpr int kSumLds = TEAM == kGroup ? 2 * kSumHalf : 1;
 
 // The sum over the team in each of its lanes, K sums at once, always in the
 // same order.  The two halves of `lds` take turns from call to call, so that
@@ -87,8 +88,10 @@ __device__ __forceinline__ void team_sum(float (&v)[K], float* lds, int& turn) {
                    (read_lane(v[k], 32) + read_lane(v[k], 48));
     }
     if constexpr (TEAM == kGroup) {
-        const int waves = blockDim.x / 64;
-        float* at = lds + turn * (K * 16);
+        // one word of each wave (slots without a wave hold 0), summed by
+        // every 16 lanes
+        static_assert(K * 16 <= kSumHalf, "the halves do not overlap");
+        float* at = lds + turn * kSumHalf;
         turn ^= 1;
         if (threadIdx.x % 64 == 0) {
 #pragma unroll
@@ -96,11 +99,22 @@ __device__ __forceinline__ void team_sum(float (&v)[K], float* lds, int& turn) {
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < K; k++) v[k] = 0.0f;
-        for (int w = 0; w < waves; w++)
-#pragma unroll
-            for (int k = 0; k < K; k++) v[k] += at[k * 16 + w];
+        for (int k = 0; k < K; k++) {
+            v[k] = at[k * 16 + threadIdx.x % 16];
+            v[k] = dpp_add<0x128>(v[k]);
+            v[k] = dpp_add<0x124>(v[k]);
+            v[k] = dpp_add<0x122>(v[k]);
+            v[k] = dpp_add<0x121>(v[k]);
+        }
     }
+}
+
+// Zeroes the slots of team_sum that no wave writes; the first sum's barrier
+// orders it.
+template <int TEAM>
+__device__ __forceinline__ void clear_sums(float* lds) {
+    for (int i = threadIdx.x; i < kSumLds<TEAM>; i += blockDim.x)
+        if (i % 16 >= static_cast<int>(blockDim.x) / 64) lds[i] = 0.0f;
 }
 
 // The workgroup's share of K sums per channel, in the row of the workspace

@@ -33,7 +33,7 @@ struct AddRow {
 template <typename T, typename R, int TEAM, int NC>
 __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormArgs q) {
     constexpr int V = kVec<T>;
-    __shared__ float lds[kSumLds<TEAM, 1>];
+    __shared__ float lds[kSumLds<TEAM>];
     const int n = static_cast<int>(q.D), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
     const bool layer = q.kind == MSS_NORM_LAYER;
     const float inv_n = 1.0f / static_cast<float>(n);
@@ -53,8 +53,6 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormA
 #pragma unroll
         for (int j = 0; j < NC; j++) {
             const int c = V * (lane + j * lanes);
-            res[j].zero();
-            x[j].zero();
             if (c < n && m < q.M) {
                 if (q.res) res[j].load(row_of<R>(q.res, m, q.ld_res), c, n);
                 x[j].load(row_of<T>(q.x, m, q.ld_x), c, n);
@@ -63,8 +61,15 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormA
     };
     int turn = 0;
     int64_t m = blockIdx.x * static_cast<int64_t>(rows) + team_of<TEAM>();
+    // (what lies past a row's end, or is not given, stays 0)
     RowVec<R, V> res[NC];
     RowVec<T, V> x[NC];
+#pragma unroll
+    for (int j = 0; j < NC; j++) {
+        res[j].zero();
+        x[j].zero();
+    }
+    clear_sums<TEAM>(lds);
     read(m, res, x);
     for (; m < q.M; m += step) {
         RowVec<R, V> s[NC];
@@ -113,7 +118,7 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormA
 template <typename T, typename R, int TEAM, int NC, bool EXTRA>
 __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(NormArgs q) {
     constexpr int V = kVec<T>, K = EXTRA ? 3 : 1;
-    __shared__ float lds[kSumLds<TEAM, 3>];
+    __shared__ float lds[kSumLds<TEAM>];
     __shared__ float part_lds[kPartLds<TEAM, NC, V>];
     const int n = static_cast<int>(q.D), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
     const bool layer = q.kind == MSS_NORM_LAYER;
@@ -138,10 +143,6 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(N
 #pragma unroll
         for (int j = 0; j < NC; j++) {
             const int c = V * (lane + j * lanes);
-            r.r[j].zero();
-            r.dy[j].zero();
-            r.ds[j].zero();
-            r.x[j].zero();
             if (c < n && m < q.M) {
                 r.r[j].load(row_of<R>(q.s, m, q.ld_s), c, n);
                 r.dy[j].load(row_of<T>(q.dy, m, q.ld_y), c, n);
@@ -152,7 +153,15 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(N
     };
     int turn = 0;
     int64_t m = blockIdx.x * static_cast<int64_t>(rows) + team_of<TEAM>();
-    Row next;
+    Row next;   // what lies past a row's end, or is not given, stays 0
+#pragma unroll
+    for (int j = 0; j < NC; j++) {
+        next.r[j].zero();
+        next.dy[j].zero();
+        next.ds[j].zero();
+        next.x[j].zero();
+    }
+    clear_sums<TEAM>(lds);
     read(m, next);
     for (; m < q.M; m += step) {
         Row r = next;
@@ -222,7 +231,7 @@ constexpr int kWide = 1024;
 
 template <typename T, typename R>
 __global__ __launch_bounds__(kWide) void add_norm_wide_kernel(NormArgs q) {
-    __shared__ float lds[kSumLds<kGroup, 1>];
+    __shared__ float lds[kSumLds<kGroup>];
     int turn = 0;
     for (int64_t m = blockIdx.x; m < q.M; m += gridDim.x) {
         const T* x = row_of<T>(q.x, m, q.ld_x);
@@ -257,7 +266,7 @@ __global__ __launch_bounds__(kWide) void add_norm_wide_kernel(NormArgs q) {
 
 template <typename T, typename R>
 __global__ __launch_bounds__(kWide) void add_norm_bwd_wide_kernel(NormArgs q) {
-    __shared__ float lds[kSumLds<kGroup, 3>];
+    __shared__ float lds[kSumLds<kGroup>];
     int turn = 0;
     float* part = static_cast<float*>(q.ws) + blockIdx.x * 3 * q.D;
     for (int64_t c = threadIdx.x; c < q.D; c += kWide)
