@@ -356,7 +356,9 @@ int mss_ssd_time_split(const mss_ssd_dims* dims, int64_t* segment_steps);
  *   MSS_GATE_LOG      a = exp(r),                     v = x
  * r = -inf is valid: it means a = 0 (a = 1 for MSS_GATE_DECAY).  reset_t != 0 drops the state carried into step
  * t (the start of another document packed into the same row, or the end of a
- * row's left padding).
+ * row's left padding).  Time is cut into chunks of up to 128 steps that are
+ * combined as affine maps of the state: with MSS_GATE_LOG and r > 0 (growing
+ * states) the product of a chunk's factors must stay finite.
  * The activations x, r, i, z, y and their gradients are of type dims->dtype;
  * the states, decay and its gradient are fp32.  States are carried in fp32
  * and results are rounded once, to the nearest even.                       */
@@ -368,6 +370,9 @@ int mss_ssd_time_split(const mss_ssd_dims* dims, int64_t* segment_steps);
 #define MSS_GATE_LOG 2
 /* h_ckpt holds the state entering steps 0, 64, 128, ... */
 #define MSS_GATED_CKPT_STEPS 64
+/* Most channels of these calls and of the norms below; a call whose kernel
+ * would have 2^32 threads or more is refused as well (MSS_EINVAL). */
+#define MSS_MAX_WIDTH (1 << 28)
 typedef struct mss_gated_dims {
     int32_t struct_size;    /* sizeof(mss_gated_dims) */
     int32_t flags;          /* must be 0 */
@@ -461,7 +466,7 @@ typedef struct mss_norm_dims {
     int32_t order;          /* gated_norm: MSS_GATE_*_NORM; add_norm: 0 */
     int64_t rows;           /* M */
     int64_t width;          /* D */
-    int64_t groups;         /* divides D (add_norm: 1) */
+    int64_t groups;         /* divides D, at most 2^20 (add_norm: 1) */
     float eps;              /* finite, > 0 */
     float alpha;            /* scalar factor of the residual scale, finite */
 } mss_norm_dims;

@@ -126,6 +126,7 @@ OP_GATED_SCAN_BACKWARD = 5
 OP_ADD_NORM_BACKWARD = 6
 OP_GATED_NORM_BACKWARD = 7
 GATED_CKPT_STEPS = 64                 # MSS_GATED_CKPT_STEPS
+MAX_WIDTH = 1 << 28                   # MSS_MAX_WIDTH
 NOALLOC_SCRATCH_BYTES = 256 << 20     # MSS_NOALLOC_SCRATCH_BYTES
 MSS_ESCRATCH = -6
 
@@ -738,9 +739,9 @@ def _gated_inputs(c, x, r, i, decay, z, rows, D, gate):
 
 
 def _reset(c, reset, rows):
-    if reset is not None and reset.dtype == _torch().bool:
-        reset = reset.view(_torch().uint8)
-    return c.dense(reset, "reset", (rows,), _torch().uint8)
+    if isinstance(reset, c.Tensor) and reset.dtype is c.torch.bool:
+        reset = reset.view(c.torch.uint8)
+    return c.dense(reset, "reset", (rows,), c.torch.uint8)
 
 
 def gated_ckpt_steps(seq_len) -> int:

@@ -130,6 +130,7 @@ bool gated_ok(const mss_gated_dims* d, const mss_gated_strides* s, bool need_l) 
     if (d->gate == MSS_GATE_DECAY && !(std::isfinite(d->gate_scale) && d->gate_scale > 0.0f))
         return false;
     if (d->batch < 0 || d->d_inner < 0 || (need_l && d->seq_len < 0)) return false;
+    if (d->d_inner > MSS_MAX_WIDTH) return false;
     return !s || (s->struct_size == static_cast<int32_t>(sizeof(mss_gated_strides)) &&
                   s->reserved == 0);
 }
@@ -179,6 +180,7 @@ bool norm_ok(const mss_norm_dims* d, const mss_norm_strides* s, bool add) {
         return false;
     if (d->kind != MSS_NORM_RMS && d->kind != MSS_NORM_LAYER) return false;
     if (d->rows < 0 || d->width < 0 || d->groups < 1 || d->width % d->groups != 0) return false;
+    if (d->width > MSS_MAX_WIDTH || d->groups > (1 << 20)) return false;
     if (!(std::isfinite(d->eps) && d->eps > 0.0f) || !std::isfinite(d->alpha)) return false;
     if (add) {
         if (d->groups != 1 || d->order != 0) return false;

@@ -453,6 +453,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
     __shared__ unsigned ticket;
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int waves = blockDim.x / 64;   // kWaves, or fewer where they hold all steps
     const unsigned id = take(g, &ticket);
     const unsigned tile = id % g.tiles;
     const int64_t turn = id / g.tiles;   // turn 0: the last chunk
@@ -543,7 +544,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
 #pragma unroll
         for (int v = 0; v < V; v++) mates[wave][v][lane] = e[v];
     }
-    if (wave == kWaves - 1) {
+    if (wave == waves - 1) {
         Map e[V];
         if (first > 0)
             wait_for<V>(g.states + (int64_t{tile} * g.groups + first / kWaves) * words + lane, e);
@@ -559,7 +560,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
     for (int p = 0; p < mate; p++)
 #pragma unroll
         for (int v = 0; v < V; v++) Q[v] = mates[p][v][lane](Q[v]);
-    for (int p = kWaves - 1; p > wave; p--)
+    for (int p = waves - 1; p > wave; p--)
 #pragma unroll
         for (int v = 0; v < V; v++) Q[v] = rev[p][v][lane](Q[v]);
     if (wave == 0 && mate == kWaves - 1 && turn + 1 < g.chunks) {
@@ -648,8 +649,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
 #pragma unroll
             for (int v = 0; v < V; v++) {
                 float all = 0.0f;
-#pragma unroll
-                for (int p = 0; p < kWaves; p++) all += fwd[p][v][lane].A;
+                for (int p = 0; p < waves; p++) all += fwd[p][v][lane].A;
                 part[(int64_t{b} * g.chunks + chunk) * q.D + c + v] = all;
             }
         }
@@ -737,6 +737,15 @@ hipError_t dispatch(const GatedArgs& a, F f) {
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
+// Threads of a workgroup: eight waves, or as many as a single chunk has pieces.
+unsigned threads_of(int64_t L, int64_t steps) {
+    const int64_t waves = cdiv(L, steps);
+    return static_cast<unsigned>(64 * (waves < kWaves ? waves : kWaves));
+}
+
+// A launch's threads are counted in 32 bits.
+constexpr int64_t kMaxThreads = int64_t{UINT32_MAX};
+
 // Words handed over for chunks of `len` steps, over tiles of whole pairs of
 // waves' channels (what either V needs).
 int64_t chain_words(int64_t B, int64_t L, int64_t D, int64_t len) {
@@ -748,7 +757,7 @@ bool chain_bytes(int64_t B, int64_t L, int64_t D, int64_t len, int64_t& bytes) {
     // a workgroup per chunk and tile; the word counts stay far below 2^63
     // (8 bytes for every `len` steps of a channel whose elements were counted)
     // byte offsets in a row stay below 2^31
-    if (D > (1 << 29) - 128 || cdiv(L, len) > INT32_MAX / (B * cdiv(D, 64))) return false;
+    if (D > MSS_MAX_WIDTH || cdiv(L, len) > kMaxThreads / (64 * kWaves) / (B * cdiv(D, 64))) return false;
     const int64_t words = chain_words(B, L, D, len);
     bytes = words == 0 ? 0 : align256(256 + 8 * words);
     return true;
@@ -779,7 +788,7 @@ hipError_t unset(const Chain& g, int V, hipStream_t st) {
 }  // namespace
 
 bool gated_step_fits(int64_t B, int64_t D) {
-    return D <= INT32_MAX - 64 && (B == 0 || cdiv(D, kStepVec) <= (int64_t{INT32_MAX} - 1) * 64 / B);
+    return D <= MSS_MAX_WIDTH && (B == 0 || cdiv(D, kStepVec) <= (kMaxThreads - 63) / B);
 }
 
 bool gated_scan_workspace(int64_t B, int64_t L, int64_t D, int64_t& bytes) {
@@ -798,10 +807,11 @@ hipError_t launch_gated_scan(const GatedArgs& a, hipStream_t st) {
         const Chain g = chain_of(a, v.value, kChunk);
         if (unset(g, v.value, st) != hipSuccess) return;
         const unsigned grid = g.tiles * static_cast<unsigned>(g.chunks);
+        const unsigned threads = threads_of(a.L, kSteps);
         if (a.z)
-            gated_scan_kernel<T, v.value, gate.value, true><<<grid, 64 * kWaves, 0, st>>>(a, g);
+            gated_scan_kernel<T, v.value, gate.value, true><<<grid, threads, 0, st>>>(a, g);
         else
-            gated_scan_kernel<T, v.value, gate.value, false><<<grid, 64 * kWaves, 0, st>>>(a, g);
+            gated_scan_kernel<T, v.value, gate.value, false><<<grid, threads, 0, st>>>(a, g);
     });
 }
 
@@ -815,12 +825,11 @@ hipError_t launch_gated_scan_bwd(const GatedArgs& a, hipStream_t st) {
         const Chain g = chain_of(a, v.value, kBwdChunk);
         if (unset(g, v.value, st) != hipSuccess) return;
         const unsigned grid = g.tiles * static_cast<unsigned>(g.chunks);
+        const unsigned threads = threads_of(a.L, kBwdSteps);
         if (a.z)
-            gated_scan_bwd_kernel<T, v.value, gate.value, true>
-                <<<grid, 64 * kWaves, 0, st>>>(a, g, part);
+            gated_scan_bwd_kernel<T, v.value, gate.value, true><<<grid, threads, 0, st>>>(a, g, part);
         else
-            gated_scan_bwd_kernel<T, v.value, gate.value, false>
-                <<<grid, 64 * kWaves, 0, st>>>(a, g, part);
+            gated_scan_bwd_kernel<T, v.value, gate.value, false><<<grid, threads, 0, st>>>(a, g, part);
     });
     if (e != hipSuccess || a.gate != MSS_GATE_DECAY) return e;
     gated_ddecay_kernel<<<static_cast<unsigned>(cdiv(a.D, 32)), 1024, 0, st>>>(

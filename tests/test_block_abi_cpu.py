@@ -193,6 +193,21 @@ def test_gate_arguments(L):
     assert call(L, "mss_gated_scan", gated(L=-1), ws_size=0) == EINVAL
 
 
+def test_limits(L):
+    """Widths, groups and launches past what the kernels count in 32 bits."""
+    w = mss.MAX_WIDTH
+    assert need(L, gated(B=1, L=2, D=w), 4)[0] == 0 and need(L, gated(B=1, L=2, D=w + 1), 4)[0] == EINVAL
+    assert call(L, "mss_gated_step", gated(B=1, D=w + 1)) == EINVAL
+    assert need(L, norm(M=1, D=w), 6)[0] == 0 and need(L, norm(M=1, D=w + 1), 6)[0] == EINVAL
+    assert need(L, norm(M=1, D=1 << 20, groups=1 << 20), 7)[0] == 0
+    assert need(L, norm(M=1, D=1 << 21, groups=1 << 21), 7)[0] == EINVAL
+    # 2^32 threads: 2^23 workgroups of 512, each 128 (forward) or 64 (backward) steps of a tile
+    for op, steps in ((4, 128), (5, 64)):
+        assert need(L, gated(B=1, L=steps * ((1 << 23) - 1), D=1), op)[0] == 0
+        assert need(L, gated(B=1, L=steps * (1 << 23), D=1), op)[0] == EINVAL
+    assert call(L, "mss_gated_step", gated(B=1 << 32, D=1)) == EINVAL
+
+
 def test_norm_arguments(L):
     for name in ("mss_add_norm", "mss_add_norm_backward", "mss_gated_norm", "mss_gated_norm_backward"):
         kw = dict(ws_size=1 << 40) if name in OPS else {}

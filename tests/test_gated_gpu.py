@@ -82,6 +82,12 @@ def test_long_sequence_few_channels(gate, dtype):
     run_case(1, 5000, 34, gate, dtype, z=False, h0=True, decay_mean=-7.0)
 
 
+@pytest.mark.parametrize("L", (1, 7, 8, 9, 15, 16, 17, 24, 31, 33, 47, 56, 57, 95, 113))
+def test_many_short_sequences(L):
+    """Workgroups of fewer waves, where one chunk holds the whole sequence."""
+    run_case(9, L, 70, "decay", "bf16", z=L % 2 == 0, h0=True, reset=True, seed=L)
+
+
 def test_many_rows():
     run_case(40, 70, 96, "sigmoid", "f16", z=True, h0=False)
 
@@ -351,6 +357,8 @@ def test_binding_refuses():
     with pytest.raises(mss.MssError) as err:
         mss.gated_scan(x, x, out=x, **kw)
     assert err.value.status == -3
+    with pytest.raises(TypeError, match="reset must be"):
+        mss.gated_scan(x, x, reset=[0] * 12, **kw)
     with pytest.raises(ValueError, match="on the GPU"):
         mss.gated_scan(x.cpu(), x, **kw)
     with pytest.raises(ValueError, match="current device"):
