@@ -393,15 +393,16 @@ hipError_t launch_gated_norm(const NormArgs& a, hipStream_t st) {
     return dispatch(a, [&](auto t) {
         using T = decltype(t);
         const bool held = by_width<kVec<T>>(a.D / a.G, [&](auto s) {
-            const auto grid = a.G * row_groups(a.M, a.G, s.threads, s.rows);
             by_kind(a, [&](auto before, auto layer) {
-                gated_norm_kernel<T, s.TEAM, s.NC, before.value, layer.value>
-                    <<<static_cast<unsigned>(grid), s.threads, 0, st>>>(a);
+                constexpr auto kernel = gated_norm_kernel<T, s.TEAM, s.NC, before.value, layer.value>;
+                const auto grid = a.G * row_groups<kernel>(a.M, a.G, s.threads, s.rows);
+                kernel<<<static_cast<unsigned>(grid), s.threads, 0, st>>>(a);
             });
         });
         if (!held) {
-            const auto grid = a.G * row_groups(a.M, a.G, kWide, 1);
-            gated_norm_wide_kernel<T><<<static_cast<unsigned>(grid), kWide, 0, st>>>(a);
+            constexpr auto kernel = gated_norm_wide_kernel<T>;
+            const auto grid = a.G * row_groups<kernel>(a.M, a.G, kWide, 1);
+            kernel<<<static_cast<unsigned>(grid), kWide, 0, st>>>(a);
         }
     });
 }
@@ -413,22 +414,22 @@ hipError_t launch_gated_norm_bwd(const NormArgs& a, hipStream_t st) {
     const hipError_t e = dispatch(a, [&](auto t) {
         using T = decltype(t);
         const bool held = by_width<kVec<T>>(a.D / a.G, [&](auto s) {
-            rows = part_groups(a.M, a.G, s.threads, s.rows);
-            const unsigned grid = static_cast<unsigned>(rows * a.G);
             by_kind(a, [&](auto before, auto layer) {
-                if (extra)
-                    gated_norm_bwd_kernel<T, s.TEAM, s.NC, before.value, layer.value, true>
-                        <<<grid, s.threads, 0, st>>>(a);
-                else
-                    gated_norm_bwd_kernel<T, s.TEAM, s.NC, before.value, layer.value, false>
-                        <<<grid, s.threads, 0, st>>>(a);
+                auto go = [&](auto more) {
+                    constexpr auto kernel = gated_norm_bwd_kernel<T, s.TEAM, s.NC, before.value,
+                                                                  layer.value, more.value>;
+                    rows = row_groups<kernel>(a.M, a.G, s.threads, s.rows,
+                                              most_parts(a.M, s.threads));
+                    kernel<<<static_cast<unsigned>(rows * a.G), s.threads, 0, st>>>(a);
+                };
+                extra ? go(std::true_type{}) : go(std::false_type{});
             });
         });
         if (!held) {
-            rows = part_groups(a.M, a.G, kWide, 1);
+            constexpr auto kernel = gated_norm_bwd_wide_kernel<T>;
+            rows = row_groups<kernel>(a.M, a.G, kWide, 1, most_parts(a.M, kWide));
             K = 2;
-            gated_norm_bwd_wide_kernel<T>
-                <<<static_cast<unsigned>(rows * a.G), kWide, 0, st>>>(a);
+            kernel<<<static_cast<unsigned>(rows * a.G), kWide, 0, st>>>(a);
         }
     });
     return e == hipSuccess ? launch_norm_params(a, true, rows, K, st) : e;

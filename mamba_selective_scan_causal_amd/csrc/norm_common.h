@@ -16,6 +16,7 @@
 // backward keeps its sums of the parameter gradients in registers.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "block_math.h"
@@ -180,24 +181,47 @@ struct Shape {
     int threads, rows;
 };
 
-// Workgroups per group of channels: two thousand lanes for each of 256 CUs
-// over all groups (a CU's waves, or twice what its registers hold: the next
-// ones start as others end), none without a row of its own.
+// Workgroups of `kernel` that a CU holds at once; asked for once per kernel and
+// number of waves.
+template <typename Kernel>
+inline int resident(Kernel* kernel, std::atomic<int> (&known)[17], int threads) {
+    std::atomic<int>& at = known[threads / 64];
+    int n = at.load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, reinterpret_cast<const void*>(kernel),
+                                                         threads, 0) != hipSuccess ||
+            n < 1) {
+            (void)hipGetLastError();
+            return 1;
+        }
+        at.store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// Workgroups per group of channels: what 256 CUs hold at once over all groups
+// (they walk the rows, so a second, partly filled round only lengthens the
+// launch: with 2048 lanes a CU whatever it holds, gated_norm forward and
+// backward of M 32768 D 5120 bf16 took 582 us, like this 528), none without a
+// row of its own.
+template <auto kernel>
 inline int64_t row_groups(int64_t M, int64_t G, int threads, int rows, int64_t most = 1 << 20) {
-    int64_t p = 256 * 2048 / threads;
+    static std::atomic<int> known[17];
+    int64_t p = 256 * static_cast<int64_t>(resident(kernel, known, threads));
     if (p > most) p = most;
     p = (p + G - 1) / G;
     const int64_t all = (M + rows - 1) / rows;
     return p < all ? p : all;
 }
 
-// The same for the backward passes, whose workgroups each write a row of
-// partial sums: eight rows of input to each, but four waves for each CU at
-// least, and 1024 workgroups at most.
-inline int64_t part_groups(int64_t M, int64_t G, int threads, int rows) {
+// The backward's workgroups each write a row of partial sums: at most 1024,
+// and with few rows of input one for every eight of them, but four waves for
+// each CU.
+constexpr int64_t kMostParts = 1024;
+inline int64_t most_parts(int64_t M, int threads) {
     int64_t most = 256 * 4 * 64 / threads;
     if (most < M / 8) most = M / 8;
-    return row_groups(M, G, threads, rows, most < 1024 ? most : 1024);
+    return most < kMostParts ? most : kMostParts;
 }
 
 // f(Shape) for groups of n channels, V to a vector: a quarter of a wave or a

@@ -368,7 +368,9 @@ hipError_t dispatch(const NormArgs& a, F f) {
 }  // namespace
 
 bool norm_bwd_workspace(int64_t M, int64_t D, int64_t G, int64_t& bytes) {
-    bytes = (part_groups(M, G, 64, 1) * 3 * D * 4 + 255) / 256 * 256;
+    int64_t rows = (kMostParts + G - 1) / G;   // of partial sums, at most
+    if (rows > M) rows = M;
+    bytes = (rows * 3 * D * 4 + 255) / 256 * 256;
     return true;
 }
 
@@ -383,13 +385,14 @@ hipError_t launch_add_norm(const NormArgs& a, hipStream_t st) {
         using T = decltype(t);
         using R = decltype(r);
         const bool held = by_width<kVec<T>>(a.D, [&](auto s) {
-            const auto grid = row_groups(a.M, 1, s.threads, s.rows);
-            add_norm_kernel<T, R, s.TEAM, s.NC>
-                <<<static_cast<unsigned>(grid), s.threads, 0, st>>>(a);
+            constexpr auto kernel = add_norm_kernel<T, R, s.TEAM, s.NC>;
+            const auto grid = row_groups<kernel>(a.M, 1, s.threads, s.rows);
+            kernel<<<static_cast<unsigned>(grid), s.threads, 0, st>>>(a);
         });
         if (!held) {
-            const auto grid = row_groups(a.M, 1, kWide, 1);
-            add_norm_wide_kernel<T, R><<<static_cast<unsigned>(grid), kWide, 0, st>>>(a);
+            constexpr auto kernel = add_norm_wide_kernel<T, R>;
+            const auto grid = row_groups<kernel>(a.M, 1, kWide, 1);
+            kernel<<<static_cast<unsigned>(grid), kWide, 0, st>>>(a);
         }
     });
 }
@@ -402,17 +405,18 @@ hipError_t launch_add_norm_bwd(const NormArgs& a, hipStream_t st) {
         using T = decltype(t);
         using R = decltype(r);
         const bool held = by_width<kVec<T>>(a.D, [&](auto s) {
-            rows = part_groups(a.M, 1, s.threads, s.rows);
-            const unsigned grid = static_cast<unsigned>(rows);
-            if (extra)
-                add_norm_bwd_kernel<T, R, s.TEAM, s.NC, true><<<grid, s.threads, 0, st>>>(a);
-            else
-                add_norm_bwd_kernel<T, R, s.TEAM, s.NC, false><<<grid, s.threads, 0, st>>>(a);
+            auto go = [&](auto more) {
+                constexpr auto kernel = add_norm_bwd_kernel<T, R, s.TEAM, s.NC, more.value>;
+                rows = row_groups<kernel>(a.M, 1, s.threads, s.rows, most_parts(a.M, s.threads));
+                kernel<<<static_cast<unsigned>(rows), s.threads, 0, st>>>(a);
+            };
+            extra ? go(std::true_type{}) : go(std::false_type{});
         });
         if (!held) {
-            rows = part_groups(a.M, 1, kWide, 1);
+            constexpr auto kernel = add_norm_bwd_wide_kernel<T, R>;
+            rows = row_groups<kernel>(a.M, 1, kWide, 1, most_parts(a.M, kWide));
             K = 3;
-            add_norm_bwd_wide_kernel<T, R><<<static_cast<unsigned>(rows), kWide, 0, st>>>(a);
+            kernel<<<static_cast<unsigned>(rows), kWide, 0, st>>>(a);
         }
     });
     return e == hipSuccess ? launch_norm_params(a, false, rows, K, st) : e;
