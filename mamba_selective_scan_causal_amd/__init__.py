@@ -722,10 +722,10 @@ def _ref(block):
     return ctypes.byref(block)
 
 
-def _flag(t, shape, call, dtype=None):
-    """An optional output given as False / True (allocate) or a tensor."""
+def _flag(t, shape, call, like=None):
+    """An optional float32 output given as False / True (allocate) or a tensor."""
     if isinstance(t, bool):
-        return call.empty(shape, dtype or call.f32) if t else None
+        return call.empty(shape, call.f32, like) if t else None
     return t
 
 
@@ -770,7 +770,7 @@ def gated_scan(x, r, i=None, decay=None, z=None, h0=None, reset=None, *, batch, 
     (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, M, D, gate)
     y, py, ly = c.output(out, "out", M, D)
     ck = _flag(h_ckpt, (batch, gated_ckpt_steps(seq_len), D), c)
-    hl = _flag(h_last, (batch, D), c)
+    hl = _flag(h_last, (batch, D), c, h0)
     need = gated_workspace_bytes(OP_GATED_SCAN, batch=batch, seq_len=seq_len, d_inner=D, gate=gate)
     wp, wn, _keep = c.workspace(need, workspace, stream)
     _check("mss_gated_scan", lib().mss_gated_scan(
