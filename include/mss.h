@@ -18,16 +18,19 @@
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers to dense, row-major fp32 arrays
- *     (the activations of the gated recurrence and the block norms below may
- *     be bf16 or fp16) on the current HIP device, allocated and owned by the
- *     caller.  The
- *     library allocates nothing and never frees a caller buffer; the backward
- *     passes take a caller workspace.  Its only device state is the static
- *     scratch array of mss_selective_scan_backward_noalloc.
+ *     (the activations of the gated recurrence and the block norms may be bf16
+ *     or fp16) on the current HIP device, allocated and owned by the caller.
+ *     The library allocates nothing and never frees a caller buffer; the
+ *     backward passes and mss_gated_scan take a caller workspace.  Its only
+ *     device state is the static scratch array of
+ *     mss_selective_scan_backward_noalloc.
  *   - Every pointer must be 16-byte aligned (MSS_EALIGN otherwise), except
- *     the activation and B/C tensors of the *_strided entry points (4 bytes).
+ *     the activation and B/C tensors of the *_strided entry points (4 bytes),
+ *     the activations of the gated recurrence and the block norms when strides
+ *     are given (their element), reset flags (any) and workspaces (256).
  *   - Outputs may not overlap any input (MSS_EALIAS), except the state
- *     buffers of mss_selective_step, which are updated in place by design.
+ *     buffers of mss_selective_step and mss_gated_step, which are updated in
+ *     place by design, and the residual stream of mss_add_norm, which may be.
  *   - Work is enqueued on `stream` (NULL = the null stream) and the call
  *     returns without synchronising.  Arguments are validated before any
  *     launch; a call that returns an error has written nothing.

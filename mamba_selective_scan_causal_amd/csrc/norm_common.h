@@ -226,9 +226,10 @@ inline int64_t most_parts(int64_t M, int threads) {
 
 // f(Shape) for groups of n channels, V to a vector: a quarter of a wave or a
 // wave where one vector a lane is enough, else a workgroup with one (two past
-// 1024 lanes).  One vector a lane keeps the backward passes at four waves or
-// more on a SIMD (the backward of gated_norm in bf16 takes about 100 registers
-// with one vector and over 200 with two).  False for wider groups.
+// 1024 lanes, up to 1536 vectors).  One vector a lane keeps the backward
+// passes at four waves or more on a SIMD (gated_norm's in bf16 takes 90
+// registers with one vector and 150 with two, add_norm's 127 and over 168).
+// False for wider groups.
 template <int V, typename F>
 bool by_width(int64_t n, F f) {
     const int64_t nv = (n + V - 1) / V;

@@ -5,6 +5,8 @@
 //
 // Bound by HBM: the forward reads x and the residual and writes s and y, the
 // backward reads s, dy, ds (and x) and writes dresidual and dx, each once.
+// M 32768 D 2560 bf16 with an fp32 stream: forward 181 us (5.5 TB/s), backward
+// with dscale 300 us (5.0 TB/s).
 // The outputs go through the cache: with the nontemporal hint the forward and
 // backward of M 32768 D 2560 in turn take 561 us, without it 538.
 #include "norm_common.h"
@@ -312,7 +314,8 @@ __global__ __launch_bounds__(kWide) void add_norm_bwd_wide_kernel(NormArgs q) {
     }
 }
 
-// One workgroup sums 32 channels: 32 lanes side by side, 32 rows at a time.
+// One workgroup sums 32 channels: 32 lanes side by side, 32 rows at a time, in
+// a fixed order.  4 to 7 us, most of it latency (512 rows of D 5120: 10 MB).
 __global__ __launch_bounds__(1024) void norm_params_kernel(NormArgs q, bool gated, int64_t rows,
                                                            int K) {
     __shared__ float lds[32][33];
