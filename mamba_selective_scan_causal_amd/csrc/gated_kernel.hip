@@ -140,14 +140,17 @@ struct Chain {
     Word* states;              // [tile][group][V][64]: the state entering a group
 };
 
-// The affine map h -> A h + H.  A = 0 drops what was carried whatever it is.
+// The affine map h -> A h + H.  A = 0 drops what was carried whatever it is:
+// rows on the other side of a reset may hold anything, NaN among it.
 struct Map {
     float A, H;
     __device__ __forceinline__ float operator()(float h) const {
         return A != 0.0f ? __builtin_fmaf(A, h, H) : H;
     }
     // this after first
-    __device__ __forceinline__ Map after(const Map& first) const { return {A * first.A, (*this)(first.H)}; }
+    __device__ __forceinline__ Map after(const Map& first) const {
+        return {A != 0.0f ? A * first.A : 0.0f, (*this)(first.H)};
+    }
 };
 
 __device__ __forceinline__ void put(Word* p, float lo, float hi) {
@@ -268,30 +271,54 @@ __device__ __forceinline__ unsigned reset_bits(const uint8_t* reset, int64_t row
         __builtin_amdgcn_ballot_w64(lane < S && t < L && reset[row0 + t] != 0));
 }
 
-// Steps past the end of the sequence carry the state as it is; a reset's
-// carry factor is 0.  Both are rare, and the same for all lanes.
+// Steps past the end of the sequence carry the state as it is.
 template <int S, int V>
-__device__ __forceinline__ void mend(float (&a)[S][V], float (&u)[S][V], int n, unsigned resets) {
-    if (n < S) {
+__device__ __forceinline__ void end_at(float (&a)[S][V], float (&u)[S][V], int n) {
+    if (n == S) return;
 #pragma unroll
-        for (int s = 0; s < S; s++)
+    for (int s = 0; s < S; s++)
 #pragma unroll
-            for (int v = 0; v < V; v++) {
-                a[s][v] = s < n ? a[s][v] : 1.0f;
-                u[s][v] = s < n ? u[s][v] : 0.0f;
+        for (int v = 0; v < V; v++) {
+            a[s][v] = s < n ? a[s][v] : 1.0f;
+            u[s][v] = s < n ? u[s][v] : 0.0f;
+        }
+}
+
+// A piece's map of the state, f, and (REVERSE) of the adjoint, w, in which
+// dy(s, v) enters at step s.  With resets (a branch that is the same for all
+// lanes and rarely taken) the steps on either side of one are kept apart by
+// selection, not by a factor 0.
+template <bool REVERSE, int S, int V, typename F>
+__device__ __forceinline__ void maps_of(const float (&a)[S][V], const float (&u)[S][V],
+                                        unsigned resets, Map (&f)[V], Map (&w)[V], F dy) {
+    auto run = [&](auto some) {
+        constexpr bool SOME = decltype(some)::value;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            f[v] = {1.0f, 0.0f};
+            w[v].H = 0.0f;
+#pragma unroll
+            for (int s = 0; s < S; s++) {
+                const bool drop = SOME && (resets >> s & 1);
+                f[v].A = drop ? 0.0f : f[v].A * a[s][v];
+                f[v].H = drop ? u[s][v] : __builtin_fmaf(a[s][v], f[v].H, u[s][v]);
+                // nothing from a reset on reaches what is before the piece
+                if constexpr (REVERSE)
+                    if (!SOME || !(resets & ((2u << s) - 1)))
+                        w[v].H = __builtin_fmaf(f[v].A, dy(s, v), w[v].H);
             }
-    }
-    if (resets) {
-#pragma unroll
-        for (int s = 0; s < S; s++)
-#pragma unroll
-            for (int v = 0; v < V; v++) a[s][v] = resets >> s & 1 ? 0.0f : a[s][v];
-    }
+            if (SOME && resets) f[v].A = 0.0f;
+            w[v].A = f[v].A;
+        }
+    };
+    if (resets)
+        run(std::true_type{});
+    else
+        run(std::false_type{});
 }
 
 // The states after each step in the place of the input terms, from the state
-// h that enters; h: the last.  Where a step resets, an infinite state goes no
-// further (0 times it would be NaN).
+// h that enters; h: the last.
 template <int S, int V>
 __device__ __forceinline__ void states(const float (&a)[S][V], float (&u)[S][V], float (&h)[V],
                                        unsigned resets) {
@@ -356,15 +383,10 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
     // flight in a wave, one more than can be counted (B1 L65536 D2560 bf16
     // decay: 399 us, here 316)
     if constexpr (Z) load_rows<S>(z, q.z, row, q.ld_z, n, at);
-    mend<S, V>(a, u, n, resets);
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        m[v] = {1.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < S; s++) {
-            m[v].A *= a[s][v];
-            m[v].H = __builtin_fmaf(a[s][v], m[v].H, u[s][v]);
-        }
+    end_at<S, V>(a, u, n);
+    {
+        Map none[V];
+        maps_of<false, S, V>(a, u, resets, m, none, 0);
     }
 #pragma unroll
     for (int v = 0; v < V; v++) own[wave][v][lane] = m[v];
@@ -506,7 +528,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
             if constexpr (GATE == MSS_GATE_DECAY) ei[s][v] = e.ei;
         }
     }
-    mend<S, V>(a, u, n, resets);
+    end_at<S, V>(a, u, n);
     if (n < S) {
 #pragma unroll
         for (int s = 0; s < S; s++)
@@ -514,22 +536,15 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
             for (int v = 0; v < V; v++)
                 if (s >= n) dout[s].set(v, 0.0f);
     }
+    maps_of<true, S, V>(a, u, resets, f, w, [&](int s, int v) {
+        const float dy = dout[s].get(v);
+        if constexpr (Z)
+            return dy * silu(z[s].get(v));
+        else
+            return dy;
+    });
 #pragma unroll
     for (int v = 0; v < V; v++) {
-        f[v] = {1.0f, 0.0f};
-        w[v].H = 0.0f;
-#pragma unroll
-        for (int s = 0; s < S; s++) {
-            float dy = dout[s].get(v);
-            if constexpr (Z) dy *= silu(z[s].get(v));
-            f[v].A *= a[s][v];
-            f[v].H = __builtin_fmaf(a[s][v], f[v].H, u[s][v]);
-            w[v].H = __builtin_fmaf(f[v].A, dy, w[v].H);
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        w[v].A = f[v].A;
         fwd[wave][v][lane] = f[v];
         rev[wave][v][lane] = w[v];
     }
@@ -629,7 +644,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
             float gx, gr, gi = 0.0f, ws = 0.0f;
             Gates<GATE>::grads(er[s][v], GATE == MSS_GATE_DECAY ? ei[s][v] : 0.0f, G, p, xv, k[v], gx,
                                gr, gi, ws);
-            Q[v] = a[s][v] * G;
+            Q[v] = drop ? 0.0f : a[s][v] * G;
             sum[v] += ws;
             dx.set(v, gx);
             dr.set(v, gr);

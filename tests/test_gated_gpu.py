@@ -137,6 +137,44 @@ def test_reset_as_bool_and_packed_documents_equal_separate_ones():
 
 
 @pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("z", (False, True))
+def test_nan_beyond_a_reset_stays_there(gate, z):
+    """Documents of NaN and infinities (padding that nobody filled) before, between and after real
+    ones, inside a piece of steps and across many chunks: the real ones' outputs and gradients are
+    those of each alone."""
+    import torch
+    rng = np.random.default_rng(21)
+    D, plan = 36, [(5, False), (3, True), (700, False), (130, True), (2, False), (64, False), (1, True), (9, False),
+                   (300, False), (21, True)]                     # (length, real?)
+    L = sum(n for n, _ in plan)
+    a = gated_inputs(rng, 1, L, D, gate, z=z, h0=False)
+    a["dout"] = rng.normal(size=(L, D))
+    a["reset"] = np.zeros(L, np.uint8)
+    starts = np.cumsum([0] + [n for n, _ in plan[:-1]])
+    a["reset"][starts] = 1
+    junk = np.concatenate([np.full(n, not real) for n, real in plan])
+    for k in ("x", "r", "i", "z", "dout"):
+        if a[k] is not None:
+            a[k][junk] = rng.choice([np.nan, np.inf, -np.inf], size=(junk.sum(), D))
+    for dtype in ("f32", "bf16"):
+        g, e = to_gpu(a, dtype)
+        kw = dict(batch=1, seq_len=L, gate=gate)
+        y, ck, hl = forward(g, kw, h_ckpt=True, h_last=True)
+        grads = backward(g, kw, ck, g["dout"])
+        torch.cuda.synchronize()
+        for s, (n, real) in zip(starts, plan):
+            if not real:
+                continue
+            part = {k: None if e[k] is None else e[k][s:s + n] for k in ("x", "r", "i", "z", "dout")}
+            val, tol = ref.gated_scan(**part, decay=e["decay"], batch=1, seq_len=n, gate=gate)
+            check(y[s:s + n], val["y"], tol["y"], dtype, f"y of {n} at {s}")
+            for k in ("dx", "dr", "di", "dz"):
+                if grads[k] is not None:
+                    check(grads[k][s:s + n], val[k], tol[k], dtype, f"{k} of {n} at {s}")
+        check(hl, val["h_last"], tol["h_last"], "f32", "h_last")
+
+
+@pytest.mark.parametrize("gate", GATES)
 @pytest.mark.parametrize("dtype", ("f32", "bf16"))
 def test_closed_and_open_gates(gate, dtype):
     """r of -inf, very negative and very positive: the state is dropped, or kept untouched, and
