@@ -16,11 +16,11 @@
 //   waits for the state entering its chunk, and only then steps through its
 //   registers a second time, now with the true state, and writes the outputs.
 //
-// The state entering chunk c is formed from the state entering the group of
-// kWaves chunks that c lies in, published by the last chunk of the group
+// The state entering chunk c is formed from the state entering the group of 8
+// (or 32) chunks that c lies in, published by the last chunk of the group
 // before, and the maps of the group's chunks before c, in that order: a
-// serial chain of one handover per kWaves chunks, and results that do not
-// depend on which workgroup runs when.
+// serial chain of one handover per group, and results that do not depend on
+// which workgroup runs when.
 //
 // Workgroups take their chunk from a counter, time first, so a workgroup waits
 // only for ones that have taken a lower number, and the lowest number that is
@@ -117,7 +117,7 @@ struct Gates {
     }
 };
 
-constexpr int kWaves = 8;                        // waves of a workgroup, chunks of a group
+constexpr int kWaves = 8;                        // waves of a workgroup
 // S of the forward.  Half of it leaves room for three workgroups on a CU
 // instead of two, and measures slower for the handovers it adds: 480 -> 568 us
 // on B4 L8192 D5120 fp32 with a gate, 59 -> 60 us on B8 L2048 D1536 bf16.
@@ -136,6 +136,7 @@ struct Chain {
     unsigned tiles, ctiles;    // B * ctiles tiles of 64 V channels
     int64_t chunks, groups;
     unsigned* ticket;
+    int per;                   // chunks of a group for each wave: a group is kWaves * per
     Word* maps;                // [tile][chunk][V][64]: (A, H)
     Word* states;              // [tile][group][V][64]: the state entering a group
 };
@@ -198,6 +199,26 @@ __device__ __forceinline__ unsigned take(const Chain& g, unsigned* lds) {
     if (threadIdx.x == 0) *lds = atomicAdd(g.ticket, 1u);
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(*lds);
+}
+
+// Waits for the maps of the group's chunks that this wave looks after, those of
+// [per wave, per (wave + 1)) that come before the group's `mate`-th, and leaves
+// their composition in `mates`.
+template <int V>
+__device__ __forceinline__ void meet(const Chain& g, Word* first, int wave, int mate, int lane,
+                                     Map (*mates)[V][64]) {
+    const int from = wave * g.per;
+    if (from >= mate) return;
+    const int to = from + g.per < mate ? from + g.per : mate;
+    Map all[V], e[V];
+    wait_for<V>(first + int64_t{from} * (64 * V) + lane, all);
+    for (int m = from + 1; m < to; m++) {
+        wait_for<V>(first + int64_t{m} * (64 * V) + lane, e);
+#pragma unroll
+        for (int v = 0; v < V; v++) all[v] = e[v].after(all[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; v++) mates[wave][v][lane] = all[v];
 }
 
 // V channels of one row; an odd row's last lane takes the last V channels, so
@@ -393,10 +414,10 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
     __syncthreads();
 
     float h[V];
-    const int mate = static_cast<int>(chunk % kWaves);
+    const int group = kWaves * g.per, mate = static_cast<int>(chunk % group);
     if (g.chunks > 1) {
         const int64_t first = chunk - mate, words = 64 * V;
-        if (wave == 0 && mate != kWaves - 1 && chunk + 1 < g.chunks) {
+        if (wave == 0 && mate != group - 1 && chunk + 1 < g.chunks) {
 #pragma unroll
             for (int v = 0; v < V; v++) {
                 Map all = own[0][v][lane];
@@ -405,16 +426,11 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
                 put(g.maps + (int64_t{tile} * g.chunks + chunk) * words + 64 * v + lane, all.A, all.H);
             }
         }
-        if (wave < mate) {
-            Map e[V];
-            wait_for<V>(g.maps + (int64_t{tile} * g.chunks + first + wave) * words + lane, e);
-#pragma unroll
-            for (int v = 0; v < V; v++) mates[wave][v][lane] = e[v];
-        }
+        meet<V>(g, g.maps + (int64_t{tile} * g.chunks + first) * words, wave, mate, lane, mates);
         if (wave == kWaves - 1) {
             Map e[V];
             if (first > 0)
-                wait_for<V>(g.states + (int64_t{tile} * g.groups + first / kWaves) * words + lane, e);
+                wait_for<V>(g.states + (int64_t{tile} * g.groups + first / group) * words + lane, e);
             else
 #pragma unroll
                 for (int v = 0; v < V; v++) e[v].H = q.h0 ? q.h0[int64_t{b} * q.D + c + v] : 0.0f;
@@ -424,7 +440,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
         __syncthreads();
 #pragma unroll
         for (int v = 0; v < V; v++) h[v] = entering[v][lane];
-        for (int w = 0; w < mate; w++)
+        for (int w = 0; w * g.per < mate; w++)
 #pragma unroll
             for (int v = 0; v < V; v++) h[v] = mates[w][v][lane](h[v]);
     } else {
@@ -434,10 +450,10 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
     for (int w = 0; w < wave; w++)
 #pragma unroll
         for (int v = 0; v < V; v++) h[v] = own[w][v][lane](h[v]);
-    if (wave == kWaves - 1 && mate == kWaves - 1 && chunk + 1 < g.chunks) {
+    if (wave == kWaves - 1 && mate == group - 1 && chunk + 1 < g.chunks) {
 #pragma unroll
         for (int v = 0; v < V; v++)
-            put(g.states + (int64_t{tile} * g.groups + chunk / kWaves + 1) * (64 * V) + 64 * v + lane, 0.0f,
+            put(g.states + (int64_t{tile} * g.groups + chunk / group + 1) * (64 * V) + 64 * v + lane, 0.0f,
                 m[v](h[v]));
     }
     if (q.h_ckpt && t0 % MSS_GATED_CKPT_STEPS == 0 && n > 0 && live) {
@@ -551,9 +567,9 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
     __syncthreads();
 
     float Q[V];
-    const int mate = static_cast<int>(turn % kWaves);
+    const int group = kWaves * g.per, mate = static_cast<int>(turn % group);
     const int64_t first = turn - mate, words = 64 * V;
-    if (wave == 0 && mate != kWaves - 1 && turn + 1 < g.chunks) {
+    if (wave == 0 && mate != group - 1 && turn + 1 < g.chunks) {
 #pragma unroll
         for (int v = 0; v < V; v++) {
             Map all = rev[kWaves - 1][v][lane];
@@ -562,16 +578,11 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
             put(g.maps + (int64_t{tile} * g.chunks + turn) * words + 64 * v + lane, all.A, all.H);
         }
     }
-    if (wave < mate) {
-        Map e[V];
-        wait_for<V>(g.maps + (int64_t{tile} * g.chunks + first + wave) * words + lane, e);
-#pragma unroll
-        for (int v = 0; v < V; v++) mates[wave][v][lane] = e[v];
-    }
+    meet<V>(g, g.maps + (int64_t{tile} * g.chunks + first) * words, wave, mate, lane, mates);
     if (wave == waves - 1) {
         Map e[V];
         if (first > 0)
-            wait_for<V>(g.states + (int64_t{tile} * g.groups + first / kWaves) * words + lane, e);
+            wait_for<V>(g.states + (int64_t{tile} * g.groups + first / group) * words + lane, e);
         else
 #pragma unroll
             for (int v = 0; v < V; v++) e[v].H = q.dh_last ? q.dh_last[int64_t{b} * q.D + c + v] : 0.0f;
@@ -581,16 +592,16 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; v++) Q[v] = entering[v][lane];
-    for (int p = 0; p < mate; p++)
+    for (int p = 0; p * g.per < mate; p++)
 #pragma unroll
         for (int v = 0; v < V; v++) Q[v] = mates[p][v][lane](Q[v]);
     for (int p = waves - 1; p > wave; p--)
 #pragma unroll
         for (int v = 0; v < V; v++) Q[v] = rev[p][v][lane](Q[v]);
-    if (wave == 0 && mate == kWaves - 1 && turn + 1 < g.chunks) {
+    if (wave == 0 && mate == group - 1 && turn + 1 < g.chunks) {
 #pragma unroll
         for (int v = 0; v < V; v++)
-            put(g.states + (int64_t{tile} * g.groups + turn / kWaves + 1) * words + 64 * v + lane, 0.0f,
+            put(g.states + (int64_t{tile} * g.groups + turn / group + 1) * words + 64 * v + lane, 0.0f,
                 w[v](Q[v]));
     }
     for (int p = 0; p < wave; p++)
@@ -795,7 +806,13 @@ Chain chain_of(const GatedArgs& a, int V, int64_t len) {
     g.ctiles = static_cast<unsigned>(cdiv(a.D, 64 * V));
     g.tiles = static_cast<unsigned>(a.B * g.ctiles);
     g.chunks = cdiv(a.L, len);
-    g.groups = cdiv(g.chunks, kWaves);
+    // With few tiles the handovers between groups are what takes the time, and
+    // groups of 32 chunks have a quarter of them; with many, the words that a
+    // chunk then reads cost more.  Forward and backward in bf16, groups of 8 /
+    // of 32: 2 tiles L12294 72.8 / 39.8 us, 8 tiles L65536 408 / 390, 12 tiles
+    // L4096 67.9 / 65.8, 16 tiles L8192 75.4 / 80.2, 20 tiles L16384 251 / 260.
+    g.per = g.tiles <= 12 ? 4 : 1;
+    g.groups = cdiv(g.chunks, kWaves * g.per);
     g.ticket = static_cast<unsigned*>(a.ws);
     g.maps = static_cast<Word*>(a.ws) + 32;
     g.states = g.maps + int64_t{g.tiles} * g.chunks * 64 * V;
