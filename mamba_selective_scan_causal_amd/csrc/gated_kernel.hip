@@ -134,8 +134,9 @@ constexpr Word kUnset = ~0ull;
 // What a launch's workgroups share (chain: chunks > 1).
 struct Chain {
     unsigned tiles, ctiles;    // B * ctiles tiles of 64 V channels
+    unsigned sets, each;       // 1 or 8 sets of `each` neighbouring tiles
     int64_t chunks, groups;
-    unsigned* ticket;
+    unsigned* ticket;          // a counter per set, 8 words apart
     int per;                   // chunks of a group for each wave: a group is kWaves * per
     Word* maps;                // [tile][chunk][V][64]: (A, H)
     Word* states;              // [tile][group][V][64]: the state entering a group
@@ -193,12 +194,23 @@ __global__ __launch_bounds__(256) void gated_unset_kernel(ulonglong2* ws, int64_
         ws[i] = i < 16 ? make_ulonglong2(0, 0) : make_ulonglong2(kUnset, kUnset);
 }
 
-// The number of this workgroup's piece of work.
-__device__ __forceinline__ unsigned take(const Chain& g, unsigned* lds) {
-    if (g.chunks == 1) return blockIdx.x;
-    if (threadIdx.x == 0) *lds = atomicAdd(g.ticket, 1u);
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(*lds);
+// This workgroup's turn (the chunk, or in the backward its distance from the
+// last) and tile.  Workgroup i works for set i % sets, which with eight sets
+// puts a set on one XCD, where neighbouring tiles that share cache lines meet in
+// one L2.  A set counts its own workgroups, so each waits only for some of its
+// set that started before it.
+__device__ __forceinline__ unsigned take(const Chain& g, unsigned* lds, unsigned& tile) {
+    const unsigned set = blockIdx.x & (g.sets - 1);   // 1 or 8 sets
+    unsigned n = g.sets == 1 ? blockIdx.x : blockIdx.x >> 3;
+    if (g.chunks > 1) {
+        if (threadIdx.x == 0) *lds = atomicAdd(g.ticket + 8 * set, 1u);
+        __syncthreads();
+        n = *lds;
+    }
+    n = __builtin_amdgcn_readfirstlane(n);
+    const unsigned turn = n / g.each;
+    tile = __builtin_amdgcn_readfirstlane(set * g.each + n - turn * g.each);
+    return __builtin_amdgcn_readfirstlane(turn);
 }
 
 // Waits for the maps of the group's chunks that this wave looks after, those of
@@ -365,9 +377,8 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
     __shared__ unsigned ticket;
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const unsigned id = take(g, &ticket);
-    const unsigned tile = id % g.tiles;
-    const int64_t chunk = id / g.tiles;
+    unsigned tile;
+    const int64_t chunk = take(g, &ticket, tile);
     const unsigned b = tile / g.ctiles;
     unsigned c = tile % g.ctiles * (64 * V) + lane * V;
     const bool live = c < q.D;
@@ -501,9 +512,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int waves = blockDim.x / 64;   // kWaves, or fewer where they hold all steps
-    const unsigned id = take(g, &ticket);
-    const unsigned tile = id % g.tiles;
-    const int64_t turn = id / g.tiles;   // turn 0: the last chunk
+    unsigned tile;
+    const int64_t turn = take(g, &ticket, tile);   // 0: the last chunk
     const int64_t chunk = g.chunks - 1 - turn;
     const unsigned b = tile / g.ctiles;
     unsigned c = tile % g.ctiles * (64 * V) + lane * V;
@@ -805,6 +815,17 @@ Chain chain_of(const GatedArgs& a, int V, int64_t len) {
     Chain g;
     g.ctiles = static_cast<unsigned>(cdiv(a.D, 64 * V));
     g.tiles = static_cast<unsigned>(a.B * g.ctiles);
+    // Sets of tiles that stay on an XCD read the lines that neighbouring tiles
+    // share once, but move the XCDs' places in the tensors apart, which costs
+    // more the wider the rows are.  Forward and backward, without / with sets:
+    // fp32 64 tiles 71 / 59 us, 256 tiles 398 / 385, 320 tiles 936 / 963, but
+    // 320 and 1024 tiles of rows that start inside a 128-byte line 620 / 581
+    // and 633 / 540; bf16 decay 64 tiles 199 / 192, 96 tiles 156 / 147, 128
+    // tiles 641 / 680.  Only equal sets, so that the XCDs end together.
+    const bool off_line = a.dtype == MSS_F32 && (a.ld_x | a.ld_r | a.ld_y) % 32 != 0;
+    const unsigned most = off_line ? UINT32_MAX : a.dtype == MSS_F32 ? 288 : 112;
+    g.sets = g.tiles % 8 == 0 && g.tiles >= 64 && g.tiles <= most ? 8 : 1;
+    g.each = g.tiles / g.sets;
     g.chunks = cdiv(a.L, len);
     // With few tiles the handovers between groups are what takes the time, and
     // groups of 32 chunks have a quarter of them; with many, the words that a
@@ -819,7 +840,7 @@ Chain chain_of(const GatedArgs& a, int V, int64_t len) {
     return g;
 }
 
-// Marks the words of a chain as not written and zeroes its counter.
+// Marks the words of a chain as not written and zeroes its counters.
 hipError_t unset(const Chain& g, int V, hipStream_t st) {
     if (g.chunks == 1) return hipSuccess;
     const int64_t n = 32 + g.tiles * (g.chunks + g.groups) * 64 * V;

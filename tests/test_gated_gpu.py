@@ -96,6 +96,17 @@ def test_batch_and_width_past_one_wave_of_blocks():
     run_case(3, 300, 2000, "decay", "bf16", z=False, h0=False, reset=True)
 
 
+# tiles of 64 (fp32) or 128 channels: counts around 64, multiples of eight and
+# others, rows that start inside a cache line, where the tiles of a launch are
+# kept together by eighths
+@pytest.mark.parametrize("B,L,D,dtype", [(4, 300, 1000, "f32"), (4, 300, 1024, "f32"), (4, 150, 1473, "f32"),
+                                         (1, 129, 4097, "f32"), (8, 40, 2303, "f32"), (8, 100, 2560, "f32"),
+                                         (4, 300, 2047, "bf16"), (4, 300, 2048, "bf16"), (7, 140, 2045, "f16"),
+                                         (7, 20, 2048, "bf16"), (8, 140, 2048, "bf16")])
+def test_many_tiles(B, L, D, dtype):
+    run_case(B, L, D, "sigmoid" if D % 2 else "decay", dtype, z=D % 3 == 0, h0=True, reset=L != 300)
+
+
 @pytest.mark.parametrize("gate", GATES)
 def test_every_step_reset(gate):
     """Nothing is ever carried: h = v, dh0 = 0, and what h0 holds does not matter."""
