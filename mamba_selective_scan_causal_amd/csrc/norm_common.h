@@ -215,12 +215,13 @@ inline int64_t row_groups(int64_t M, int64_t G, int threads, int rows, int64_t m
 }
 
 // The backward's workgroups each write a row of partial sums: at most 1024,
-// and with few rows of input one for every eight of them, but four waves for
-// each CU.
+// and with few rows of input one for every four of them, but four waves for
+// each CU (one for every eight, forward and backward, bf16: gated_norm M 1024
+// D 5120 32.9 us, like this 25.8; add_norm M 1024 D 2560 23.4 and 20.8).
 constexpr int64_t kMostParts = 1024;
 inline int64_t most_parts(int64_t M, int threads) {
     int64_t most = 256 * 4 * 64 / threads;
-    if (most < M / 8) most = M / 8;
+    if (most < M / 4) most = M / 4;
     return most < kMostParts ? most : kMostParts;
 }
 
