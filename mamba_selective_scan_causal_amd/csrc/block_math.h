@@ -9,6 +9,33 @@ namespace mss {
 using bf16 = __bf16;
 using f16 = _Float16;
 
+// How a row ends: with a whole vector (kWhole), with a partial one that is read
+// as the V channels up to the row's end (kTail, rows of V channels or more), or
+// with one that goes element by element (kEdge).
+enum Ends { kWhole, kTail, kEdge };
+
+// Where a lane's vector starts in a row, and how many of its first channels are
+// another lane's.
+template <Ends ENDS>
+struct Spot {
+    int at;
+    static constexpr int lo = 0;
+};
+template <>
+struct Spot<kTail> {
+    int at, lo;
+};
+
+// Vector v of a row of n channels.
+template <int V, Ends ENDS>
+__device__ __forceinline__ Spot<ENDS> spot(int v, int n) {
+    const int c = V * v;
+    if constexpr (ENDS == kTail)
+        return c < n && c + V > n ? Spot<kTail>{n - V, c + V - n} : Spot<kTail>{c, 0};
+    else
+        return {c};
+}
+
 // V channels as memory holds them.
 template <typename T, int V>
 struct RowVec {
@@ -37,6 +64,34 @@ struct RowVec {
             for (int e = 0; e < V; e++)
                 if (c + e < n) p[c + e] = t[e];
         }
+    }
+    // The same by spots.  In kTail no lane goes element by element when it
+    // reads (2-byte elements would have to arrive before they are packed, and
+    // hold up the loads behind them).
+    template <Ends ENDS>
+    __device__ __forceinline__ void load(const T* p, Spot<ENDS> s, int n) {
+        if constexpr (ENDS == kEdge)
+            load(p, s.at, n);
+        else
+            t = *reinterpret_cast<const type*>(p + s.at);
+    }
+    template <bool STREAM, Ends ENDS>
+    __device__ __forceinline__ void store(T* p, Spot<ENDS> s, int n) const {
+        if constexpr (ENDS == kEdge) {
+            store<STREAM>(p, s.at, n);
+        } else if (s.lo == 0) {
+            store<STREAM>(p + s.at, 0, V);
+        } else {
+#pragma unroll
+            for (int e = 1; e < V; e++)
+                if (e >= s.lo) p[s.at + e] = t[e];
+        }
+    }
+    // Zeroes the channels that are another lane's.
+    template <Ends ENDS>
+    __device__ __forceinline__ void clear(Spot<ENDS> s) {
+#pragma unroll
+        for (int e = 0; e < V; e++) t[e] = e >= s.lo ? t[e] : static_cast<T>(0.0f);
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll

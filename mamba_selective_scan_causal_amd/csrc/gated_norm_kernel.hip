@@ -24,22 +24,23 @@ __device__ __forceinline__ Place place(const NormArgs& q) {
     return {g * (q.D / q.G), p * rows + team, gridDim.x / q.G * rows};
 }
 
-template <typename T, int TEAM, int NC, bool before, bool layer>
+template <typename T, int TEAM, int NC, Ends ENDS, bool before, bool layer>
 __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(NormArgs q) {
     constexpr int V = kVec<T>;
     __shared__ float lds[kSumLds<TEAM>];
-    const int n = static_cast<int>(q.D / q.G), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
+    const int n = static_cast<int>(q.D / q.G);
+    const Spots<V, NC, ENDS> spots(team_lane<TEAM>(), team_lanes<TEAM>(), n);
     const float inv_n = 1.0f / static_cast<float>(n);
     const Place at = place<TEAM>(q);
     // k (norm w + b) with k = alpha scale folded into w and b
     float w[NC][V], b[NC][V];
 #pragma unroll
     for (int j = 0; j < NC; j++) {
-        const int c = V * (lane + j * lanes);
+        const auto c = spots.s[j];
         float k[V];
-        load_param<V>(q.w + at.g0, c, n, 1.0f, w[j]);
-        load_param<V>(q.b ? q.b + at.g0 : nullptr, c, n, 0.0f, b[j]);
-        load_param<V>(q.scale ? q.scale + at.g0 : nullptr, c, n, 1.0f, k);
+        load_param(q.w + at.g0, c, n, 1.0f, w[j]);
+        load_param(q.b ? q.b + at.g0 : nullptr, c, n, 0.0f, b[j]);
+        load_param(q.scale ? q.scale + at.g0 : nullptr, c, n, 1.0f, k);
 #pragma unroll
         for (int e = 0; e < V; e++) {
             w[j][e] *= q.alpha * k[e];
@@ -52,8 +53,8 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
     auto read = [&](int64_t m, Row& r) {
 #pragma unroll
         for (int j = 0; j < NC; j++) {
-            const int c = V * (lane + j * lanes);
-            if (c < n && m < q.M) {
+            const auto c = spots.s[j];
+            if (c.at < n && m < q.M) {
                 r.x[j].load(row_of<T>(q.x, m, q.ld_x, at.g0), c, n);
                 if (q.z) r.z[j].load(row_of<T>(q.z, m, q.ld_z, at.g0), c, n);
                 if (q.res) r.res[j].load(row_of<T>(q.res, m, q.ld_res, at.g0), c, n);
@@ -72,8 +73,12 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
     clear_sums<TEAM>(lds);
     read(m, next);
     for (; m < q.M; m += at.step) {
-        const Row r = next;
+        Row r = next;
         read(m + at.step, next);
+        if (spots.shared) {
+#pragma unroll
+            for (int j = 0; j < NC; j++) r.x[j].clear(spots.s[j]);
+        }
         float v[NC][V];
         float mean = 0.0f;
         float sum[1] = {0.0f};
@@ -96,14 +101,14 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
             for (int e = 0; e < V; e++) {
                 // (past the end an RMS norm's v is 0 already)
                 if constexpr (layer)
-                    v[j][e] = V * (lane + j * lanes) + e < n ? v[j][e] - mean : 0.0f;
+                    v[j][e] = spots.own(j, e, n) ? v[j][e] - mean : 0.0f;
                 sum[0] = __builtin_fmaf(v[j][e], v[j][e], sum[0]);
             }
         team_sum<TEAM>(sum, lds, turn);
         const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], inv_n, q.eps));
 #pragma unroll
         for (int j = 0; j < NC; j++) {
-            const int c = V * (lane + j * lanes);
+            const auto c = spots.s[j];
             RowVec<T, V> y;
 #pragma unroll
             for (int e = 0; e < V; e++) {
@@ -116,28 +121,29 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
             }
 #pragma unroll
             for (int e = 0; e < V; e++) y.set(e, v[j][e]);
-            if (c < n) y.template store<true>(row_of<T>(q.y, m, q.ld_y, at.g0), c, n);
+            if (c.at < n) y.template store<true>(row_of<T>(q.y, m, q.ld_y, at.g0), c, n);
         }
     }
 }
 
 // EXTRA: the sum of the gradients alone is wanted too (for db, and for dscale
 // where there is a bias).
-template <typename T, int TEAM, int NC, bool before, bool layer, bool EXTRA>
+template <typename T, int TEAM, int NC, Ends ENDS, bool before, bool layer, bool EXTRA>
 __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel(NormArgs q) {
     constexpr int V = kVec<T>, K = EXTRA ? 2 : 1;
     __shared__ float lds[kSumLds<TEAM>];
     __shared__ float part_lds[kPartLds<TEAM, NC, V>];
-    const int n = static_cast<int>(q.D / q.G), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
+    const int n = static_cast<int>(q.D / q.G);
+    const Spots<V, NC, ENDS> spots(team_lane<TEAM>(), team_lanes<TEAM>(), n);
     const float inv_n = 1.0f / static_cast<float>(n);
     const Place at = place<TEAM>(q);
     float w[NC][V], acc[K][NC][V];   // w: k w, k = alpha scale
 #pragma unroll
     for (int j = 0; j < NC; j++) {
-        const int c = V * (lane + j * lanes);
+        const auto c = spots.s[j];
         float k[V];
-        load_param<V>(q.w + at.g0, c, n, 1.0f, w[j]);
-        load_param<V>(q.scale ? q.scale + at.g0 : nullptr, c, n, 1.0f, k);
+        load_param(q.w + at.g0, c, n, 1.0f, w[j]);
+        load_param(q.scale ? q.scale + at.g0 : nullptr, c, n, 1.0f, k);
 #pragma unroll
         for (int e = 0; e < V; e++) {
             w[j][e] *= q.alpha * k[e];
@@ -151,8 +157,8 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
     auto read = [&](int64_t m, Row& r) {
 #pragma unroll
         for (int j = 0; j < NC; j++) {
-            const int c = V * (lane + j * lanes);
-            if (c < n && m < q.M) {
+            const auto c = spots.s[j];
+            if (c.at < n && m < q.M) {
                 r.x[j].load(row_of<T>(q.x, m, q.ld_x, at.g0), c, n);
                 if (q.z) r.z[j].load(row_of<T>(q.z, m, q.ld_z, at.g0), c, n);
                 r.d[j].load(row_of<T>(q.dy, m, q.ld_y, at.g0), c, n);
@@ -173,6 +179,13 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
     for (; m < q.M; m += at.step) {
         Row r = next;
         read(m + at.step, next);
+        if (spots.shared) {
+#pragma unroll
+            for (int j = 0; j < NC; j++) {
+                r.x[j].clear(spots.s[j]);
+                r.d[j].clear(spots.s[j]);
+            }
+        }
         // the gate's sigma(z), kept between the two halves of the row's work
         float sig[NC][V];
 #pragma unroll
@@ -207,7 +220,7 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
 #pragma unroll
             for (int e = 0; e < V; e++) {
                 float v = normed(j, e);
-                if constexpr (layer) v = V * (lane + j * lanes) + e < n ? v - mean : 0.0f;
+                if constexpr (layer) v = spots.own(j, e, n) ? v - mean : 0.0f;
                 const float gw = grad(j, e) * w[j][e];
                 sums[0] = __builtin_fmaf(v, v, sums[0]);
                 sums[1] = __builtin_fmaf(gw, v, sums[1]);
@@ -225,12 +238,12 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
         const float c2 = layer ? sums[S - 1] * inv_n : 0.0f;
 #pragma unroll
         for (int j = 0; j < NC; j++) {
-            const int c = V * (lane + j * lanes);
+            const auto c = spots.s[j];
             RowVec<T, V> dx, dz;
             float kb[V], ks[V];
             if (!before && q.z) {   // k b, which enters dz
-                load_param<V>(q.b ? q.b + at.g0 : nullptr, c, n, 0.0f, kb);
-                load_param<V>(q.scale ? q.scale + at.g0 : nullptr, c, n, 1.0f, ks);
+                load_param(q.b ? q.b + at.g0 : nullptr, c, n, 0.0f, kb);
+                load_param(q.scale ? q.scale + at.g0 : nullptr, c, n, 1.0f, ks);
             }
 #pragma unroll
             for (int e = 0; e < V; e++) {
@@ -249,15 +262,15 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
                                                                            q.alpha * ks[e] * kb[e])));
                 }
             }
-            if (c < n) {
+            if (c.at < n) {
                 dx.template store<true>(row_of<T>(q.dx, m, q.ld_dx, at.g0), c, n);
                 if (q.z) dz.template store<true>(row_of<T>(q.dz, m, q.ld_dz, at.g0), c, n);
             }
         }
     }
-    write_part<TEAM, NC, V, K>(acc, part_lds,
+    write_part<TEAM, NC, V, K, ENDS>(acc, part_lds,
                                static_cast<float*>(q.ws) + blockIdx.x / q.G * K * q.D, q.D, at.g0,
-                               n);
+                               n, spots);
 }
 
 // ---- groups too wide for the registers -------------------------------------------
@@ -393,9 +406,9 @@ void by_kind(const NormArgs& a, F f) {
 hipError_t launch_gated_norm(const NormArgs& a, hipStream_t st) {
     return dispatch(a, [&](auto t) {
         using T = decltype(t);
-        const bool held = by_width<kVec<T>>(a.D / a.G, [&](auto s) {
+        const bool held = by_width<T>(a.D / a.G, [&](auto s) {
             by_kind(a, [&](auto before, auto layer) {
-                constexpr auto kernel = gated_norm_kernel<T, s.TEAM, s.NC, before.value, layer.value>;
+                constexpr auto kernel = gated_norm_kernel<T, s.TEAM, s.NC, s.ENDS, before.value, layer.value>;
                 const auto grid = a.G * row_groups<kernel>(a.M, a.G, s.threads, s.rows);
                 kernel<<<static_cast<unsigned>(grid), s.threads, 0, st>>>(a);
             });
@@ -414,10 +427,10 @@ hipError_t launch_gated_norm_bwd(const NormArgs& a, hipStream_t st) {
     int K = extra ? 2 : 1;
     const hipError_t e = dispatch(a, [&](auto t) {
         using T = decltype(t);
-        const bool held = by_width<kVec<T>>(a.D / a.G, [&](auto s) {
+        const bool held = by_width<T>(a.D / a.G, [&](auto s) {
             by_kind(a, [&](auto before, auto layer) {
                 auto go = [&](auto more) {
-                    constexpr auto kernel = gated_norm_bwd_kernel<T, s.TEAM, s.NC, before.value,
+                    constexpr auto kernel = gated_norm_bwd_kernel<T, s.TEAM, s.NC, s.ENDS, before.value,
                                                                   layer.value, more.value>;
                     rows = row_groups<kernel>(a.M, a.G, s.threads, s.rows,
                                               most_parts(a.M, s.threads));

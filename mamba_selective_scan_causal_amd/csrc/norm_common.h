@@ -10,8 +10,9 @@
 // variance is that of the centred values) are all the lanes exchange.
 // Vectors are read and written with the element's alignment (global memory
 // takes unaligned vector accesses), so strided rows and odd widths run the
-// same code and give the same bits; only a row's last, partial vector goes
-// element by element.  A team walks several rows, reading the next one while
+// same code and give the same bits.  A row's last, partial vector is read as
+// the V channels up to the row's end, those of the lane before it set to 0, and
+// written element by element.  A team walks several rows, reading the next one while
 // it works on this one; the per-channel parameters are read once, and the
 // backward keeps its sums of the parameter gradients in registers.
 #pragma once
@@ -30,15 +31,36 @@ template <typename T>
 constexpr int kVec = sizeof(T) == 4 ? 4 : 8;
 
 // A per-channel parameter, or `otherwise` where it is not given; 0 past the end.
-template <int V>
-__device__ __forceinline__ void load_param(const float* p, int c, int n, float otherwise,
+template <int V, Ends ENDS>
+__device__ __forceinline__ void load_param(const float* p, Spot<ENDS> s, int n, float otherwise,
                                            float (&v)[V]) {
     RowVec<float, V> t;
     t.zero();
-    if (p && c < n) t.load(p, c, n);
+    if (p && s.at < n) t.load(p, s, n);
 #pragma unroll
-    for (int e = 0; e < V; e++) v[e] = p ? t[e] : c + e < n ? otherwise : 0.0f;
+    for (int e = 0; e < V; e++) v[e] = p ? t[e] : s.at + (ENDS == kEdge ? e : 0) < n ? otherwise : 0.0f;
 }
+
+// The spots of a lane's vectors, and whether one of the wave's is shared.
+template <int V, int NC, Ends ENDS>
+struct Spots {
+    Spot<ENDS> s[NC];
+    bool shared = false;
+    __device__ __forceinline__ Spots(int lane, int lanes, int n) {
+#pragma unroll
+        for (int j = 0; j < NC; j++) s[j] = spot<V, ENDS>(lane + j * lanes, n);
+        if constexpr (ENDS == kTail) {
+            bool p = false;
+#pragma unroll
+            for (int j = 0; j < NC; j++) p |= s[j].lo > 0;
+            shared = __builtin_amdgcn_ballot_w64(p) != 0;
+        }
+    }
+    // The lane's own channel of the row?
+    __device__ __forceinline__ bool own(int j, int e, int n) const {
+        return e >= s[j].lo && s[j].at + (ENDS == kEdge ? e : 0) < n;
+    }
+};
 
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {
@@ -121,21 +143,20 @@ __device__ __forceinline__ void clear_sums(float* lds) {
 // The workgroup's share of K sums per channel, in the row of the workspace
 // that is its own: acc[k] of its teams added in order through `lds`.  Every
 // thread of the workgroup calls it.
-template <int TEAM, int NC, int V, int K>
+template <int TEAM, int NC, int V, int K, Ends ENDS>
 __device__ __forceinline__ void write_part(float (&acc)[K][NC][V], float* lds, float* part,
-                                           int64_t D, int64_t g0, int n) {
-    const int lane = team_lane<TEAM>();
+                                           int64_t D, int64_t g0, int n,
+                                           const Spots<V, NC, ENDS>& spots) {
 #pragma unroll
     for (int k = 0; k < K; k++) {
         float* out = part + k * D + g0;
         if constexpr (TEAM == kGroup) {
 #pragma unroll
             for (int j = 0; j < NC; j++) {
-                const int c = V * (lane + j * blockDim.x);
                 RowVec<float, V> t;
 #pragma unroll
                 for (int e = 0; e < V; e++) t.set(e, acc[k][j][e]);
-                if (c < n) t.template store<false>(out, c, n);
+                if (spots.s[j].at < n) t.template store<false>(out, spots.s[j], n);
             }
         } else {
             constexpr int slots = TEAM * NC * V, teams = 256 / (TEAM ? TEAM : 1);
@@ -144,7 +165,8 @@ __device__ __forceinline__ void write_part(float (&acc)[K][NC][V], float* lds, f
             for (int j = 0; j < NC; j++)
 #pragma unroll
                 for (int e = 0; e < V; e++)
-                    lds[team_of<TEAM>() * slots + V * (lane + j * TEAM) + e] = acc[k][j][e];
+                    if (e >= spots.s[j].lo)
+                        lds[team_of<TEAM>() * slots + spots.s[j].at + e] = acc[k][j][e];
             __syncthreads();
             for (int c = threadIdx.x; c < n; c += 256) {
                 float s = 0.0f;
@@ -173,11 +195,12 @@ hipError_t launch_norm_params(const NormArgs& a, bool gated, int64_t rows, int K
 
 // ---- sizes -------------------------------------------------------------------
 
-// A launch: the team, its workgroup's threads, and the rows that a workgroup
-// takes at a time.
-template <int TEAM_, int NC_>
+// A launch: the team, how rows end, its workgroup's threads, and the rows that
+// a workgroup takes at a time.
+template <int TEAM_, int NC_, Ends ENDS_>
 struct Shape {
     static constexpr int TEAM = TEAM_, NC = NC_;
+    static constexpr Ends ENDS = ENDS_;
     int threads, rows;
 };
 
@@ -231,20 +254,32 @@ inline int64_t most_parts(int64_t M, int threads) {
 // passes at four waves or more on a SIMD (gated_norm's in bf16 takes 90
 // registers with one vector and 150 with two, add_norm's 127 and over 168).
 // False for wider groups.
-template <int V, typename F>
+template <int V, Ends ENDS, typename F>
 bool by_width(int64_t n, F f) {
     const int64_t nv = (n + V - 1) / V;
     if (nv <= 16)
-        f(Shape<16, 1>{256, 16});
+        f(Shape<16, 1, ENDS>{256, 16});
     else if (nv <= 64)
-        f(Shape<64, 1>{256, 4});
+        f(Shape<64, 1, ENDS>{256, 4});
     else if (nv <= 1024)
-        f(Shape<kGroup, 1>{static_cast<int>((nv + 63) / 64 * 64), 1});
+        f(Shape<kGroup, 1, ENDS>{static_cast<int>((nv + 63) / 64 * 64), 1});
     else if (nv <= 1536)
-        f(Shape<kGroup, 2>{static_cast<int>((nv + 127) / 128 * 64), 1});
+        f(Shape<kGroup, 2, ENDS>{static_cast<int>((nv + 127) / 128 * 64), 1});
     else
         return false;
     return true;
+}
+template <typename T, typename F>
+bool by_width(int64_t n, F f) {
+    constexpr int V = kVec<T>;
+    if (n % V == 0) return by_width<V, kWhole>(n, f);
+    if constexpr (sizeof(T) == 4) {
+        return by_width<V, kEdge>(n, f);
+    } else {
+        if (n >= V) return by_width<V, kTail>(n, f);
+        f(Shape<16, 1, kEdge>{256, 16});
+        return true;
+    }
 }
 
 // Threads of a kernel's largest workgroup.

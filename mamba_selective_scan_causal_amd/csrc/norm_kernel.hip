@@ -32,11 +32,12 @@ struct AddRow {
     RowVec<T, V> x[NC], dy[NC];
 };
 
-template <typename T, typename R, int TEAM, int NC>
+template <typename T, typename R, int TEAM, int NC, Ends ENDS>
 __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormArgs q) {
     constexpr int V = kVec<T>;
     __shared__ float lds[kSumLds<TEAM>];
-    const int n = static_cast<int>(q.D), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
+    const int n = static_cast<int>(q.D), lanes = team_lanes<TEAM>();
+    const Spots<V, NC, ENDS> spots(team_lane<TEAM>(), lanes, n);
     const bool layer = q.kind == MSS_NORM_LAYER;
     const float inv_n = 1.0f / static_cast<float>(n);
     const int rows = TEAM == kGroup ? 1 : 256 / lanes;
@@ -44,18 +45,18 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormA
     float w[NC][V], b[NC][V], k[NC][V];
 #pragma unroll
     for (int j = 0; j < NC; j++) {
-        const int c = V * (lane + j * lanes);
-        load_param<V>(q.w, c, n, 1.0f, w[j]);
-        load_param<V>(q.b, c, n, 0.0f, b[j]);
-        load_param<V>(q.scale, c, n, 1.0f, k[j]);
+        const auto c = spots.s[j];
+        load_param(q.w, c, n, 1.0f, w[j]);
+        load_param(q.b, c, n, 0.0f, b[j]);
+        load_param(q.scale, c, n, 1.0f, k[j]);
 #pragma unroll
         for (int e = 0; e < V; e++) k[j][e] *= q.alpha;
     }
     auto read = [&](int64_t m, RowVec<R, V>(&res)[NC], RowVec<T, V>(&x)[NC]) {
 #pragma unroll
         for (int j = 0; j < NC; j++) {
-            const int c = V * (lane + j * lanes);
-            if (c < n && m < q.M) {
+            const auto c = spots.s[j];
+            if (c.at < n && m < q.M) {
                 if (q.res) res[j].load(row_of<R>(q.res, m, q.ld_res), c, n);
                 x[j].load(row_of<T>(q.x, m, q.ld_x), c, n);
             }
@@ -74,13 +75,20 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormA
     clear_sums<TEAM>(lds);
     read(m, res, x);
     for (; m < q.M; m += step) {
+        if (spots.shared) {
+#pragma unroll
+            for (int j = 0; j < NC; j++) {
+                res[j].clear(spots.s[j]);
+                x[j].clear(spots.s[j]);
+            }
+        }
         RowVec<R, V> s[NC];
 #pragma unroll
         for (int j = 0; j < NC; j++) {
-            const int c = V * (lane + j * lanes);
+            const auto c = spots.s[j];
 #pragma unroll
             for (int e = 0; e < V; e++) s[j].set(e, scaled_sum(res[j][e], k[j][e], x[j][e]));
-            if (c < n) s[j].template store<false>(row_of<R>(q.s, m, q.ld_s), c, n);
+            if (c.at < n) s[j].template store<false>(row_of<R>(q.s, m, q.ld_s), c, n);
         }
         // the next row; this one has been read, so s may be the residual
         read(m + step, res, x);
@@ -99,30 +107,31 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_kernel(NormA
         for (int j = 0; j < NC; j++)
 #pragma unroll
             for (int e = 0; e < V; e++) {
-                const float v = V * (lane + j * lanes) + e < n ? s[j][e] - mean : 0.0f;
+                const float v = spots.own(j, e, n) ? s[j][e] - mean : 0.0f;
                 sum[0] = __builtin_fmaf(v, v, sum[0]);
             }
         team_sum<TEAM>(sum, lds, turn);
         const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(sum[0], inv_n, q.eps));
 #pragma unroll
         for (int j = 0; j < NC; j++) {
-            const int c = V * (lane + j * lanes);
+            const auto c = spots.s[j];
             RowVec<T, V> y;
 #pragma unroll
             for (int e = 0; e < V; e++)
                 y.set(e, __builtin_fmaf((s[j][e] - mean) * rstd, w[j][e], b[j][e]));
-            if (c < n) y.template store<false>(row_of<T>(q.y, m, q.ld_y), c, n);
+            if (c.at < n) y.template store<false>(row_of<T>(q.y, m, q.ld_y), c, n);
         }
     }
 }
 
 // EXTRA: db or dscale is wanted besides dw.
-template <typename T, typename R, int TEAM, int NC, bool EXTRA>
+template <typename T, typename R, int TEAM, int NC, Ends ENDS, bool EXTRA>
 __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(NormArgs q) {
     constexpr int V = kVec<T>, K = EXTRA ? 3 : 1;
     __shared__ float lds[kSumLds<TEAM>];
     __shared__ float part_lds[kPartLds<TEAM, NC, V>];
-    const int n = static_cast<int>(q.D), lane = team_lane<TEAM>(), lanes = team_lanes<TEAM>();
+    const int n = static_cast<int>(q.D), lanes = team_lanes<TEAM>();
+    const Spots<V, NC, ENDS> spots(team_lane<TEAM>(), lanes, n);
     const bool layer = q.kind == MSS_NORM_LAYER;
     const float inv_n = 1.0f / static_cast<float>(n);
     const int rows = TEAM == kGroup ? 1 : 256 / lanes;
@@ -130,9 +139,9 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(N
     float w[NC][V], k[NC][V], acc[K][NC][V];
 #pragma unroll
     for (int j = 0; j < NC; j++) {
-        const int c = V * (lane + j * lanes);
-        load_param<V>(q.w, c, n, 1.0f, w[j]);
-        load_param<V>(q.scale, c, n, 1.0f, k[j]);
+        const auto c = spots.s[j];
+        load_param(q.w, c, n, 1.0f, w[j]);
+        load_param(q.scale, c, n, 1.0f, k[j]);
 #pragma unroll
         for (int e = 0; e < V; e++) {
             k[j][e] *= q.alpha;
@@ -144,8 +153,8 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(N
     auto read = [&](int64_t m, Row& r) {
 #pragma unroll
         for (int j = 0; j < NC; j++) {
-            const int c = V * (lane + j * lanes);
-            if (c < n && m < q.M) {
+            const auto c = spots.s[j];
+            if (c.at < n && m < q.M) {
                 r.r[j].load(row_of<R>(q.s, m, q.ld_s), c, n);
                 r.dy[j].load(row_of<T>(q.dy, m, q.ld_y), c, n);
                 if (q.ds) r.ds[j].load(row_of<R>(q.ds, m, q.ld_ds), c, n);
@@ -168,6 +177,13 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(N
     for (; m < q.M; m += step) {
         Row r = next;
         read(m + step, next);
+        if (spots.shared) {
+#pragma unroll
+            for (int j = 0; j < NC; j++) {
+                r.r[j].clear(spots.s[j]);
+                r.dy[j].clear(spots.s[j]);
+            }
+        }
         float mean = 0.0f;
         if (layer) {
             float sum[1] = {0.0f};
@@ -184,7 +200,7 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(N
         for (int j = 0; j < NC; j++)
 #pragma unroll
             for (int e = 0; e < V; e++) {
-                const float v = V * (lane + j * lanes) + e < n ? r.r[j][e] - mean : 0.0f;
+                const float v = spots.own(j, e, n) ? r.r[j][e] - mean : 0.0f;
                 const float gw = r.dy[j][e] * w[j][e];
                 sums[0] = __builtin_fmaf(v, v, sums[0]);
                 sums[1] = __builtin_fmaf(gw, v, sums[1]);
@@ -201,7 +217,7 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(N
         const float c2 = layer ? sums[2] * inv_n : 0.0f;
 #pragma unroll
         for (int j = 0; j < NC; j++) {
-            const int c = V * (lane + j * lanes);
+            const auto c = spots.s[j];
             RowVec<R, V> dres;
             RowVec<T, V> dx;
 #pragma unroll
@@ -217,14 +233,14 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void add_norm_bwd_kernel(N
                 dres.set(e, d);
                 dx.set(e, d * k[j][e]);
             }
-            if (c < n) {
+            if (c.at < n) {
                 dres.template store<false>(row_of<R>(q.dres, m, q.ld_dres), c, n);
                 if (q.dx) dx.template store<false>(row_of<T>(q.dx, m, q.ld_dx), c, n);
             }
         }
     }
-    write_part<TEAM, NC, V, K>(acc, part_lds, static_cast<float*>(q.ws) + blockIdx.x * K * q.D,
-                               q.D, 0, n);
+    write_part<TEAM, NC, V, K, ENDS>(acc, part_lds, static_cast<float*>(q.ws) + blockIdx.x * K * q.D,
+                               q.D, 0, n, spots);
 }
 
 // ---- rows too wide for the registers -------------------------------------------
@@ -387,8 +403,8 @@ hipError_t launch_add_norm(const NormArgs& a, hipStream_t st) {
     return dispatch(a, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const bool held = by_width<kVec<T>>(a.D, [&](auto s) {
-            constexpr auto kernel = add_norm_kernel<T, R, s.TEAM, s.NC>;
+        const bool held = by_width<T>(a.D, [&](auto s) {
+            constexpr auto kernel = add_norm_kernel<T, R, s.TEAM, s.NC, s.ENDS>;
             const auto grid = row_groups<kernel>(a.M, 1, s.threads, s.rows);
             kernel<<<static_cast<unsigned>(grid), s.threads, 0, st>>>(a);
         });
@@ -407,9 +423,9 @@ hipError_t launch_add_norm_bwd(const NormArgs& a, hipStream_t st) {
     const hipError_t e = dispatch(a, [&](auto t, auto r) {
         using T = decltype(t);
         using R = decltype(r);
-        const bool held = by_width<kVec<T>>(a.D, [&](auto s) {
+        const bool held = by_width<T>(a.D, [&](auto s) {
             auto go = [&](auto more) {
-                constexpr auto kernel = add_norm_bwd_kernel<T, R, s.TEAM, s.NC, more.value>;
+                constexpr auto kernel = add_norm_bwd_kernel<T, R, s.TEAM, s.NC, s.ENDS, more.value>;
                 rows = row_groups<kernel>(a.M, 1, s.threads, s.rows, most_parts(a.M, s.threads));
                 kernel<<<static_cast<unsigned>(rows), s.threads, 0, st>>>(a);
             };
