@@ -331,31 +331,31 @@ __global__ __launch_bounds__(kWide) void add_norm_bwd_wide_kernel(NormArgs q) {
 }
 
 // One workgroup sums 32 channels: 32 lanes side by side, 32 rows at a time, in
-// a fixed order.  4 to 7 us, most of it latency (512 rows of D 5120: 10 MB).
-__global__ __launch_bounds__(1024) void norm_params_kernel(NormArgs q, bool gated, int64_t rows,
-                                                           int K) {
-    __shared__ float lds[32][33];
+// a fixed order, all K sums at once.  3 to 5 us, most of it latency (512 rows of
+// D 5120: 10 MB).
+template <int K>
+__global__ __launch_bounds__(1024) void norm_params_kernel(NormArgs q, bool gated, int64_t rows) {
+    __shared__ float lds[K][32][33];
     const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
     const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     const float* part = static_cast<const float*>(q.ws);
     float S[3] = {0.0f, 0.0f, 0.0f};
-    for (int k = 0; k < K; k++) {
-        float s = 0.0f;
-        if (d < q.D) {
+    if (d < q.D) {
 #pragma unroll 8
-            for (int64_t p = group; p < rows; p += 32) s += part[(p * K + k) * q.D + d];
-        }
-        __syncthreads();
-        lds[group][lane] = s;
-        __syncthreads();
-        if (group == 0) {
-            s = 0.0f;
+        for (int64_t p = group; p < rows; p += 32)
 #pragma unroll
-            for (int g = 0; g < 32; g++) s += lds[g][lane];
+            for (int k = 0; k < K; k++) S[k] += part[(p * K + k) * q.D + d];
+    }
+#pragma unroll
+    for (int k = 0; k < K; k++) lds[k][group][lane] = S[k];
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+        for (int k = 0; k < K; k++) {
+            S[k] = 0.0f;
+#pragma unroll
+            for (int g = 0; g < 32; g++) S[k] += lds[k][g][lane];
         }
-        S[0] = k == 0 ? s : S[0];
-        S[1] = k == 1 ? s : S[1];
-        S[2] = k == 2 ? s : S[2];
     }
     if (group != 0 || d >= q.D) return;
     if (gated) {
@@ -395,7 +395,9 @@ bool norm_bwd_workspace(int64_t M, int64_t D, int64_t G, int64_t& bytes) {
 
 hipError_t launch_norm_params(const NormArgs& a, bool gated, int64_t rows, int K, hipStream_t st) {
     if (!a.dw && !a.db && !a.dscale) return hipGetLastError();
-    norm_params_kernel<<<static_cast<unsigned>((a.D + 31) / 32), 1024, 0, st>>>(a, gated, rows, K);
+    const unsigned grid = static_cast<unsigned>((a.D + 31) / 32);
+    auto kernel = K == 1 ? norm_params_kernel<1> : K == 2 ? norm_params_kernel<2> : norm_params_kernel<3>;
+    kernel<<<grid, 1024, 0, st>>>(a, gated, rows);
     return hipGetLastError();
 }
 
