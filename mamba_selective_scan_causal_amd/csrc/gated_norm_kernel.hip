@@ -4,8 +4,8 @@
 // Bound by HBM: the forward reads x, z (and the residual) and writes y, the
 // backward reads x, z, dout and writes dx, dz, each once.  The outputs carry
 // the nontemporal hint (M 32768 D 5120 bf16: forward 197 -> 188 us, backward
-// 418 -> 405).  That size now: forward 193 us (5.2 TB/s), backward 312 us
-// (5.4 TB/s; VALU busy 65 %).
+// 418 -> 405).  That size now: forward 194 us (5.2 TB/s), backward 307 us
+// (5.5 TB/s; VALU busy 65 %).
 #include "norm_common.h"
 
 namespace mss {

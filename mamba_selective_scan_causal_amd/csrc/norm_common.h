@@ -10,9 +10,13 @@
 // variance is that of the centred values) are all the lanes exchange.
 // Vectors are read and written with the element's alignment (global memory
 // takes unaligned vector accesses), so strided rows and odd widths run the
-// same code and give the same bits.  A row's last, partial vector is read as
-// the V channels up to the row's end, those of the lane before it set to 0, and
-// written element by element.  A team walks several rows, reading the next one while
+// same code and give the same bits.  A row's last, partial vector of a 2-byte
+// type is read as the V channels up to the row's end, those of the lane before
+// it set to 0, and written element by element; read by elements, they would
+// hold up the loads behind them until they are packed (gated_norm forward and
+// backward, M 16384 bf16: D 2559 265 us, like this 166; D 2560 132).  In fp32,
+// with nothing to pack, it is read by elements (add_norm forward and backward,
+// M 16384 D 1499: 187 us, the other way 210).  A team walks several rows, reading the next one while
 // it works on this one; the per-channel parameters are read once, and the
 // backward keeps its sums of the parameter gradients in registers.
 #pragma once
@@ -225,7 +229,7 @@ inline int resident(Kernel* kernel, std::atomic<int> (&known)[17], int threads) 
 // Workgroups per group of channels: what 256 CUs hold at once over all groups
 // (they walk the rows, so a second, partly filled round only lengthens the
 // launch: with 2048 lanes a CU whatever it holds, gated_norm forward and
-// backward of M 32768 D 5120 bf16 took 582 us, like this 528), none without a
+// backward of M 32768 D 5120 bf16 took a tenth longer), none without a
 // row of its own.
 template <auto kernel>
 inline int64_t row_groups(int64_t M, int64_t G, int threads, int rows, int64_t most = 1 << 20) {
@@ -252,7 +256,7 @@ inline int64_t most_parts(int64_t M, int threads) {
 // wave where one vector a lane is enough, else a workgroup with one (two past
 // 1024 lanes, up to 1536 vectors).  One vector a lane keeps the backward
 // passes at four waves or more on a SIMD (gated_norm's in bf16 takes 90
-// registers with one vector and 150 with two, add_norm's 127 and over 168).
+// registers with one vector and 150 with two, add_norm's 119 and over 168).
 // False for wider groups.
 template <int V, Ends ENDS, typename F>
 bool by_width(int64_t n, F f) {

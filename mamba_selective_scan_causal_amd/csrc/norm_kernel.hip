@@ -5,8 +5,8 @@
 //
 // Bound by HBM: the forward reads x and the residual and writes s and y, the
 // backward reads s, dy, ds (and x) and writes dresidual and dx, each once.
-// M 32768 D 2560 bf16 with an fp32 stream: forward 181 us (5.5 TB/s), backward
-// with dscale 300 us (5.0 TB/s).
+// M 32768 D 2560 bf16 with an fp32 stream: forward 182 us (5.5 TB/s), backward
+// with dscale 298 us (5.1 TB/s).
 // The outputs go through the cache: with the nontemporal hint the forward and
 // backward of M 32768 D 2560 in turn take 561 us, without it 538.
 #include "norm_common.h"
@@ -331,8 +331,9 @@ __global__ __launch_bounds__(kWide) void add_norm_bwd_wide_kernel(NormArgs q) {
 }
 
 // One workgroup sums 32 channels: 32 lanes side by side, 32 rows at a time, in
-// a fixed order, all K sums at once.  3 to 5 us, most of it latency (512 rows of
-// D 5120: 10 MB).
+// a fixed order, all K sums at once.  4 to 13 us, most of it latency (768 rows of
+// 3 x 2560 sums: 24 MB).  With 16 channels to a workgroup gated_norm forward and
+// backward of M 32768 D 5120 take 521 us, like this 518; with 8 525.
 template <int K>
 __global__ __launch_bounds__(1024) void norm_params_kernel(NormArgs q, bool gated, int64_t rows) {
     __shared__ float lds[K][32][33];

@@ -214,6 +214,44 @@ def test_residual_in_place(D):
     assert s2 is stream and torch.equal(s, s2) and torch.equal(y, y2)
 
 
+@pytest.mark.parametrize("dtype", ("bf16", "f32"))
+@pytest.mark.parametrize("M,D", [(5000, 121), (700, 509), (3000, 1027), (600, 2561), (40, 8197)])
+def test_residual_in_place_at_odd_widths(dtype, M, D):
+    """A row's end is read together with channels of the lane before, which may
+    have written its own already."""
+    import torch
+    rng = np.random.default_rng(D)
+    x, res = put(rng.normal(size=(M, D)), dtype), put(rng.normal(size=(M, D)), dtype)
+    w, b = put(rng.normal(size=D)), put(rng.normal(size=D))
+    for kind in ("rms", "layer"):
+        y, s = mss.add_norm(x, res, w, b, kind=kind)
+        assert torch.equal(s, (res.float() + x.float()).to(s.dtype))
+        for _ in range(3):
+            stream = res.clone()
+            y2, _ = mss.add_norm(x, stream, w, b, kind=kind, residual_out=stream)
+            assert torch.equal(s, stream) and torch.equal(y, y2)
+
+
+# every length of a last vector, in each team: 16 lanes, a wave, workgroups of
+# some waves whose last has one lane, workgroups with two vectors a lane
+@pytest.mark.parametrize("D", [*range(1, 18), 121, 127, 129, 130, 135, 509, 511, 513, 515, 517, 518, 1023, 2562,
+                               4091, 4099, 8190, 8193, 8199, 12281])
+@pytest.mark.parametrize("dtype", ("f16", "bf16", "f32"))
+def test_row_ends(dtype, D):
+    kind = ("rms", "layer")[D % 2]
+    add_case(37, D, dtype, dtype if D % 3 else "f32", kind, seed=D)
+    gated_case(37, D, dtype, kind, ("before", "after")[D % 3 > 0], seed=D)
+
+
+@pytest.mark.parametrize("D,groups", [(286, 2), (1001, 7), (1030, 2), (2050, 5), (16394, 2), (20, 4), (22, 2)])
+@pytest.mark.parametrize("dtype", ("f16", "f32"))
+def test_group_ends(dtype, D, groups):
+    """Group ends inside a row: the channels read before and after them are
+    another group's."""
+    gated_case(29, D, dtype, "layer", "before", groups, seed=groups)
+    gated_case(29, D, dtype, "rms", "after", groups, seed=groups)
+
+
 def test_empty():
     import torch
     f = dict(device="cuda")
