@@ -357,13 +357,14 @@ int mss_ssd_time_split(const mss_ssd_dims* dims, int64_t* segment_steps);
  *   MSS_GATE_DECAY    a = exp(-c softplus(decay[d]) sigma(r)),
  *                     v = sqrt(1 - a^2) sigma(i) x    (c = gate_scale)
  *   MSS_GATE_LOG      a = exp(r),                     v = x
- * r = -inf is valid: it means a = 0 (a = 1 for MSS_GATE_DECAY).  reset_t != 0 drops the state carried into step
- * t (the start of another document packed into the same row, or the end of a
- * row's left padding).  What lies on one side of a reset, NaN and infinities
- * included, does not reach the outputs and gradients of rows on the other
- * (ddecay, a sum over all rows, excepted).  Time is cut into chunks of up to 128 steps that are
- * combined as affine maps of the state: with MSS_GATE_LOG and r > 0 (growing
- * states) the product of a chunk's factors must stay finite.
+ * r = -inf is valid: it means a = 0 (a = 1 for MSS_GATE_DECAY).  reset_t != 0
+ * drops the state carried into step t (the start of another document packed
+ * into the same row, or the end of a row's left padding).  What lies on one
+ * side of a reset, NaN and infinities included, does not reach the outputs
+ * and gradients of rows on the other (ddecay, a sum over all rows, excepted).
+ * Time is cut into chunks of up to 128 steps that are combined as affine maps
+ * of the state: with MSS_GATE_LOG and r > 0 (growing states) the product of a
+ * chunk's factors must stay finite.
  * The activations x, r, i, z, y and their gradients are of type dims->dtype;
  * the states, decay and its gradient are fp32.  States are carried in fp32
  * and results are rounded once, to the nearest even.                       */

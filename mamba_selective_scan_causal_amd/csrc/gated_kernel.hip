@@ -187,7 +187,8 @@ __device__ __forceinline__ void wait_for(Word* p, Map (&m)[V]) {
                 __builtin_bit_cast(float, static_cast<unsigned>(w[v] >> 32))};
 }
 
-// 2 us for 0.2 MB, 6 us for 24 MB.  ws holds n words, an even number: 32 for the counter, then the handed over.
+// 2 us for 0.2 MB, 6 us for 24 MB.  ws holds n words, an even number: 32 for the
+// counters, then the handed over.
 __global__ __launch_bounds__(256) void gated_unset_kernel(ulonglong2* ws, int64_t n) {
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n / 2;
          i += static_cast<int64_t>(gridDim.x) * 256)
