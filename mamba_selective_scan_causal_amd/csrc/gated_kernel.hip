@@ -763,16 +763,16 @@ template <typename T, int V, typename F>
 hipError_t by_gate(int gate, F f) {
     constexpr std::integral_constant<int, V> v{};
     switch (gate) {
-        case MSS_GATE_SIGMOID: f(T{}, v, std::integral_constant<int, MSS_GATE_SIGMOID>{}); break;
-        case MSS_GATE_DECAY: f(T{}, v, std::integral_constant<int, MSS_GATE_DECAY>{}); break;
-        case MSS_GATE_LOG: f(T{}, v, std::integral_constant<int, MSS_GATE_LOG>{}); break;
+        case MSS_GATE_SIGMOID: return f(T{}, v, std::integral_constant<int, MSS_GATE_SIGMOID>{});
+        case MSS_GATE_DECAY: return f(T{}, v, std::integral_constant<int, MSS_GATE_DECAY>{});
+        case MSS_GATE_LOG: return f(T{}, v, std::integral_constant<int, MSS_GATE_LOG>{});
         default: return hipErrorInvalidValue;
     }
-    return hipGetLastError();
 }
 
-// f(element, channels per lane, gate) for the call's types.  A single channel
-// is no pair.
+// f(element, channels per lane, gate) for the call's types; f returns what its
+// launches reported (hipGetLastError() clears an error, so each is asked for
+// once).  A single channel is no pair.
 template <typename F>
 hipError_t dispatch(const GatedArgs& a, F f) {
     switch (a.dtype) {
@@ -871,13 +871,14 @@ hipError_t launch_gated_scan(const GatedArgs& a, hipStream_t st) {
     return dispatch(a, [&](auto t, auto v, auto gate) {
         using T = decltype(t);
         const Chain g = chain_of(a, v.value, kChunk);
-        if (unset(g, v.value, st) != hipSuccess) return;
+        if (const hipError_t e = unset(g, v.value, st); e != hipSuccess) return e;
         const unsigned grid = g.tiles * static_cast<unsigned>(g.chunks);
         const unsigned threads = threads_of(a.L, kSteps);
         if (a.z)
             gated_scan_kernel<T, v.value, gate.value, true><<<grid, threads, 0, st>>>(a, g);
         else
             gated_scan_kernel<T, v.value, gate.value, false><<<grid, threads, 0, st>>>(a, g);
+        return hipGetLastError();
     });
 }
 
@@ -889,13 +890,14 @@ hipError_t launch_gated_scan_bwd(const GatedArgs& a, hipStream_t st) {
     const hipError_t e = dispatch(a, [&](auto t, auto v, auto gate) {
         using T = decltype(t);
         const Chain g = chain_of(a, v.value, kBwdChunk);
-        if (unset(g, v.value, st) != hipSuccess) return;
+        if (const hipError_t e = unset(g, v.value, st); e != hipSuccess) return e;
         const unsigned grid = g.tiles * static_cast<unsigned>(g.chunks);
         const unsigned threads = threads_of(a.L, kBwdSteps);
         if (a.z)
             gated_scan_bwd_kernel<T, v.value, gate.value, true><<<grid, threads, 0, st>>>(a, g, part);
         else
             gated_scan_bwd_kernel<T, v.value, gate.value, false><<<grid, threads, 0, st>>>(a, g, part);
+        return hipGetLastError();
     });
     if (e != hipSuccess || a.gate != MSS_GATE_DECAY) return e;
     gated_ddecay_kernel<<<static_cast<unsigned>(cdiv(a.D, 32)), 1024, 0, st>>>(
@@ -908,6 +910,7 @@ hipError_t launch_gated_step(const GatedArgs& a, hipStream_t st) {
         const int64_t per = cdiv(a.D, kStepVec);
         gated_step_kernel<decltype(t), gate.value>
             <<<static_cast<unsigned>(cdiv(a.B * per, 64)), 64, 0, st>>>(a, static_cast<unsigned>(per));
+        return hipGetLastError();
     });
 }
 
