@@ -16,6 +16,8 @@ The gated linear recurrence (``gated_scan``, ``gated_scan_backward``,
 ``gated_step``) and the norms before and after a block (``add_norm``,
 ``gated_norm`` and their backward passes) take activations in float32,
 bfloat16 or float16, row-strided where that is handy; see each function.
+Called with ``stream=``, they allocate what they return (and their workspace)
+as that stream's own memory.
 """
 from __future__ import annotations
 
@@ -270,6 +272,21 @@ def _stream(stream):
 
 def _empty(shape, like):
     return _torch().empty(shape, dtype=like.dtype, device=like.device)
+
+
+def _own_memory(stream, make):
+    """make(), a fresh tensor, in the memory of the stream that a call is given.
+
+    Memory of the current stream may be handed out again, or still be in use,
+    by that stream's own work, which is not ordered with the call's.  What the
+    call returns may be used on the current stream afterwards: dropped, it is
+    not handed out before that work is done either."""
+    torch = _torch()
+    _stream(stream)
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(torch.cuda.current_stream())
+    return t
 
 
 def conv1d_silu(x, w_conv, b_conv=None, *, batch, seq_len, out=None, stream=None):
@@ -604,12 +621,13 @@ def make_norm_strides(*strides) -> NormStrides:
 
 
 class _Call:
-    """Argument checks of one call: the current device and the activation type."""
+    """Argument checks of one call: the current device, the activation type and the stream."""
 
-    __slots__ = ("torch", "Tensor", "f32", "dev", "like", "dtype", "code")
+    __slots__ = ("torch", "Tensor", "f32", "dev", "like", "dtype", "code", "on")
 
-    def __init__(self, like, name):
+    def __init__(self, like, name, stream):
         self.torch = torch = _torch()
+        self.on = stream
         self.Tensor, self.f32 = torch.Tensor, torch.float32
         if not isinstance(like, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -661,6 +679,9 @@ class _Call:
 
     def empty(self, shape, dtype=None, like=None):
         """An uninitialised tensor; ``like``: one that may be of its shape and type (cheaper)."""
+        if self.on is not None:
+            return _own_memory(self.on, lambda: self.torch.empty(shape, dtype=dtype or self.dtype,
+                                                                 device=self.like.device))
         dtype, like = dtype or self.dtype, self.like if like is None else like
         if like.shape == shape and like.dtype is dtype and like.is_contiguous():
             return self.torch.empty_like(like)
@@ -673,20 +694,18 @@ class _Call:
             return t, t.data_ptr() or None, cols
         return (t, *self.rows(t, name, rows, cols, dtype))
 
-    def stream(self, stream):
-        """The stream's handle (the current stream's without a stream)."""
-        if stream is None:
+    def stream(self):
+        """The handle of the call's stream (the current stream's where none is given)."""
+        if self.on is None:
             return self.torch._C._cuda_getCurrentRawStream(self.dev)
-        return _stream(stream)
+        return _stream(self.on)
 
-    def workspace(self, need, workspace, stream):
+    def workspace(self, need, workspace):
         """(pointer, bytes, tensor) of the caller's workspace, or of a fresh one."""
         if workspace is None:
             if need == 0:
                 return None, 0, None
             workspace = self.empty((need + 256,), self.torch.uint8)
-            if stream is not None:
-                workspace.record_stream(stream)
         elif (not isinstance(workspace, self.torch.Tensor)
               or workspace.dtype != self.torch.uint8 or workspace.get_device() != self.dev
               or not workspace.is_contiguous()):
@@ -765,20 +784,20 @@ def gated_scan(x, r, i=None, decay=None, z=None, h0=None, reset=None, *, batch, 
     ``workspace``: uint8 GPU tensor of at least ``gated_workspace_bytes(OP_GATED_SCAN, ...)``
     + 256 bytes (allocated here when omitted)."""
     D, M = x.shape[-1], batch * seq_len
-    c = _Call(x, "x")
+    c = _Call(x, "x", stream)
     code = _choice(GATES, gate, "gate")
     (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, M, D, gate)
     y, py, ly = c.output(out, "out", M, D)
     ck = _flag(h_ckpt, (batch, gated_ckpt_steps(seq_len), D), c)
     hl = _flag(h_last, (batch, D), c, h0)
     need = gated_workspace_bytes(OP_GATED_SCAN, batch=batch, seq_len=seq_len, d_inner=D, gate=gate)
-    wp, wn, _keep = c.workspace(need, workspace, stream)
+    wp, wn, _keep = c.workspace(need, workspace)
     _check("mss_gated_scan", lib().mss_gated_scan(
         _ref(make_gated_dims(batch, seq_len, D, c.code, code, gate_scale)),
         _ref(make_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
         c.dense(h0, "h0", (batch, D)), _reset(c, reset, M), py,
         c.dense(ck, "h_ckpt", (batch, gated_ckpt_steps(seq_len), D)),
-        c.dense(hl, "h_last", (batch, D)), wp, wn, c.stream(stream)))
+        c.dense(hl, "h_last", (batch, D)), wp, wn, c.stream()))
     return y, ck, hl
 
 
@@ -794,7 +813,7 @@ def gated_scan_backward(x, r, i, decay, z, reset, h_ckpt, dout, *, batch, seq_le
     ``need_dh0``.  ``out``: optional dict of output tensors for some of them (dx, dr, di, dz
     may be row-strided).  ``workspace`` as in gated_scan, with OP_GATED_SCAN_BACKWARD."""
     D, M = x.shape[-1], batch * seq_len
-    c = _Call(x, "x")
+    c = _Call(x, "x", stream)
     code = _choice(GATES, gate, "gate")
     (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, M, D, gate)
     has_decay, MD, f32 = gate == "decay", (M, D), c.f32
@@ -807,14 +826,14 @@ def gated_scan_backward(x, r, i, decay, z, reset, h_ckpt, dout, *, batch, seq_le
     po, lo = c.rows(dout, "dout", M, D)
     need = gated_workspace_bytes(OP_GATED_SCAN_BACKWARD, batch=batch, seq_len=seq_len, d_inner=D,
                                  gate=gate)
-    wp, wn, _keep = c.workspace(need, workspace, stream)
+    wp, wn, _keep = c.workspace(need, workspace)
     _check("mss_gated_scan_backward", lib().mss_gated_scan_backward(
         _ref(make_gated_dims(batch, seq_len, D, c.code, code, gate_scale)),
         _ref(make_gated_strides(lx, lr, li, lz, lo, ldx, ldr, ldi, ldz)), px, pr, pi, pdec, pz,
         _reset(c, reset, M),
         c.dense(h_ckpt, "h_ckpt", (batch, gated_ckpt_steps(seq_len), D), required=True), po,
         c.dense(dh_last, "dh_last", (batch, D)), pdx, pdr, pdi,
-        at["ddecay"][0], pdz, at["dh0"][0], wp, wn, c.stream(stream)))
+        at["ddecay"][0], pdz, at["dh0"][0], wp, wn, c.stream()))
     return g
 
 
@@ -845,7 +864,7 @@ def gated_step(x, r, i, decay, z, h, *, gate, gate_scale=8.0, out=None, stream=N
     """One token per sequence of ``gated_scan``: x, r, i, z (batch, D); updates ``h``
     (batch, D) float32 in place.  Returns y (batch, D)."""
     batch, D = x.shape
-    c = _Call(x, "x")
+    c = _Call(x, "x", stream)
     code = _choice(GATES, gate, "gate")
     (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, batch, D,
                                                                  gate)
@@ -853,7 +872,7 @@ def gated_step(x, r, i, decay, z, h, *, gate, gate_scale=8.0, out=None, stream=N
     _check("mss_gated_step", lib().mss_gated_step(
         _ref(make_gated_dims(batch, 1, D, c.code, code, gate_scale)),
         _ref(make_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
-        c.dense(h, "h", (batch, D), required=True), py, c.stream(stream)))
+        c.dense(h, "h", (batch, D), required=True), py, c.stream()))
     return y
 
 
@@ -873,7 +892,7 @@ def add_norm(x, residual, weight, bias=None, scale=None, *, kind="rms", eps=1e-6
     holds it.  ``residual_out`` may be ``residual`` itself: updated in place.  Rows of x,
     residual and the outputs may be strided."""
     M, D = x.shape
-    c = _Call(x, "x")
+    c = _Call(x, "x", stream)
     rt = (residual.dtype if residual is not None else
           residual_out.dtype if residual_out is not None else res_dtype or c.dtype)
     rc = _res_code(c, rt, "the residual stream")
@@ -885,7 +904,7 @@ def add_norm(x, residual, weight, bias=None, scale=None, *, kind="rms", eps=1e-6
         _ref(make_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
         _ref(make_norm_strides(lx, 0, lr, ls, ly)), px, pr,
         c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)),
-        c.dense(scale, "scale", (D,)), ps, py, c.stream(stream)))
+        c.dense(scale, "scale", (D,)), ps, py, c.stream()))
     return y, s
 
 
@@ -899,7 +918,7 @@ def add_norm_backward(s, weight, dy, ds=None, x=None, scale=None, *, bias=False,
     dbias (with ``bias``) and dscale (with ``scale``) float32.  ``out`` and ``workspace`` as in
     gated_scan_backward (``norm_workspace_bytes(OP_ADD_NORM_BACKWARD, ...)``)."""
     M, D = dy.shape
-    c = _Call(dy, "dy")
+    c = _Call(dy, "dy", stream)
     rc = _res_code(c, s.dtype, "s")
     g, at = _outputs(c, out, {
         "dx": (need_dx, (M, D), None, dy, True), "dresidual": (True, (M, D), s.dtype, s, True),
@@ -912,13 +931,13 @@ def add_norm_backward(s, weight, dy, ds=None, x=None, scale=None, *, bias=False,
     px, lx = c.rows(x, "x", M, D, required=scale is not None)
     (pdx, ldx), (pdr, ldr) = at["dx"], at["dresidual"]
     wp, wn, _keep = c.workspace(norm_workspace_bytes(OP_ADD_NORM_BACKWARD, rows=M, width=D),
-                                workspace, stream)
+                                workspace)
     _check("mss_add_norm_backward", lib().mss_add_norm_backward(
         _ref(make_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
         _ref(make_norm_strides(lx, 0, 0, ls, lo, lds, ldx, 0, ldr)), ps,
         c.dense(weight, "weight", (D,), required=True), po, pds, px,
         c.dense(scale, "scale", (D,)), pdx, pdr, at["dweight"][0], at["dbias"][0], at["dscale"][0],
-        wp, wn, c.stream(stream)))
+        wp, wn, c.stream()))
     return g
 
 
@@ -932,7 +951,7 @@ def gated_norm(x, z, weight, bias=None, residual=None, scale=None, *, groups=1, 
     z, residual may be None; weight, bias, scale (D,) float32; the norm runs over each of
     ``groups`` equal groups of channels."""
     M, D = x.shape
-    c = _Call(x, "x")
+    c = _Call(x, "x", stream)
     px, lx = c.rows(x, "x", M, D)
     pz, lz = c.rows(z, "z", M, D, required=False)
     pr, lr = c.rows(residual, "residual", M, D, required=False)
@@ -942,7 +961,7 @@ def gated_norm(x, z, weight, bias=None, residual=None, scale=None, *, groups=1, 
                             _choice(GATE_ORDERS, order, "order"), groups, eps, alpha)),
         _ref(make_norm_strides(lx, lz, lr, 0, ly)), px, pz,
         c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)), pr,
-        c.dense(scale, "scale", (D,)), py, c.stream(stream)))
+        c.dense(scale, "scale", (D,)), py, c.stream()))
     return y
 
 
@@ -954,7 +973,7 @@ def gated_norm_backward(x, z, weight, bias, scale, dout, *, groups=1, order="bef
     dscale (with ``scale``) float32.  ``out`` and ``workspace`` as in gated_scan_backward
     (``norm_workspace_bytes(OP_GATED_NORM_BACKWARD, ...)``)."""
     M, D = x.shape
-    c = _Call(x, "x")
+    c = _Call(x, "x", stream)
     g, at = _outputs(c, out, {
         "dx": (True, (M, D), None, x, True), "dz": (z is not None, (M, D), None, z, True),
         "dweight": (True, (D,), c.f32, weight, False),
@@ -965,13 +984,12 @@ def gated_norm_backward(x, z, weight, bias, scale, dout, *, groups=1, order="bef
     po, lo = c.rows(dout, "dout", M, D)
     (pdx, ldx), (pdz, ldz) = at["dx"], at["dz"]
     wp, wn, _keep = c.workspace(
-        norm_workspace_bytes(OP_GATED_NORM_BACKWARD, rows=M, width=D, groups=groups), workspace,
-        stream)
+        norm_workspace_bytes(OP_GATED_NORM_BACKWARD, rows=M, width=D, groups=groups), workspace)
     _check("mss_gated_norm_backward", lib().mss_gated_norm_backward(
         _ref(make_norm_dims(M, D, c.code, c.code, _choice(NORM_KINDS, kind, "kind"),
                             _choice(GATE_ORDERS, order, "order"), groups, eps, alpha)),
         _ref(make_norm_strides(lx, lz, 0, 0, lo, 0, ldx, ldz)), px, pz,
         c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)),
         c.dense(scale, "scale", (D,)), po, pdx, pdz, at["dweight"][0], at["dbias"][0], at["dscale"][0],
-        wp, wn, c.stream(stream)))
+        wp, wn, c.stream()))
     return g
