@@ -16,8 +16,9 @@ The gated linear recurrence (``gated_scan``, ``gated_scan_backward``,
 ``gated_step``) and the norms before and after a block (``add_norm``,
 ``gated_norm`` and their backward passes) take activations in float32,
 bfloat16 or float16, row-strided where that is handy; see each function.
-Called with ``stream=``, they allocate what they return (and their workspace)
-as that stream's own memory.
+
+A call given ``stream=`` allocates what it returns, and its workspace, as that
+stream's own memory.
 """
 from __future__ import annotations
 
@@ -270,8 +271,11 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _empty(shape, like):
-    return _torch().empty(shape, dtype=like.dtype, device=like.device)
+def _empty(shape, like, stream=None, dtype=None):
+    def make():
+        return _torch().empty(shape, dtype=dtype or like.dtype, device=like.device)
+
+    return make() if stream is None else _own_memory(stream, make)
 
 
 def _own_memory(stream, make):
@@ -293,7 +297,7 @@ def conv1d_silu(x, w_conv, b_conv=None, *, batch, seq_len, out=None, stream=None
     """u = SiLU(causal depthwise conv1d(x) + b_conv), (batch*seq_len, D)."""
     D, K = w_conv.shape
     M = batch * seq_len
-    u = out if out is not None else _empty((M, D), x)
+    u = out if out is not None else _empty((M, D), x, stream)
     dims = make_dims(batch, seq_len, D, 1, K)
     _check("mss_conv1d_silu", lib().mss_conv1d_silu(
         ctypes.byref(dims), _ptr(x, "x", (M, D)), _ptr(w_conv, "w_conv", (D, K)),
@@ -306,14 +310,14 @@ def ckpt_steps(seq_len) -> int:
     return (seq_len + 7) // 8
 
 
-def _scan_outputs(x, batch, seq_len, D, N, out, h_cache, h_last, ckpt8=False):
+def _scan_outputs(x, batch, seq_len, D, N, out, h_cache, h_last, ckpt8, stream):
     M = batch * seq_len
-    y = out if out is not None else _empty((M, D), x)
+    y = out if out is not None else _empty((M, D), x, stream)
     Lc = ckpt_steps(seq_len) if ckpt8 else seq_len
     hc = (h_cache if not isinstance(h_cache, bool) else
-          (_empty((batch, Lc, D, N), x) if h_cache else None))
+          (_empty((batch, Lc, D, N), x, stream) if h_cache else None))
     hl = (h_last if not isinstance(h_last, bool) else
-          (_empty((batch, D, N), x) if h_last else None))
+          (_empty((batch, D, N), x, stream) if h_last else None))
     return y, hc, hl
 
 
@@ -329,7 +333,8 @@ def selective_scan(u, delta, A_log, B, C, D_vec=None, z=None, h0=None, *, batch,
     D, N = A_log.shape
     M = batch * seq_len
     Lc = ckpt_steps(seq_len) if ckpt8 else seq_len
-    y, hc, hl = _scan_outputs(u, batch, seq_len, D, N, out, h_cache, h_last, ckpt8)
+    y, hc, hl = _scan_outputs(u, batch, seq_len, D, N, out, h_cache, h_last, ckpt8,
+                              stream)
     dims = make_dims(batch, seq_len, D, N, 1, exact, ckpt8)
     common = (_ptr(A_log, "A_log", (D, N)),)
     tail = (_ptr(D_vec, "D_vec", (D,), False),)
@@ -368,7 +373,8 @@ def mamba1_core(x, w_conv, b_conv, delta, A_log, B, C, D_vec=None, z=None, h0=No
     K = w_conv.shape[1]
     M = batch * seq_len
     Lc = ckpt_steps(seq_len) if ckpt8 else seq_len
-    y, hc, hl = _scan_outputs(x, batch, seq_len, D, N, out, h_cache, h_last, ckpt8)
+    y, hc, hl = _scan_outputs(x, batch, seq_len, D, N, out, h_cache, h_last, ckpt8,
+                              stream)
     dims = make_dims(batch, seq_len, D, N, K, exact, ckpt8)
     conv = (_ptr(w_conv, "w_conv", (D, K)), _ptr(b_conv, "b_conv", (D,), False))
     if _dense(x, delta, B, C, z, y):
@@ -402,7 +408,7 @@ def selective_step(x, z, delta, A_log, B, C, D_vec, w_conv, b_conv, conv_state, 
     batch, D = x.shape
     N = A_log.shape[1]
     K = w_conv.shape[1]
-    y = out if out is not None else _empty((batch, D), x)
+    y = out if out is not None else _empty((batch, D), x, stream)
     dims = make_dims(batch, 1, D, N, K)
     _check("mss_selective_step", lib().mss_selective_step(
         ctypes.byref(dims), _disc(disc), _ptr(x, "x", (batch, D)),
@@ -434,11 +440,7 @@ def _workspace(op, like, workspace, stream, **dims):
         if need == 0:
             return None, 0, None
         # 256 bytes of slack so that the pointer can be aligned to 256.
-        workspace = _torch().empty(need + 256, dtype=_torch().uint8, device=like.device)
-        if stream is not None:
-            # freed when the caller drops the result: keep it alive for the
-            # work queued on that stream
-            workspace.record_stream(stream)
+        workspace = _empty(need + 256, like, stream, _torch().uint8)
     if workspace.dtype != _torch().uint8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous uint8 GPU tensor")
     _same_device(workspace, "workspace")
@@ -480,11 +482,11 @@ def selective_scan_backward(u, delta, A_log, B, C, D_vec, z, h0, dout, *, batch,
     """
     D, N = A_log.shape
     M = batch * seq_len
-    g = {"du": _empty((M, D), u), "ddelta": _empty((M, D), u), "dA_log": _empty((D, N), u),
-         "dB": _empty((M, N), u), "dC": _empty((M, N), u),
-         "dD": _empty((D,), u) if D_vec is not None else None,
-         "dz": _empty((M, D), u) if z is not None else None,
-         "dh0": _empty((batch, D, N), u) if need_dh0 else None}
+    g = {"du": _empty((M, D), u, stream), "ddelta": _empty((M, D), u, stream),
+         "dA_log": _empty((D, N), u, stream), "dB": _empty((M, N), u, stream), "dC": _empty((M, N), u, stream),
+         "dD": _empty((D,), u, stream) if D_vec is not None else None,
+         "dz": _empty((M, D), u, stream) if z is not None else None,
+         "dh0": _empty((batch, D, N), u, stream) if need_dh0 else None}
     ck = h_ckpt is not None
     wp, wn, _keep = _workspace(OP_SELECTIVE_SCAN_BACKWARD, u, workspace, stream, batch=batch,
                                seq_len=seq_len, d_inner=D, d_state=N, exact=exact, ckpt8=ck)
@@ -519,7 +521,7 @@ def selective_scan_backward_noalloc(u, delta, A_log, B, C, D_vec, z, h0, dout, *
     want = {"du": True, "ddelta": True, "dA_log": True, "dB": True, "dC": True,
             "dD": D_vec is not None, "dz": z is not None, "dh0": need_dh0}
     out = dict(out or {})
-    g = {k: (out[k] if k in out else _empty(shapes[k], u)) if want[k] else None for k in shapes}
+    g = {k: (out[k] if k in out else _empty(shapes[k], u, stream)) if want[k] else None for k in shapes}
     dims = make_dims(batch, seq_len, D, N, 1, exact, h_ckpt is not None)
     _check("mss_selective_scan_backward_noalloc", lib().mss_selective_scan_backward_noalloc(
         ctypes.byref(dims), _disc(disc), _ptr(u, "u", (M, D)), _ptr(delta, "delta", (M, D)),
@@ -540,7 +542,7 @@ def conv1d_silu_backward(x, w_conv, b_conv, du, *, batch, seq_len, workspace=Non
     """Gradients of ``conv1d_silu`` against ``du``: (dx, dw_conv, db_conv)."""
     D, K = w_conv.shape
     M = batch * seq_len
-    dx, dw, db = _empty((M, D), x), _empty((D, K), x), _empty((D,), x)
+    dx, dw, db = (_empty(shape, x, stream) for shape in ((M, D), (D, K), (D,)))
     wp, wn, _keep = _workspace(OP_CONV1D_SILU_BACKWARD, x, workspace, stream, batch=batch,
                                seq_len=seq_len, d_inner=D, d_state=1, d_conv=K)
     dims = make_dims(batch, seq_len, D, 1, K)
@@ -560,9 +562,9 @@ def ssd_scan(x, dt, A_log, B, C, D_vec=None, dt_bias=None, h0=None, *, batch, se
     H = A_log.shape[0]
     P, N, G = head_dim, d_state, n_groups
     M = batch * seq_len
-    y = out if out is not None else _empty((M, H * P), x)
+    y = out if out is not None else _empty((M, H * P), x, stream)
     hl = (h_last if not isinstance(h_last, bool) else
-          (_empty((batch, H, P, N), x) if h_last else None))
+          (_empty((batch, H, P, N), x, stream) if h_last else None))
     dims = make_ssd_dims(batch, seq_len, H, P, N, G, exact)
     _check("mss_ssd_scan", lib().mss_ssd_scan(
         ctypes.byref(dims), _disc(disc), _ptr(x, "x", (M, H * P)), _ptr(dt, "dt", (M, H)),
@@ -680,8 +682,7 @@ class _Call:
     def empty(self, shape, dtype=None, like=None):
         """An uninitialised tensor; ``like``: one that may be of its shape and type (cheaper)."""
         if self.on is not None:
-            return _own_memory(self.on, lambda: self.torch.empty(shape, dtype=dtype or self.dtype,
-                                                                 device=self.like.device))
+            return _empty(shape, self.like, self.on, dtype or self.dtype)
         dtype, like = dtype or self.dtype, self.like if like is None else like
         if like.shape == shape and like.dtype is dtype and like.is_contiguous():
             return self.torch.empty_like(like)
