@@ -142,16 +142,22 @@ struct Chain {
     Word* states;              // [tile][group][V][64]: the state entering a group
 };
 
-// The affine map h -> A h + H.  A = 0 drops what was carried whatever it is:
-// rows on the other side of a reset may hold anything, NaN among it.
+// The affine map h -> A h + H.  A = -0, which no product of the factors is (all
+// are >= 0), marks a map that drops what was carried whatever it is: rows on the
+// other side of a reset may hold anything, NaN among it.  A product that only
+// underflows is +0: it leaves a finite state behind, but not a NaN.
+constexpr float kDrop = -0.0f;
 struct Map {
     float A, H;
+    __device__ __forceinline__ bool drops() const {
+        return __builtin_bit_cast(unsigned, A) == 0x80000000u;
+    }
     __device__ __forceinline__ float operator()(float h) const {
-        return A != 0.0f ? __builtin_fmaf(A, h, H) : H;
+        return drops() ? H : __builtin_fmaf(A, h, H);
     }
     // this after first
     __device__ __forceinline__ Map after(const Map& first) const {
-        return {A != 0.0f ? A * first.A : 0.0f, (*this)(first.H)};
+        return {drops() || first.drops() ? kDrop : A * first.A, (*this)(first.H)};
     }
 };
 
@@ -334,14 +340,14 @@ __device__ __forceinline__ void maps_of(const float (&a)[S][V], const float (&u)
 #pragma unroll
             for (int s = 0; s < S; s++) {
                 const bool drop = SOME && (resets >> s & 1);
-                f[v].A = drop ? 0.0f : f[v].A * a[s][v];
+                f[v].A = f[v].A * a[s][v];
                 f[v].H = drop ? u[s][v] : __builtin_fmaf(a[s][v], f[v].H, u[s][v]);
                 // nothing from a reset on reaches what is before the piece
                 if constexpr (REVERSE)
                     if (!SOME || !(resets & ((2u << s) - 1)))
                         w[v].H = __builtin_fmaf(f[v].A, dy(s, v), w[v].H);
             }
-            if (SOME && resets) f[v].A = 0.0f;
+            if (SOME && resets) f[v].A = kDrop;
             w[v].A = f[v].A;
         }
     };
