@@ -72,8 +72,9 @@ struct Gates {
             er = ex2(-kLog2e * r);
             ei = ex2(-kLog2e * i);
             if constexpr (KEEP) {
-                er = __builtin_fminf(er, kMost);
-                ei = __builtin_fminf(ei, kMost);
+                // (minimum hands a NaN on, fmin would make it the bound: a closed gate)
+                er = __builtin_elementwise_minimum(er, kMost);
+                ei = __builtin_elementwise_minimum(ei, kMost);
             }
             const float l2 = k * rcp(1.0f + er);
             a = ex2(l2);
@@ -102,7 +103,7 @@ struct Gates {
             const float a = ex2(l2);
             // m = sqrt(1 - a^2) and 1 / m; where m vanishes, so do sigma(r) or
             // k, and k sigma(r) / m (all that 1 / m enters) is below 2^-60
-            // with the bound on 1 / m
+            // with the bound on 1 / m (a NaN in mm is one in a as well)
             const float mm = one_minus_square(l2, a);
             const float rm = __builtin_amdgcn_rsqf(__builtin_fmaxf(mm, 0x1p-126f));
             const float as = a * s;

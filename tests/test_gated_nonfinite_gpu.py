@@ -136,3 +136,20 @@ def run_with_resets(a, L, D, gate):
         if s == 0:
             finite_where_defined(got["dh0"], val["dh0"], tol["dh0"], "f32", "dh0")
     finite_where_defined(hl, val["h_last"], tol["h_last"], "f32", "h_last")
+
+
+@pytest.mark.parametrize("gate,which", [("decay", "r"), ("decay", "i"), ("sigmoid", "r"), ("log", "r"),
+                                        ("decay", "decay"), ("sigmoid", "z")])
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("L", (60, 300))
+def test_a_nan_gate_reaches_the_gradients(gate, which, dtype, L):
+    """A gate that is NaN in one step of a few channels makes that step's gradients NaN, and with them
+    what the recurrence makes of it before and after."""
+    B, D = 2, 33
+    a = inputs(6, B, L, D, gate, z=which in ("i", "z"), h0=True)
+    if which == "decay":
+        a["decay"][[3, 8]] = np.nan
+    else:
+        a[which][[20, 41], [5, 6]] = np.nan
+        a[which][L + 17, 5] = np.nan
+    run(a, B, L, gate, dtype)
