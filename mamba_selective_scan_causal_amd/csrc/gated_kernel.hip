@@ -241,6 +241,36 @@ __device__ __forceinline__ void meet(const Chain& g, Word* first, int wave, int 
     for (int v = 0; v < V; v++) mates[wave][v][lane] = all[v];
 }
 
+// Takes h, the state entering the group (or what the adjoint carries into it), to
+// the group's `mate`-th chunk, by the waves' compositions.  With growing states
+// (GATE_LOG, r > 0) the factor of one of several chunks can overflow although h
+// and what becomes of it do not: then by the chunks' own maps, one after another.
+template <int GATE, int V>
+__device__ __forceinline__ void carry(const Chain& g, Word* first, int mate, int lane,
+                                      const Map (*mates)[V][64], float (&h)[V]) {
+    float start[V], most = 0.0f;   // most: inf or NaN where a factor is
+#pragma unroll
+    for (int v = 0; v < V; v++) start[v] = h[v];
+    for (int w = 0; w * g.per < mate; w++)
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const Map m = mates[w][v][lane];
+            h[v] = m(h[v]);
+            if constexpr (GATE == MSS_GATE_LOG) most = __builtin_elementwise_maximum(most, m.A);
+        }
+    if constexpr (GATE == MSS_GATE_LOG) {
+        if (g.per == 1 || !wave_any(!(most < __builtin_inff()))) return;
+#pragma unroll
+        for (int v = 0; v < V; v++) h[v] = start[v];
+        for (int m = 0; m < mate; m++) {
+            Map e[V];
+            wait_for<V>(first + int64_t{m} * (64 * V) + lane, e);
+#pragma unroll
+            for (int v = 0; v < V; v++) h[v] = e[v](h[v]);
+        }
+    }
+}
+
 // V channels of one row; an odd row's last lane takes the last V channels, so
 // its first is its neighbour's too, computed twice to the same bits.
 template <typename T, int V>
@@ -445,7 +475,8 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
                 put(g.maps + (int64_t{tile} * g.chunks + chunk) * words + 64 * v + lane, all.A, all.H);
             }
         }
-        meet<V>(g, g.maps + (int64_t{tile} * g.chunks + first) * words, wave, mate, lane, mates);
+        Word* maps = g.maps + (int64_t{tile} * g.chunks + first) * words;
+        meet<V>(g, maps, wave, mate, lane, mates);
         if (wave == kWaves - 1) {
             Map e[V];
             if (first > 0)
@@ -459,9 +490,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_scan_kernel(GatedArgs q, Ch
         __syncthreads();
 #pragma unroll
         for (int v = 0; v < V; v++) h[v] = entering[v][lane];
-        for (int w = 0; w * g.per < mate; w++)
-#pragma unroll
-            for (int v = 0; v < V; v++) h[v] = mates[w][v][lane](h[v]);
+        carry<GATE, V>(g, maps, mate, lane, mates, h);
     } else {
 #pragma unroll
         for (int v = 0; v < V; v++) h[v] = q.h0 ? q.h0[int64_t{b} * q.D + c + v] : 0.0f;
@@ -596,7 +625,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
             put(g.maps + (int64_t{tile} * g.chunks + turn) * words + 64 * v + lane, all.A, all.H);
         }
     }
-    meet<V>(g, g.maps + (int64_t{tile} * g.chunks + first) * words, wave, mate, lane, mates);
+    Word* maps = g.maps + (int64_t{tile} * g.chunks + first) * words;
+    meet<V>(g, maps, wave, mate, lane, mates);
     if (wave == waves - 1) {
         Map e[V];
         if (first > 0)
@@ -610,9 +640,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void gated_scan_bwd_kernel(GatedArg
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; v++) Q[v] = entering[v][lane];
-    for (int p = 0; p * g.per < mate; p++)
-#pragma unroll
-        for (int v = 0; v < V; v++) Q[v] = mates[p][v][lane](Q[v]);
+    carry<GATE, V>(g, maps, mate, lane, mates, Q);
     for (int p = waves - 1; p > wave; p--)
 #pragma unroll
         for (int v = 0; v < V; v++) Q[v] = rev[p][v][lane](Q[v]);
