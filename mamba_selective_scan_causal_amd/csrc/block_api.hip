@@ -69,13 +69,16 @@ class Checks {
                                                                : MSS_OK;
         if (p) outs_[n_outs_++] = {p, 1, need, need};
     }
-    // `out` may be exactly `in` (same pointer and stride), updated in place.
-    int finish(const void* in_place = nullptr) {
+    // The input added last, for finish.
+    int last() const { return n_ins_ - 1; }
+    // An output may be exactly the input number `in_place` (same pointer, width
+    // and stride), updated in place.
+    int finish(int in_place = -1) {
         if (status_ != MSS_OK) return status_;
         for (int i = 0; i < n_outs_; i++) {
             for (int j = 0; j < n_ins_; j++) {
                 const Rows& s = ins_[j];
-                if (in_place && outs_[i].p == in_place && s.p == in_place &&
+                if (j == in_place && outs_[i].p == s.p && outs_[i].width == s.width &&
                     outs_[i].stride == s.stride)
                     continue;
                 if (overlap(outs_[i], s)) return MSS_EALIAS;
@@ -400,12 +403,13 @@ int mss_add_norm(const mss_norm_dims* dims, const mss_norm_strides* strides, con
     Checks ck(strides != nullptr);
     ck.in(x, a.M, a.D, a.ld_x, e, true);
     if (residual) ck.in(residual, a.M, a.D, a.ld_res, er, false);
+    const int in_place = residual && residual == s ? ck.last() : -1;
     ck.in(w, a.D, 4, true);
     ck.in(b, a.D, 4, false);
     ck.in(scale, a.D, 4, false);
     ck.out(s, a.M, a.D, a.ld_s, er, true);
     ck.out(y, a.M, a.D, a.ld_y, e, true);
-    const int st = ck.finish(residual == s ? residual : nullptr);
+    const int st = ck.finish(in_place);
     if (st != MSS_OK || n == 0) return st;
     return launched(mss::launch_add_norm(a, stream));
 }
