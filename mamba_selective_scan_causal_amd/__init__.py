@@ -25,6 +25,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+from operator import index as _index
 
 from . import inputs  # noqa: F401  (seeded synthetic inputs; no method arithmetic)
 
@@ -595,20 +596,17 @@ def _dtype_codes():
     return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}     # MSS_F32, ...
 
 
-@functools.lru_cache(maxsize=1024)
 def make_gated_dims(batch, seq_len, d_inner, dtype, gate, gate_scale=8.0) -> GatedDims:
     """Parameter block of the mss_gated_* calls (dtype, gate: MSS_* codes)."""
     return GatedDims(ctypes.sizeof(GatedDims), 0, dtype, gate, batch, seq_len, d_inner,
                      gate_scale, 0)
 
 
-@functools.lru_cache(maxsize=1024)
 def make_gated_strides(*strides) -> GatedStrides:
     """Row strides x, r, i, z, y, dx, dr, di, dz (trailing ones may be left out)."""
     return GatedStrides(ctypes.sizeof(GatedStrides), 0, *strides)
 
 
-@functools.lru_cache(maxsize=1024)
 def make_norm_dims(rows, width, dtype, res_dtype, kind, order=0, groups=1, eps=1e-6,
                    alpha=1.0) -> NormDims:
     """Parameter block of the norm calls (dtype, res_dtype, kind, order: MSS_* codes)."""
@@ -616,10 +614,18 @@ def make_norm_dims(rows, width, dtype, res_dtype, kind, order=0, groups=1, eps=1
                     eps, alpha)
 
 
-@functools.lru_cache(maxsize=1024)
 def make_norm_strides(*strides) -> NormStrides:
     """Row strides x, z, residual, s, y, ds, dx, dz, dresidual (trailing ones may be left out)."""
     return NormStrides(ctypes.sizeof(NormStrides), 0, *strides)
+
+
+# The blocks that the calls below pass, which nobody else holds.  They are kept by
+# the values in them, so the calls make plain numbers of what they are given
+# first (a tensor would be kept by its identity, and alpha = -0.0 taken for 0.0).
+_gated_dims = functools.lru_cache(maxsize=1024)(make_gated_dims)
+_gated_strides = functools.lru_cache(maxsize=1024)(make_gated_strides)
+_norm_dims = functools.lru_cache(maxsize=1024)(make_norm_dims)
+_norm_strides = functools.lru_cache(maxsize=1024)(make_norm_strides)
 
 
 class _Call:
@@ -716,21 +722,29 @@ class _Call:
         return base + pad, max(0, workspace.numel() - pad), workspace
 
 
-@functools.lru_cache(maxsize=1024)
 def gated_workspace_bytes(op, *, batch, seq_len, d_inner, gate) -> int:
     """Workspace bytes of ``gated_scan`` (OP_GATED_SCAN) or ``gated_scan_backward``
     (OP_GATED_SCAN_BACKWARD)."""
-    dims = make_gated_dims(batch, seq_len, d_inner, 0, _choice(GATES, gate, "gate"))
+    return _gated_need(op, _index(batch), _index(seq_len), _index(d_inner), _choice(GATES, gate, "gate"))
+
+
+@functools.lru_cache(maxsize=1024)
+def _gated_need(op, batch, seq_len, d_inner, gate):
+    dims = make_gated_dims(batch, seq_len, d_inner, 0, gate)
     n = ctypes.c_size_t(0)
     _check("mss_gated_workspace_bytes",
            lib().mss_gated_workspace_bytes(ctypes.byref(dims), op, ctypes.byref(n)))
     return int(n.value)
 
 
-@functools.lru_cache(maxsize=1024)
 def norm_workspace_bytes(op, *, rows, width, groups=1) -> int:
     """Workspace bytes of ``add_norm_backward`` (OP_ADD_NORM_BACKWARD) or
     ``gated_norm_backward`` (OP_GATED_NORM_BACKWARD)."""
+    return _norm_need(op, _index(rows), _index(width), _index(groups))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_need(op, rows, width, groups):
     dims = make_norm_dims(rows, width, 0, 0, 0, 0, groups)
     n = ctypes.c_size_t(0)
     _check("mss_norm_workspace_bytes",
@@ -784,6 +798,7 @@ def gated_scan(x, r, i=None, decay=None, z=None, h0=None, reset=None, *, batch, 
     the final state (batch, D), both float32.
     ``workspace``: uint8 GPU tensor of at least ``gated_workspace_bytes(OP_GATED_SCAN, ...)``
     + 256 bytes (allocated here when omitted)."""
+    batch, seq_len, gate_scale = _index(batch), _index(seq_len), float(gate_scale)
     D, M = x.shape[-1], batch * seq_len
     c = _Call(x, "x", stream)
     code = _choice(GATES, gate, "gate")
@@ -791,11 +806,11 @@ def gated_scan(x, r, i=None, decay=None, z=None, h0=None, reset=None, *, batch, 
     y, py, ly = c.output(out, "out", M, D)
     ck = _flag(h_ckpt, (batch, gated_ckpt_steps(seq_len), D), c)
     hl = _flag(h_last, (batch, D), c, h0)
-    need = gated_workspace_bytes(OP_GATED_SCAN, batch=batch, seq_len=seq_len, d_inner=D, gate=gate)
+    need = _gated_need(OP_GATED_SCAN, batch, seq_len, D, code)
     wp, wn, _keep = c.workspace(need, workspace)
     _check("mss_gated_scan", lib().mss_gated_scan(
-        _ref(make_gated_dims(batch, seq_len, D, c.code, code, gate_scale)),
-        _ref(make_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
+        _ref(_gated_dims(batch, seq_len, D, c.code, code, gate_scale)),
+        _ref(_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
         c.dense(h0, "h0", (batch, D)), _reset(c, reset, M), py,
         c.dense(ck, "h_ckpt", (batch, gated_ckpt_steps(seq_len), D)),
         c.dense(hl, "h_last", (batch, D)), wp, wn, c.stream()))
@@ -813,6 +828,7 @@ def gated_scan_backward(x, r, i, decay, z, reset, h_ckpt, dout, *, batch, seq_le
     di and ddecay are None unless gate is "decay", dz is None when z is, dh0 unless
     ``need_dh0``.  ``out``: optional dict of output tensors for some of them (dx, dr, di, dz
     may be row-strided).  ``workspace`` as in gated_scan, with OP_GATED_SCAN_BACKWARD."""
+    batch, seq_len, gate_scale = _index(batch), _index(seq_len), float(gate_scale)
     D, M = x.shape[-1], batch * seq_len
     c = _Call(x, "x", stream)
     code = _choice(GATES, gate, "gate")
@@ -825,12 +841,11 @@ def gated_scan_backward(x, r, i, decay, z, reset, h_ckpt, dout, *, batch, seq_le
         "dh0": (need_dh0, (batch, D), f32, dh_last, False)})
     (pdx, ldx), (pdr, ldr), (pdi, ldi), (pdz, ldz) = at["dx"], at["dr"], at["di"], at["dz"]
     po, lo = c.rows(dout, "dout", M, D)
-    need = gated_workspace_bytes(OP_GATED_SCAN_BACKWARD, batch=batch, seq_len=seq_len, d_inner=D,
-                                 gate=gate)
+    need = _gated_need(OP_GATED_SCAN_BACKWARD, batch, seq_len, D, code)
     wp, wn, _keep = c.workspace(need, workspace)
     _check("mss_gated_scan_backward", lib().mss_gated_scan_backward(
-        _ref(make_gated_dims(batch, seq_len, D, c.code, code, gate_scale)),
-        _ref(make_gated_strides(lx, lr, li, lz, lo, ldx, ldr, ldi, ldz)), px, pr, pi, pdec, pz,
+        _ref(_gated_dims(batch, seq_len, D, c.code, code, gate_scale)),
+        _ref(_gated_strides(lx, lr, li, lz, lo, ldx, ldr, ldi, ldz)), px, pr, pi, pdec, pz,
         _reset(c, reset, M),
         c.dense(h_ckpt, "h_ckpt", (batch, gated_ckpt_steps(seq_len), D), required=True), po,
         c.dense(dh_last, "dh_last", (batch, D)), pdx, pdr, pdi,
@@ -865,14 +880,14 @@ def gated_step(x, r, i, decay, z, h, *, gate, gate_scale=8.0, out=None, stream=N
     """One token per sequence of ``gated_scan``: x, r, i, z (batch, D); updates ``h``
     (batch, D) float32 in place.  Returns y (batch, D)."""
     batch, D = x.shape
-    c = _Call(x, "x", stream)
+    c, gate_scale = _Call(x, "x", stream), float(gate_scale)
     code = _choice(GATES, gate, "gate")
     (px, lx), (pr, lr), (pi, li), pdec, (pz, lz) = _gated_inputs(c, x, r, i, decay, z, batch, D,
                                                                  gate)
     y, py, ly = c.output(out, "out", batch, D)
     _check("mss_gated_step", lib().mss_gated_step(
-        _ref(make_gated_dims(batch, 1, D, c.code, code, gate_scale)),
-        _ref(make_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
+        _ref(_gated_dims(batch, 1, D, c.code, code, gate_scale)),
+        _ref(_gated_strides(lx, lr, li, lz, ly)), px, pr, pi, pdec, pz,
         c.dense(h, "h", (batch, D), required=True), py, c.stream()))
     return y
 
@@ -893,7 +908,7 @@ def add_norm(x, residual, weight, bias=None, scale=None, *, kind="rms", eps=1e-6
     holds it.  ``residual_out`` may be ``residual`` itself: updated in place.  Rows of x,
     residual and the outputs may be strided."""
     M, D = x.shape
-    c = _Call(x, "x", stream)
+    c, eps, alpha = _Call(x, "x", stream), float(eps), float(alpha) + 0.0
     rt = (residual.dtype if residual is not None else
           residual_out.dtype if residual_out is not None else res_dtype or c.dtype)
     rc = _res_code(c, rt, "the residual stream")
@@ -902,8 +917,8 @@ def add_norm(x, residual, weight, bias=None, scale=None, *, kind="rms", eps=1e-6
     pr, lr = c.rows(residual, "residual", M, D, rt, False)
     y, py, ly = c.output(out, "out", M, D)
     _check("mss_add_norm", lib().mss_add_norm(
-        _ref(make_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
-        _ref(make_norm_strides(lx, 0, lr, ls, ly)), px, pr,
+        _ref(_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
+        _ref(_norm_strides(lx, 0, lr, ls, ly)), px, pr,
         c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)),
         c.dense(scale, "scale", (D,)), ps, py, c.stream()))
     return y, s
@@ -919,7 +934,7 @@ def add_norm_backward(s, weight, dy, ds=None, x=None, scale=None, *, bias=False,
     dbias (with ``bias``) and dscale (with ``scale``) float32.  ``out`` and ``workspace`` as in
     gated_scan_backward (``norm_workspace_bytes(OP_ADD_NORM_BACKWARD, ...)``)."""
     M, D = dy.shape
-    c = _Call(dy, "dy", stream)
+    c, eps, alpha = _Call(dy, "dy", stream), float(eps), float(alpha) + 0.0
     rc = _res_code(c, s.dtype, "s")
     g, at = _outputs(c, out, {
         "dx": (need_dx, (M, D), None, dy, True), "dresidual": (True, (M, D), s.dtype, s, True),
@@ -931,11 +946,10 @@ def add_norm_backward(s, weight, dy, ds=None, x=None, scale=None, *, bias=False,
     pds, lds = c.rows(ds, "ds", M, D, s.dtype, False)
     px, lx = c.rows(x, "x", M, D, required=scale is not None)
     (pdx, ldx), (pdr, ldr) = at["dx"], at["dresidual"]
-    wp, wn, _keep = c.workspace(norm_workspace_bytes(OP_ADD_NORM_BACKWARD, rows=M, width=D),
-                                workspace)
+    wp, wn, _keep = c.workspace(_norm_need(OP_ADD_NORM_BACKWARD, M, D, 1), workspace)
     _check("mss_add_norm_backward", lib().mss_add_norm_backward(
-        _ref(make_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
-        _ref(make_norm_strides(lx, 0, 0, ls, lo, lds, ldx, 0, ldr)), ps,
+        _ref(_norm_dims(M, D, c.code, rc, _choice(NORM_KINDS, kind, "kind"), 0, 1, eps, alpha)),
+        _ref(_norm_strides(lx, 0, 0, ls, lo, lds, ldx, 0, ldr)), ps,
         c.dense(weight, "weight", (D,), required=True), po, pds, px,
         c.dense(scale, "scale", (D,)), pdx, pdr, at["dweight"][0], at["dbias"][0], at["dscale"][0],
         wp, wn, c.stream()))
@@ -952,15 +966,15 @@ def gated_norm(x, z, weight, bias=None, residual=None, scale=None, *, groups=1, 
     z, residual may be None; weight, bias, scale (D,) float32; the norm runs over each of
     ``groups`` equal groups of channels."""
     M, D = x.shape
-    c = _Call(x, "x", stream)
+    c, groups, eps, alpha = _Call(x, "x", stream), _index(groups), float(eps), float(alpha) + 0.0
     px, lx = c.rows(x, "x", M, D)
     pz, lz = c.rows(z, "z", M, D, required=False)
     pr, lr = c.rows(residual, "residual", M, D, required=False)
     y, py, ly = c.output(out, "out", M, D)
     _check("mss_gated_norm", lib().mss_gated_norm(
-        _ref(make_norm_dims(M, D, c.code, c.code, _choice(NORM_KINDS, kind, "kind"),
+        _ref(_norm_dims(M, D, c.code, c.code, _choice(NORM_KINDS, kind, "kind"),
                             _choice(GATE_ORDERS, order, "order"), groups, eps, alpha)),
-        _ref(make_norm_strides(lx, lz, lr, 0, ly)), px, pz,
+        _ref(_norm_strides(lx, lz, lr, 0, ly)), px, pz,
         c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)), pr,
         c.dense(scale, "scale", (D,)), py, c.stream()))
     return y
@@ -974,7 +988,7 @@ def gated_norm_backward(x, z, weight, bias, scale, dout, *, groups=1, order="bef
     dscale (with ``scale``) float32.  ``out`` and ``workspace`` as in gated_scan_backward
     (``norm_workspace_bytes(OP_GATED_NORM_BACKWARD, ...)``)."""
     M, D = x.shape
-    c = _Call(x, "x", stream)
+    c, groups, eps, alpha = _Call(x, "x", stream), _index(groups), float(eps), float(alpha) + 0.0
     g, at = _outputs(c, out, {
         "dx": (True, (M, D), None, x, True), "dz": (z is not None, (M, D), None, z, True),
         "dweight": (True, (D,), c.f32, weight, False),
@@ -984,12 +998,11 @@ def gated_norm_backward(x, z, weight, bias, scale, dout, *, groups=1, order="bef
     pz, lz = c.rows(z, "z", M, D, required=False)
     po, lo = c.rows(dout, "dout", M, D)
     (pdx, ldx), (pdz, ldz) = at["dx"], at["dz"]
-    wp, wn, _keep = c.workspace(
-        norm_workspace_bytes(OP_GATED_NORM_BACKWARD, rows=M, width=D, groups=groups), workspace)
+    wp, wn, _keep = c.workspace(_norm_need(OP_GATED_NORM_BACKWARD, M, D, groups), workspace)
     _check("mss_gated_norm_backward", lib().mss_gated_norm_backward(
-        _ref(make_norm_dims(M, D, c.code, c.code, _choice(NORM_KINDS, kind, "kind"),
+        _ref(_norm_dims(M, D, c.code, c.code, _choice(NORM_KINDS, kind, "kind"),
                             _choice(GATE_ORDERS, order, "order"), groups, eps, alpha)),
-        _ref(make_norm_strides(lx, lz, 0, 0, lo, 0, ldx, ldz)), px, pz,
+        _ref(_norm_strides(lx, lz, 0, 0, lo, 0, ldx, ldz)), px, pz,
         c.dense(weight, "weight", (D,), required=True), c.dense(bias, "bias", (D,)),
         c.dense(scale, "scale", (D,)), po, pdx, pdz, at["dweight"][0], at["dbias"][0], at["dscale"][0],
         wp, wn, c.stream()))
