@@ -77,7 +77,10 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_kernel(Nor
         read(m + at.step, next);
         if (spots.shared) {
 #pragma unroll
-            for (int j = 0; j < NC; j++) r.x[j].clear(spots.s[j]);
+            for (int j = 0; j < NC; j++) {
+                r.x[j].clear(spots.s[j]);
+                r.z[j].clear(spots.s[j]);   // 0 times an infinite gate is NaN
+            }
         }
         float v[NC][V];
         float mean = 0.0f;
@@ -183,6 +186,7 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
 #pragma unroll
             for (int j = 0; j < NC; j++) {
                 r.x[j].clear(spots.s[j]);
+                r.z[j].clear(spots.s[j]);
                 r.d[j].clear(spots.s[j]);
             }
         }
