@@ -851,16 +851,25 @@ Chain chain_of(const GatedArgs& a, int V, int64_t len) {
     Chain g;
     g.ctiles = static_cast<unsigned>(cdiv(a.D, 64 * V));
     g.tiles = static_cast<unsigned>(a.B * g.ctiles);
-    // Sets of tiles that stay on an XCD read the lines that neighbouring tiles
-    // share once, but move the XCDs' places in the tensors apart, which costs
-    // more the wider the rows are.  Forward and backward, without / with sets:
-    // fp32 64 tiles 71 / 59 us, 256 tiles 398 / 385, 320 tiles 936 / 963, but
-    // 320 and 1024 tiles of rows that start inside a 128-byte line 620 / 581
-    // and 633 / 540; bf16 decay 64 tiles 199 / 192, 96 tiles 156 / 147, 128
-    // tiles 641 / 680.  Only equal sets, so that the XCDs end together.
-    const bool off_line = a.dtype == MSS_F32 && (a.ld_x | a.ld_r | a.ld_y) % 32 != 0;
-    const unsigned most = off_line ? UINT32_MAX : a.dtype == MSS_F32 ? 288 : 112;
-    g.sets = g.tiles % 8 == 0 && g.tiles >= 64 && g.tiles <= most ? 8 : 1;
+    // Sets of tiles that stay on an XCD let neighbouring tiles meet in one L2,
+    // where they share lines if rows start inside one (a stride that is no
+    // multiple of 128 bytes), but move the XCDs' places in the tensors apart,
+    // which costs once a tensor is as large as the last-level cache.  Forward and
+    // backward in us, without / with sets (sigmoid gate but where said), for
+    // strides that end inside a line: fp32 B4 D5119 277 / 244 (126 MB a tensor)
+    // and 1293 / 1178 (598 MB), B8 D511 1391 / 1207 (600 MB), bf16 B8 D2047 279 /
+    // 256 (130 MB) and 1389 / 1228 (599 MB); for whole lines: fp32 B8 L1920 D2048
+    // 200 / 183, B8 L12160 D512 303 / 302 (199 MB), B8 L16384 D512 390 / 408 (268
+    // MB), B4 L8192 D5120 935 / 967 (671 MB), B8 L4096 D4096 768 / 833 (537 MB);
+    // bf16 B8 D1536 decay L2048 147 / 141 and L8128 488 / 489 (200 MB), L16384 623
+    // / 651 (403 MB).  (Beyond 200 MB some gain: fp32 B8 L9152 D2048 903 / 863.)
+    // A tensor that only begins inside a line, or one of several with such a
+    // stride, is within 3 % either way.  Only equal sets, so that the XCDs end
+    // together, of eight tiles or more.
+    const int64_t elem = a.dtype == MSS_F32 ? 4 : 2;
+    const bool off_line = (a.ld_x | a.ld_r | a.ld_y) * elem % 128 != 0;
+    const bool small = a.B * a.L * a.D * elem <= int64_t{200} << 20;
+    g.sets = g.tiles % 8 == 0 && g.tiles >= 64 && (off_line || small) ? 8 : 1;
     g.each = g.tiles / g.sets;
     g.chunks = cdiv(a.L, len);
     // With few tiles the handovers between groups are what takes the time, and
