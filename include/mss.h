@@ -364,7 +364,11 @@ int mss_ssd_time_split(const mss_ssd_dims* dims, int64_t* segment_steps);
  * and gradients of rows on the other (ddecay, a sum over all rows, excepted).
  * Time is cut into chunks of up to 128 steps that are combined as affine maps
  * of the state: with MSS_GATE_LOG and r > 0 (growing states) the product of a
- * chunk's factors must stay finite.
+ * chunk's factors must stay finite.  A chunk waits for the state that enters it
+ * from the one before: the wait ends by itself (a launch hands its chunks out in
+ * order), and is bounded besides.  Past the bound, seconds for what takes
+ * microseconds, the call's outputs are NaN from there on, although it returned
+ * MSS_OK.
  * The activations x, r, i, z, y and their gradients are of type dims->dtype;
  * the states, decay and its gradient are fp32.  States are carried in fp32
  * and results are rounded once, to the nearest even.                       */

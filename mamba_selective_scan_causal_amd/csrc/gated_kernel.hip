@@ -31,11 +31,12 @@
 // no fences.  A first small kernel sets them, and the counter, in the
 // workspace.
 //
-// Measured (median of a trace): forward B1 L65536 D2560 bf16 decay + gate
-// 316 us (5.3 TB/s), B4 L8192 D5120 fp32 sigmoid + gate 440 us (6.1 TB/s),
-// B8 L2048 D1536 bf16 decay 52 us (VALU busy 63 %); backward of the last two
-// 812 us (5.8 TB/s) and 88 us (VALU busy 85 %, its bound: 90 instructions per
-// element).  HBM traffic is 1.03 times what the tensors hold.
+// Measured, a call of a row of calls (its other launches included) and the
+// kernel's median in a trace: forward B1 L65536 D2560 bf16 decay + gate 319 and
+// 328 us (5.3 TB/s), B4 L8192 D5120 fp32 sigmoid + gate 457 and 444 us (6.1
+// TB/s), B8 L2048 D1536 bf16 decay 56 and 46 us (VALU busy 67 %); backward of the
+// last two 839 and 811 us (5.8 TB/s), 97 and 86 us (VALU busy 86 %, its bound: 89
+// instructions per element).  HBM traffic is 1.03 times what the tensors hold.
 #include "block_math.h"
 #include "launch_block.h"
 
@@ -762,8 +763,8 @@ __global__ __launch_bounds__(1024) void gated_ddecay_kernel(const float* __restr
 }
 
 // One token: lanes side by side over (sequence, vector of 4 channels), every
-// access 8 or 16 bytes.  B4 D1536 bf16 3.4 us (a launch's latency), B256 D5120
-// fp32 4.7 us (31 MB from the last-level cache).
+// access 8 or 16 bytes.  B4 D1536 bf16 3.3 us (a launch's latency), B256 D5120
+// fp32 4.8 us (31 MB from the last-level cache).
 constexpr int kStepVec = 4;
 template <typename T, int GATE>
 __global__ __launch_bounds__(64) void gated_step_kernel(GatedArgs q, unsigned per) {

@@ -4,8 +4,8 @@
 // Bound by HBM: the forward reads x, z (and the residual) and writes y, the
 // backward reads x, z, dout and writes dx, dz, each once.  The outputs carry
 // the nontemporal hint (M 32768 D 5120 bf16: forward 197 -> 188 us, backward
-// 418 -> 405).  That size now: forward 194 us (5.2 TB/s), backward 307 us
-// (5.5 TB/s; VALU busy 65 %).
+// 418 -> 405).  That size now, a call of a row of calls (with the parameters'
+// sums): forward 209 us (4.8 TB/s), backward 318 us (5.3 TB/s; VALU busy 65 %).
 #include "norm_common.h"
 
 namespace mss {
@@ -278,6 +278,9 @@ __global__ __launch_bounds__((kMaxThreads<TEAM, NC>)) void gated_norm_bwd_kernel
 }
 
 // ---- groups too wide for the registers -------------------------------------------
+// A pass over the row per round of sums, element by element, and parameter sums
+// in memory: M 8192 D 8192 fp32 301 us forward and 837 us backward, where 805 and
+// 1342 MB would take 158 and 264 at a copy's rate (D 6144, held: 106 and 190).
 
 constexpr int kWide = 1024;
 
