@@ -273,10 +273,9 @@ def _stream(stream):
 
 
 def _empty(shape, like, stream=None, dtype=None):
-    def make():
-        return _torch().empty(shape, dtype=dtype or like.dtype, device=like.device)
-
-    return make() if stream is None else _own_memory(stream, make)
+    if stream is not None:
+        return _own_memory(stream, lambda: _empty(shape, like, dtype=dtype))
+    return _torch().empty(shape, dtype=dtype or like.dtype, device=like.device)
 
 
 def _own_memory(stream, make):
