@@ -477,7 +477,7 @@ typedef struct mss_norm_dims {
     int64_t rows;           /* M */
     int64_t width;          /* D */
     int64_t groups;         /* divides D, at most 2^20 (add_norm: 1) */
-    float eps;              /* finite, > 0 */
+    float eps;              /* > 0, a normal number (2^-126 or more, finite) */
     float alpha;            /* scalar factor of the residual scale, finite */
 } mss_norm_dims;
 

@@ -184,7 +184,7 @@ bool norm_ok(const mss_norm_dims* d, const mss_norm_strides* s, bool add) {
     if (d->kind != MSS_NORM_RMS && d->kind != MSS_NORM_LAYER) return false;
     if (d->rows < 0 || d->width < 0 || d->groups < 1 || d->width % d->groups != 0) return false;
     if (d->width > MSS_MAX_WIDTH || d->groups > (1 << 20)) return false;
-    if (!(std::isfinite(d->eps) && d->eps > 0.0f) || !std::isfinite(d->alpha)) return false;
+    if (!(std::isnormal(d->eps) && d->eps > 0.0f) || !std::isfinite(d->alpha)) return false;
     if (add) {
         if (d->groups != 1 || d->order != 0) return false;
         if (d->res_dtype != d->dtype && d->res_dtype != MSS_F32) return false;
