@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define MSS_VERSION 3
+#define MSS_VERSION 4
 
 /* Status codes. */
 #define MSS_OK 0
@@ -540,6 +540,142 @@ int mss_gated_norm_backward(const mss_norm_dims* dims, const mss_norm_strides* s
                             const float* scale, const void* dout, void* dx, void* dz, float* dw,
                             float* db, float* dscale, void* workspace, size_t workspace_bytes,
                             hipStream_t stream);
+
+/* ---- The ends of a model ------------------------------------------------------
+ * What stands before the first block and after the last one (the pages'
+ * cpuModelForward / cpuModelLoss / cpuModelBackward: token rows of a table,
+ * the head on the final norm and its cross entropy), and the clipping of the
+ * gradients before the update (the trainer's maxGradNorm).  Tables, rows and
+ * their gradients are of type MSS_F32, MSS_BF16 or MSS_F16; losses, log sums
+ * and norms are fp32, sums at least that.  Results are deterministic (every
+ * sum runs in a fixed order), gradients are written once and rounded once.
+ *
+ * Token ids and targets are int32 or int64 (id_bytes 4 or 8).  One outside
+ * 0 .. vocab-1 is no error: it marks a padded place (or a token that another
+ * shard of the table holds).
+ *
+ * Row strides in elements, as in mss_gated_strides (NULL: dense rows).  With
+ * strides given the tensors need only their element's alignment, except x and
+ * weight of the head where a row is a multiple of 16 bytes long: their rows
+ * must then start at multiples of 16 bytes (MSS_EALIGN).  Ids, targets and
+ * tensors of one value per row need their element's alignment.             */
+#define MSS_EMBED_ACCUMULATE 1
+typedef struct mss_embed_dims {
+    int32_t struct_size;    /* sizeof(mss_embed_dims) */
+    int32_t flags;          /* 0, or MSS_EMBED_ACCUMULATE (backward only) */
+    int32_t dtype;          /* of the table and its gradient */
+    int32_t out_dtype;      /* of y and dy: dtype or MSS_F32; any where dtype is MSS_F32 */
+    int32_t id_bytes;       /* 4 or 8 */
+    int32_t reserved;       /* must be 0 */
+    int64_t rows;           /* M, below 2^26 */
+    int64_t vocab;          /* V, below 2^26 */
+    int64_t width;          /* D, at most MSS_MAX_WIDTH */
+    float scale;            /* finite */
+    int32_t reserved2;      /* must be 0 */
+} mss_embed_dims;
+
+typedef struct mss_embed_strides {
+    int32_t struct_size;    /* sizeof(mss_embed_strides) */
+    int32_t reserved;       /* must be 0 */
+    int64_t weight;         /* the table, or its gradient */
+    int64_t y;              /* y, or dy */
+} mss_embed_strides;
+
+/* y_m = scale weight[id_m]; zeros where id_m marks a padded place.
+ *   ids (M);  weight (V, D) dtype;  y (M, D) out_dtype                     */
+int mss_embedding(const mss_embed_dims* dims, const mss_embed_strides* strides, const void* ids,
+                  const void* weight, void* y, hipStream_t stream);
+
+/* Its gradient: dweight_v = scale sum_{m: id_m = v} dy_m, in the order of m.
+ * Every row of dweight is written (zeros where v does not occur); with
+ * MSS_EMBED_ACCUMULATE the sums are added to what dweight holds, and only the
+ * rows that occur are touched (a table tied to the head: after
+ * mss_head_loss_backward has written its part).
+ *   ids (M);  dy (M, D) out_dtype;  dweight (V, D) dtype                    */
+int mss_embedding_backward(const mss_embed_dims* dims, const mss_embed_strides* strides,
+                           const void* ids, const void* dy, void* dweight, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace size in bytes of mss_embedding_backward, under the rules of
+ * mss_gated_workspace_bytes. */
+int mss_embed_workspace_bytes(const mss_embed_dims* dims, size_t* bytes);
+
+typedef struct mss_head_dims {
+    int32_t struct_size;    /* sizeof(mss_head_dims) */
+    int32_t flags;          /* must be 0 */
+    int32_t dtype;          /* of x, weight and their gradients */
+    int32_t id_bytes;       /* of the targets: 4 or 8 */
+    int64_t rows;           /* M, below 2^26 */
+    int64_t vocab;          /* V, 1 .. 2^26 - 1 */
+    int64_t width;          /* D, 1 .. MSS_MAX_WIDTH */
+    float logit_scale;      /* finite */
+    int32_t reserved;       /* must be 0 */
+} mss_head_dims;
+
+typedef struct mss_head_strides {
+    int32_t struct_size;    /* sizeof(mss_head_strides) */
+    int32_t reserved;       /* must be 0 */
+    int64_t x, weight, dx, dweight;
+} mss_head_strides;
+
+#define MSS_OP_HEAD_LOSS 8
+#define MSS_OP_HEAD_LOSS_BACKWARD 9
+/* Workspace size in bytes of the head calls, under the rules of
+ * mss_gated_workspace_bytes. */
+int mss_head_workspace_bytes(const mss_head_dims* dims, int op, size_t* bytes);
+
+/* Softmax cross entropy of the logits l_mv = logit_scale x_m . weight_v,
+ * which are never stored (the vocabulary goes by in tiles):
+ *   lse_m  = log sum_v exp(l_mv)
+ *   loss_m = lse_m - l_{m, t_m}; 0 where t_m marks a padded place
+ *   x (M, D), weight (V, D) dtype;  targets (M);  loss, lse (M) fp32
+ * Logits are sums of exact products in fp32.                               */
+int mss_head_loss(const mss_head_dims* dims, const mss_head_strides* strides, const void* x,
+                  const void* weight, const void* targets, float* loss, float* lse,
+                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Its gradients against dloss (M) and dlse (M) (NULL = 0), with the forward's
+ * lse:
+ *   dl_mv = (dloss_m + dlse_m) exp(l_mv - lse_m) - dloss_m [v = t_m]
+ *   dx = logit_scale dl weight,  dweight = logit_scale dl^T x
+ * A padded row takes no part: its dx is 0, and its x, dloss and dlse are not
+ * used (they may be NaN).  dl is computed a piece of the vocabulary at a time
+ * and held in dtype for the two products, times a power of two that brings
+ * the largest |dloss| + |dlse| near 2^13 (so that fp16 does not lose the
+ * small ones): in 2-byte types each of its values is rounded once.
+ *   dx (M, D), dweight (V, D) dtype: each computed where given.            */
+int mss_head_loss_backward(const mss_head_dims* dims, const mss_head_strides* strides,
+                           const void* x, const void* weight, const void* targets,
+                           const float* lse, const float* dloss, const float* dlse, void* dx,
+                           void* dweight, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/* One of a list of tensors: numel elements, dense, at their element's
+ * alignment.  The list itself is host memory, read before the call returns. */
+typedef struct mss_tensor {
+    const void* in;
+    void* out;              /* mss_clip_grads: may be `in` (updated in place) */
+    int64_t numel;
+    int32_t dtype;          /* MSS_F32, MSS_BF16 or MSS_F16 */
+    int32_t out_dtype;      /* dtype or MSS_F32 */
+} mss_tensor;
+
+/* Workspace size in bytes of the two calls below for `count` tensors, under
+ * the rules of mss_gated_workspace_bytes. */
+int mss_clip_workspace_bytes(int64_t count, size_t* bytes);
+
+/* norm[0] = scale sqrt(sum of all elements' squares); squares and sums are
+ * fp64.  `out` and `out_dtype` are ignored; scale is finite and > 0.
+ * An empty list has norm 0.                                                */
+int mss_grad_norm(const mss_tensor* tensors, int64_t count, float scale, float* norm,
+                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The norm, and out = in * scale * min(1, max_norm / norm).  Where a value is
+ * infinite or NaN out = in: nothing is lost, and the caller sees it in norm[0]
+ * (where finite values' norm exceeds fp32, norm[0] is infinite as well, but they
+ * are clipped).  max_norm is finite and >= 0.  No tensor may overlap another, in place apart.  */
+int mss_clip_grads(const mss_tensor* tensors, int64_t count, float scale, float max_norm,
+                   float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Human-readable text for a status code (static storage). */
 const char* mss_strerror(int status);

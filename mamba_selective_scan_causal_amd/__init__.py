@@ -15,7 +15,10 @@ Single-token step: x, z, delta, y : (batch, D); B, C : (batch, N);
 The gated linear recurrence (``gated_scan``, ``gated_scan_backward``,
 ``gated_step``) and the norms before and after a block (``add_norm``,
 ``gated_norm`` and their backward passes) take activations in float32,
-bfloat16 or float16, row-strided where that is handy; see each function.
+bfloat16 or float16, row-strided where that is handy; see each function.  So do
+the two ends of a model, the embedding (``embedding``) and the head with its
+loss (``head_loss``), with their backward passes; ``grad_norm`` and
+``clip_grads`` take lists of gradients of any of these types.
 
 A call given ``stream=`` allocates what it returns, and its workspace, as that
 stream's own memory.
@@ -112,6 +115,36 @@ class NormStrides(ctypes.Structure):
                                                 "dresidual"))]
 
 
+class EmbedDims(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("id_bytes", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("reserved2", ctypes.c_int32)]
+
+
+class EmbedStrides(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("weight", ctypes.c_int64), ("y", ctypes.c_int64)]
+
+
+class HeadDims(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("id_bytes", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("logit_scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class HeadStrides(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                *((n, ctypes.c_int64) for n in ("x", "weight", "dx", "dweight"))]
+
+
+class ListTensor(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
 EXPORTS = ("mss_conv1d_silu", "mss_selective_scan", "mss_mamba1_core", "mss_selective_step",
            "mss_selective_scan_strided", "mss_mamba1_core_strided",
            "mss_workspace_bytes", "mss_selective_scan_backward", "mss_conv1d_silu_backward",
@@ -120,6 +153,9 @@ EXPORTS = ("mss_conv1d_silu", "mss_selective_scan", "mss_mamba1_core", "mss_sele
            "mss_gated_workspace_bytes", "mss_gated_scan", "mss_gated_scan_backward",
            "mss_gated_step", "mss_norm_workspace_bytes", "mss_add_norm", "mss_add_norm_backward",
            "mss_gated_norm", "mss_gated_norm_backward",
+           "mss_embedding", "mss_embedding_backward", "mss_embed_workspace_bytes",
+           "mss_head_workspace_bytes", "mss_head_loss", "mss_head_loss_backward",
+           "mss_clip_workspace_bytes", "mss_grad_norm", "mss_clip_grads",
            "mss_strerror", "mss_version", "mss_last_hip_error")
 
 OP_SELECTIVE_SCAN_BACKWARD = 1
@@ -129,6 +165,9 @@ OP_GATED_SCAN = 4
 OP_GATED_SCAN_BACKWARD = 5
 OP_ADD_NORM_BACKWARD = 6
 OP_GATED_NORM_BACKWARD = 7
+OP_HEAD_LOSS = 8
+OP_HEAD_LOSS_BACKWARD = 9
+EMBED_ACCUMULATE = 1                  # MSS_EMBED_ACCUMULATE
 GATED_CKPT_STEPS = 64                 # MSS_GATED_CKPT_STEPS
 MAX_WIDTH = 1 << 28                   # MSS_MAX_WIDTH
 NOALLOC_SCRATCH_BYTES = 256 << 20     # MSS_NOALLOC_SCRATCH_BYTES
@@ -178,6 +217,22 @@ def lib():
         L.mss_add_norm_backward.argtypes = [nd, ns] + [p] * 12 + [sz, p]
         L.mss_gated_norm.argtypes = [nd, ns] + [p] * 8
         L.mss_gated_norm_backward.argtypes = [nd, ns] + [p] * 12 + [sz, p]
+        ed, es = ctypes.POINTER(EmbedDims), ctypes.POINTER(EmbedStrides)
+        hd, hs = ctypes.POINTER(HeadDims), ctypes.POINTER(HeadStrides)
+        lt, f32, i64 = ctypes.POINTER(ListTensor), ctypes.c_float, ctypes.c_int64
+        L.mss_embedding.argtypes = [ed, es] + [p] * 4
+        L.mss_embedding_backward.argtypes = [ed, es] + [p] * 4 + [sz, p]
+        L.mss_embed_workspace_bytes.argtypes = [ed, ctypes.POINTER(sz)]
+        L.mss_head_workspace_bytes.argtypes = [hd, i, ctypes.POINTER(sz)]
+        L.mss_head_loss.argtypes = [hd, hs] + [p] * 6 + [sz, p]
+        L.mss_head_loss_backward.argtypes = [hd, hs] + [p] * 9 + [sz, p]
+        L.mss_clip_workspace_bytes.argtypes = [i64, ctypes.POINTER(sz)]
+        L.mss_grad_norm.argtypes = [lt, i64, f32, p, p, sz, p]
+        L.mss_clip_grads.argtypes = [lt, i64, f32, f32, p, p, sz, p]
+        for f in ("mss_embedding", "mss_embedding_backward", "mss_embed_workspace_bytes",
+                  "mss_head_workspace_bytes", "mss_head_loss", "mss_head_loss_backward",
+                  "mss_clip_workspace_bytes", "mss_grad_norm", "mss_clip_grads"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("mss_gated_workspace_bytes", "mss_gated_scan", "mss_gated_scan_backward",
                   "mss_gated_step", "mss_norm_workspace_bytes", "mss_add_norm",
                   "mss_add_norm_backward", "mss_gated_norm", "mss_gated_norm_backward"):
@@ -1006,3 +1061,278 @@ def gated_norm_backward(x, z, weight, bias, scale, dout, *, groups=1, order="bef
         c.dense(scale, "scale", (D,)), po, pdx, pdz, at["dweight"][0], at["dbias"][0], at["dscale"][0],
         wp, wn, c.stream()))
     return g
+
+
+# ---- the ends of a model -------------------------------------------------------
+
+def make_embed_dims(rows, vocab, width, dtype, out_dtype, id_bytes, scale=1.0, accumulate=False) -> EmbedDims:
+    """Parameter block of the embedding calls (dtype: the table's, out_dtype: the rows', MSS_* codes)."""
+    return EmbedDims(ctypes.sizeof(EmbedDims), EMBED_ACCUMULATE if accumulate else 0, dtype, out_dtype,
+                     id_bytes, 0, rows, vocab, width, scale, 0)
+
+
+def make_embed_strides(weight, y) -> EmbedStrides:
+    return EmbedStrides(ctypes.sizeof(EmbedStrides), 0, weight, y)
+
+
+def make_head_dims(rows, vocab, width, dtype, id_bytes, logit_scale=1.0) -> HeadDims:
+    """Parameter block of the head calls (dtype: MSS_* code)."""
+    return HeadDims(ctypes.sizeof(HeadDims), 0, dtype, id_bytes, rows, vocab, width, logit_scale, 0)
+
+
+def make_head_strides(*strides) -> HeadStrides:
+    """Row strides x, weight, dx, dweight (trailing ones may be left out)."""
+    return HeadStrides(ctypes.sizeof(HeadStrides), 0, *strides)
+
+
+_embed_dims = functools.lru_cache(maxsize=1024)(make_embed_dims)
+_embed_strides = functools.lru_cache(maxsize=1024)(make_embed_strides)
+_head_dims = functools.lru_cache(maxsize=1024)(make_head_dims)
+_head_strides = functools.lru_cache(maxsize=1024)(make_head_strides)
+
+
+def embed_workspace_bytes(*, rows, vocab, width) -> int:
+    """Workspace bytes of ``embedding_backward``."""
+    return _embed_need(_index(rows), _index(vocab), _index(width))
+
+
+@functools.lru_cache(maxsize=1024)
+def _embed_need(rows, vocab, width):
+    dims = make_embed_dims(rows, vocab, width, 0, 0, 8)
+    n = ctypes.c_size_t(0)
+    _check("mss_embed_workspace_bytes", lib().mss_embed_workspace_bytes(ctypes.byref(dims), ctypes.byref(n)))
+    return int(n.value)
+
+
+def head_workspace_bytes(op, *, rows, vocab, width, dtype) -> int:
+    """Workspace bytes of ``head_loss`` (OP_HEAD_LOSS) or ``head_loss_backward``
+    (OP_HEAD_LOSS_BACKWARD); ``dtype``: the torch type of x."""
+    return _head_need(op, _index(rows), _index(vocab), _index(width), _dtype_code(dtype, "dtype"))
+
+
+@functools.lru_cache(maxsize=1024)
+def _head_need(op, rows, vocab, width, code):
+    dims = make_head_dims(rows, vocab, width, code, 8)
+    n = ctypes.c_size_t(0)
+    _check("mss_head_workspace_bytes", lib().mss_head_workspace_bytes(ctypes.byref(dims), op, ctypes.byref(n)))
+    return int(n.value)
+
+
+def clip_workspace_bytes(count) -> int:
+    """Workspace bytes of ``grad_norm`` and ``clip_grads`` for ``count`` tensors."""
+    return _clip_need(_index(count))
+
+
+@functools.lru_cache(maxsize=1024)
+def _clip_need(count):
+    n = ctypes.c_size_t(0)
+    _check("mss_clip_workspace_bytes", lib().mss_clip_workspace_bytes(count, ctypes.byref(n)))
+    return int(n.value)
+
+
+def _dtype_code(dtype, name):
+    code = _dtype_codes().get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _ids(c, t, name, rows):
+    """(pointer, bytes of an id) of a tensor of token ids."""
+    if not isinstance(t, c.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is c.torch.int64:
+        return c.dense(t, name, (rows,), c.torch.int64, True), 8
+    return c.dense(t, name, (rows,), c.torch.int32, True), 4
+
+
+def _id_rows(ids, name):
+    """The number of ids, before there is anything to check them against."""
+    if not isinstance(ids, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if ids.dim() != 1:
+        raise ValueError(f"{name} must have one dimension, got shape {tuple(ids.shape)}")
+    return ids.shape[0]
+
+
+def embedding(ids, weight, *, scale=1.0, out_dtype=None, out=None, stream=None):
+    """Rows of a table by token: y_m = scale weight[ids_m].  Returns y (M, D).
+
+    ids (M,) int64 or int32; one outside 0 .. V-1 marks a padded place (or a token that another
+    shard of the table holds): its row is zeros.  weight (V, D) float32, bfloat16 or float16;
+    y of ``out_dtype`` (weight's by default): weight's type or float32, or any of the three where
+    weight is float32.  Rows of weight and out may be strided."""
+    M = _id_rows(ids, "ids")
+    c, scale = _Call(weight, "weight", stream), float(scale) + 0.0
+    V, D = weight.shape
+    yt = out.dtype if out is not None else out_dtype or c.dtype
+    yc = _dtype_code(yt, "the output")
+    if yc and c.code and yc != c.code:
+        raise TypeError(f"the output must be {c.dtype} or float32, got {yt}")
+    pid, nid = _ids(c, ids, "ids", M)
+    pw, lw = c.rows(weight, "weight", V, D)
+    y, py, ly = c.output(out, "out", M, D, yt)
+    _check("mss_embedding", lib().mss_embedding(
+        _ref(_embed_dims(M, V, D, c.code, yc, nid, scale)), _ref(_embed_strides(lw, ly)), pid, pw, py,
+        c.stream()))
+    return y
+
+
+def embedding_backward(ids, dy, *, vocab, scale=1.0, dtype=None, accumulate=False, out=None,
+                       workspace=None, stream=None):
+    """Gradient of ``embedding`` against dy (M, D): dweight (vocab, D), in ``dtype`` (dy's by default).
+
+    Row v is scale times the sum of the dy of the places where v stands, in their order, in fp32;
+    zeros where it does not occur.  ``accumulate``: the sums are added to ``out``, which is then
+    required, and its other rows are left as they are (a table tied to the head: ``out`` holds
+    the dweight of ``head_loss_backward``).  dy and dweight of the same type, or one of them
+    float32; rows of dy and out may be strided.  ``workspace``: uint8 GPU tensor of at least
+    ``embed_workspace_bytes(...)`` + 256 bytes (allocated here when omitted)."""
+    M, V = _id_rows(ids, "ids"), _index(vocab)
+    c, scale = _Call(dy, "dy", stream), float(scale) + 0.0
+    D = dy.shape[-1]
+    wt = out.dtype if out is not None else dtype or c.dtype
+    wc = _dtype_code(wt, "dweight")
+    if wc and c.code and wc != c.code:
+        raise TypeError(f"dweight must be {c.dtype} or float32, got {wt}")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out, the gradient to add to")
+    if V < 0:
+        raise ValueError(f"vocab must not be negative, got {V}")
+    pid, nid = _ids(c, ids, "ids", M)
+    pd, ld = c.rows(dy, "dy", M, D)
+    dw, pw, lw = c.output(out, "out", V, D, wt)
+    wp, wn, _keep = c.workspace(_embed_need(M, V, D), workspace)
+    _check("mss_embedding_backward", lib().mss_embedding_backward(
+        _ref(_embed_dims(M, V, D, wc, c.code, nid, scale, bool(accumulate))), _ref(_embed_strides(lw, ld)),
+        pid, pd, pw, wp, wn, c.stream()))
+    return dw
+
+
+def head_loss(x, weight, targets, *, logit_scale=1.0, out=None, workspace=None, stream=None):
+    """Softmax cross entropy of the logits logit_scale x weight^T, which are not kept.
+    Returns (loss, lse), both (M,) float32.
+
+    x (M, D), weight (V, D) float32, bfloat16 or float16, both the same, rows may be strided
+    (starting at multiples of 16 bytes where a row is a multiple of 16 bytes long);
+    targets (M,) int64 or int32.  lse_m is the log of the sum of the exponentials, loss_m = lse_m
+    minus the target's logit; a target outside 0 .. V-1 marks a padded row, whose loss is 0.
+    ``out``: optional pair of output tensors.  ``workspace``: uint8 GPU tensor of at least
+    ``head_workspace_bytes(OP_HEAD_LOSS, ...)`` + 256 bytes (allocated here when omitted)."""
+    c, logit_scale = _Call(x, "x", stream), float(logit_scale) + 0.0
+    M, D = x.shape
+    V = weight.shape[0]
+    px, lx = c.rows(x, "x", M, D)
+    pw, lw = c.rows(weight, "weight", V, D)
+    pt, nt = _ids(c, targets, "targets", M)
+    loss, lse = out if out is not None else (c.empty((M,), c.f32), c.empty((M,), c.f32))
+    wp, wn, _keep = c.workspace(_head_need(OP_HEAD_LOSS, M, V, D, c.code), workspace)
+    _check("mss_head_loss", lib().mss_head_loss(
+        _ref(_head_dims(M, V, D, c.code, nt, logit_scale)), _ref(_head_strides(lx, lw)), px, pw, pt,
+        c.dense(loss, "loss", (M,), required=True), c.dense(lse, "lse", (M,), required=True), wp, wn,
+        c.stream()))
+    return loss, lse
+
+
+def head_loss_backward(x, weight, targets, lse, dloss, dlse=None, *, logit_scale=1.0, need_dx=True,
+                       need_dweight=True, out=None, workspace=None, stream=None):
+    """Gradients of ``head_loss`` against dloss (M,) and dlse (M,) (0 when None), float32.
+
+    ``lse``: the forward's.  Returns a dict: dx (M, D) and dweight (V, D) in x's type, None where
+    not needed.  A padded row takes no part: its dx is 0, and its x, dloss and dlse are not used.
+    In 2-byte types the gradient of each logit is rounded once before the products that make
+    dx and dweight.  ``out`` and ``workspace`` as in gated_scan_backward
+    (``head_workspace_bytes(OP_HEAD_LOSS_BACKWARD, ...)``)."""
+    c, logit_scale = _Call(x, "x", stream), float(logit_scale) + 0.0
+    M, D = x.shape
+    V = weight.shape[0]
+    px, lx = c.rows(x, "x", M, D)
+    pw, lw = c.rows(weight, "weight", V, D)
+    pt, nt = _ids(c, targets, "targets", M)
+    g, at = _outputs(c, out, {"dx": (need_dx, (M, D), None, x, True),
+                              "dweight": (need_dweight, (V, D), None, weight, True)})
+    (pdx, ldx), (pdw, ldw) = at["dx"], at["dweight"]
+    need = _head_need(OP_HEAD_LOSS_BACKWARD, M, V, D, c.code)
+    wp, wn, _keep = c.workspace(need, workspace)
+    _check("mss_head_loss_backward", lib().mss_head_loss_backward(
+        _ref(_head_dims(M, V, D, c.code, nt, logit_scale)), _ref(_head_strides(lx, lw, ldx, ldw)), px, pw, pt,
+        c.dense(lse, "lse", (M,), required=True), c.dense(dloss, "dloss", (M,), required=True),
+        c.dense(dlse, "dlse", (M,)), pdx, pdw, wp, wn, c.stream()))
+    return g
+
+
+def _tensor_list(c, grads, out):
+    """The list of mss_tensor of the tensors that are not None, with their outputs."""
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"out has {len(out)} tensors, grads {len(grads)}")
+    codes, dev, Tensor = _dtype_codes(), c.dev, c.Tensor
+    entries = []
+    for k, g in enumerate(grads):
+        o = g if out is None else out[k]
+        if g is None:
+            if o is not None:
+                raise ValueError(f"grads[{k}] is None, out[{k}] is not")
+            continue
+        for t, name in ((g, "grads"), (o, "out")) if o is not g else ((g, "grads"),):
+            if not isinstance(t, Tensor):
+                raise TypeError(f"{name}[{k}] must be a torch.Tensor")
+            if t.dtype not in codes:
+                raise TypeError(f"{name}[{k}] must be float32, bfloat16 or float16, got {t.dtype}")
+            if t.get_device() != dev:
+                raise ValueError(f"{name}[{k}] is on {t.device}, the current device is cuda:{dev}")
+        if not g.is_contiguous():
+            raise ValueError(f"grads[{k}] must be contiguous")
+        if o is not g:
+            if not o.is_contiguous():
+                raise ValueError(f"out[{k}] must be contiguous")
+            if o.shape != g.shape:
+                raise ValueError(f"out[{k}]: expected shape {tuple(g.shape)}, got {tuple(o.shape)}")
+            if o.dtype is not g.dtype and o.dtype is not c.f32:
+                raise TypeError(f"out[{k}] must be {g.dtype} or float32, got {o.dtype}")
+        entries.append((g.data_ptr(), o.data_ptr(), g.numel(), codes[g.dtype], codes[o.dtype]))
+    return (ListTensor * len(entries))(*entries), len(entries)
+
+
+def _list_call(grads, stream):
+    like = next((g for g in grads if g is not None), None)
+    if like is None:
+        raise ValueError("grads holds no tensor")
+    return _Call(like, "grads", stream)
+
+
+def grad_norm(grads, *, scale=1.0, out=None, workspace=None, stream=None):
+    """scale times the 2-norm of all elements of a list of tensors: a float32 tensor without dimensions.
+
+    Tensors are float32, bfloat16 or float16, of any sizes, dense; None is passed over.  Squares
+    and sums are fp64.  ``workspace``: uint8 GPU tensor of at least
+    ``clip_workspace_bytes(len(grads))`` + 256 bytes (allocated here when omitted)."""
+    grads = list(grads)
+    c, scale = _list_call(grads, stream), float(scale)
+    entries, n = _tensor_list(c, grads, None)
+    norm = out if out is not None else c.empty((), c.f32)
+    wp, wn, _keep = c.workspace(_clip_need(n), workspace)
+    _check("mss_grad_norm", lib().mss_grad_norm(entries, n, scale, c.dense(norm, "out", (), required=True),
+                                                wp, wn, c.stream()))
+    return norm
+
+
+def clip_grads(grads, max_norm, *, scale=1.0, out=None, norm=None, workspace=None, stream=None):
+    """The norm of ``grad_norm`` and the tensors times scale min(1, max_norm / norm).
+    Returns (tensors, norm).
+
+    ``scale``: what the gradients are to be multiplied with first (1 / the loss scale, or 1 / the
+    number of micro-batches in them).  The tensors are updated in place, or written to ``out``, a
+    list of tensors of their types or float32 (each may be its input).  Where a value is infinite or
+    NaN they are left as they are (``out``: copied), so that the caller can look at the norm, which
+    is not finite then, and pass over the step.  ``norm``: optional output tensor without dimensions.  ``workspace`` as in
+    ``grad_norm``."""
+    grads = list(grads)
+    c, scale, max_norm = _list_call(grads, stream), float(scale), float(max_norm)
+    out = grads if out is None else list(out)
+    entries, n = _tensor_list(c, grads, out)
+    norm = norm if norm is not None else c.empty((), c.f32)
+    wp, wn, _keep = c.workspace(_clip_need(n), workspace)
+    _check("mss_clip_grads", lib().mss_clip_grads(entries, n, scale, max_norm,
+                                                  c.dense(norm, "norm", (), required=True), wp, wn,
+                                                  c.stream()))
+    return out, norm

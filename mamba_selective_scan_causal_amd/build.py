@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libmss.so")
 SOURCES = ["mss_api.hip", "scan_kernel.hip", "conv_kernel.hip", "step_kernel.hip",
            "scan_bwd_kernel.hip", "conv_bwd_kernel.hip", "ssd_kernel.hip",
            "block_api.hip", "gated_kernel.hip", "norm_kernel.hip",
-           "gated_norm_kernel.hip"]
+           "gated_norm_kernel.hip", "ends_api.hip", "embed_kernel.hip", "head_kernel.hip",
+           "clip_kernel.hip"]
 ARCH = "gfx950"
 FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",

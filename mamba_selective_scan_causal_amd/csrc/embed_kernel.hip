@@ -1,0 +1,450 @@
+// embed_kernel.hip -- rows of a table by token id, and the table's gradient.
+//
+// Forward: y_m = scale W[id_m].  A wave copies a row, 16 bytes of the narrower
+// type to a lane.
+//
+// Backward: dW_v = scale sum over the m with id_m = v of dy_m.  No sum goes
+// through float atomics, so its order is fixed:
+//   1. The positions m are sorted by id, stably, by a radix sort of up to ten
+//      bits a pass (ids that mark a padded place sort as V, to the end).
+//   2. The sorted positions are cut into runs of kRun.  A workgroup sums a
+//      run's rows of dy in that order, for a slice of the columns, and writes
+//      every token's sum that begins and ends within it.  What reaches over
+//      its ends goes to two rows of partial sums.
+//   3. The workgroup in whose run a token begins that goes on beyond it adds
+//      up the partial sums.
+// The work is cut by position, so a token that makes up much of the batch costs
+// no more than any others.  Rows of tokens that do not occur are zeroed by
+// further workgroups of step 2, which look each row up in the sorted ids.
+#include <type_traits>
+
+#include "block_math.h"
+#include "launch_ends.h"
+
+namespace mss {
+namespace {
+
+constexpr int kSortThreads = 256;
+constexpr int kSortRounds = 8;                                  // of 64 keys a wave
+constexpr int kSortTile = kSortThreads * kSortRounds;
+constexpr int kMaxBits = 10;
+constexpr int kMaxBins = 1 << kMaxBits;
+constexpr int kScanThreads = 1024;
+constexpr int kRun = 32;
+constexpr int kZeroRows = 16;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The sort key of an id: the id, or V where it marks a padded place.
+__device__ __forceinline__ uint32_t key_of(const void* ids, bool wide, int64_t m, int64_t V) {
+    const int64_t id = wide ? static_cast<const int64_t*>(ids)[m] : static_cast<const int32_t*>(ids)[m];
+    return static_cast<uint32_t>(id >= 0 && id < V ? id : V);
+}
+
+// ---- forward -----------------------------------------------------------------
+
+template <typename TW, typename TY>
+constexpr int kVec = sizeof(TW) == 2 || sizeof(TY) == 2 ? 8 : 4;
+
+template <typename TW, typename TY>
+__global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a) {
+    constexpr int V = kVec<TW, TY>;
+    const int64_t m = blockIdx.x * int64_t{4} + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if (m >= a.M) return;
+    const uint32_t key = key_of(a.ids, a.wide_ids, m, a.V);
+    const int n = static_cast<int>(a.D);
+    TY* y = static_cast<TY*>(a.y) + m * a.ld_y;
+    const bool in = key < static_cast<uint64_t>(a.V);
+    const TW* w = static_cast<const TW*>(a.w) + (in ? key * a.ld_w : 0);
+    for (int c = (threadIdx.x % kWave) * V; c < n; c += kWave * V) {
+        RowVec<TW, V> r;
+        RowVec<TY, V> o;
+        if (in)
+            r.load(w, c, n);
+        else
+            r.zero();
+#pragma unroll
+        for (int e = 0; e < V; e++) o.set(e, in ? a.scale * r[e] : 0.0f);
+        o.template store<false>(y, c, n);
+    }
+}
+
+// ---- the sort ------------------------------------------------------------------
+
+struct SortArgs {
+    const void* ids;          // first pass
+    bool wide;
+    int64_t M, V;
+    const uint32_t* key_in;   // later passes
+    const uint32_t* pos_in;
+    uint32_t* key_out;
+    uint32_t* pos_out;
+    uint32_t* counts;         // [bin][tile]
+    int64_t tiles;
+    int shift, bits;
+};
+
+__device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t m) {
+    return a.ids ? key_of(a.ids, a.wide, m, a.V) : a.key_in[m];
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
+    __shared__ uint32_t bins[kMaxBins];
+    const int n = 1 << a.bits;
+    for (int b = threadIdx.x; b < n; b += kSortThreads) bins[b] = 0;
+    __syncthreads();
+    const int64_t m0 = blockIdx.x * int64_t{kSortTile};
+    for (int i = 0; i < kSortRounds; i++) {
+        const int64_t m = m0 + i * kSortThreads + threadIdx.x;
+        if (m < a.M) atomicAdd(&bins[sort_key(a, m) >> a.shift & (n - 1)], 1u);
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < n; b += kSortThreads) a.counts[b * a.tiles + blockIdx.x] = bins[b];
+}
+
+// counts -> the sum of those before it, in place, by one workgroup.
+__global__ __launch_bounds__(kScanThreads) void sort_scan_kernel(uint32_t* counts, int64_t n) {
+    __shared__ uint32_t part[kScanThreads];
+    const int64_t each = (n + kScanThreads - 1) / kScanThreads;
+    const int64_t from = threadIdx.x * each, to = from + each < n ? from + each : n;
+    uint32_t sum = 0;
+    for (int64_t i = from; i < to; i++) sum += counts[i];
+    part[threadIdx.x] = sum;
+    for (int d = 1; d < kScanThreads; d *= 2) {
+        __syncthreads();
+        const uint32_t below = static_cast<int>(threadIdx.x) >= d ? part[threadIdx.x - d] : 0;
+        __syncthreads();
+        part[threadIdx.x] += below;
+    }
+    uint32_t before = part[threadIdx.x] - sum;
+    for (int64_t i = from; i < to; i++) {
+        const uint32_t c = counts[i];
+        counts[i] = before;
+        before += c;
+    }
+}
+
+// Each wave takes 512 keys in a row; a key's place is that of its bin, plus
+// the keys of that bin in the tile's earlier waves, in the wave's earlier
+// rounds and in the lanes before it.
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
+    constexpr int kWaves = kSortThreads / kWave;
+    __shared__ uint32_t at[kWaves][kMaxBins];
+    const int n = 1 << a.bits, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    for (int b = threadIdx.x; b < kWaves * n; b += kSortThreads) at[b / n][b % n] = 0;
+    __syncthreads();
+    const int64_t m0 = blockIdx.x * int64_t{kSortTile} + wave * (kSortRounds * kWave) + lane;
+    uint32_t key[kSortRounds], pos[kSortRounds];
+#pragma unroll
+    for (int i = 0; i < kSortRounds; i++) {
+        const int64_t m = m0 + i * kWave;
+        key[i] = pos[i] = 0;
+        if (m < a.M) {
+            key[i] = sort_key(a, m);
+            pos[i] = a.ids ? static_cast<uint32_t>(m) : a.pos_in[m];
+            atomicAdd(&at[wave][key[i] >> a.shift & (n - 1)], 1u);
+        }
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < n; b += kSortThreads) {
+        uint32_t first = a.counts[b * a.tiles + blockIdx.x];
+        for (int w = 0; w < kWaves; w++) {
+            const uint32_t c = at[w][b];
+            at[w][b] = first;
+            first += c;
+        }
+    }
+    __syncthreads();
+    volatile uint32_t* mine = at[wave];      // this wave's alone from here on
+#pragma unroll
+    for (int i = 0; i < kSortRounds; i++) {
+        const bool in = m0 + i * kWave < a.M;
+        const uint32_t digit = key[i] >> a.shift & (n - 1);
+        uint64_t same = __builtin_amdgcn_ballot_w64(in);
+        for (int b = 0; b < a.bits; b++) {
+            const uint64_t ones = __builtin_amdgcn_ballot_w64(digit >> b & 1);
+            same &= digit >> b & 1 ? ones : ~ones;
+        }
+        const uint64_t below = same & ((uint64_t{1} << lane) - 1);
+        if (in) {
+            const uint32_t base = mine[digit];
+            const uint32_t to = base + __builtin_popcountll(below);
+            // the lanes of a digit have all read its place before its first lane moves it on
+            __builtin_amdgcn_wave_barrier();
+            if (below == 0) mine[digit] = base + __builtin_popcountll(same);
+            a.key_out[to] = key[i];
+            a.pos_out[to] = pos[i];
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// ---- sums of the sorted rows -------------------------------------------------------
+
+struct SumArgs {
+    int64_t M, V, D, ld_dy, ld_dw;
+    float scale;
+    bool accumulate;
+    const void* dy;
+    void* dw;
+    const uint32_t* key;      // sorted
+    const uint32_t* pos;
+    float* head;              // [run][D]: of the token that came in from the run before
+    float* tail;              // [run][D]: of the token that goes on in the next run
+    int64_t runs, slices;
+};
+
+template <typename TW, int V>
+__device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t key, int c, const float (&sum)[V]) {
+    const int n = static_cast<int>(a.D);
+    TW* dw = static_cast<TW*>(a.dw) + key * a.ld_dw;
+    RowVec<TW, V> o;
+    if (a.accumulate) o.load(dw, c, n);
+#pragma unroll
+    for (int e = 0; e < V; e++) {
+        const float v = a.scale * sum[e];
+        o.set(e, a.accumulate ? o[e] + v : v);
+    }
+    o.template store<false>(dw, c, n);
+}
+
+template <typename TW, typename TD, int V>
+__device__ __forceinline__ void zero_rows(const SumArgs& a, int64_t block, bool* found) {
+    const int64_t v0 = block * kZeroRows;
+    if (threadIdx.x < kZeroRows) {
+        const int64_t v = v0 + threadIdx.x;
+        int64_t lo = 0, hi = a.M;             // the first place whose key is v or more
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            if (a.key[mid] < v) lo = mid + 1;
+            else hi = mid;
+        }
+        found[threadIdx.x] = v >= a.V || (lo < a.M && a.key[lo] == v);
+    }
+    __syncthreads();
+    const int n = static_cast<int>(a.D);
+    RowVec<TW, V> z;
+    z.zero();
+    for (int i = 0; i < kZeroRows; i++) {
+        if (found[i]) continue;
+        TW* dw = static_cast<TW*>(a.dw) + (v0 + i) * a.ld_dw;
+        for (int c = threadIdx.x * V; c < n; c += blockDim.x * V) z.template store<false>(dw, c, n);
+    }
+}
+
+template <typename TW, typename TD>
+__global__ __launch_bounds__(256) void embed_sum_kernel(SumArgs a) {
+    constexpr int V = kVec<TW, TD>;
+    constexpr int kAhead = 8;
+    __shared__ uint32_t keys[kRun + 2], places[kRun];
+    __shared__ bool found[kZeroRows];
+    const int64_t sums = a.runs * a.slices;
+    if (blockIdx.x >= sums) {
+        zero_rows<TW, TD, V>(a, blockIdx.x - sums, found);
+        return;
+    }
+    const int64_t run = blockIdx.x / a.slices;
+    const int n = static_cast<int>(a.D);
+    const int c = (static_cast<int>(blockIdx.x % a.slices) * blockDim.x + threadIdx.x) * V;
+    // keys[1 + i] is the run's i-th; the places beyond the ends hold V, a key without a row
+    const int64_t m0 = run * kRun;
+    if (threadIdx.x < kRun + 2) {
+        const int64_t m = m0 + threadIdx.x - 1;
+        keys[threadIdx.x] = m >= 0 && m < a.M ? a.key[m] : static_cast<uint32_t>(a.V);
+        if (threadIdx.x < kRun) places[threadIdx.x] = m + 1 < a.M ? a.pos[m + 1] : 0;
+    }
+    __syncthreads();
+    if (c >= n || keys[1] >= a.V) return;
+    const TD* dy = static_cast<const TD*>(a.dy);
+    float sum[V];
+#pragma unroll
+    for (int e = 0; e < V; e++) sum[e] = 0.0f;
+    bool first = keys[0] != keys[1];            // the current token begins in this run
+    for (int i0 = 0; i0 < kRun; i0 += kAhead) {
+        RowVec<TD, V> r[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; i++)
+            if (keys[1 + i0 + i] < a.V) r[i].load(dy + places[i0 + i] * a.ld_dy, c, n);
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) {
+            const uint32_t key = keys[1 + i0 + i], next = keys[2 + i0 + i];
+            if (key >= a.V) return;
+#pragma unroll
+            for (int e = 0; e < V; e++) sum[e] += r[i][e];
+            const bool last = i0 + i == kRun - 1;
+            if (key == next && !last) continue;
+            if (first && key != next) {
+                write_sum<TW, V>(a, key, c, sum);
+            } else {
+                float* to = (first ? a.tail : a.head) + run * a.D;
+#pragma unroll
+                for (int e = 0; e < V; e++)
+                    if (c + e < n) to[c + e] = sum[e];
+            }
+            first = true;
+#pragma unroll
+            for (int e = 0; e < V; e++) sum[e] = 0.0f;
+        }
+    }
+}
+
+// The tokens that reach over the end of the run they begin in.
+template <typename TW, typename TD>
+__global__ __launch_bounds__(256) void embed_join_kernel(SumArgs a) {
+    constexpr int V = kVec<TW, TD>;
+    constexpr int kAhead = 4;
+    const int64_t run = blockIdx.x / a.slices;
+    const int n = static_cast<int>(a.D);
+    const int c = (static_cast<int>(blockIdx.x % a.slices) * blockDim.x + threadIdx.x) * V;
+    const int64_t m0 = run * kRun, end = m0 + kRun;
+    if (c >= n || end >= a.M) return;
+    const uint32_t key = a.key[end - 1];
+    if (key >= a.V || a.key[end] != key) return;
+    if (a.key[m0] == key && m0 > 0 && a.key[m0 - 1] == key) return;      // began earlier
+    // the last run that starts with the token
+    int64_t lo = run + 1, hi = a.runs;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (a.key[mid * kRun] == key) lo = mid + 1;
+        else hi = mid;
+    }
+    float sum[V];
+#pragma unroll
+    for (int e = 0; e < V; e++) sum[e] = c + e < n ? a.tail[run * a.D + c + e] : 0.0f;
+    for (int64_t r = run + 1; r < lo; r += kAhead) {
+        RowVec<float, V> p[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; i++)
+            if (r + i < lo) p[i].load(a.head + (r + i) * a.D, c, n);
+            else p[i].zero();
+#pragma unroll
+        for (int i = 0; i < kAhead; i++)
+#pragma unroll
+            for (int e = 0; e < V; e++) sum[e] += p[i][e];
+    }
+    write_sum<TW, V>(a, key, c, sum);
+}
+
+// ---- host ------------------------------------------------------------------------
+
+struct Plan {
+    int passes, bits;         // bits per pass
+    int64_t tiles, runs;
+    int64_t key[2], pos[2], counts, head, tail, bytes;      // offsets
+};
+
+bool plan_of(int64_t M, int64_t V, int64_t D, Plan& p) {
+    int bits = 1;
+    while (V >> bits) bits++;
+    p.passes = (bits + kMaxBits - 1) / kMaxBits;
+    p.bits = (bits + p.passes - 1) / p.passes;
+    p.tiles = ceil_div(M, kSortTile);
+    p.runs = ceil_div(M, kRun);
+    int64_t at = 0;
+    const auto take = [&](int64_t n) {
+        const int64_t here = at;
+        at += ceil_div(n * 4, 256) * 256;
+        return here;
+    };
+    for (int i = 0; i < 2; i++) p.key[i] = take(M), p.pos[i] = take(M);
+    p.counts = take(p.tiles << p.bits);
+    if (p.runs > (int64_t{1} << 60) / (D > 0 ? D : 1)) return false;
+    p.head = take(p.runs * D);
+    p.tail = take(p.runs * D);
+    p.bytes = at;
+    // grids: every launch below 2^32 threads
+    const int64_t slices = ceil_div(D, 64 * 4);
+    return p.runs < (int64_t{1} << 24) && slices * 256 < (int64_t{1} << 32) / (p.runs + 1) &&
+           p.runs * slices * 256 + ceil_div(V, kZeroRows) * 256 < (int64_t{1} << 32);
+}
+
+template <typename F>
+hipError_t by_types(int table, int rows, F&& f) {
+    const auto second = [&](auto w) {
+        using TW = decltype(w);
+        if (rows == MSS_F32) return f(w, 0.0f);
+        if constexpr (!std::is_same_v<TW, f16>)
+            if (rows == MSS_BF16) return f(w, bf16{});
+        if constexpr (!std::is_same_v<TW, bf16>)
+            if (rows == MSS_F16) return f(w, f16{});
+        return hipErrorInvalidValue;
+    };
+    return table == MSS_F32 ? second(0.0f) : table == MSS_BF16 ? second(bf16{}) : second(f16{});
+}
+
+}  // namespace
+
+bool embed_bwd_workspace(int64_t M, int64_t V, int64_t D, int64_t& bytes) {
+    Plan p;
+    if (!plan_of(M, V, D, p)) return false;
+    bytes = p.bytes;
+    return true;
+}
+
+hipError_t launch_embed(const EmbedArgs& a, hipStream_t st) {
+    const int64_t blocks = ceil_div(a.M, 4);
+    return by_types(a.dtype, a.out_dtype, [&](auto w, auto y) {
+        embed_kernel<decltype(w), decltype(y)><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(a);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_embed_bwd(const EmbedArgs& a, hipStream_t st) {
+    Plan p;
+    if (!plan_of(a.M, a.V, a.D, p)) return hipErrorInvalidValue;
+    char* ws = static_cast<char*>(a.ws);
+    const auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
+    int from = 1;
+    for (int i = 0; i < p.passes && a.M > 0; i++) {
+        SortArgs s{};
+        s.ids = i == 0 ? a.ids : nullptr;
+        s.wide = a.wide_ids;
+        s.M = a.M;
+        s.V = a.V;
+        s.key_in = words(p.key[from]);
+        s.pos_in = words(p.pos[from]);
+        s.key_out = words(p.key[from ^ 1]);
+        s.pos_out = words(p.pos[from ^ 1]);
+        s.counts = words(p.counts);
+        s.tiles = p.tiles;
+        s.shift = i * p.bits;
+        s.bits = p.bits;
+        from ^= 1;
+        sort_count_kernel<<<static_cast<uint32_t>(p.tiles), kSortThreads, 0, st>>>(s);
+        if (hipError_t e = hipGetLastError()) return e;
+        sort_scan_kernel<<<1, kScanThreads, 0, st>>>(s.counts, p.tiles << p.bits);
+        if (hipError_t e = hipGetLastError()) return e;
+        sort_place_kernel<<<static_cast<uint32_t>(p.tiles), kSortThreads, 0, st>>>(s);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    return by_types(a.dtype, a.out_dtype, [&](auto w, auto y) {
+        using TW = decltype(w);
+        using TD = decltype(y);
+        const int64_t vecs = ceil_div(a.D, kVec<TW, TD>);
+        const int threads = vecs > 192 ? 256 : static_cast<int>(ceil_div(vecs, 64) * 64);
+        SumArgs s{};
+        s.M = a.M;
+        s.V = a.V;
+        s.D = a.D;
+        s.ld_dy = a.ld_y;
+        s.ld_dw = a.ld_w;
+        s.scale = a.scale;
+        s.accumulate = a.accumulate;
+        s.dy = a.y;
+        s.dw = a.dw;
+        s.key = words(p.key[from]);
+        s.pos = words(p.pos[from]);
+        s.head = reinterpret_cast<float*>(ws + p.head);
+        s.tail = reinterpret_cast<float*>(ws + p.tail);
+        s.runs = p.runs;
+        s.slices = ceil_div(vecs, threads);
+        const int64_t zeros = a.accumulate ? 0 : ceil_div(a.V, kZeroRows);
+        embed_sum_kernel<TW, TD><<<static_cast<uint32_t>(s.runs * s.slices + zeros), threads, 0, st>>>(s);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || a.M == 0) return e;
+        embed_join_kernel<TW, TD><<<static_cast<uint32_t>(s.runs * s.slices), threads, 0, st>>>(s);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace mss

@@ -1,0 +1,660 @@
+// head_kernel.hip -- softmax cross entropy of x W^T over a large vocabulary, and
+// its gradients, without keeping the logits.
+//
+// Forward, with l = c x W^T in units of log2 (c = logit_scale log2 e): each
+// tile of logits leaves, for each of its rows, the largest logit and the sum of
+// 2^(l - largest) of the columns of one wave; a second kernel joins those of a
+// row and takes the target's logit, which the tile that has it wrote.
+//
+// Backward, a piece of the vocabulary at a time:
+//   dl = (dloss + dlse) p - dloss [v = t],  p = 2^(l - lse),  recomputed from
+// the logits' tiles, in the operands' type, as dl (rows, piece) and its
+// transpose; then dx += dl W and dW = dl^T x.  All three are products of rows
+// (row_product.h), for which x and the piece of W are transposed first: that
+// reads and writes each once, against products that take hundreds of
+// operations for each of their values.
+//
+// dl is held times a factor that brings the largest |dloss| + |dlse| to just
+// below 2^13: fp16 would lose what a mean over many rows leaves of it, and right
+// below a power of two a value's rounding is smallest against it -- where a mean
+// gives all rows one factor, the dl of unlikely targets, which weigh most, all lie
+// there (bf16, M8192 V32768 D1536: dx is off by 0.0020 of its norm, of which 0.0017
+// is its own rounding; with the same dl right above a power of two, 0.0028).  dx and
+// dW are scaled back in fp32.
+#include "launch_ends.h"
+#include "row_product.h"
+
+namespace mss {
+namespace {
+
+constexpr int kGroup = 8;                    // tiles along l that share their r tile in an XCD's L2
+constexpr int kPadRows = 64;                 // dl^T and x^T have rows of a multiple of this many values
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The two tile shapes: one workgroup of eight waves on a CU, or two of four.
+template <typename T>
+using Large = RowProduct<T, 256, 256, 4, 2>;
+template <typename T>
+using Small = RowProduct<T, 128, 128, 2, 2>;
+template <typename P>
+struct Shape;
+template <typename T, int BL_, int BR_, int WL_, int WR_>
+struct Shape<RowProduct<T, BL_, BR_, WL_, WR_>> {
+    using type = T;
+    static constexpr int BL = BL_, BR = BR_, WL = WL_, WR = WR_;
+    static constexpr int kSlab = BR / WR;    // columns of one wave
+};
+
+// Where a wave's part of the tile lies.
+template <typename P>
+struct Part {
+    using S = Shape<P>;
+    int64_t l, r;             // the lane's: l of acc[.][0], r of acc[0][.] element 0
+    int64_t l0, r0;           // the tile's
+    int lane, wave;
+    __device__ __forceinline__ Part(const ProductArgs& a) {
+        int64_t tl, tr;
+        tile_of<kGroup>(blockIdx.x, gridDim.x, a.tiles_l, a.tiles_r, tl, tr);
+        lane = threadIdx.x % kWave;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        l0 = tl * S::BL;
+        r0 = tr * S::BR;
+        l = l0 + wave % S::WL * (S::BL / S::WL) + lane % 16;
+        r = r0 + wave / S::WL * S::kSlab + 4 * (lane / 16);
+    }
+};
+
+// ---- forward -----------------------------------------------------------------
+
+struct LossArgs {
+    float c;                  // logit_scale log2(e)
+    int64_t first;            // vocabulary row of the piece's first
+    int64_t m0;               // row of the rows' first
+    const void* targets;
+    bool wide;
+    float2* part;             // [slab][nl]
+    float* at_target;         // [M]
+};
+
+__device__ __forceinline__ int64_t target_of(const void* t, bool wide, int64_t m) {
+    return wide ? static_cast<const int64_t*>(t)[m] : static_cast<const int32_t*>(t)[m];
+}
+
+__device__ __forceinline__ float over_quads_max(float v) {
+    v = __builtin_fmaxf(v, __shfl_xor(v, 16));
+    return __builtin_fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float over_quads_sum(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+template <typename P>
+__global__ __launch_bounds__(P::kThreads) void head_loss_kernel(ProductArgs a, LossArgs h) {
+    using S = Shape<P>;
+    __shared__ __align__(1024) char lds[P::kLds];
+    const Part<P> at(a);
+    v4f acc[P::kTR][P::kTL];
+    P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
+    const int64_t slab0 = at.r0 + at.wave / S::WL * S::kSlab;
+    if (slab0 >= a.nr) return;
+    const int valid = static_cast<int>(a.nr - at.r < S::kSlab ? a.nr - at.r : S::kSlab);   // from the lane's r on
+#pragma unroll
+    for (int j = 0; j < P::kTL; j++) {
+        const int64_t m = at.l + 16 * j;
+        const bool in = m < a.nl;
+        const int64_t t = in ? target_of(h.targets, h.wide, h.m0 + m) : -1;
+        const int64_t hit = t - h.first - at.r;                  // the target's place from the lane's r on
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < P::kTR; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float v = 16 * i + e < valid ? acc[i][j][e] * h.c : -INFINITY;
+                acc[i][j][e] = v;
+                top = __builtin_fmaxf(top, v);
+                if (hit == 16 * i + e && 16 * i + e < valid && in) h.at_target[h.m0 + m] = v;
+            }
+        top = over_quads_max(top);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < P::kTR; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) sum += ex2(acc[i][j][e] - top);
+        sum = over_quads_sum(sum);
+        if (at.lane < 16 && in) h.part[slab0 / S::kSlab * a.nl + m] = make_float2(top, sum);
+    }
+}
+
+struct JoinArgs {
+    const float2* part;       // [slabs][rows]
+    int64_t slabs, rows, m0, V;
+    const float* at_target;
+    const void* targets;
+    bool wide;
+    float* loss;
+    float* lse;
+};
+
+__device__ __forceinline__ void join(float& top, float& sum, float2 p) {
+    const float t = __builtin_fmaxf(top, p.x);
+    // equal infinities would give NaN here: a slab without a finite logit adds 2^(l - top) as it is
+    const float from = top == t ? sum : sum * ex2(top - t);
+    const float add = p.x == t ? p.y : p.y * ex2(p.x - t);
+    sum = from + add;
+    top = t;
+}
+
+// ROWS rows to a workgroup of 256 / ROWS threads each.
+template <int ROWS>
+__global__ __launch_bounds__(256) void head_join_kernel(JoinArgs h) {
+    constexpr int kTeam = 256 / ROWS;
+    __shared__ float2 team[kTeam][ROWS];
+    const int row = threadIdx.x % ROWS, member = threadIdx.x / ROWS;
+    const int64_t m = blockIdx.x * int64_t{ROWS} + row;
+    float top = -INFINITY, sum = 0.0f;
+    if (m < h.rows) {
+        int64_t s = member;
+        for (; s + 3 * kTeam < h.slabs; s += 4 * kTeam) {
+            float2 p[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) p[i] = h.part[(s + i * kTeam) * h.rows + m];
+#pragma unroll
+            for (int i = 0; i < 4; i++) join(top, sum, p[i]);
+        }
+        for (; s < h.slabs; s += kTeam) join(top, sum, h.part[s * h.rows + m]);
+    }
+    team[member][row] = make_float2(top, sum);
+    for (int d = kTeam / 2; d > 0; d /= 2) {
+        __syncthreads();
+        if (member < d) {
+            join(top, sum, team[member + d][row]);
+            team[member][row] = make_float2(top, sum);
+        }
+    }
+    if (member != 0 || m >= h.rows) return;
+    const float lse2 = top + log2f(sum);
+    const int64_t at = h.m0 + m, t = target_of(h.targets, h.wide, at);
+    h.lse[at] = lse2 * kLn2;
+    h.loss[at] = t >= 0 && t < h.V ? (lse2 - h.at_target[at]) * kLn2 : 0.0f;
+}
+
+// ---- copies ---------------------------------------------------------------------
+
+// Rows of n values to rows of ld_out values, zeros behind.
+template <typename T>
+__global__ __launch_bounds__(256) void pad_rows_kernel(const T* in, int64_t ld_in, int64_t rows, int64_t n, T* out,
+                                                       int64_t ld_out) {
+    const int64_t row = blockIdx.x * int64_t{4} + threadIdx.x / kWave;
+    if (row >= rows) return;
+    for (int64_t c = threadIdx.x % kWave * 8; c < ld_out; c += kWave * 8) {
+        T v[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) v[e] = c + e < n ? in[row * ld_in + c + e] : static_cast<T>(0.0f);
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            if (c + e < ld_out) out[row * ld_out + c + e] = v[e];
+    }
+}
+
+// in (rows, n) to out (n, ld_out), ld_out >= rows, zeros behind and in the
+// columns of rows that are `off` (t < 0).
+template <typename T>
+__global__ __launch_bounds__(256) void transpose_kernel(const T* in, int64_t ld_in, int64_t rows, int64_t n, T* out,
+                                                        int64_t ld_out, const int* t) {
+    constexpr int kTile = 64, kPad = sizeof(T) == 2 ? 2 : 1;
+    __shared__ T tile[kTile][kTile + kPad];
+    const int64_t across = (n + kTile - 1) / kTile;
+    const int64_t r0 = blockIdx.x / across * kTile, c0 = blockIdx.x % across * kTile;
+    const int x = threadIdx.x % kTile;
+    for (int y = threadIdx.x / kTile; y < kTile; y += 4) {
+        const int64_t r = r0 + y, c = c0 + x;
+        const bool ok = r < rows && c < n && (!t || t[r] >= 0);
+        tile[y][x] = ok ? in[r * ld_in + c] : static_cast<T>(0.0f);
+    }
+    __syncthreads();
+    for (int y = threadIdx.x / kTile; y < kTile; y += 4) {
+        const int64_t c = c0 + y, r = r0 + x;
+        if (c < n && r < ld_out) out[c * ld_out + r] = tile[x][y];
+    }
+}
+
+// ---- backward --------------------------------------------------------------------
+
+// What a row brings to dl: a = (dloss + dlse) s, b = dloss s, its lse in units
+// of log2 and its target (-1: a padded row, all zeros).
+struct RowGrads {
+    float* a;
+    float* b;
+    float* lse2;
+    int* t;
+    float* back;              // [0]: logit_scale / s
+};
+
+constexpr float kMostDl = 8190.0f;       // rounds to less than 2^13 in every type
+
+__global__ __launch_bounds__(1024) void row_grads_kernel(HeadArgs h, RowGrads g) {
+    __shared__ float most[16];
+    float top = 0.0f;
+    for (int64_t m = threadIdx.x; m < h.M; m += 1024) {
+        const int64_t t = target_of(h.targets, h.wide_ids, m);
+        if (t < 0 || t >= h.V) continue;
+        top = __builtin_fmaxf(top, __builtin_fabsf(h.dloss[m]) + (h.dlse ? __builtin_fabsf(h.dlse[m]) : 0.0f));
+    }
+    for (int d = 32; d > 0; d /= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    if (threadIdx.x % kWave == 0) most[threadIdx.x / kWave] = top;
+    __syncthreads();
+    for (int w = 0; w < 16; w++) top = __builtin_fmaxf(top, most[w]);
+    // 1 where nothing or not a number would come of it; bounded, so that 1 / s is a normal number
+    float s = 1.0f;
+    if (top > 0.0f && top < INFINITY) s = __builtin_fminf(kMostDl / top, 0x1p120f);
+    if (threadIdx.x == 0) g.back[0] = h.logit_scale / s;
+    for (int64_t m = threadIdx.x; m < h.M; m += 1024) {
+        const int64_t t = target_of(h.targets, h.wide_ids, m);
+        const bool on = t >= 0 && t < h.V;
+        const float up = on ? h.dloss[m] : 0.0f;
+        g.a[m] = on ? (up + (h.dlse ? h.dlse[m] : 0.0f)) * s : 0.0f;
+        g.b[m] = up * s;
+        g.lse2[m] = on ? h.lse[m] * kLog2e : 0.0f;
+        g.t[m] = on ? static_cast<int>(t) : -1;
+    }
+}
+
+struct DlArgs {
+    float c;
+    int64_t first;
+    RowGrads g;
+    void* dl;                 // (M, ld_dl)
+    void* dlt;                // (piece, ld_dlt)
+    int64_t ld_dl, ld_dlt;
+};
+
+template <typename P>
+__global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlArgs h) {
+    using S = Shape<P>;
+    using T = typename S::type;
+    __shared__ __align__(1024) char lds[P::kLds];
+    const Part<P> at(a);
+    v4f acc[P::kTR][P::kTL];
+    P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
+    T* dl = static_cast<T*>(h.dl);
+    T* dlt = static_cast<T*>(h.dlt);
+#pragma unroll
+    for (int j = 0; j < P::kTL; j++) {
+        const int64_t m = at.l + 16 * j;
+        const bool in = m < a.nl;
+        const int t = in ? h.g.t[m] : -1;
+        const float up = in ? h.g.a[m] : 0.0f, own = in ? h.g.b[m] : 0.0f, lse2 = in ? h.g.lse2[m] : 0.0f;
+        const int64_t hit = t - h.first - at.r;
+#pragma unroll
+        for (int i = 0; i < P::kTR; i++) {
+            T v[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                float p = ex2(__builtin_fmaf(acc[i][j][e], h.c, -lse2)) * up;
+                p = hit == 16 * i + e ? p - own : p;
+                v[e] = static_cast<T>(t >= 0 && at.r + 16 * i + e < a.nr ? p : 0.0f);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int64_t r = at.r + 16 * i + e;
+                if (in && r < h.ld_dl) dl[m * h.ld_dl + r] = v[e];
+                if (m < h.ld_dlt && r < a.nr) dlt[r * h.ld_dlt + m] = v[e];
+            }
+        }
+    }
+}
+
+struct GradArgs {
+    const float* back;
+    void* out;                // (nl, ld) of T; or null:
+    int64_t ld;
+    float* acc;               // [split][nl][nr] fp32, added to unless it is the first piece
+    bool first;
+    int split;                // of K
+};
+
+template <typename P>
+__global__ __launch_bounds__(P::kThreads) void head_grad_kernel(ProductArgs a, GradArgs h) {
+    using S = Shape<P>;
+    using T = typename S::type;
+    __shared__ __align__(1024) char lds[P::kLds];
+    const Part<P> at(a);
+    v4f acc[P::kTR][P::kTL];
+    // this workgroup's part of K, whole stages
+    const int64_t stages = (a.kbytes + kStage - 1) / kStage;
+    const int64_t k0 = stages * blockIdx.y / h.split * kStage, k1 = stages * (blockIdx.y + 1) / h.split * kStage;
+    P::run(a, at.l0, at.r0, k0, k1 < a.kbytes ? k1 : a.kbytes, lds, acc);
+    const float back = h.back[0];
+#pragma unroll
+    for (int j = 0; j < P::kTL; j++) {
+        const int64_t l = at.l + 16 * j;
+        if (l >= a.nl) continue;
+#pragma unroll
+        for (int i = 0; i < P::kTR; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int64_t r = at.r + 16 * i + e;
+                if (r >= a.nr) continue;
+                if (h.out) {
+                    static_cast<T*>(h.out)[l * h.ld + r] = static_cast<T>(acc[i][j][e] * back);
+                } else {
+                    float& to = h.acc[(blockIdx.y * a.nl + l) * a.nr + r];
+                    to = h.first ? acc[i][j][e] : to + acc[i][j][e];
+                }
+            }
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void head_finish_kernel(const float* acc, int split, int64_t rows, int64_t n,
+                                                          const float* back, T* out, int64_t ld) {
+    const int64_t row = blockIdx.x * int64_t{4} + threadIdx.x / kWave;
+    if (row >= rows) return;
+    const float s = back[0];
+    for (int64_t c = threadIdx.x % kWave; c < n; c += kWave) {
+        float v = 0.0f;
+        for (int k = 0; k < split; k++) v += acc[(k * rows + row) * n + c];
+        out[row * ld + c] = static_cast<T>(v * s);
+    }
+}
+
+// ---- plans -------------------------------------------------------------------------
+
+constexpr int64_t kPartBytes = int64_t{256} << 20;      // partial sums of the forward at a time
+constexpr int64_t kDlBytes = int64_t{512} << 20;        // dl and its transpose
+constexpr int64_t kCus = 256;
+
+int64_t align_up(int64_t n, int64_t a) { return ceil_div(n, a) * a; }
+
+// Rounds of large tiles that a product of nl x nr takes, K apart, and whether
+// small tiles (two workgroups to a CU, at 1 / 1.13 of the rate) take less.
+struct Rounds {
+    double cost;
+    bool large;
+};
+Rounds rounds(int64_t nl, int64_t nr, int64_t split = 1) {
+    const double big = static_cast<double>(ceil_div(ceil_div(nl, 256) * ceil_div(nr, 256) * split, kCus));
+    const double small =
+        0.5 * 1.13 * static_cast<double>(ceil_div(ceil_div(nl, 128) * ceil_div(nr, 128) * split, 2 * kCus));
+    return {big <= small ? big : small, big <= small};
+}
+
+struct Plan {
+    bool whole;               // rows are read as they lie
+    int64_t Dk;               // values in a copied row
+    int64_t piece;            // vocabulary rows at a time
+    int64_t chunk;            // rows at a time (forward)
+    int split;                // of dx's K
+    bool accumulate;          // dx goes through fp32 partial sums
+    int64_t ld_m;             // values in a row of dl^T and x^T
+    int64_t x, w, part, at_target, dl, dlt, xt, wt, acc, rows, bytes;
+};
+
+bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p) {
+    const int64_t e = dtype == MSS_F32 ? 4 : 2;
+    p = Plan{};
+    p.whole = head_rows_whole(D, e);
+    p.Dk = align_up(D, 16 / e);
+    p.ld_m = align_up(M, kPadRows);
+    bool fits = true;
+    const auto take = [&](int64_t a, int64_t b, int64_t c) {
+        const int64_t here = p.bytes;
+        int64_t n = a;
+        for (int64_t f : {b, c}) {
+            if (f > 0 && n > (int64_t{1} << 60) / f) fits = false;
+            else n *= f;
+        }
+        if (fits) p.bytes += align_up(n, 256);
+        if (p.bytes > (int64_t{1} << 60)) fits = false;
+        return here;
+    };
+    if (!backward) {
+        p.piece = p.whole ? int64_t{1} << 18 : align_up((int64_t{64} << 20) / (p.Dk * e) + 1, 256);
+        if (p.piece > (int64_t{1} << 18)) p.piece = int64_t{1} << 18;
+        if (p.piece > V) p.piece = V;
+        const int64_t slabs = ceil_div(V, 64);
+        p.chunk = kPartBytes / (slabs * 8) / 256 * 256;
+        if (p.chunk < 256) p.chunk = 256;
+        if (p.chunk > M) p.chunk = M;
+        p.part = take(slabs, p.chunk, 8);
+        p.at_target = take(M, 4, 1);
+        if (!p.whole) {
+            p.x = take(M, p.Dk, e);
+            p.w = take(p.piece, p.Dk, e);
+        }
+        return fits;
+    }
+    // The piece, in steps of 256 vocabulary rows: what makes the three products
+    // take the fewest rounds of tiles, launches counted as a hundred values of K.
+    const int64_t steps = ceil_div(V, 256);
+    int64_t most = kDlBytes / (2 * 256 * e * p.ld_m);
+    most = most < 1 ? 1 : most > 1024 ? 1024 : most > steps ? steps : most;
+    double best = 0;
+    const int64_t stride = ceil_div(most, 64);
+    for (int64_t n = most; n > 0 && n > most / 4; n -= stride) {
+        const int64_t full = steps / n, rest = steps % n;
+        const auto one = [&](int64_t k) {
+            return k == 0 ? 0.0
+                          : rounds(M, 256 * k).cost * D + rounds(256 * k, D).cost * M + rounds(M, D).cost * 256 * k + 400;
+        };
+        const double cost = full * one(n) + one(rest);
+        if (best == 0 || cost < best) best = cost, p.piece = 256 * n;
+    }
+    // dx has few tiles and a long K: it is split until the tiles fill the CUs
+    p.split = 1;
+    double least = rounds(M, D).cost;
+    for (int s = 2; s <= 16 && p.piece / s >= 512; s++) {
+        const double cost = rounds(M, D, s).cost / s * 1.02;
+        if (cost < 0.95 * least) least = cost, p.split = s;
+    }
+    p.accumulate = p.split > 1 || p.piece < V;
+    p.dl = take(M, p.piece, e);
+    p.dlt = take(p.piece, p.ld_m, e);
+    p.xt = take(D, p.ld_m, e);
+    p.wt = take(D, p.piece, e);
+    if (!p.whole) {
+        p.x = take(M, p.Dk, e);
+        p.w = take(p.piece, p.Dk, e);
+    }
+    if (p.accumulate) p.acc = take(M * int64_t{4}, D, p.split);
+    p.rows = take(align_up(M, 64) * int64_t{16} + 256, 1, 1);
+    return fits;
+}
+
+template <typename F>
+hipError_t by_type(int dtype, F&& f) {
+    return dtype == MSS_F32 ? f(0.0f) : dtype == MSS_BF16 ? f(bf16{}) : f(f16{});
+}
+
+ProductArgs product(const void* l, int64_t ld_l, int64_t nl, const void* r, int64_t ld_r, int64_t nr, int64_t kbytes,
+                    bool large) {
+    const int64_t t = large ? 256 : 128;
+    return {static_cast<const char*>(l), static_cast<const char*>(r), ld_l, ld_r, nl, nr, kbytes, ceil_div(nl, t),
+            ceil_div(nr, t)};
+}
+
+template <typename T>
+hipError_t pad_rows(const T* in, int64_t ld, int64_t rows, int64_t n, T* out, int64_t ld_out, hipStream_t st) {
+    pad_rows_kernel<T><<<static_cast<uint32_t>(ceil_div(rows, 4)), 256, 0, st>>>(in, ld, rows, n, out, ld_out);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t transpose(const T* in, int64_t ld, int64_t rows, int64_t n, T* out, int64_t ld_out, const int* t,
+                     hipStream_t st) {
+    const int64_t blocks = ceil_div(ld_out, 64) * ceil_div(n, 64);
+    transpose_kernel<T><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(in, ld, rows, n, out, ld_out, t);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t grad(const ProductArgs& a, bool large, const GradArgs& g, hipStream_t st) {
+    const dim3 grid(static_cast<uint32_t>(a.tiles_l * a.tiles_r), g.split);
+    if (large) head_grad_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, g);
+    else head_grad_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, g);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t forward(const HeadArgs& h, const Plan& p, hipStream_t st) {
+    char* ws = static_cast<char*>(h.ws);
+    constexpr int64_t e = sizeof(T);
+    const char* x = static_cast<const char*>(h.x);
+    int64_t ld_x = h.ld_x * e;
+    float* at_target = reinterpret_cast<float*>(ws + p.at_target);
+    float2* part = reinterpret_cast<float2*>(ws + p.part);
+    if (!p.whole) {
+        T* to = reinterpret_cast<T*>(ws + p.x);
+        if (hipError_t r = pad_rows(static_cast<const T*>(h.x), h.ld_x, h.M, h.D, to, p.Dk, st)) return r;
+        x = ws + p.x;
+        ld_x = p.Dk * e;
+    }
+    for (int64_t m0 = 0; m0 < h.M; m0 += p.chunk) {
+        const int64_t rows = h.M - m0 < p.chunk ? h.M - m0 : p.chunk;
+        const bool large = rounds(rows, h.V < p.piece ? h.V : p.piece).large;
+        const int64_t slab = large ? Shape<Large<T>>::kSlab : Shape<Small<T>>::kSlab;
+        for (int64_t v0 = 0; v0 < h.V; v0 += p.piece) {
+            const int64_t n = h.V - v0 < p.piece ? h.V - v0 : p.piece;
+            const T* w = static_cast<const T*>(h.w) + v0 * h.ld_w;
+            int64_t ld_w = h.ld_w * e;
+            if (!p.whole) {
+                T* to = reinterpret_cast<T*>(ws + p.w);
+                if (hipError_t r = pad_rows(w, h.ld_w, n, h.D, to, p.Dk, st)) return r;
+                w = to;
+                ld_w = p.Dk * e;
+            }
+            const ProductArgs a = product(x + m0 * ld_x, ld_x, rows, w, ld_w, n, p.Dk * e, large);
+            // a piece is a multiple of 256 rows, or all of them: slabs do not cross pieces
+            const LossArgs l{h.logit_scale * kLog2e, v0, m0, h.targets, h.wide_ids, part + v0 / slab * rows, at_target};
+            const uint32_t grid = static_cast<uint32_t>(a.tiles_l * a.tiles_r);
+            if (large) head_loss_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, l);
+            else head_loss_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, l);
+            if (hipError_t r = hipGetLastError()) return r;
+        }
+        const JoinArgs j{part, ceil_div(h.V, slab), rows, m0, h.V, at_target, h.targets, h.wide_ids, h.loss, h.lse};
+        if (rows < 1024) head_join_kernel<1><<<static_cast<uint32_t>(rows), 256, 0, st>>>(j);
+        else head_join_kernel<16><<<static_cast<uint32_t>(ceil_div(rows, 16)), 256, 0, st>>>(j);
+        if (hipError_t r = hipGetLastError()) return r;
+    }
+    return hipSuccess;
+}
+
+template <typename T>
+hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
+    char* ws = static_cast<char*>(h.ws);
+    constexpr int64_t e = sizeof(T);
+    const int64_t M = h.M, D = h.D;
+    RowGrads g;
+    const int64_t padded = align_up(M, 64);
+    g.a = reinterpret_cast<float*>(ws + p.rows);
+    g.b = g.a + padded;
+    g.lse2 = g.b + padded;
+    g.t = reinterpret_cast<int*>(g.lse2 + padded);
+    g.back = reinterpret_cast<float*>(g.t + padded);
+    row_grads_kernel<<<1, 1024, 0, st>>>(h, g);
+    if (hipError_t r = hipGetLastError()) return r;
+    const T* x = static_cast<const T*>(h.x);
+    int64_t ld_x = h.ld_x;
+    if (!p.whole) {
+        T* to = reinterpret_cast<T*>(ws + p.x);
+        if (hipError_t r = pad_rows(x, ld_x, M, D, to, p.Dk, st)) return r;
+        x = to;
+        ld_x = p.Dk;
+    }
+    T* xt = reinterpret_cast<T*>(ws + p.xt);
+    T* wt = reinterpret_cast<T*>(ws + p.wt);
+    T* dl = reinterpret_cast<T*>(ws + p.dl);
+    T* dlt = reinterpret_cast<T*>(ws + p.dlt);
+    if (h.dw)
+        if (hipError_t r = transpose(x, ld_x, M, D, xt, p.ld_m, g.t, st)) return r;
+    for (int64_t v0 = 0; v0 < h.V; v0 += p.piece) {
+        const int64_t n = h.V - v0 < p.piece ? h.V - v0 : p.piece;
+        const int64_t ld_n = align_up(n, kPadRows);      // at most the piece, a multiple of 256
+        const T* w = static_cast<const T*>(h.w) + v0 * h.ld_w;
+        int64_t ld_w = h.ld_w;
+        if (!p.whole) {
+            T* to = reinterpret_cast<T*>(ws + p.w);
+            if (hipError_t r = pad_rows(w, ld_w, n, D, to, p.Dk, st)) return r;
+            w = to;
+            ld_w = p.Dk;
+        }
+        bool large = rounds(M, n).large;
+        const ProductArgs a = product(x, ld_x * e, M, w, ld_w * e, n, p.Dk * e, large);
+        const DlArgs d{h.logit_scale * kLog2e, v0, g, dl, dlt, ld_n, p.ld_m};
+        const uint32_t grid = static_cast<uint32_t>(a.tiles_l * a.tiles_r);
+        if (large) head_dl_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, d);
+        else head_dl_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, d);
+        if (hipError_t r = hipGetLastError()) return r;
+        if (h.dx) {
+            if (hipError_t r = transpose(w, ld_w, n, D, wt, ld_n, static_cast<const int*>(nullptr), st)) return r;
+            large = rounds(M, D, p.split).large;
+            const GradArgs to{g.back, p.accumulate ? nullptr : h.dx, h.ld_dx, reinterpret_cast<float*>(ws + p.acc),
+                              v0 == 0, p.split};
+            if (hipError_t r = grad<T>(product(dl, ld_n * e, M, wt, ld_n * e, D, ld_n * e, large), large, to, st))
+                return r;
+        }
+        if (h.dw) {
+            large = rounds(n, D).large;
+            const GradArgs to{g.back, static_cast<T*>(h.dw) + v0 * h.ld_dw, h.ld_dw, nullptr, false, 1};
+            if (hipError_t r =
+                    grad<T>(product(dlt, p.ld_m * e, n, xt, p.ld_m * e, D, p.ld_m * e, large), large, to, st))
+                return r;
+        }
+    }
+    if (h.dx && p.accumulate) {
+        head_finish_kernel<T><<<static_cast<uint32_t>(ceil_div(M, 4)), 256, 0, st>>>(
+            reinterpret_cast<const float*>(ws + p.acc), p.split, M, D, g.back, static_cast<T*>(h.dx), h.ld_dx);
+        return hipGetLastError();
+    }
+    return hipSuccess;
+}
+
+__global__ __launch_bounds__(256) void zero_rows_kernel(char* p, int64_t rows, int64_t width, int64_t ld) {
+    // bytes, in pieces of two: every element type's size is a multiple
+    const int64_t row = blockIdx.x * int64_t{4} + threadIdx.x / kWave;
+    if (row >= rows) return;
+    for (int64_t c = threadIdx.x % kWave * 2; c < width; c += kWave * 2)
+        *reinterpret_cast<uint16_t*>(p + row * ld + c) = 0;
+}
+
+}  // namespace
+
+bool head_workspace(int dtype, int64_t M, int64_t V, int64_t D, bool bwd, int64_t& bytes) {
+    Plan p;
+    bytes = 0;
+    if (M == 0) return true;
+    if (!plan_of(dtype, M, V, D, bwd, p)) return false;
+    // every launch below 2^32 threads: 256 to a small tile, to 64 x 64 values of a transposition and to
+    // four rows (of at most 2^26) of the others
+    const int64_t across = ceil_div(bwd ? M : p.chunk, 128), down = ceil_div(p.piece, 128), wide = ceil_div(D, 128);
+    const int64_t most = int64_t{1} << 24;
+    if (across * down >= most || across * wide * (bwd ? p.split : 1) >= most || down * wide >= most ||
+        ceil_div(p.ld_m, 64) * ceil_div(D, 64) >= most || ceil_div(p.piece, 64) * ceil_div(D, 64) >= most)
+        return false;
+    bytes = p.bytes;
+    return true;
+}
+
+hipError_t launch_head(const HeadArgs& a, hipStream_t st) {
+    Plan p;
+    if (!plan_of(a.dtype, a.M, a.V, a.D, false, p)) return hipErrorInvalidValue;
+    return by_type(a.dtype, [&](auto t) { return forward<decltype(t)>(a, p, st); });
+}
+
+hipError_t launch_head_bwd(const HeadArgs& a, hipStream_t st) {
+    if (a.M == 0) {
+        if (!a.dw) return hipSuccess;
+        const int64_t e = a.dtype == MSS_F32 ? 4 : 2;
+        zero_rows_kernel<<<static_cast<uint32_t>(ceil_div(a.V, 4)), 256, 0, st>>>(static_cast<char*>(a.dw), a.V,
+                                                                                 a.D * e, a.ld_dw * e);
+        return hipGetLastError();
+    }
+    if (!a.dx && !a.dw) return hipSuccess;
+    Plan p;
+    if (!plan_of(a.dtype, a.M, a.V, a.D, true, p)) return hipErrorInvalidValue;
+    return by_type(a.dtype, [&](auto t) { return backward<decltype(t)>(a, p, st); });
+}
+
+}  // namespace mss

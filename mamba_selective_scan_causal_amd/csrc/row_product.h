@@ -1,0 +1,170 @@
+// row_product.h -- products of rows on the matrix cores of gfx950:
+//   C[l][r] = sum_k L[l][k] R[r][k]
+// with L (nl, K) and R (nr, K) row-major (K contiguous), as the head's logits
+// and both of its gradients are computed.
+//
+// A workgroup computes a BL x BR tile of C.  128 bytes of every row (64 values
+// of two bytes, 32 of four) go to LDS per stage by direct loads, one stage
+// ahead of the matrix instructions.  Chunk c (16 bytes) of row i lies at chunk
+// c ^ (i & 7) of the row's 128 bytes: the 16 rows that a fragment reads at one
+// c then fall on different banks.  A lane's 16 bytes are a fragment of one
+// 16x16x32 instruction (two-byte types) or of four 16x16x4 ones (fp32; which k
+// goes to which instruction does not matter as long as both operands agree).
+// R is the instruction's row operand, so that a lane ends up with four
+// neighbouring r of one l: runs of C's rows.
+#pragma once
+
+#include "block_math.h"
+
+namespace mss {
+
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+constexpr int kStage = 128;                       // bytes of a row per stage
+constexpr int kXcds = 8;
+constexpr int kNoLoads = 0x0f70;                  // s_waitcnt: vmcnt 0, the other counters as they are
+
+template <typename T>
+struct Mma;
+template <>
+struct Mma<bf16> {
+    typedef bf16 frag __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ v4f run(v4i r, v4i l, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(frag, r),
+                                                       __builtin_bit_cast(frag, l), c, 0, 0, 0);
+    }
+};
+template <>
+struct Mma<f16> {
+    typedef f16 frag __attribute__((ext_vector_type(8)));
+    static __device__ __forceinline__ v4f run(v4i r, v4i l, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(frag, r),
+                                                      __builtin_bit_cast(frag, l), c, 0, 0, 0);
+    }
+};
+template <>
+struct Mma<float> {
+    static __device__ __forceinline__ v4f run(v4i r, v4i l, v4f c) {
+        const v4f a = __builtin_bit_cast(v4f, r), b = __builtin_bit_cast(v4f, l);
+#pragma unroll
+        for (int e = 0; e < 4; e++) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+        return c;
+    }
+};
+
+struct ProductArgs {
+    const char* l;            // row-strided operands, 16-byte aligned rows
+    const char* r;
+    int64_t ld_l, ld_r;       // bytes
+    int64_t nl, nr;           // rows of each (at least 1)
+    int64_t kbytes;           // bytes of a row that count, a multiple of 16
+    int64_t tiles_l, tiles_r;
+};
+
+// The tile of C that workgroup b computes.  Neighbouring workgroups go to
+// different XCDs, so each XCD gets a contiguous part of the tiles; within it
+// GL tiles along l share their r tile, so that the tiles computed at one time
+// on an XCD form a block, whose operands its L2 holds.
+template <int GL>
+__device__ __forceinline__ void tile_of(int64_t b, int64_t n, int64_t tiles_l, int64_t tiles_r, int64_t& tl,
+                                        int64_t& tr) {
+    const int64_t xcd = b % kXcds, per = n / kXcds, rest = n % kXcds;
+    const int64_t t = xcd * per + (xcd < rest ? xcd : rest) + b / kXcds;
+    const int64_t group = t / (GL * tiles_r), first = group * GL;
+    const int64_t high = tiles_l - first < GL ? tiles_l - first : GL;
+    const int64_t in = t - group * (GL * tiles_r);
+    tl = first + in % high;
+    tr = in / high;
+}
+
+typedef const __attribute__((address_space(1))) void* gmem;
+typedef __attribute__((address_space(3))) void* lmem;
+
+static __device__ const v4i kZeros = {0, 0, 0, 0};
+
+// A stage of ROWS rows of one operand: where this lane's chunks come from.
+template <int ROWS, int WAVES>
+struct Stager {
+    static constexpr int kLoads = ROWS / 8 / WAVES;
+    const char* p[kLoads];
+    int64_t at;               // this lane's byte of the row
+
+    __device__ __forceinline__ void init(const char* base, int64_t ld, int64_t row0, int64_t n, int wave, int lane) {
+        at = ((lane & 7) ^ (lane >> 3)) * 16;
+#pragma unroll
+        for (int s = 0; s < kLoads; s++) {
+            // rows past the last read the last one again: their products are not used
+            int64_t row = row0 + (s * WAVES + wave) * 8 + (lane >> 3);
+            row = row < n ? row : n - 1;
+            p[s] = base + row * ld;
+        }
+    }
+    // The chunks of the stage that starts at byte k of the rows, to LDS.  Past
+    // the end of a row both operands read zeros.
+    __device__ __forceinline__ void load(char* lds, int64_t k, int64_t kbytes, int wave) {
+        const bool in = k + at < kbytes;
+#pragma unroll
+        for (int s = 0; s < kLoads; s++) {
+            const char* q = in ? p[s] + k + at : reinterpret_cast<const char*>(&kZeros);
+            __builtin_amdgcn_global_load_lds((gmem)q, (lmem)(lds + (s * WAVES + wave) * 1024), 16, 0, 0);
+        }
+    }
+};
+
+// acc[i][j]: the 16 x 16 tile of C at r = 16 i, l = 16 j of the wave's part; a
+// lane holds r = 4 (lane / 16) + 0..3, l = lane % 16 of it.
+template <typename T, int BL, int BR, int WL, int WR>
+struct RowProduct {
+    static constexpr int kWaves = WL * WR, kThreads = kWaves * kWave;
+    static constexpr int kTL = BL / WL / 16, kTR = BR / WR / 16;
+    static constexpr int kLds = 2 * (BL + BR) * kStage;
+
+    static __device__ __forceinline__ void run(const ProductArgs& a, int64_t l0, int64_t r0, int64_t kbegin,
+                                               int64_t kend, char* lds, v4f (&acc)[kTR][kTL]) {
+        const int lane = threadIdx.x % kWave;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        const int wl = wave % WL, wr = wave / WL;
+        Stager<BL, kWaves> sl;
+        Stager<BR, kWaves> sr;
+        sl.init(a.l, a.ld_l, l0, a.nl, wave, lane);
+        sr.init(a.r, a.ld_r, r0, a.nr, wave, lane);
+#pragma unroll
+        for (int i = 0; i < kTR; i++)
+#pragma unroll
+            for (int j = 0; j < kTL; j++) acc[i][j] = v4f{0, 0, 0, 0};
+        if (kbegin >= kend) return;
+        sl.load(lds, kbegin, kend, wave);
+        sr.load(lds + BL * kStage, kbegin, kend, wave);
+        int buf = 0;
+        const int row = lane % 16, quad = lane / 16;
+        for (int64_t k = kbegin; k < kend; k += kStage) {
+            // this stage has landed for every wave, and every wave has read the other one
+            __builtin_amdgcn_s_waitcnt(kNoLoads);
+            __syncthreads();
+            char* next = lds + (buf ^ 1) * (BL + BR) * kStage;
+            if (k + kStage < kend) {
+                sl.load(next, k + kStage, kend, wave);
+                sr.load(next + BL * kStage, k + kStage, kend, wave);
+            }
+            const char* pl = lds + buf * (BL + BR) * kStage + (wl * (BL / WL) + row) * kStage;
+            const char* pr = lds + buf * (BL + BR) * kStage + (BL + wr * (BR / WR) + row) * kStage;
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) {
+                const int c = ((kk * 4 + quad) ^ (row & 7)) * 16;
+                v4i fl[kTL], fr[kTR];
+#pragma unroll
+                for (int j = 0; j < kTL; j++) fl[j] = *reinterpret_cast<const v4i*>(pl + j * 16 * kStage + c);
+#pragma unroll
+                for (int i = 0; i < kTR; i++) fr[i] = *reinterpret_cast<const v4i*>(pr + i * 16 * kStage + c);
+#pragma unroll
+                for (int i = 0; i < kTR; i++)
+#pragma unroll
+                    for (int j = 0; j < kTL; j++) acc[i][j] = Mma<T>::run(fr[i], fl[j], acc[i][j]);
+            }
+            buf ^= 1;
+        }
+    }
+};
+
+}  // namespace mss

@@ -1,0 +1,222 @@
+"""The head's loss and its gradients against float64."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import ends_ref as ref
+import mamba_selective_scan_causal_amd as mss
+from ends_util import TYPES, check, generator, normal, some_ids, spread
+from gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+
+# rows, vocabulary, width: below, at and past the tiles' 128 and 256 and their 128 bytes of a row
+SIZES = [(1, 1, 1), (1, 300, 64), (5, 2, 8), (8, 4097, 128), (17, 129, 33), (64, 256, 64), (65, 255, 72),
+         (128, 128, 136), (129, 1000, 100), (257, 513, 200), (300, 2000, 65), (700, 300, 320)]
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    announce(request.node.nodeid)
+    yield
+
+
+def case(seed, M, V, D, t, idt=torch.int64, spread_out=3.0):
+    """Logits with a standard deviation of about `spread_out` on top of which rows lean to targets."""
+    g = generator(seed)
+    w = normal(g, V, D, std=D ** -0.5, dtype=t)
+    targets = some_ids(g, M, V, idt)
+    lean = torch.rand(M, 1, generator=g) * 6
+    x = (normal(g, M, D, std=spread_out) + lean * w.float()[targets.clamp(0, V - 1).long()]).to(t)
+    return x, w, targets, normal(g, M, std=1.0 / M), normal(g, M, std=0.1 / M)
+
+
+def run(x, w, targets, dloss, dlse, **kw):
+    a = [v.cuda() for v in (x, w, targets)]
+    loss, lse = mss.head_loss(*a, **kw)
+    grads = mss.head_loss_backward(*a, lse, dloss.cuda(), None if dlse is None else dlse.cuda(), **kw)
+    torch.cuda.synchronize()
+    return dict(grads, loss=loss, lse=lse)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,V,D", SIZES)
+def test_loss_and_gradients(dtype, M, V, D):
+    x, w, targets, dloss, dlse = case(M + V + D, M, V, D, TYPES[dtype], torch.int32 if M % 2 else torch.int64)
+    dlse = dlse if D % 2 else None
+    got = run(x, w, targets, dloss, dlse, logit_scale=0.8)
+    want = ref.head(x, w, targets, 0.8, dloss, dlse)
+    for k in want:
+        announce(f"{k} {check(got[k], want[k], k):.2f} of the bound")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_several_pieces_of_the_vocabulary(dtype):
+    """Sizes whose gradients of the logits do not fit the workspace at once, and whose dx is split."""
+    t = TYPES[dtype]
+    M, V, D = (40000, 6001, 24) if dtype != "f32" else (40000, 3001, 20)
+    need = mss.head_workspace_bytes(mss.OP_HEAD_LOSS_BACKWARD, rows=M, vocab=V, width=D, dtype=t)
+    assert need < 2 * M * V * t.itemsize
+    x, w, targets, dloss, dlse = case(1, M, V, D, t)
+    got = run(x, w, targets, dloss, dlse)
+    want = ref.head(x, w, targets, 1.0, dloss, dlse)
+    for k in want:
+        check(got[k], want[k], k)
+
+
+def test_a_long_vocabulary_of_few_rows():
+    x, w, targets, dloss, _ = case(2, 9, 70001, 40, torch.bfloat16)
+    got = run(x, w, targets, dloss, None)
+    want = ref.head(x, w, targets, 1.0, dloss)
+    for k in want:
+        check(got[k], want[k], k)
+
+
+def test_large_logits():
+    """Logits of some thousands: nothing overflows, a certain row has loss 0 and no gradient."""
+    t = torch.float32
+    M, V, D = 40, 300, 64
+    x, w, targets, dloss, _ = case(3, M, V, D, t, spread_out=1000.0)
+    x[5] = 4000.0 * w[targets[5].clamp(0, V - 1)] / w[targets[5].clamp(0, V - 1)].norm()
+    got = run(x, w, targets, dloss, None)
+    want = ref.head(x, w, targets, 1.0, dloss)
+    for k in want:
+        check(got[k], want[k], k)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_padded_rows_take_no_part(dtype):
+    """NaN in a padded row's x, dloss and dlse reaches nothing; a batch of padding only has no gradients."""
+    t = TYPES[dtype]
+    x, w, targets, dloss, dlse = case(4, 150, 200, 48, t)
+    off = (targets < 0) | (targets >= 200)
+    assert off.any() and not off.all()
+    clean = run(x, w, targets, dloss, dlse)
+    x[off], dloss[off], dlse[off] = float("nan"), float("nan"), float("inf")
+    got = run(x, w, targets, dloss, dlse)
+    on = ~off.cuda()
+    assert (got["loss"][~on] == 0).all() and (got["dx"][~on] == 0).all()
+    for k in ("loss", "lse", "dx"):
+        assert torch.equal(got[k][on], clean[k][on])
+    assert torch.equal(got["dweight"], clean["dweight"])
+    none = run(x, w, torch.full_like(targets, -100), dloss, dlse)
+    assert (none["loss"] == 0).all() and (none["dx"] == 0).all() and (none["dweight"] == 0).all()
+
+
+def test_a_row_of_nan_stays_in_its_row():
+    x, w, targets, dloss, _ = case(5, 70, 90, 64, torch.bfloat16)
+    targets = targets.clamp(0, 89)
+    clean = run(x, w, targets, dloss, None)
+    x[3] = float("nan")
+    got = run(x, w, targets, dloss, None)
+    rest = torch.arange(70, device="cuda") != 3
+    assert torch.isnan(got["loss"][3]) and torch.isnan(got["lse"][3]) and torch.isnan(got["dx"][3]).all()
+    for k in ("loss", "lse", "dx"):
+        assert torch.equal(got[k][rest], clean[k][rest])
+    assert torch.isnan(got["dweight"]).all()
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-12, 1.0, 65536.0, 1e25])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gradients_of_any_size(dtype, size):
+    """dloss scaled by a power of two, as a mean over many rows or a loss scale brings it: the
+    gradients keep their digits (they are compared before the scale would round them away)."""
+    t = TYPES[dtype]
+    x, w, targets, dloss, dlse = case(6, 100, 500, 64, t)
+    base = run(x, w, targets, dloss, dlse)
+    scale = 2.0 ** round(torch.log2(torch.tensor(size)).item())
+    got = run(x, w, targets, dloss * scale, dlse * scale)
+    fits = torch.finfo(t)
+    for k in ("dx", "dweight"):
+        want = base[k].double() * scale
+        # the same digits where neither side is a subnormal or overflows
+        clear = (want.abs() >= 4 * fits.tiny) & (want.abs() <= fits.max / 2) & (base[k].abs() >= 4 * fits.tiny)
+        assert torch.allclose(got[k].double()[clear], want[clear], rtol=2 * ref.HALF[t], atol=0), (k, dtype, size)
+
+
+def test_no_gradient_at_all():
+    x, w, targets, dloss, _ = case(7, 40, 60, 32, torch.float16)
+    got = run(x, w, targets, torch.zeros_like(dloss), None)
+    assert (got["dx"] == 0).all() and (got["dweight"] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 72), ("f32", 36), ("bf16", 71), ("f32", 33), ("f16", 129)])
+def test_strided_rows_and_what_lies_around(dtype, D):
+    t = TYPES[dtype]
+    M, V = 140, 270
+    x, w, targets, dloss, dlse = [v.cuda() for v in case(8, M, V, D, t)]
+    want = run(x, w, targets, dloss, dlse)
+    whole = D * t.itemsize % 16 == 0
+    pad = 16 // t.itemsize if whole else 3
+    xs, _ = spread(x, 2 * pad if whole else 3, pad if whole else 1)
+    ws, _ = spread(w, 2 * pad if whole else 3, pad if whole else 1)
+    dxs, dxw = spread(torch.zeros_like(x))
+    dws, dww = spread(torch.zeros_like(w))
+    loss = torch.full((M + 2,), 7.0, device="cuda")
+    lse = torch.full((M + 2,), 7.0, device="cuda")
+    mss.head_loss(xs, ws, targets, out=(loss[1:-1], lse[1:-1]))
+    mss.head_loss_backward(xs, ws, targets, lse[1:-1], dloss, dlse, out=dict(dx=dxs, dweight=dws))
+    torch.cuda.synchronize()
+    for got, k in ((loss[1:-1], "loss"), (lse[1:-1], "lse"), (dxs, "dx"), (dws, "dweight")):
+        assert torch.equal(got, want[k]), k
+    assert (loss[[0, -1]] == 7).all() and (lse[[0, -1]] == 7).all()
+    for wide in (dxw, dww):
+        assert torch.isnan(wide[:, :1]).all() and torch.isnan(wide[:, D + 1:]).all()
+
+
+def test_one_gradient_alone():
+    x, w, targets, dloss, dlse = [v.cuda() for v in case(9, 200, 700, 96, torch.bfloat16)]
+    _, lse = mss.head_loss(x, w, targets)
+    both = mss.head_loss_backward(x, w, targets, lse, dloss, dlse)
+    a = mss.head_loss_backward(x, w, targets, lse, dloss, dlse, need_dweight=False)
+    b = mss.head_loss_backward(x, w, targets, lse, dloss, dlse, need_dx=False)
+    assert a["dweight"] is None and torch.equal(a["dx"], both["dx"])
+    assert b["dx"] is None and torch.equal(b["dweight"], both["dweight"])
+    assert mss.head_loss_backward(x, w, targets, lse, dloss, need_dx=False, need_dweight=False) == dict(
+        dx=None, dweight=None)
+
+
+def test_no_rows():
+    w = torch.ones(30, 16, device="cuda")
+    x, t, f = torch.empty(0, 16, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
+    loss, lse = mss.head_loss(x, w, t)
+    assert loss.shape == lse.shape == (0,)
+    g = mss.head_loss_backward(x, w, t, f, f, out=dict(dweight=torch.ones(30, 16, device="cuda")))
+    assert (g["dweight"] == 0).all() and g["dx"].shape == (0, 16)
+
+
+def test_gradients_against_differences_of_the_kernels():
+    """fp32, along a direction: (loss(x + h d) - loss(x - h d)) / 2h against <dx, d>.  The losses are
+    off by the reference's bounds; the difference by h^2 / 6 times the third derivative, a third
+    cumulant of the logits' slopes, which is at most their range cubed."""
+    M, V, D, h = 60, 150, 64, 0.05
+    x, w, targets, _, _ = case(10, M, V, D, torch.float32, spread_out=1.0)
+    targets = targets.clamp(0, V - 1)
+    got = run(x, w, targets, torch.ones(M), None)
+    want = ref.head(x, w, targets, 1.0, torch.ones(M))
+    g = generator(11)
+    d, e = normal(g, M, D, std=D ** -0.5), normal(g, V, D, std=0.1 * D ** -0.5)
+
+    def slopes(x1, w1, x0, w0, along):
+        sides = [mss.head_loss(a.cuda(), b.cuda(), targets.cuda())[0].double().cpu() for a, b in ((x1, w1), (x0, w0))]
+        off = sum(ref.head(a, b, targets, 1.0)["loss"][1] for a, b in ((x1, w1), (x0, w0))) / (2 * h)
+        reach = along.max(1).values - along.min(1).values
+        return (sides[0] - sides[1]) / (2 * h), off + h * h / 6 * (1.1 * reach) ** 3
+
+    slope, off = slopes(x + h * d, w, x - h * d, w, d.double() @ w.double().t())
+    announce(f"slopes of {slope.abs().mean():.2g} within {off.max():.2g}")
+    assert off.max() < 0.02 * slope.abs().max()
+    exact = (got["dx"].double().cpu() * d.double()).sum(1)
+    assert ((slope - exact).abs() <= off + (want["dx"][1] * d.abs().double()).sum(1)).all()
+    slope, off = slopes(x, w + h * e, x, w - h * e, x.double() @ e.double().t())
+    exact = (got["dweight"].double().cpu() * e.double()).sum()
+    assert abs(slope.sum() - exact) <= off.sum() + (want["dweight"][1] * e.abs().double()).sum()
+
+
+def test_same_bits_every_time():
+    x, w, targets, dloss, dlse = [v.cuda() for v in case(12, 1000, 3000, 128, torch.bfloat16)]
+    first = run(x, w, targets, dloss, dlse)
+    for _ in range(4):
+        again = run(x, w, targets, dloss, dlse)
+        assert all(torch.equal(first[k], again[k]) for k in first)
