@@ -52,6 +52,7 @@ struct Part {
     using S = Shape<P>;
     int64_t l, r;             // the lane's: l of acc[.][0], r of acc[0][.] element 0
     int64_t l0, r0;           // the tile's
+    int64_t lw, rw;           // the wave's
     int lane, wave;
     __device__ __forceinline__ Part(const ProductArgs& a) {
         int64_t tl, tr;
@@ -60,8 +61,10 @@ struct Part {
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         l0 = tl * S::BL;
         r0 = tr * S::BR;
-        l = l0 + wave % S::WL * (S::BL / S::WL) + lane % 16;
-        r = r0 + wave / S::WL * S::kSlab + 4 * (lane / 16);
+        lw = l0 + wave % S::WL * (S::BL / S::WL);
+        rw = r0 + wave / S::WL * S::kSlab;
+        l = lw + lane % 16;
+        r = rw + 4 * (lane / 16);
     }
 };
 
@@ -97,8 +100,7 @@ __global__ __launch_bounds__(P::kThreads) void head_loss_kernel(ProductArgs a, L
     const Part<P> at(a);
     v4f acc[P::kTR][P::kTL];
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
-    const int64_t slab0 = at.r0 + at.wave / S::WL * S::kSlab;
-    if (slab0 >= a.nr) return;
+    if (at.rw >= a.nr) return;
     const int valid = static_cast<int>(a.nr - at.r < S::kSlab ? a.nr - at.r : S::kSlab);   // from the lane's r on
 #pragma unroll
     for (int j = 0; j < P::kTL; j++) {
@@ -123,7 +125,7 @@ __global__ __launch_bounds__(P::kThreads) void head_loss_kernel(ProductArgs a, L
 #pragma unroll
             for (int e = 0; e < 4; e++) sum += ex2(acc[i][j][e] - top);
         sum = over_quads_sum(sum);
-        if (at.lane < 16 && in) h.part[slab0 / S::kSlab * a.nl + m] = make_float2(top, sum);
+        if (at.lane < 16 && in) h.part[at.rw / S::kSlab * a.nl + m] = make_float2(top, sum);
     }
 }
 
@@ -188,35 +190,45 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const T* in, int64_t ld_i
                                                        int64_t ld_out) {
     const int64_t row = blockIdx.x * int64_t{4} + threadIdx.x / kWave;
     if (row >= rows) return;
-    for (int64_t c = threadIdx.x % kWave * 8; c < ld_out; c += kWave * 8) {
-        T v[8];
-#pragma unroll
-        for (int e = 0; e < 8; e++) v[e] = c + e < n ? in[row * ld_in + c + e] : static_cast<T>(0.0f);
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            if (c + e < ld_out) out[row * ld_out + c + e] = v[e];
+    constexpr int V = 16 / sizeof(T);           // ld_out is a multiple
+    for (int64_t c = threadIdx.x % kWave * V; c < ld_out; c += kWave * V) {
+        RowVec<T, V> v;
+        v.load(in + row * ld_in, static_cast<int>(c), static_cast<int>(n));
+        v.template store<false>(out + row * ld_out + c, 0, V);
     }
 }
 
 // in (rows, n) to out (n, ld_out), ld_out >= rows, zeros behind and in the
-// columns of rows that are `off` (t < 0).
+// columns of rows that are off (t < 0).  A tile of 64 x 64 values goes through
+// LDS, read and written in pieces of 16 bytes; in's rows start at multiples of 16
+// bytes (ld_in, a copied row's or the caller's), out's too.
 template <typename T>
 __global__ __launch_bounds__(256) void transpose_kernel(const T* in, int64_t ld_in, int64_t rows, int64_t n, T* out,
                                                         int64_t ld_out, const int* t) {
-    constexpr int kTile = 64, kPad = sizeof(T) == 2 ? 2 : 1;
-    __shared__ T tile[kTile][kTile + kPad];
+    constexpr int kTile = 64, V = 16 / sizeof(T), kPieces = kTile / V;
+    // one word (or a half) more than a multiple of the banks: neighbours along r are in different ones
+    __shared__ T tile[kTile][kTile + 4 / sizeof(T)];
     const int64_t across = (n + kTile - 1) / kTile;
     const int64_t r0 = blockIdx.x / across * kTile, c0 = blockIdx.x % across * kTile;
-    const int x = threadIdx.x % kTile;
-    for (int y = threadIdx.x / kTile; y < kTile; y += 4) {
+#pragma unroll
+    for (int k = 0; k < kTile * kPieces / 256; k++) {
+        const int at = k * 256 + threadIdx.x, y = at / kPieces, x = at % kPieces * V;
         const int64_t r = r0 + y, c = c0 + x;
-        const bool ok = r < rows && c < n && (!t || t[r] >= 0);
-        tile[y][x] = ok ? in[r * ld_in + c] : static_cast<T>(0.0f);
+        RowVec<T, V> v;
+        v.zero();
+        if (r < rows && c < n && (!t || t[r] >= 0)) v.load(in + r * ld_in + c, 0, n - c < V ? static_cast<int>(n - c) : V);
+#pragma unroll
+        for (int e = 0; e < V; e++) tile[y][x + e] = v.t[e];
     }
     __syncthreads();
-    for (int y = threadIdx.x / kTile; y < kTile; y += 4) {
+#pragma unroll
+    for (int k = 0; k < kTile * kPieces / 256; k++) {
+        const int at = k * 256 + threadIdx.x, y = at / kPieces, x = at % kPieces * V;
         const int64_t c = c0 + y, r = r0 + x;
-        if (c < n && r < ld_out) out[c * ld_out + r] = tile[x][y];
+        RowVec<T, V> v;
+#pragma unroll
+        for (int e = 0; e < V; e++) v.t[e] = tile[x + e][y];
+        if (c < n && r < ld_out) v.template store<false>(out + c * ld_out + r, 0, V);
     }
 }
 
@@ -234,13 +246,27 @@ struct RowGrads {
 
 constexpr float kMostDl = 8190.0f;       // rounds to less than 2^13 in every type
 
+// Each workgroup finds the largest factor of all rows for itself (12 to 16 bytes
+// a row, from L2) and writes 1024 rows: one launch, and no wait between workgroups.
 __global__ __launch_bounds__(1024) void row_grads_kernel(HeadArgs h, RowGrads g) {
+    constexpr int kAhead = 8;
     __shared__ float most[16];
     float top = 0.0f;
-    for (int64_t m = threadIdx.x; m < h.M; m += 1024) {
-        const int64_t t = target_of(h.targets, h.wide_ids, m);
-        if (t < 0 || t >= h.V) continue;
-        top = __builtin_fmaxf(top, __builtin_fabsf(h.dloss[m]) + (h.dlse ? __builtin_fabsf(h.dlse[m]) : 0.0f));
+    for (int64_t m0 = threadIdx.x; m0 < h.M; m0 += 1024 * kAhead) {
+        int64_t t[kAhead];
+        float up[kAhead], more[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) {
+            const int64_t m = m0 + 1024 * i;
+            const bool in = m < h.M;
+            t[i] = in ? target_of(h.targets, h.wide_ids, m) : -1;
+            up[i] = in ? h.dloss[m] : 0.0f;
+            more[i] = in && h.dlse ? h.dlse[m] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; i++)
+            if (t[i] >= 0 && t[i] < h.V)
+                top = __builtin_fmaxf(top, __builtin_fabsf(up[i]) + __builtin_fabsf(more[i]));
     }
     for (int d = 32; d > 0; d /= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d));
     if (threadIdx.x % kWave == 0) most[threadIdx.x / kWave] = top;
@@ -249,16 +275,16 @@ __global__ __launch_bounds__(1024) void row_grads_kernel(HeadArgs h, RowGrads g)
     // 1 where nothing or not a number would come of it; bounded, so that 1 / s is a normal number
     float s = 1.0f;
     if (top > 0.0f && top < INFINITY) s = __builtin_fminf(kMostDl / top, 0x1p120f);
-    if (threadIdx.x == 0) g.back[0] = h.logit_scale / s;
-    for (int64_t m = threadIdx.x; m < h.M; m += 1024) {
-        const int64_t t = target_of(h.targets, h.wide_ids, m);
-        const bool on = t >= 0 && t < h.V;
-        const float up = on ? h.dloss[m] : 0.0f;
-        g.a[m] = on ? (up + (h.dlse ? h.dlse[m] : 0.0f)) * s : 0.0f;
-        g.b[m] = up * s;
-        g.lse2[m] = on ? h.lse[m] * kLog2e : 0.0f;
-        g.t[m] = on ? static_cast<int>(t) : -1;
-    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) g.back[0] = h.logit_scale / s;
+    const int64_t m = blockIdx.x * int64_t{1024} + threadIdx.x;
+    if (m >= h.M) return;
+    const int64_t t = target_of(h.targets, h.wide_ids, m);
+    const bool on = t >= 0 && t < h.V;
+    const float up = on ? h.dloss[m] : 0.0f;
+    g.a[m] = on ? (up + (h.dlse ? h.dlse[m] : 0.0f)) * s : 0.0f;
+    g.b[m] = up * s;
+    g.lse2[m] = on ? h.lse[m] * kLog2e : 0.0f;
+    g.t[m] = on ? static_cast<int>(t) : -1;
 }
 
 struct DlArgs {
@@ -270,16 +296,24 @@ struct DlArgs {
     int64_t ld_dl, ld_dlt;
 };
 
+// LDS of a kernel whose waves store T's through it when the product is done.
+template <typename P>
+constexpr int kStoreLds = P::kWaves * ColStore<typename Shape<P>::type, P::kTR, P::kTL>::kBytes;
+template <typename P>
+constexpr int kLdsWithStore = P::kLds > kStoreLds<P> ? P::kLds : kStoreLds<P>;
+
 template <typename P>
 __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlArgs h) {
-    using S = Shape<P>;
-    using T = typename S::type;
-    __shared__ __align__(1024) char lds[P::kLds];
+    using T = typename Shape<P>::type;
+    using Rows = RowStore<T, P::kTR, P::kTL>;
+    using Cols = ColStore<T, P::kTR, P::kTL>;
+    typedef T quad __attribute__((ext_vector_type(4)));
+    static_assert(Rows::kBytes <= Cols::kBytes, "one region for both");
+    __shared__ __align__(1024) char lds[kLdsWithStore<P>];
     const Part<P> at(a);
     v4f acc[P::kTR][P::kTL];
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
-    T* dl = static_cast<T*>(h.dl);
-    T* dlt = static_cast<T*>(h.dlt);
+    const bool whole = at.rw + 16 * P::kTR <= a.nr;
 #pragma unroll
     for (int j = 0; j < P::kTL; j++) {
         const int64_t m = at.l + 16 * j;
@@ -288,37 +322,42 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
         const float up = in ? h.g.a[m] : 0.0f, own = in ? h.g.b[m] : 0.0f, lse2 = in ? h.g.lse2[m] : 0.0f;
         const int64_t hit = t - h.first - at.r;
 #pragma unroll
-        for (int i = 0; i < P::kTR; i++) {
-            T v[4];
+        for (int i = 0; i < P::kTR; i++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 float p = ex2(__builtin_fmaf(acc[i][j][e], h.c, -lse2)) * up;
                 p = hit == 16 * i + e ? p - own : p;
-                v[e] = static_cast<T>(t >= 0 && at.r + 16 * i + e < a.nr ? p : 0.0f);
+                acc[i][j][e] = t >= 0 && (whole || at.r + 16 * i + e < a.nr) ? p : 0.0f;
             }
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int64_t r = at.r + 16 * i + e;
-                if (in && r < h.ld_dl) dl[m * h.ld_dl + r] = v[e];
-                if (m < h.ld_dlt && r < a.nr) dlt[r * h.ld_dlt + m] = v[e];
-            }
-        }
     }
+    const auto get = [&](int i, int j) {
+        quad v;
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = static_cast<T>(acc[i][j][e]);
+        return v;
+    };
+    __syncthreads();          // the last stage is read
+    char* mine = lds + at.wave * Cols::kBytes;
+    Rows::run(mine, at.lane, static_cast<T*>(h.dl) + at.lw * h.ld_dl + at.rw, h.ld_dl, a.nl - at.lw, h.ld_dl - at.rw, get);
+    Cols::run(mine, at.lane, static_cast<T*>(h.dlt) + at.rw * h.ld_dlt + at.lw, h.ld_dlt, h.ld_dlt - at.lw, a.nr - at.rw,
+              get);
 }
 
 struct GradArgs {
     const float* back;
     void* out;                // (nl, ld) of T; or null:
     int64_t ld;
-    float* acc;               // [split][nl][nr] fp32, added to unless it is the first piece
+    float* acc;               // [split][nl][ld] fp32, ld a multiple of 4; added to unless it is the first piece
     bool first;
     int split;                // of K
 };
 
 template <typename P>
 __global__ __launch_bounds__(P::kThreads) void head_grad_kernel(ProductArgs a, GradArgs h) {
-    using S = Shape<P>;
-    using T = typename S::type;
+    using T = typename Shape<P>::type;
+    using Rows = RowStore<T, P::kTR, P::kTL>;
+    typedef T quad __attribute__((ext_vector_type(4)));
+    static_assert(P::kWaves * Rows::kBytes <= P::kLds, "stored through the stages' LDS");
     __shared__ __align__(1024) char lds[P::kLds];
     const Part<P> at(a);
     v4f acc[P::kTR][P::kTL];
@@ -326,37 +365,46 @@ __global__ __launch_bounds__(P::kThreads) void head_grad_kernel(ProductArgs a, G
     const int64_t stages = (a.kbytes + kStage - 1) / kStage;
     const int64_t k0 = stages * blockIdx.y / h.split * kStage, k1 = stages * (blockIdx.y + 1) / h.split * kStage;
     P::run(a, at.l0, at.r0, k0, k1 < a.kbytes ? k1 : a.kbytes, lds, acc);
-    const float back = h.back[0];
+    if (!h.out) {
+        // fp32 sums: a lane's four are 16 bytes of a row
+        float* to = h.acc + (blockIdx.y * a.nl + at.l) * h.ld + at.r;
 #pragma unroll
-    for (int j = 0; j < P::kTL; j++) {
-        const int64_t l = at.l + 16 * j;
-        if (l >= a.nl) continue;
+        for (int j = 0; j < P::kTL; j++) {
+            if (at.l + 16 * j >= a.nl) continue;
 #pragma unroll
-        for (int i = 0; i < P::kTR; i++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int64_t r = at.r + 16 * i + e;
-                if (r >= a.nr) continue;
-                if (h.out) {
-                    static_cast<T*>(h.out)[l * h.ld + r] = static_cast<T>(acc[i][j][e] * back);
-                } else {
-                    float& to = h.acc[(blockIdx.y * a.nl + l) * a.nr + r];
-                    to = h.first ? acc[i][j][e] : to + acc[i][j][e];
-                }
+            for (int i = 0; i < P::kTR; i++) {
+                if (at.r + 16 * i >= a.nr) continue;
+                v4f* p = reinterpret_cast<v4f*>(to + 16 * j * h.ld + 16 * i);
+                *p = h.first ? acc[i][j] : *p + acc[i][j];
             }
+        }
+        return;
     }
+    const float back = h.back[0];
+    __syncthreads();          // the last stage is read
+    Rows::run(lds + at.wave * Rows::kBytes, at.lane, static_cast<T*>(h.out) + at.lw * h.ld + at.rw, h.ld, a.nl - at.lw,
+              a.nr - at.rw, [&](int i, int j) {
+                  quad v;
+#pragma unroll
+                  for (int e = 0; e < 4; e++) v[e] = static_cast<T>(acc[i][j][e] * back);
+                  return v;
+              });
 }
 
+// out = back * the sum of the parts of K, 16 bytes of them to a lane.
 template <typename T>
-__global__ __launch_bounds__(256) void head_finish_kernel(const float* acc, int split, int64_t rows, int64_t n,
-                                                          const float* back, T* out, int64_t ld) {
+__global__ __launch_bounds__(256) void head_finish_kernel(const float* acc, int64_t ld_acc, int split, int64_t rows,
+                                                          int64_t n, const float* back, T* out, int64_t ld) {
     const int64_t row = blockIdx.x * int64_t{4} + threadIdx.x / kWave;
     if (row >= rows) return;
     const float s = back[0];
-    for (int64_t c = threadIdx.x % kWave; c < n; c += kWave) {
-        float v = 0.0f;
-        for (int k = 0; k < split; k++) v += acc[(k * rows + row) * n + c];
-        out[row * ld + c] = static_cast<T>(v * s);
+    for (int64_t c = threadIdx.x % kWave * 4; c < n; c += kWave * 4) {
+        v4f v = {0, 0, 0, 0};
+        for (int k = 0; k < split; k++) v += *reinterpret_cast<const v4f*>(acc + (k * rows + row) * ld_acc + c);
+        RowVec<T, 4> o;
+#pragma unroll
+        for (int e = 0; e < 4; e++) o.set(e, v[e] * s);
+        o.template store<false>(out + row * ld, static_cast<int>(c), static_cast<int>(n));
     }
 }
 
@@ -389,6 +437,7 @@ struct Plan {
     int split;                // of dx's K
     bool accumulate;          // dx goes through fp32 partial sums
     int64_t ld_m;             // values in a row of dl^T and x^T
+    int64_t ld_acc;           // and of dx's partial sums
     int64_t x, w, part, at_target, dl, dlt, xt, wt, acc, rows, bytes;
 };
 
@@ -458,7 +507,8 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
         p.x = take(M, p.Dk, e);
         p.w = take(p.piece, p.Dk, e);
     }
-    if (p.accumulate) p.acc = take(M * int64_t{4}, D, p.split);
+    p.ld_acc = align_up(D, 4);
+    if (p.accumulate) p.acc = take(M * int64_t{4}, p.ld_acc, p.split);
     p.rows = take(align_up(M, 64) * int64_t{16} + 256, 1, 1);
     return fits;
 }
@@ -553,7 +603,7 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     g.lse2 = g.b + padded;
     g.t = reinterpret_cast<int*>(g.lse2 + padded);
     g.back = reinterpret_cast<float*>(g.t + padded);
-    row_grads_kernel<<<1, 1024, 0, st>>>(h, g);
+    row_grads_kernel<<<static_cast<uint32_t>(ceil_div(M, 1024)), 1024, 0, st>>>(h, g);
     if (hipError_t r = hipGetLastError()) return r;
     const T* x = static_cast<const T*>(h.x);
     int64_t ld_x = h.ld_x;
@@ -590,7 +640,7 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
         if (h.dx) {
             if (hipError_t r = transpose(w, ld_w, n, D, wt, ld_n, static_cast<const int*>(nullptr), st)) return r;
             large = rounds(M, D, p.split).large;
-            const GradArgs to{g.back, p.accumulate ? nullptr : h.dx, h.ld_dx, reinterpret_cast<float*>(ws + p.acc),
+            const GradArgs to{g.back, p.accumulate ? nullptr : h.dx, p.accumulate ? p.ld_acc : h.ld_dx, reinterpret_cast<float*>(ws + p.acc),
                               v0 == 0, p.split};
             if (hipError_t r = grad<T>(product(dl, ld_n * e, M, wt, ld_n * e, D, ld_n * e, large), large, to, st))
                 return r;
@@ -605,7 +655,7 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     }
     if (h.dx && p.accumulate) {
         head_finish_kernel<T><<<static_cast<uint32_t>(ceil_div(M, 4)), 256, 0, st>>>(
-            reinterpret_cast<const float*>(ws + p.acc), p.split, M, D, g.back, static_cast<T*>(h.dx), h.ld_dx);
+            reinterpret_cast<const float*>(ws + p.acc), p.ld_acc, p.split, M, D, g.back, static_cast<T*>(h.dx), h.ld_dx);
         return hipGetLastError();
     }
     return hipSuccess;

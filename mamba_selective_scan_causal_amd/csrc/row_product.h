@@ -167,4 +167,87 @@ struct RowProduct {
     }
 };
 
+// Orders a wave's LDS writes before its lanes' reads of them (the hardware
+// does; this is for the compiler).
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// 16 bytes of T's to p, which may lie at any element, n of them.
+template <typename T>
+__device__ __forceinline__ void store_piece(T* p, v4i piece, int64_t n) {
+    constexpr int V = 16 / sizeof(T);
+    RowVec<T, V> r;
+    r.t = __builtin_bit_cast(typename RowVec<T, V>::type, piece);
+    if (n > 0) r.template store<false>(p, 0, n < V ? static_cast<int>(n) : V);
+}
+
+// A wave's part of C, 16 * TR values along r for 16 * TL along l, to memory
+// through LDS, so that whole lines are written: a lane's own four values are 8
+// bytes of a row, and rows are far apart.
+//
+// Rows of l: out[l * ld + r], l < nl, r < nr, from the wave's first l and r;
+// get(i, j) gives the four values of acc[i][j].  `lds` is the wave's own.
+template <typename T, int TR, int TL>
+struct RowStore {
+    static constexpr int kRow = 16 * TR * sizeof(T) + 16;       // 16 bytes apart from a multiple of all banks
+    static constexpr int kBytes = 16 * kRow;
+    template <typename F>
+    static __device__ __forceinline__ void run(char* lds, int lane, T* out, int64_t ld, int64_t nl, int64_t nr, F get) {
+        typedef T quad __attribute__((ext_vector_type(4)));
+        constexpr int kPieces = TR * sizeof(T);                  // of a row
+#pragma unroll
+        for (int j = 0; j < TL; j++) {
+#pragma unroll
+            for (int i = 0; i < TR; i++) {
+                const quad v = get(i, j);
+                *reinterpret_cast<quad*>(lds + lane % 16 * kRow + (16 * i + lane / 16 * 4) * sizeof(T)) = v;
+            }
+            wave_lds_fence();
+#pragma unroll
+            for (int k = 0; k < 16 * kPieces / kWave; k++) {
+                const int at = k * kWave + lane, row = at / kPieces, c = at % kPieces;
+                const v4i piece = *reinterpret_cast<const v4i*>(lds + row * kRow + c * 16);
+                const int64_t l = 16 * j + row, r = c * (16 / sizeof(T));
+                if (l < nl) store_piece(out + l * ld + r, piece, nr - r);
+            }
+            wave_lds_fence();
+        }
+    }
+};
+
+// Rows of r: out[r * ld + l].  Four tiles along r at a time.
+template <typename T, int TR, int TL>
+struct ColStore {
+    static constexpr int kRow = 16 * TL * sizeof(T) + 16;
+    static constexpr int kBytes = 64 * kRow;
+    template <typename F>
+    static __device__ __forceinline__ void run(char* lds, int lane, T* out, int64_t ld, int64_t nl, int64_t nr, F get) {
+        constexpr int kPieces = TL * sizeof(T);
+#pragma unroll
+        for (int i0 = 0; i0 < TR; i0 += 4) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int j = 0; j < TL; j++) {
+                    const auto v = get(i0 + i, j);
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        *reinterpret_cast<T*>(lds + (16 * i + lane / 16 * 4 + e) * kRow +
+                                              (16 * j + lane % 16) * sizeof(T)) = v[e];
+                }
+            wave_lds_fence();
+#pragma unroll
+            for (int k = 0; k < 64 * kPieces / kWave; k++) {
+                const int at = k * kWave + lane, row = at / kPieces, c = at % kPieces;
+                const v4i piece = *reinterpret_cast<const v4i*>(lds + row * kRow + c * 16);
+                const int64_t r = 16 * i0 + row, l = c * (16 / sizeof(T));
+                if (r < nr) store_piece(out + r * ld + l, piece, nl - l);
+            }
+            wave_lds_fence();
+        }
+    }
+};
+
 }  // namespace mss
