@@ -66,6 +66,15 @@ struct Part {
         l = lw + lane % 16;
         r = rw + 4 * (lane / 16);
     }
+    // The place of column v (any number) from the lane's r on: 16 i + e of acc[i][.][e], or one
+    // that no e has.
+    __device__ __forceinline__ int place(int64_t v) const {
+        return v >= r && v < r + S::kSlab ? static_cast<int>(v - r) : -1;
+    }
+    // Whether the lane's tiles hold column v of nr.
+    __device__ __forceinline__ bool holds(int64_t v, int64_t nr) const {
+        return v >= r && v < rw + S::kSlab && v < nr && (v - r) % 16 < 4;
+    }
 };
 
 // ---- forward -----------------------------------------------------------------
@@ -101,23 +110,25 @@ __global__ __launch_bounds__(P::kThreads) void head_loss_kernel(ProductArgs a, L
     v4f acc[P::kTR][P::kTL];
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
     if (at.rw >= a.nr) return;
-    const int valid = static_cast<int>(a.nr - at.r < S::kSlab ? a.nr - at.r : S::kSlab);   // from the lane's r on
+    const bool whole = at.rw + S::kSlab <= a.nr;
+    const int valid = static_cast<int>(a.nr - at.rw) - (at.r - at.rw);       // from the lane's r on, where not whole
 #pragma unroll
     for (int j = 0; j < P::kTL; j++) {
         const int64_t m = at.l + 16 * j;
         const bool in = m < a.nl;
         const int64_t t = in ? target_of(h.targets, h.wide, h.m0 + m) : -1;
-        const int64_t hit = t - h.first - at.r;                  // the target's place from the lane's r on
-        float top = -INFINITY;
+        const int hit = at.place(t - h.first);
+        float top = -INFINITY, own = 0.0f;
 #pragma unroll
         for (int i = 0; i < P::kTR; i++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const float v = 16 * i + e < valid ? acc[i][j][e] * h.c : -INFINITY;
+                const float v = whole || 16 * i + e < valid ? acc[i][j][e] * h.c : -INFINITY;
                 acc[i][j][e] = v;
                 top = __builtin_fmaxf(top, v);
-                if (hit == 16 * i + e && 16 * i + e < valid && in) h.at_target[h.m0 + m] = v;
+                own = hit == 16 * i + e ? v : own;
             }
+        if (in && at.holds(t - h.first, a.nr)) h.at_target[h.m0 + m] = own;
         top = over_quads_max(top);
         float sum = 0.0f;
 #pragma unroll
@@ -320,7 +331,7 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
         const bool in = m < a.nl;
         const int t = in ? h.g.t[m] : -1;
         const float up = in ? h.g.a[m] : 0.0f, own = in ? h.g.b[m] : 0.0f, lse2 = in ? h.g.lse2[m] : 0.0f;
-        const int64_t hit = t - h.first - at.r;
+        const int hit = at.place(t - h.first);
 #pragma unroll
         for (int i = 0; i < P::kTR; i++)
 #pragma unroll
@@ -417,7 +428,7 @@ constexpr int64_t kCus = 256;
 int64_t align_up(int64_t n, int64_t a) { return ceil_div(n, a) * a; }
 
 // Rounds of large tiles that a product of nl x nr takes, K apart, and whether
-// small tiles (two workgroups to a CU, at 1 / 1.13 of the rate) take less.
+// small tiles (two workgroups to a CU, at 1 / 1.16 of the rate) take less.
 struct Rounds {
     double cost;
     bool large;
@@ -425,7 +436,7 @@ struct Rounds {
 Rounds rounds(int64_t nl, int64_t nr, int64_t split = 1) {
     const double big = static_cast<double>(ceil_div(ceil_div(nl, 256) * ceil_div(nr, 256) * split, kCus));
     const double small =
-        0.5 * 1.13 * static_cast<double>(ceil_div(ceil_div(nl, 128) * ceil_div(nr, 128) * split, 2 * kCus));
+        0.5 * 1.16 * static_cast<double>(ceil_div(ceil_div(nl, 128) * ceil_div(nr, 128) * split, 2 * kCus));
     return {big <= small ? big : small, big <= small};
 }
 
