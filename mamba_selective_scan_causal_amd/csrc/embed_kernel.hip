@@ -25,12 +25,12 @@ namespace mss {
 namespace {
 
 constexpr int kSortThreads = 256;
-constexpr int kSortRounds = 8;                                  // of 64 keys a wave
-constexpr int kSortTile = kSortThreads * kSortRounds;
+constexpr int kMostTiles = 64;
 constexpr int kMaxBits = 10;
 constexpr int kMaxBins = 1 << kMaxBits;
-constexpr int kScanThreads = 1024;
-constexpr int kRun = 32;
+constexpr bool kStream = true;            // y and dW pass the caches by
+constexpr int kSumThreads = 512;
+constexpr int kRun = 16;
 constexpr int kZeroRows = 16;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -43,8 +43,10 @@ __device__ __forceinline__ uint32_t key_of(const void* ids, bool wide, int64_t m
 
 // ---- forward -----------------------------------------------------------------
 
+// Values to a lane: 16 bytes of the wider type, so that its lines are read or
+// written whole by one instruction.
 template <typename TW, typename TY>
-constexpr int kVec = sizeof(TW) == 2 || sizeof(TY) == 2 ? 8 : 4;
+constexpr int kVec = sizeof(TW) == 4 || sizeof(TY) == 4 ? 4 : 8;
 
 template <typename TW, typename TY>
 __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a) {
@@ -56,20 +58,33 @@ __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a) {
     TY* y = static_cast<TY*>(a.y) + m * a.ld_y;
     const bool in = key < static_cast<uint64_t>(a.V);
     const TW* w = static_cast<const TW*>(a.w) + (in ? key * a.ld_w : 0);
-    for (int c = (threadIdx.x % kWave) * V; c < n; c += kWave * V) {
-        RowVec<TW, V> r;
-        RowVec<TY, V> o;
-        if (in)
-            r.load(w, c, n);
-        else
-            r.zero();
+    constexpr int kAhead = 4;
+    for (int c0 = (threadIdx.x % kWave) * V; c0 < n; c0 += kAhead * kWave * V) {
+        RowVec<TW, V> r[kAhead];
 #pragma unroll
-        for (int e = 0; e < V; e++) o.set(e, in ? a.scale * r[e] : 0.0f);
-        o.template store<false>(y, c, n);
+        for (int i = 0; i < kAhead; i++) {
+            const int c = c0 + i * kWave * V;
+            if (in && c < n) r[i].load(w, c, n);
+            else r[i].zero();
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) {
+            const int c = c0 + i * kWave * V;
+            RowVec<TY, V> o;
+#pragma unroll
+            for (int e = 0; e < V; e++) o.set(e, in ? a.scale * r[i][e] : 0.0f);
+            if (c < n) o.template store<kStream>(y, c, n);
+        }
     }
 }
 
 // ---- the sort ------------------------------------------------------------------
+// A pass over one digit: every workgroup takes a tile of the positions, of the
+// same size, and counts[tile][digit] says how many of the tile's keys have the
+// digit.  The counts of the first pass are made by a launch of their own; a pass
+// counts for the next one as it places its keys.  A workgroup works out where its
+// keys go from the counts of all tiles (at most kMostTiles), so that no launch
+// between only adds them up.
 
 struct SortArgs {
     const void* ids;          // first pass
@@ -79,8 +94,11 @@ struct SortArgs {
     const uint32_t* pos_in;
     uint32_t* key_out;
     uint32_t* pos_out;
-    uint32_t* counts;         // [bin][tile]
+    uint32_t* counts;         // [tiles][1 << bits]
+    uint32_t* next;           // of the next pass (right behind); null in the last
+    int later;                // passes behind the first, whose counts sort_count_kernel zeroes
     int64_t tiles;
+    int tile;                 // positions, a multiple of kSortThreads
     int shift, bits;
 };
 
@@ -91,75 +109,81 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t m) {
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
     __shared__ uint32_t bins[kMaxBins];
     const int n = 1 << a.bits;
-    for (int b = threadIdx.x; b < n; b += kSortThreads) bins[b] = 0;
-    __syncthreads();
-    const int64_t m0 = blockIdx.x * int64_t{kSortTile};
-    for (int i = 0; i < kSortRounds; i++) {
-        const int64_t m = m0 + i * kSortThreads + threadIdx.x;
-        if (m < a.M) atomicAdd(&bins[sort_key(a, m) >> a.shift & (n - 1)], 1u);
+    for (int b = threadIdx.x; b < n; b += kSortThreads) {
+        bins[b] = 0;
+        for (int p = 0; p < a.later; p++) a.next[(p * a.tiles + blockIdx.x) * n + b] = 0;
     }
     __syncthreads();
-    for (int b = threadIdx.x; b < n; b += kSortThreads) a.counts[b * a.tiles + blockIdx.x] = bins[b];
+    const int64_t m0 = blockIdx.x * int64_t{a.tile}, end = m0 + a.tile < a.M ? m0 + a.tile : a.M;
+    for (int64_t m = m0 + threadIdx.x; m < end; m += kSortThreads)
+        atomicAdd(&bins[sort_key(a, m) >> a.shift & (n - 1)], 1u);
+    __syncthreads();
+    for (int b = threadIdx.x; b < n; b += kSortThreads) a.counts[blockIdx.x * n + b] = bins[b];
 }
 
-// counts -> the sum of those before it, in place, by one workgroup.
-__global__ __launch_bounds__(kScanThreads) void sort_scan_kernel(uint32_t* counts, int64_t n) {
-    __shared__ uint32_t part[kScanThreads];
-    const int64_t each = (n + kScanThreads - 1) / kScanThreads;
-    const int64_t from = threadIdx.x * each, to = from + each < n ? from + each : n;
-    uint32_t sum = 0;
-    for (int64_t i = from; i < to; i++) sum += counts[i];
-    part[threadIdx.x] = sum;
-    for (int d = 1; d < kScanThreads; d *= 2) {
-        __syncthreads();
-        const uint32_t below = static_cast<int>(threadIdx.x) >= d ? part[threadIdx.x - d] : 0;
-        __syncthreads();
-        part[threadIdx.x] += below;
-    }
-    uint32_t before = part[threadIdx.x] - sum;
-    for (int64_t i = from; i < to; i++) {
-        const uint32_t c = counts[i];
-        counts[i] = before;
-        before += c;
-    }
-}
-
-// Each wave takes 512 keys in a row; a key's place is that of its bin, plus
-// the keys of that bin in the tile's earlier waves, in the wave's earlier
-// rounds and in the lanes before it.
+// Each wave takes a quarter of the tile in a row; a key's place is that of its
+// digit, plus the keys of that digit in earlier tiles, in the tile's earlier
+// waves, in the wave's earlier rounds and in the lanes before it.
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
-    constexpr int kWaves = kSortThreads / kWave;
+    constexpr int kWaves = kSortThreads / kWave, kEach = kMaxBins / kSortThreads, kTogether = 32;
     __shared__ uint32_t at[kWaves][kMaxBins];
+    __shared__ uint32_t sums[kWaves];
     const int n = 1 << a.bits, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     for (int b = threadIdx.x; b < kWaves * n; b += kSortThreads) at[b / n][b % n] = 0;
     __syncthreads();
-    const int64_t m0 = blockIdx.x * int64_t{kSortTile} + wave * (kSortRounds * kWave) + lane;
-    uint32_t key[kSortRounds], pos[kSortRounds];
+    const int quarter = a.tile / kWaves;
+    const int64_t m0 = blockIdx.x * int64_t{a.tile} + wave * quarter;
+    const int64_t end = m0 + quarter < a.M ? m0 + quarter : a.M;
+    for (int64_t m = m0 + lane; m < end; m += kWave) atomicAdd(&at[wave][sort_key(a, m) >> a.shift & (n - 1)], 1u);
+    // digits kEach t .. of thread t: all tiles' keys, and those of the tiles before
+    uint32_t all[kEach] = {}, before[kEach] = {}, sum = 0;
+    const int each = n > kSortThreads ? n / kSortThreads : 1, d0 = threadIdx.x * each;
+    if (d0 < n) {
 #pragma unroll
-    for (int i = 0; i < kSortRounds; i++) {
-        const int64_t m = m0 + i * kWave;
-        key[i] = pos[i] = 0;
-        if (m < a.M) {
-            key[i] = sort_key(a, m);
-            pos[i] = a.ids ? static_cast<uint32_t>(m) : a.pos_in[m];
-            atomicAdd(&at[wave][key[i] >> a.shift & (n - 1)], 1u);
+        for (int i = 0; i < kEach; i++) {
+            if (i >= each) break;
+            for (int64_t t0 = 0; t0 < a.tiles; t0 += kTogether) {
+                uint32_t c[kTogether];
+#pragma unroll
+                for (int k = 0; k < kTogether; k++) c[k] = t0 + k < a.tiles ? a.counts[(t0 + k) * n + d0 + i] : 0;
+#pragma unroll
+                for (int k = 0; k < kTogether; k++) {
+                    all[i] += c[k];
+                    before[i] += t0 + k < blockIdx.x ? c[k] : 0;
+                }
+            }
+            sum += all[i];
         }
     }
+    uint32_t upto = sum;                          // of the digits of this and the lower lanes
+    for (int d = 1; d < kWave; d *= 2) {
+        const uint32_t below = __shfl_up(upto, d);
+        if (lane >= d) upto += below;
+    }
+    if (lane == kWave - 1) sums[wave] = upto;
     __syncthreads();
-    for (int b = threadIdx.x; b < n; b += kSortThreads) {
-        uint32_t first = a.counts[b * a.tiles + blockIdx.x];
-        for (int w = 0; w < kWaves; w++) {
-            const uint32_t c = at[w][b];
-            at[w][b] = first;
-            first += c;
+    uint32_t first = upto - sum;
+    for (int w = 0; w < wave; w++) first += sums[w];
+    if (d0 < n)
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            if (i >= each) break;
+            uint32_t to = first + before[i];
+            for (int w = 0; w < kWaves; w++) {
+                const uint32_t c = at[w][d0 + i];
+                at[w][d0 + i] = to;
+                to += c;
+            }
+            first += all[i];
         }
-    }
     __syncthreads();
     volatile uint32_t* mine = at[wave];      // this wave's alone from here on
-#pragma unroll
-    for (int i = 0; i < kSortRounds; i++) {
-        const bool in = m0 + i * kWave < a.M;
-        const uint32_t digit = key[i] >> a.shift & (n - 1);
+    for (int64_t base = m0; base < end; base += kWave) {
+        const int64_t m = base + lane;
+        const bool in = m < end;
+        const uint32_t key = in ? sort_key(a, m) : 0;
+        const uint32_t pos = !in ? 0 : a.ids ? static_cast<uint32_t>(m) : a.pos_in[m];
+        const uint32_t digit = key >> a.shift & (n - 1);
         uint64_t same = __builtin_amdgcn_ballot_w64(in);
         for (int b = 0; b < a.bits; b++) {
             const uint64_t ones = __builtin_amdgcn_ballot_w64(digit >> b & 1);
@@ -167,13 +191,14 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
         }
         const uint64_t below = same & ((uint64_t{1} << lane) - 1);
         if (in) {
-            const uint32_t base = mine[digit];
-            const uint32_t to = base + __builtin_popcountll(below);
+            const uint32_t place = mine[digit];
+            const uint32_t to = place + __builtin_popcountll(below);
             // the lanes of a digit have all read its place before its first lane moves it on
             __builtin_amdgcn_wave_barrier();
-            if (below == 0) mine[digit] = base + __builtin_popcountll(same);
-            a.key_out[to] = key[i];
-            a.pos_out[to] = pos[i];
+            if (below == 0) mine[digit] = place + __builtin_popcountll(same);
+            a.key_out[to] = key;
+            a.pos_out[to] = pos;
+            if (a.next) atomicAdd(&a.next[to / a.tile * n + (key >> (a.shift + a.bits) & (n - 1))], 1u);
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -194,18 +219,17 @@ struct SumArgs {
     int64_t runs, slices;
 };
 
+// `o`: what dW holds there, where it is added to.
 template <typename TW, int V>
-__device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t key, int c, const float (&sum)[V]) {
+__device__ __forceinline__ void write_sum(const SumArgs& a, uint32_t key, int c, const float (&sum)[V], RowVec<TW, V> o) {
     const int n = static_cast<int>(a.D);
     TW* dw = static_cast<TW*>(a.dw) + key * a.ld_dw;
-    RowVec<TW, V> o;
-    if (a.accumulate) o.load(dw, c, n);
 #pragma unroll
     for (int e = 0; e < V; e++) {
         const float v = a.scale * sum[e];
         o.set(e, a.accumulate ? o[e] + v : v);
     }
-    o.template store<false>(dw, c, n);
+    o.template store<kStream>(dw, c, n);
 }
 
 template <typename TW, typename TD, int V>
@@ -228,14 +252,14 @@ __device__ __forceinline__ void zero_rows(const SumArgs& a, int64_t block, bool*
     for (int i = 0; i < kZeroRows; i++) {
         if (found[i]) continue;
         TW* dw = static_cast<TW*>(a.dw) + (v0 + i) * a.ld_dw;
-        for (int c = threadIdx.x * V; c < n; c += blockDim.x * V) z.template store<false>(dw, c, n);
+        for (int c = threadIdx.x * V; c < n; c += blockDim.x * V) z.template store<kStream>(dw, c, n);
     }
 }
 
 template <typename TW, typename TD>
-__global__ __launch_bounds__(256) void embed_sum_kernel(SumArgs a) {
+__global__ __launch_bounds__(kSumThreads) void embed_sum_kernel(SumArgs a) {
     constexpr int V = kVec<TW, TD>;
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     __shared__ uint32_t keys[kRun + 2], places[kRun];
     __shared__ bool found[kZeroRows];
     const int64_t sums = a.runs * a.slices;
@@ -262,9 +286,14 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumArgs a) {
     bool first = keys[0] != keys[1];            // the current token begins in this run
     for (int i0 = 0; i0 < kRun; i0 += kAhead) {
         RowVec<TD, V> r[kAhead];
+        RowVec<TW, V> old[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; i++)
-            if (keys[1 + i0 + i] < a.V) r[i].load(dy + places[i0 + i] * a.ld_dy, c, n);
+        for (int i = 0; i < kAhead; i++) {
+            const uint32_t key = keys[1 + i0 + i];
+            if (key >= a.V) continue;
+            r[i].load(dy + places[i0 + i] * a.ld_dy, c, n);
+            if (a.accumulate && key != keys[2 + i0 + i]) old[i].load(static_cast<const TW*>(a.dw) + key * a.ld_dw, c, n);
+        }
 #pragma unroll
         for (int i = 0; i < kAhead; i++) {
             const uint32_t key = keys[1 + i0 + i], next = keys[2 + i0 + i];
@@ -274,12 +303,12 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumArgs a) {
             const bool last = i0 + i == kRun - 1;
             if (key == next && !last) continue;
             if (first && key != next) {
-                write_sum<TW, V>(a, key, c, sum);
+                write_sum<TW, V>(a, key, c, sum, old[i]);
             } else {
-                float* to = (first ? a.tail : a.head) + run * a.D;
+                RowVec<float, V> o;
 #pragma unroll
-                for (int e = 0; e < V; e++)
-                    if (c + e < n) to[c + e] = sum[e];
+                for (int e = 0; e < V; e++) o.set(e, sum[e]);
+                o.template store<false>((first ? a.tail : a.head) + run * a.D, c, n);
             }
             first = true;
 #pragma unroll
@@ -290,9 +319,9 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumArgs a) {
 
 // The tokens that reach over the end of the run they begin in.
 template <typename TW, typename TD>
-__global__ __launch_bounds__(256) void embed_join_kernel(SumArgs a) {
+__global__ __launch_bounds__(kSumThreads) void embed_join_kernel(SumArgs a) {
     constexpr int V = kVec<TW, TD>;
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 16;
     const int64_t run = blockIdx.x / a.slices;
     const int n = static_cast<int>(a.D);
     const int c = (static_cast<int>(blockIdx.x % a.slices) * blockDim.x + threadIdx.x) * V;
@@ -308,6 +337,8 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumArgs a) {
         if (a.key[mid * kRun] == key) lo = mid + 1;
         else hi = mid;
     }
+    RowVec<TW, V> old;
+    if (a.accumulate) old.load(static_cast<const TW*>(a.dw) + key * a.ld_dw, c, n);
     float sum[V];
 #pragma unroll
     for (int e = 0; e < V; e++) sum[e] = c + e < n ? a.tail[run * a.D + c + e] : 0.0f;
@@ -322,7 +353,7 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumArgs a) {
 #pragma unroll
             for (int e = 0; e < V; e++) sum[e] += p[i][e];
     }
-    write_sum<TW, V>(a, key, c, sum);
+    write_sum<TW, V>(a, key, c, sum, old);
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -330,7 +361,8 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumArgs a) {
 struct Plan {
     int passes, bits;         // bits per pass
     int64_t tiles, runs;
-    int64_t key[2], pos[2], counts, head, tail, bytes;      // offsets
+    int tile;
+    int64_t key[2], pos[2], counts, head, tail, bytes;   // offsets
 };
 
 bool plan_of(int64_t M, int64_t V, int64_t D, Plan& p) {
@@ -338,7 +370,10 @@ bool plan_of(int64_t M, int64_t V, int64_t D, Plan& p) {
     while (V >> bits) bits++;
     p.passes = (bits + kMaxBits - 1) / kMaxBits;
     p.bits = (bits + p.passes - 1) / p.passes;
-    p.tiles = ceil_div(M, kSortTile);
+    // enough tiles to spread the work, few enough to add their counts up in every one of them
+    p.tile = static_cast<int>(ceil_div(ceil_div(M, kMostTiles), 2 * kSortThreads) * 2 * kSortThreads);
+    if (p.tile < 2 * kSortThreads) p.tile = 2 * kSortThreads;
+    p.tiles = ceil_div(M, p.tile);
     p.runs = ceil_div(M, kRun);
     int64_t at = 0;
     const auto take = [&](int64_t n) {
@@ -347,15 +382,14 @@ bool plan_of(int64_t M, int64_t V, int64_t D, Plan& p) {
         return here;
     };
     for (int i = 0; i < 2; i++) p.key[i] = take(M), p.pos[i] = take(M);
-    p.counts = take(p.tiles << p.bits);
+    p.counts = take((p.tiles << p.bits) * p.passes);
     if (p.runs > (int64_t{1} << 60) / (D > 0 ? D : 1)) return false;
     p.head = take(p.runs * D);
     p.tail = take(p.runs * D);
     p.bytes = at;
     // grids: every launch below 2^32 threads
-    const int64_t slices = ceil_div(D, 64 * 4);
-    return p.runs < (int64_t{1} << 24) && slices * 256 < (int64_t{1} << 32) / (p.runs + 1) &&
-           p.runs * slices * 256 + ceil_div(V, kZeroRows) * 256 < (int64_t{1} << 32);
+    const int64_t blocks = p.runs * ceil_div(D, 4 * kSumThreads) + ceil_div(V, kZeroRows);
+    return p.runs < (int64_t{1} << 23) && D <= MSS_MAX_WIDTH && blocks < (int64_t{1} << 32) / kSumThreads;
 }
 
 template <typename F>
@@ -405,15 +439,18 @@ hipError_t launch_embed_bwd(const EmbedArgs& a, hipStream_t st) {
         s.pos_in = words(p.pos[from]);
         s.key_out = words(p.key[from ^ 1]);
         s.pos_out = words(p.pos[from ^ 1]);
-        s.counts = words(p.counts);
+        s.counts = words(p.counts) + i * (p.tiles << p.bits);
+        s.next = i + 1 < p.passes ? s.counts + (p.tiles << p.bits) : nullptr;
+        s.later = p.passes - 1;
         s.tiles = p.tiles;
+        s.tile = p.tile;
         s.shift = i * p.bits;
         s.bits = p.bits;
         from ^= 1;
-        sort_count_kernel<<<static_cast<uint32_t>(p.tiles), kSortThreads, 0, st>>>(s);
-        if (hipError_t e = hipGetLastError()) return e;
-        sort_scan_kernel<<<1, kScanThreads, 0, st>>>(s.counts, p.tiles << p.bits);
-        if (hipError_t e = hipGetLastError()) return e;
+        if (i == 0) {
+            sort_count_kernel<<<static_cast<uint32_t>(p.tiles), kSortThreads, 0, st>>>(s);
+            if (hipError_t e = hipGetLastError()) return e;
+        }
         sort_place_kernel<<<static_cast<uint32_t>(p.tiles), kSortThreads, 0, st>>>(s);
         if (hipError_t e = hipGetLastError()) return e;
     }
@@ -421,7 +458,8 @@ hipError_t launch_embed_bwd(const EmbedArgs& a, hipStream_t st) {
         using TW = decltype(w);
         using TD = decltype(y);
         const int64_t vecs = ceil_div(a.D, kVec<TW, TD>);
-        const int threads = vecs > 192 ? 256 : static_cast<int>(ceil_div(vecs, 64) * 64);
+        const int64_t slices = ceil_div(vecs, kSumThreads);
+        const int threads = static_cast<int>(ceil_div(ceil_div(vecs, slices), 64) * 64);
         SumArgs s{};
         s.M = a.M;
         s.V = a.V;
@@ -437,7 +475,7 @@ hipError_t launch_embed_bwd(const EmbedArgs& a, hipStream_t st) {
         s.head = reinterpret_cast<float*>(ws + p.head);
         s.tail = reinterpret_cast<float*>(ws + p.tail);
         s.runs = p.runs;
-        s.slices = ceil_div(vecs, threads);
+        s.slices = slices;
         const int64_t zeros = a.accumulate ? 0 : ceil_div(a.V, kZeroRows);
         embed_sum_kernel<TW, TD><<<static_cast<uint32_t>(s.runs * s.slices + zeros), threads, 0, st>>>(s);
         const hipError_t e = hipGetLastError();

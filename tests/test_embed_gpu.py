@@ -52,6 +52,15 @@ def test_few_tokens_in_many_places(M, V):
     check(dw, ref.embedding_backward(ids, dy, V, 1.0, torch.float32), "dweight")
 
 
+@pytest.mark.parametrize("M,V", [(3000, 2 ** 21 + 5), (40000, 3), (150000, 1000)])
+def test_more_digits_and_larger_tiles(M, V):
+    """Ids of three digits; more positions than fit the smallest tiles of the sort."""
+    g = generator(M)
+    ids, dy = some_ids(g, M, V), normal(g, M, 4)
+    dw = mss.embedding_backward(ids.cuda(), dy.cuda(), vocab=V)
+    check(dw, ref.embedding_backward(ids, dy, V, 1.0, torch.float32), "dweight")
+
+
 def test_all_padding_and_none():
     g = generator(1)
     dy = normal(g, 50, 40)
