@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
 // digit, plus the keys of that digit in earlier tiles, in the tile's earlier
 // waves, in the wave's earlier rounds and in the lanes before it.
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
-    constexpr int kWaves = kSortThreads / kWave, kEach = kMaxBins / kSortThreads, kTogether = 32;
+    constexpr int kWaves = kSortThreads / kWave, kEach = kMaxBins / kSortThreads, kTogether = 16;
     __shared__ uint32_t at[kWaves][kMaxBins];
     __shared__ uint32_t sums[kWaves];
     const int n = 1 << a.bits, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -139,21 +139,23 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
     uint32_t all[kEach] = {}, before[kEach] = {}, sum = 0;
     const int each = n > kSortThreads ? n / kSortThreads : 1, d0 = threadIdx.x * each;
     if (d0 < n) {
+        for (int64_t t0 = 0; t0 < a.tiles; t0 += kTogether) {
+            uint32_t c[kTogether][kEach];
 #pragma unroll
-        for (int i = 0; i < kEach; i++) {
-            if (i >= each) break;
-            for (int64_t t0 = 0; t0 < a.tiles; t0 += kTogether) {
-                uint32_t c[kTogether];
+            for (int k = 0; k < kTogether; k++)
 #pragma unroll
-                for (int k = 0; k < kTogether; k++) c[k] = t0 + k < a.tiles ? a.counts[(t0 + k) * n + d0 + i] : 0;
+                for (int i = 0; i < kEach; i++)
+                    c[k][i] = t0 + k < a.tiles && i < each ? a.counts[(t0 + k) * n + d0 + i] : 0;
 #pragma unroll
-                for (int k = 0; k < kTogether; k++) {
-                    all[i] += c[k];
-                    before[i] += t0 + k < blockIdx.x ? c[k] : 0;
+            for (int k = 0; k < kTogether; k++)
+#pragma unroll
+                for (int i = 0; i < kEach; i++) {
+                    all[i] += c[k][i];
+                    before[i] += t0 + k < blockIdx.x ? c[k][i] : 0;
                 }
-            }
-            sum += all[i];
         }
+#pragma unroll
+        for (int i = 0; i < kEach; i++) sum += all[i];
     }
     uint32_t upto = sum;                          // of the digits of this and the lower lanes
     for (int d = 1; d < kWave; d *= 2) {
@@ -217,6 +219,7 @@ struct SumArgs {
     float* head;              // [run][D]: of the token that came in from the run before
     float* tail;              // [run][D]: of the token that goes on in the next run
     int64_t runs, slices;
+    int64_t joins;            // slices of embed_join_kernel
 };
 
 // `o`: what dW holds there, where it is added to.
@@ -317,43 +320,98 @@ __global__ __launch_bounds__(kSumThreads) void embed_sum_kernel(SumArgs a) {
     }
 }
 
-// The tokens that reach over the end of the run they begin in.
+// The tokens that reach over the end of the run they begin in, for 64 V columns: a
+// wave looks at one end, and adds up a token's parts if they are few.  Those of a
+// token in many runs are added up by the workgroup, in equal shares in order, and
+// the shares in order.
+constexpr int kJoinThreads = 512;
+constexpr int kEnds = kJoinThreads / kWave;
+
 template <typename TW, typename TD>
-__global__ __launch_bounds__(kSumThreads) void embed_join_kernel(SumArgs a) {
-    constexpr int V = kVec<TW, TD>;
-    constexpr int kAhead = 16;
-    const int64_t run = blockIdx.x / a.slices;
-    const int n = static_cast<int>(a.D);
-    const int c = (static_cast<int>(blockIdx.x % a.slices) * blockDim.x + threadIdx.x) * V;
-    const int64_t m0 = run * kRun, end = m0 + kRun;
-    if (c >= n || end >= a.M) return;
-    const uint32_t key = a.key[end - 1];
-    if (key >= a.V || a.key[end] != key) return;
-    if (a.key[m0] == key && m0 > 0 && a.key[m0 - 1] == key) return;      // began earlier
-    // the last run that starts with the token
-    int64_t lo = run + 1, hi = a.runs;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a.key[mid * kRun] == key) lo = mid + 1;
-        else hi = mid;
-    }
-    RowVec<TW, V> old;
-    if (a.accumulate) old.load(static_cast<const TW*>(a.dw) + key * a.ld_dw, c, n);
+__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(SumArgs a) {
+    constexpr int V = kVec<TW, TD>, kAhead = 8;
+    __shared__ float parts[kEnds][kWave * V];
+    __shared__ int64_t many[kEnds];              // one past the last run of a token in many, or 0
+    const int n = static_cast<int>(a.D), lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int c = (static_cast<int>(blockIdx.x % a.joins) * kWave + lane) * V;
+    const int64_t run0 = blockIdx.x / a.joins * kEnds;
+    // adds head[from .. to)
+    const auto add = [&](float (&sum)[V], int64_t from, int64_t to) {
+        for (int64_t r = from; r < to; r += kAhead) {
+            RowVec<float, V> p[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; i++)
+                if (r + i < to && c < n) p[i].load(a.head + (r + i) * a.D, c, n);
+                else p[i].zero();
+#pragma unroll
+            for (int i = 0; i < kAhead; i++)
+#pragma unroll
+                for (int e = 0; e < V; e++) sum[e] += p[i][e];
+        }
+    };
+    const auto begin = [&](float (&sum)[V], RowVec<TW, V>& old, int64_t run, uint32_t key) {
+        if (a.accumulate && c < n) old.load(static_cast<const TW*>(a.dw) + key * a.ld_dw, c, n);
+#pragma unroll
+        for (int e = 0; e < V; e++) sum[e] = c + e < n ? a.tail[run * a.D + c + e] : 0.0f;
+    };
     float sum[V];
-#pragma unroll
-    for (int e = 0; e < V; e++) sum[e] = c + e < n ? a.tail[run * a.D + c + e] : 0.0f;
-    for (int64_t r = run + 1; r < lo; r += kAhead) {
-        RowVec<float, V> p[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; i++)
-            if (r + i < lo) p[i].load(a.head + (r + i) * a.D, c, n);
-            else p[i].zero();
-#pragma unroll
-        for (int i = 0; i < kAhead; i++)
-#pragma unroll
-            for (int e = 0; e < V; e++) sum[e] += p[i][e];
+    RowVec<TW, V> old;
+    int64_t last = 0;
+    {
+        const int64_t run = run0 + wave, m0 = run * kRun, end = m0 + kRun;
+        const bool inside = end < a.M;
+        const uint32_t before = inside && m0 > 0 ? a.key[m0 - 1] : static_cast<uint32_t>(a.V);
+        const uint32_t first = inside ? a.key[m0] : 0, key = inside ? a.key[end - 1] : 0;
+        const uint32_t next = inside ? a.key[end] : 1;
+        if (key == next && key < a.V && !(first == key && before == key)) {
+            // one past the last run that starts with the token: doubling steps, then halving ones
+            int64_t lo = run + 1, hi = run + 2;
+            while (hi < a.runs && a.key[hi * kRun] == key) {
+                lo = hi;
+                hi += hi - run;
+            }
+            if (hi > a.runs) hi = a.runs;
+            lo++;
+            while (lo < hi) {
+                const int64_t mid = (lo + hi) / 2;
+                if (a.key[mid * kRun] == key) lo = mid + 1;
+                else hi = mid;
+            }
+            if (lo - run - 1 > 2 * kAhead) {
+                last = lo;
+            } else {
+                begin(sum, old, run, key);
+                add(sum, run + 1, lo);
+                if (c < n) write_sum<TW, V>(a, key, c, sum, old);
+            }
+        }
     }
-    write_sum<TW, V>(a, key, c, sum, old);
+    if (lane == 0) many[wave] = last;
+    __syncthreads();
+    for (int i = 0; i < kEnds; i++) {
+        if (many[i] == 0) continue;
+        const int64_t run = run0 + i, each = (many[i] - run - 1 + kEnds - 1) / kEnds;
+        const int64_t from = run + 1 + wave * each, to = from + each < many[i] ? from + each : many[i];
+        const uint32_t key = a.key[run * kRun + kRun - 1];
+        if (wave == 0) {
+            begin(sum, old, run, key);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; e++) sum[e] = 0.0f;
+        }
+        add(sum, from, to);
+#pragma unroll
+        for (int e = 0; e < V; e++) parts[wave][lane * V + e] = sum[e];
+        __syncthreads();
+        if (wave == 0 && c < n) {
+            for (int w = 1; w < kEnds; w++)
+#pragma unroll
+                for (int e = 0; e < V; e++) sum[e] += parts[w][lane * V + e];
+            write_sum<TW, V>(a, key, c, sum, old);
+        }
+        __syncthreads();
+    }
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -388,7 +446,9 @@ bool plan_of(int64_t M, int64_t V, int64_t D, Plan& p) {
     p.tail = take(p.runs * D);
     p.bytes = at;
     // grids: every launch below 2^32 threads
-    const int64_t blocks = p.runs * ceil_div(D, 4 * kSumThreads) + ceil_div(V, kZeroRows);
+    const int64_t sums = p.runs * ceil_div(D, 4 * kSumThreads) + ceil_div(V, kZeroRows);
+    const int64_t joins = ceil_div(p.runs, kEnds) * ceil_div(D, 4 * kWave);
+    const int64_t blocks = sums > joins ? sums : joins;
     return p.runs < (int64_t{1} << 23) && D <= MSS_MAX_WIDTH && blocks < (int64_t{1} << 32) / kSumThreads;
 }
 
@@ -480,7 +540,9 @@ hipError_t launch_embed_bwd(const EmbedArgs& a, hipStream_t st) {
         embed_sum_kernel<TW, TD><<<static_cast<uint32_t>(s.runs * s.slices + zeros), threads, 0, st>>>(s);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || a.M == 0) return e;
-        embed_join_kernel<TW, TD><<<static_cast<uint32_t>(s.runs * s.slices), threads, 0, st>>>(s);
+        s.joins = ceil_div(vecs, kWave);
+        const uint32_t groups = static_cast<uint32_t>(ceil_div(s.runs, kEnds) * s.joins);
+        embed_join_kernel<TW, TD><<<groups, kJoinThreads, 0, st>>>(s);
         return hipGetLastError();
     });
 }
