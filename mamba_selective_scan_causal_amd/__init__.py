@@ -28,6 +28,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from operator import index as _index
 
 from . import inputs  # noqa: F401  (seeded synthetic inputs; no method arithmetic)
@@ -140,7 +141,7 @@ class HeadStrides(ctypes.Structure):
                 *((n, ctypes.c_int64) for n in ("x", "weight", "dx", "dweight"))]
 
 
-class ListTensor(ctypes.Structure):
+class ListTensor(ctypes.Structure):      # mss_tensor; struct format PPqii
     _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
@@ -219,7 +220,7 @@ def lib():
         L.mss_gated_norm_backward.argtypes = [nd, ns] + [p] * 12 + [sz, p]
         ed, es = ctypes.POINTER(EmbedDims), ctypes.POINTER(EmbedStrides)
         hd, hs = ctypes.POINTER(HeadDims), ctypes.POINTER(HeadStrides)
-        lt, f32, i64 = ctypes.POINTER(ListTensor), ctypes.c_float, ctypes.c_int64
+        f32, i64 = ctypes.c_float, ctypes.c_int64
         L.mss_embedding.argtypes = [ed, es] + [p] * 4
         L.mss_embedding_backward.argtypes = [ed, es] + [p] * 4 + [sz, p]
         L.mss_embed_workspace_bytes.argtypes = [ed, ctypes.POINTER(sz)]
@@ -227,8 +228,8 @@ def lib():
         L.mss_head_loss.argtypes = [hd, hs] + [p] * 6 + [sz, p]
         L.mss_head_loss_backward.argtypes = [hd, hs] + [p] * 9 + [sz, p]
         L.mss_clip_workspace_bytes.argtypes = [i64, ctypes.POINTER(sz)]
-        L.mss_grad_norm.argtypes = [lt, i64, f32, p, p, sz, p]
-        L.mss_clip_grads.argtypes = [lt, i64, f32, f32, p, p, sz, p]
+        L.mss_grad_norm.argtypes = [p, i64, f32, p, p, sz, p]
+        L.mss_clip_grads.argtypes = [p, i64, f32, f32, p, p, sz, p]
         for f in ("mss_embedding", "mss_embedding_backward", "mss_embed_workspace_bytes",
                   "mss_head_workspace_bytes", "mss_head_loss", "mss_head_loss_backward",
                   "mss_clip_workspace_bytes", "mss_grad_norm", "mss_clip_grads"):
@@ -1261,36 +1262,45 @@ def head_loss_backward(x, weight, targets, lse, dloss, dlse=None, *, logit_scale
     return g
 
 
+def _refuse_tensor(c, t, name):
+    if not isinstance(t, c.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _dtype_codes():
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if t.get_device() != c.dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{c.dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
 def _tensor_list(c, grads, out):
-    """The list of mss_tensor of the tensors that are not None, with their outputs."""
-    if out is not None and len(out) != len(grads):
+    """The mss_tensors of the tensors that are not None, with their outputs: (bytes, how many)."""
+    if len(out) != len(grads):
         raise ValueError(f"out has {len(out)} tensors, grads {len(grads)}")
     codes, dev, Tensor = _dtype_codes(), c.dev, c.Tensor
-    entries = []
+    flat = []
     for k, g in enumerate(grads):
-        o = g if out is None else out[k]
+        o = out[k]
         if g is None:
             if o is not None:
                 raise ValueError(f"grads[{k}] is None, out[{k}] is not")
             continue
-        for t, name in ((g, "grads"), (o, "out")) if o is not g else ((g, "grads"),):
-            if not isinstance(t, Tensor):
-                raise TypeError(f"{name}[{k}] must be a torch.Tensor")
-            if t.dtype not in codes:
-                raise TypeError(f"{name}[{k}] must be float32, bfloat16 or float16, got {t.dtype}")
-            if t.get_device() != dev:
-                raise ValueError(f"{name}[{k}] is on {t.device}, the current device is cuda:{dev}")
-        if not g.is_contiguous():
-            raise ValueError(f"grads[{k}] must be contiguous")
-        if o is not g:
-            if not o.is_contiguous():
-                raise ValueError(f"out[{k}] must be contiguous")
-            if o.shape != g.shape:
-                raise ValueError(f"out[{k}]: expected shape {tuple(g.shape)}, got {tuple(o.shape)}")
-            if o.dtype is not g.dtype and o.dtype is not c.f32:
-                raise TypeError(f"out[{k}] must be {g.dtype} or float32, got {o.dtype}")
-        entries.append((g.data_ptr(), o.data_ptr(), g.numel(), codes[g.dtype], codes[o.dtype]))
-    return (ListTensor * len(entries))(*entries), len(entries)
+        code = codes.get(g.dtype) if isinstance(g, Tensor) else None
+        if code is None or g.get_device() != dev or not g.is_contiguous():
+            _refuse_tensor(c, g, f"grads[{k}]")
+        at = g.data_ptr()
+        if o is g:
+            flat += at, at, g.numel(), code, code
+            continue
+        to = codes.get(o.dtype) if isinstance(o, Tensor) else None
+        if to is None or o.get_device() != dev or not o.is_contiguous():
+            _refuse_tensor(c, o, f"out[{k}]")
+        if o.shape != g.shape:
+            raise ValueError(f"out[{k}]: expected shape {tuple(g.shape)}, got {tuple(o.shape)}")
+        if to != code and to != 0:
+            raise TypeError(f"out[{k}] must be {g.dtype} or float32, got {o.dtype}")
+        flat += at, o.data_ptr(), g.numel(), code, to
+    n = len(flat) // 5
+    return struct.pack("PPqii" * n, *flat), n
 
 
 def _list_call(grads, stream):
@@ -1308,7 +1318,7 @@ def grad_norm(grads, *, scale=1.0, out=None, workspace=None, stream=None):
     ``clip_workspace_bytes(len(grads))`` + 256 bytes (allocated here when omitted)."""
     grads = list(grads)
     c, scale = _list_call(grads, stream), float(scale)
-    entries, n = _tensor_list(c, grads, None)
+    entries, n = _tensor_list(c, grads, grads)
     norm = out if out is not None else c.empty((), c.f32)
     wp, wn, _keep = c.workspace(_clip_need(n), workspace)
     _check("mss_grad_norm", lib().mss_grad_norm(entries, n, scale, c.dense(norm, "out", (), required=True),

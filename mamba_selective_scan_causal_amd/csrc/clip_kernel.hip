@@ -2,11 +2,13 @@
 //
 // The list of tensors goes to the kernels in their arguments, kList tensors a
 // launch (nothing is copied to the device, so that a captured graph holds it).
-// Tensors are cut into chunks of kChunk elements, which the workgroups take in
-// turn; a workgroup leaves one partial sum of squares.  Squares and sums are
+// Tensors are cut into chunks, which the workgroups take in turn (neighbours at one
+// time: a range of its own for each workgroup took 180 + 323 us in place of 173 + 298
+// over 830 MB); a workgroup leaves one partial sum of squares.  Squares and sums are
 // fp64: no square of a finite fp32 value overflows, and at two operations a
 // value the sums hide behind the reads.  One workgroup adds the partial sums in
-// order and writes the norm and the factor; the second pass scales.
+// order and writes the norm and the factor (or, of one list, every workgroup of the
+// second pass for itself); the second pass scales.
 #include "block_math.h"
 #include "launch_ends.h"
 
@@ -15,7 +17,7 @@ namespace {
 
 constexpr int kList = 96;
 constexpr int kThreads = 256;
-constexpr int kChunk = 16384;
+constexpr int kLeastChunk = 2048, kMostChunk = 16384;      // elements; a power of two between them
 constexpr int kMostBlocks = 2048;               // all resident at once: 256 CUs x 8
 
 struct List {
@@ -24,7 +26,7 @@ struct List {
     int64_t numel[kList];
     uint32_t first[kList];    // number of the tensor's first chunk
     uint8_t dtype[kList], out_dtype[kList];
-    int32_t count;
+    int32_t count, chunk;     // tensors, elements of a chunk
     uint32_t chunks;
 };
 static_assert(sizeof(List) < 3584, "fits the kernel's arguments");
@@ -75,10 +77,11 @@ __device__ __forceinline__ double group_sum(double v, double* lds) {
 __global__ __launch_bounds__(kThreads) void square_kernel(List l, double* part) {
     __shared__ double lds[kThreads / kWave];
     double sum = 0.0;
+    int i = tensor_of(l, blockIdx.x);
     for (uint32_t chunk = blockIdx.x; chunk < l.chunks; chunk += gridDim.x) {
-        const int i = tensor_of(l, chunk);
-        const int64_t from = int64_t{chunk - l.first[i]} * kChunk;
-        const int64_t n = l.numel[i] - from < kChunk ? l.numel[i] - from : kChunk;
+        while (i + 1 < l.count && l.first[i + 1] <= chunk) i++;
+        const int64_t from = int64_t{chunk - l.first[i]} * l.chunk;
+        const int64_t n = l.numel[i] - from < l.chunk ? l.numel[i] - from : l.chunk;
         if (l.dtype[i] == MSS_F32) sum += squares(static_cast<const float*>(l.in[i]) + from, n);
         else if (l.dtype[i] == MSS_BF16) sum += squares(static_cast<const bf16*>(l.in[i]) + from, n);
         else sum += squares(static_cast<const f16*>(l.in[i]) + from, n);
@@ -94,23 +97,38 @@ struct Factor {
     int exponent;
 };
 
-// The norm, and the factor of scale_kernel.
-__global__ __launch_bounds__(kThreads) void norm_kernel(const double* part, int64_t n, float scale, float max_norm,
-                                                        float* norm, Factor* factor) {
-    __shared__ double lds[kThreads / kWave];
+struct Clip {
+    const double* part;       // partial sums of squares
+    int64_t parts;
+    float scale, max_norm;
+    float* norm;
+    Factor* factor;
+};
+
+// The norm, and the factor where it is asked for, from the partial sums.
+__device__ __forceinline__ double norm_of(const Clip& c, double* lds) {
     double sum = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) sum += part[i];
-    sum = group_sum(sum, lds);
-    if (threadIdx.x != 0) return;
-    const double total = scale * sqrt(sum);
-    norm[0] = static_cast<float>(total);
-    if (!factor) return;
-    const bool finite = total < INFINITY;       // false for NaN too
-    int exponent;
-    const double most = frexp(!finite ? 1.0 : scale * (total > max_norm ? max_norm / total : 1.0), &exponent);
-    *factor = {static_cast<float>(most), exponent};
+    for (int64_t i = threadIdx.x; i < c.parts; i += kThreads) sum += c.part[i];
+    return c.scale * sqrt(group_sum(sum, lds));
 }
 
+__device__ __forceinline__ Factor factor_of(const Clip& c, double norm) {
+    const bool finite = norm < INFINITY;        // false for NaN too
+    int exponent;
+    const double part = frexp(!finite ? 1.0 : c.scale * (norm > c.max_norm ? c.max_norm / norm : 1.0), &exponent);
+    return {static_cast<float>(part), exponent};
+}
+
+__global__ __launch_bounds__(kThreads) void norm_kernel(Clip c) {
+    __shared__ double lds[kThreads / kWave];
+    const double norm = norm_of(c, lds);
+    if (threadIdx.x != 0) return;
+    c.norm[0] = static_cast<float>(norm);
+    if (c.factor) *c.factor = factor_of(c, norm);
+}
+
+// Stored past the caches, which keep more of what square_kernel read (830 MB of bf16:
+// 168 + 295 -> 137 + 290 us; without the reversed order 142 + 306).
 template <typename TI, typename TO>
 __device__ __forceinline__ void scaled(const TI* in, TO* out, int64_t n, Factor f) {
     constexpr int V = 16 / sizeof(TI);
@@ -121,7 +139,7 @@ __device__ __forceinline__ void scaled(const TI* in, TO* out, int64_t n, Factor 
         r.load(in + c, 0, have);
 #pragma unroll
         for (int e = 0; e < V; e++) o.set(e, __builtin_ldexpf(r[e] * f.part, f.exponent));
-        o.template store<false>(out + c, 0, have);
+        o.template store<true>(out + c, 0, have);
     }
 }
 
@@ -132,13 +150,27 @@ __device__ __forceinline__ void scaled_to(const void* in, void* out, bool wide, 
     else scaled(p, static_cast<TI*>(out) + from, n, f);
 }
 
-__global__ __launch_bounds__(kThreads) void scale_kernel(List l, const Factor* factor) {
-    const Factor f = *factor;
-    for (uint32_t chunk = blockIdx.x; chunk < l.chunks; chunk += gridDim.x) {
-        const int i = tensor_of(l, chunk);
+// OWN: every workgroup adds the partial sums up for itself, and the first writes
+// the norm: a launch less (one block's gradients, 14 MB of fp32: 21.5 -> 16.9 us a call).
+template <bool OWN>
+__global__ __launch_bounds__(kThreads) void scale_kernel(List l, Clip c) {
+    __shared__ double lds[kThreads / kWave];
+    Factor f;
+    if constexpr (OWN) {
+        const double norm = norm_of(c, lds);
+        if (blockIdx.x == 0 && threadIdx.x == 0) c.norm[0] = static_cast<float>(norm);
+        f = factor_of(c, norm);
+    } else {
+        f = *c.factor;
+    }
+    // from the end, what square_kernel read last and the caches may still hold, each chunk on the XCD
+    // that read it
+    int64_t chunk = blockIdx.x + (l.chunks - 1 - blockIdx.x) / gridDim.x * gridDim.x;
+    for (int i = tensor_of(l, static_cast<uint32_t>(chunk)); chunk >= 0; chunk -= gridDim.x) {
+        while (l.first[i] > chunk) i--;
         if (f.part == 0.5f && f.exponent == 1 && l.in[i] == l.out[i] && l.dtype[i] == l.out_dtype[i]) continue;     // as it is
-        const int64_t from = int64_t{chunk - l.first[i]} * kChunk;
-        const int64_t n = l.numel[i] - from < kChunk ? l.numel[i] - from : kChunk;
+        const int64_t from = (chunk - l.first[i]) * l.chunk;
+        const int64_t n = l.numel[i] - from < l.chunk ? l.numel[i] - from : l.chunk;
         const bool wide = l.out_dtype[i] == MSS_F32;
         if (l.dtype[i] == MSS_F32) scaled_to<float>(l.in[i], l.out[i], wide, from, n, f);
         else if (l.dtype[i] == MSS_BF16) scaled_to<bf16>(l.in[i], l.out[i], wide, from, n, f);
@@ -146,36 +178,39 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(List l, const Factor* f
     }
 }
 
-// Calls f(list, workgroups) for every kList tensors.  (The entry points bound
-// the elements of all tensors, so the chunks are counted in 31 bits.)
+// Calls f(list, workgroups) for every kList tensors that are not empty.  (The
+// entry points bound the elements of all tensors, so the chunks are counted in 31
+// bits.)
 template <typename F>
 hipError_t each_list(const mss_tensor* t, int64_t count, F&& f) {
     List l;
-    l.count = 0;
-    uint64_t chunks = 0;
-    const auto send = [&]() -> hipError_t {
-        if (l.count == 0) return hipSuccess;
+    for (int64_t i = 0; i < count;) {
+        l.count = 0;
+        int64_t total = 0;
+        for (; i < count && l.count < kList; i++) {
+            if (t[i].numel == 0) continue;
+            l.in[l.count] = t[i].in;
+            l.out[l.count] = t[i].out;
+            l.numel[l.count] = t[i].numel;
+            l.dtype[l.count] = static_cast<uint8_t>(t[i].dtype);
+            l.out_dtype[l.count] = static_cast<uint8_t>(t[i].out_dtype);
+            l.count++;
+            total += t[i].numel;
+        }
+        if (l.count == 0) continue;
+        // a few chunks to a workgroup where there is enough for all of them
+        l.chunk = kLeastChunk;
+        while (l.chunk < kMostChunk && total / l.chunk > 4 * kMostBlocks) l.chunk *= 2;
+        int64_t chunks = 0;
+        for (int k = 0; k < l.count; k++) {
+            l.first[k] = static_cast<uint32_t>(chunks);
+            chunks += (l.numel[k] + l.chunk - 1) / l.chunk;
+        }
         l.chunks = static_cast<uint32_t>(chunks);
         const hipError_t e = f(l, chunks < kMostBlocks ? static_cast<uint32_t>(chunks) : kMostBlocks);
-        l.count = 0;
-        chunks = 0;
-        return e;
-    };
-    for (int64_t i = 0; i < count; i++) {
-        if (t[i].numel == 0) continue;
-        const uint64_t more = (static_cast<uint64_t>(t[i].numel) + kChunk - 1) / kChunk;
-        if (l.count == kList)
-            if (hipError_t e = send()) return e;
-        l.in[l.count] = t[i].in;
-        l.out[l.count] = t[i].out;
-        l.numel[l.count] = t[i].numel;
-        l.first[l.count] = static_cast<uint32_t>(chunks);
-        l.dtype[l.count] = static_cast<uint8_t>(t[i].dtype);
-        l.out_dtype[l.count] = static_cast<uint8_t>(t[i].out_dtype);
-        l.count++;
-        chunks += more;
+        if (e != hipSuccess) return e;
     }
-    return send();
+    return hipSuccess;
 }
 
 }  // namespace
@@ -185,19 +220,25 @@ int64_t clip_workspace(int64_t count) { return 256 + (count + kList - 1) / kList
 
 hipError_t launch_clip(const mss_tensor* t, int64_t count, float scale, float max_norm, bool write, float* norm,
                        void* ws, hipStream_t st) {
-    Factor* factor = static_cast<Factor*>(ws);
     double* part = reinterpret_cast<double*>(static_cast<char*>(ws) + 256);
-    int64_t used = 0;
+    Clip c{part, 0, scale, max_norm, norm, write ? static_cast<Factor*>(ws) : nullptr};
+    int lists = 0;
     hipError_t e = each_list(t, count, [&](const List& l, uint32_t blocks) {
-        square_kernel<<<blocks, kThreads, 0, st>>>(l, part + used);
-        used += blocks;
+        square_kernel<<<blocks, kThreads, 0, st>>>(l, part + c.parts);
+        c.parts += blocks;
+        lists++;
         return hipGetLastError();
     });
     if (e != hipSuccess) return e;
-    norm_kernel<<<1, kThreads, 0, st>>>(part, used, scale, max_norm, norm, write ? factor : nullptr);
+    if (write && lists == 1)
+        return each_list(t, count, [&](const List& l, uint32_t blocks) {
+            scale_kernel<true><<<blocks, kThreads, 0, st>>>(l, c);
+            return hipGetLastError();
+        });
+    norm_kernel<<<1, kThreads, 0, st>>>(c);
     if ((e = hipGetLastError()) != hipSuccess || !write) return e;
     return each_list(t, count, [&](const List& l, uint32_t blocks) {
-        scale_kernel<<<blocks, kThreads, 0, st>>>(l, factor);
+        scale_kernel<false><<<blocks, kThreads, 0, st>>>(l, c);
         return hipGetLastError();
     });
 }
