@@ -50,13 +50,14 @@ struct Shape<RowProduct<T, BL_, BR_, WL_, WR_>> {
 template <typename P>
 struct Part {
     using S = Shape<P>;
+    // workgroup b of n
     int64_t l, r;             // the lane's: l of acc[.][0], r of acc[0][.] element 0
     int64_t l0, r0;           // the tile's
     int64_t lw, rw;           // the wave's
     int lane, wave;
-    __device__ __forceinline__ Part(const ProductArgs& a) {
+    __device__ __forceinline__ Part(const ProductArgs& a, int64_t b, int64_t n) {
         int64_t tl, tr;
-        tile_of<kGroup>(blockIdx.x, gridDim.x, a.tiles_l, a.tiles_r, tl, tr);
+        tile_of<kGroup>(b, n, a.tiles_l, a.tiles_r, tl, tr);
         lane = threadIdx.x % kWave;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         l0 = tl * S::BL;
@@ -106,7 +107,7 @@ template <typename P>
 __global__ __launch_bounds__(P::kThreads) void head_loss_kernel(ProductArgs a, LossArgs h) {
     using S = Shape<P>;
     __shared__ __align__(1024) char lds[P::kLds];
-    const Part<P> at(a);
+    const Part<P> at(a, blockIdx.x, gridDim.x);
     v4f acc[P::kTR][P::kTL];
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
     if (at.rw >= a.nr) return;
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
     typedef T quad __attribute__((ext_vector_type(4)));
     static_assert(Rows::kBytes <= Cols::kBytes, "one region for both");
     __shared__ __align__(1024) char lds[kLdsWithStore<P>];
-    const Part<P> at(a);
+    const Part<P> at(a, blockIdx.x, gridDim.x);
     v4f acc[P::kTR][P::kTL];
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
     const bool whole = at.rw + 16 * P::kTR <= a.nr;
@@ -363,22 +364,36 @@ struct GradArgs {
     int split;                // of K
 };
 
+// The products of a piece, dx's and dW's, in one launch, the tiles of the longer K
+// first: those of the other fill the CUs that a last, partial round would leave idle.
+struct TwoProducts {
+    ProductArgs a[2];
+    GradArgs g[2];
+    int64_t first;            // workgroups of the first
+};
+
 template <typename P>
-__global__ __launch_bounds__(P::kThreads) void head_grad_kernel(ProductArgs a, GradArgs h) {
+__global__ __launch_bounds__(P::kThreads) void head_grad_kernel(TwoProducts two) {
     using T = typename Shape<P>::type;
     using Rows = RowStore<T, P::kTR, P::kTL>;
     typedef T quad __attribute__((ext_vector_type(4)));
     static_assert(P::kWaves * Rows::kBytes <= P::kLds, "stored through the stages' LDS");
     __shared__ __align__(1024) char lds[P::kLds];
-    const Part<P> at(a);
+    const bool second = blockIdx.x >= two.first;
+    const ProductArgs a = two.a[second];
+    const GradArgs h = two.g[second];
+    // a product's workgroups: the tiles, for every part of K
+    const int64_t b = second ? blockIdx.x - two.first : blockIdx.x, tiles = a.tiles_l * a.tiles_r;
+    const int64_t part = b / tiles;
+    const Part<P> at(a, b - part * tiles, tiles);
     v4f acc[P::kTR][P::kTL];
     // this workgroup's part of K, whole stages
     const int64_t stages = (a.kbytes + kStage - 1) / kStage;
-    const int64_t k0 = stages * blockIdx.y / h.split * kStage, k1 = stages * (blockIdx.y + 1) / h.split * kStage;
+    const int64_t k0 = stages * part / h.split * kStage, k1 = stages * (part + 1) / h.split * kStage;
     P::run(a, at.l0, at.r0, k0, k1 < a.kbytes ? k1 : a.kbytes, lds, acc);
     if (!h.out) {
         // fp32 sums: a lane's four are 16 bytes of a row
-        float* to = h.acc + (blockIdx.y * a.nl + at.l) * h.ld + at.r;
+        float* to = h.acc + (part * a.nl + at.l) * h.ld + at.r;
 #pragma unroll
         for (int j = 0; j < P::kTL; j++) {
             if (at.l + 16 * j >= a.nl) continue;
@@ -422,22 +437,60 @@ __global__ __launch_bounds__(256) void head_finish_kernel(const float* acc, int6
 // ---- plans -------------------------------------------------------------------------
 
 constexpr int64_t kPartBytes = int64_t{256} << 20;      // partial sums of the forward at a time
-constexpr int64_t kDlBytes = int64_t{512} << 20;        // dl and its transpose
-constexpr int64_t kCus = 256;
+constexpr int64_t kDlBytes = int64_t{1} << 30;          // dl and its transpose
 
 int64_t align_up(int64_t n, int64_t a) { return ceil_div(n, a) * a; }
 
-// Rounds of large tiles that a product of nl x nr takes, K apart, and whether
-// small tiles (two workgroups to a CU, at 1 / 1.16 of the rate) take less.
-struct Rounds {
-    double cost;
+// What the tile shapes take on this card, in microseconds: a value of K of one
+// tile, with as many workgroups on a CU as fit it (measured at 1210 and 1040
+// TFLOP/s in bf16 and 139 and 132 in fp32), and a tile's start and end.
+struct TileCost {
+    int64_t size, slots;
+    double each, fixed;
+};
+TileCost tile_cost(bool large, int64_t elem) {
+    const double wide = elem == 4 ? 8.7 : 1.0;
+    return large ? TileCost{256, 256, 0.0277 * wide, 5.0} : TileCost{128, 512, 0.0161 * wide, 4.0};
+}
+
+// `n` tiles that take `us` each, on CUs that took `m` tiles of `first` each before.
+double spread(int64_t slots, int64_t m, double first, int64_t n, double us) {
+    const int64_t q = m / slots, r = m % slots;
+    double most = q * first + (r ? first : 0.0);
+    // slots - r are free at q first, r of them a tile later: k tiles to each of the earlier ones
+    for (int64_t k = n / slots; n > 0; k++) {
+        const double end = q * first + k * us;
+        const int64_t later = end > (q + 1) * first ? static_cast<int64_t>((end - (q + 1) * first) / us + 1e-9) : 0;
+        if ((slots - r) * k + r * later >= n) return end > most ? end : most;
+    }
+    return most;
+}
+
+struct Choice {
+    double us;
     bool large;
 };
-Rounds rounds(int64_t nl, int64_t nr, int64_t split = 1) {
-    const double big = static_cast<double>(ceil_div(ceil_div(nl, 256) * ceil_div(nr, 256) * split, kCus));
-    const double small =
-        0.5 * 1.16 * static_cast<double>(ceil_div(ceil_div(nl, 128) * ceil_div(nr, 128) * split, 2 * kCus));
-    return {big <= small ? big : small, big <= small};
+Choice product_us(int64_t elem, int64_t nl, int64_t nr, int64_t k) {
+    Choice best{0, false};
+    for (bool large : {true, false}) {
+        const TileCost c = tile_cost(large, elem);
+        const double us = spread(c.slots, 0, 0, ceil_div(nl, c.size) * ceil_div(nr, c.size), c.each * k + c.fixed);
+        if (large || us < best.us) best = {us, large};
+    }
+    return best;
+}
+
+// dx (M, D) with K = n in `split` parts, and dW (n, D) with K = M.
+Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split) {
+    Choice best{0, false};
+    for (bool large : {true, false}) {
+        const TileCost c = tile_cost(large, elem);
+        const int64_t wide = ceil_div(D, c.size), x = ceil_div(M, c.size) * wide * split, w = ceil_div(n, c.size) * wide;
+        const double ux = c.each * n / split + c.fixed, uw = c.each * M + c.fixed;
+        const double us = ux >= uw ? spread(c.slots, x, ux, w, uw) : spread(c.slots, w, uw, x, ux);
+        if (large || us < best.us) best = {us, large};
+    }
+    return best;
 }
 
 struct Plan {
@@ -486,28 +539,26 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
         }
         return fits;
     }
-    // The piece, in steps of 256 vocabulary rows: what makes the three products
-    // take the fewest rounds of tiles, launches counted as a hundred values of K.
+    // The piece, in steps of 256 vocabulary rows, and the parts of dx's K: what takes the least time
+    // by the costs above, the traffic of dx's partial sums (5 TB/s) and launches counted in
     const int64_t steps = ceil_div(V, 256);
     int64_t most = kDlBytes / (2 * 256 * e * p.ld_m);
     most = most < 1 ? 1 : most > 1024 ? 1024 : most > steps ? steps : most;
+    const double pass = 4.0 * M * D / 5e6;          // of dx's sums, one part
     double best = 0;
-    const int64_t stride = ceil_div(most, 64);
-    for (int64_t n = most; n > 0 && n > most / 4; n -= stride) {
-        const int64_t full = steps / n, rest = steps % n;
-        const auto one = [&](int64_t k) {
-            return k == 0 ? 0.0
-                          : rounds(M, 256 * k).cost * D + rounds(256 * k, D).cost * M + rounds(M, D).cost * 256 * k + 400;
-        };
-        const double cost = full * one(n) + one(rest);
-        if (best == 0 || cost < best) best = cost, p.piece = 256 * n;
-    }
-    // dx has few tiles and a long K: it is split until the tiles fill the CUs
-    p.split = 1;
-    double least = rounds(M, D).cost;
-    for (int s = 2; s <= 16 && p.piece / s >= 512; s++) {
-        const double cost = rounds(M, D, s).cost / s * 1.02;
-        if (cost < 0.95 * least) least = cost, p.split = s;
+    const int64_t stride = ceil_div(most, 32);
+    for (int64_t n = most; n > 0 && n > most / 3; n -= stride) {
+        const int64_t full = steps / n, rest = steps % n, pieces = full + (rest > 0);
+        const double before = full * product_us(e, M, 256 * n, D).us + 10.0 * pieces +
+                              (rest ? product_us(e, M, 256 * rest, D).us : 0.0);
+        for (int split : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            if (split > 1 && 256 * n / split < 512) break;
+            const bool sums = split > 1 || pieces > 1;
+            double us = before + full * gradients_us(e, M, 256 * n, D, split).us + (sums ? pass * split * 2 * pieces : 0.0);
+            if (best != 0 && us >= best) continue;
+            if (rest) us += gradients_us(e, M, 256 * rest, D, split).us;
+            if (best == 0 || us < best) best = us, p.piece = 256 * n, p.split = split;
+        }
     }
     p.accumulate = p.split > 1 || p.piece < V;
     p.dl = take(M, p.piece, e);
@@ -551,14 +602,6 @@ hipError_t transpose(const T* in, int64_t ld, int64_t rows, int64_t n, T* out, i
 }
 
 template <typename T>
-hipError_t grad(const ProductArgs& a, bool large, const GradArgs& g, hipStream_t st) {
-    const dim3 grid(static_cast<uint32_t>(a.tiles_l * a.tiles_r), g.split);
-    if (large) head_grad_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, g);
-    else head_grad_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, g);
-    return hipGetLastError();
-}
-
-template <typename T>
 hipError_t forward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     char* ws = static_cast<char*>(h.ws);
     constexpr int64_t e = sizeof(T);
@@ -574,7 +617,7 @@ hipError_t forward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     }
     for (int64_t m0 = 0; m0 < h.M; m0 += p.chunk) {
         const int64_t rows = h.M - m0 < p.chunk ? h.M - m0 : p.chunk;
-        const bool large = rounds(rows, h.V < p.piece ? h.V : p.piece).large;
+        const bool large = product_us(e, rows, h.V < p.piece ? h.V : p.piece, h.D).large;
         const int64_t slab = large ? Shape<Large<T>>::kSlab : Shape<Small<T>>::kSlab;
         for (int64_t v0 = 0; v0 < h.V; v0 += p.piece) {
             const int64_t n = h.V - v0 < p.piece ? h.V - v0 : p.piece;
@@ -641,28 +684,28 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
             w = to;
             ld_w = p.Dk;
         }
-        bool large = rounds(M, n).large;
+        bool large = product_us(e, M, n, D).large;
         const ProductArgs a = product(x, ld_x * e, M, w, ld_w * e, n, p.Dk * e, large);
         const DlArgs d{h.logit_scale * kLog2e, v0, g, dl, dlt, ld_n, p.ld_m};
         const uint32_t grid = static_cast<uint32_t>(a.tiles_l * a.tiles_r);
         if (large) head_dl_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, d);
         else head_dl_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, d);
         if (hipError_t r = hipGetLastError()) return r;
-        if (h.dx) {
+        if (h.dx)
             if (hipError_t r = transpose(w, ld_w, n, D, wt, ld_n, static_cast<const int*>(nullptr), st)) return r;
-            large = rounds(M, D, p.split).large;
-            const GradArgs to{g.back, p.accumulate ? nullptr : h.dx, p.accumulate ? p.ld_acc : h.ld_dx, reinterpret_cast<float*>(ws + p.acc),
-                              v0 == 0, p.split};
-            if (hipError_t r = grad<T>(product(dl, ld_n * e, M, wt, ld_n * e, D, ld_n * e, large), large, to, st))
-                return r;
-        }
-        if (h.dw) {
-            large = rounds(n, D).large;
-            const GradArgs to{g.back, static_cast<T*>(h.dw) + v0 * h.ld_dw, h.ld_dw, nullptr, false, 1};
-            if (hipError_t r =
-                    grad<T>(product(dlt, p.ld_m * e, n, xt, p.ld_m * e, D, p.ld_m * e, large), large, to, st))
-                return r;
-        }
+        large = gradients_us(e, M, n, D, p.split).large;
+        const ProductArgs px = product(dl, ld_n * e, M, wt, ld_n * e, D, ld_n * e, large);
+        const ProductArgs pw = product(dlt, p.ld_m * e, n, xt, p.ld_m * e, D, p.ld_m * e, large);
+        const GradArgs gx{g.back, p.accumulate ? nullptr : h.dx, p.accumulate ? p.ld_acc : h.ld_dx,
+                          reinterpret_cast<float*>(ws + p.acc), v0 == 0, p.split};
+        const GradArgs gw{g.back, h.dw ? static_cast<T*>(h.dw) + v0 * h.ld_dw : nullptr, h.ld_dw, nullptr, false, 1};
+        const int64_t nx = h.dx ? px.tiles_l * px.tiles_r * p.split : 0, nw = h.dw ? pw.tiles_l * pw.tiles_r : 0;
+        const TwoProducts two =
+            n / p.split >= M ? TwoProducts{{px, pw}, {gx, gw}, nx} : TwoProducts{{pw, px}, {gw, gx}, nw};
+        const uint32_t both = static_cast<uint32_t>(nx + nw);
+        if (large) head_grad_kernel<Large<T>><<<both, Large<T>::kThreads, 0, st>>>(two);
+        else head_grad_kernel<Small<T>><<<both, Small<T>::kThreads, 0, st>>>(two);
+        if (hipError_t r = hipGetLastError()) return r;
     }
     if (h.dx && p.accumulate) {
         head_finish_kernel<T><<<static_cast<uint32_t>(ceil_div(M, 4)), 256, 0, st>>>(
@@ -691,7 +734,7 @@ bool head_workspace(int dtype, int64_t M, int64_t V, int64_t D, bool bwd, int64_
     // four rows (of at most 2^26) of the others
     const int64_t across = ceil_div(bwd ? M : p.chunk, 128), down = ceil_div(p.piece, 128), wide = ceil_div(D, 128);
     const int64_t most = int64_t{1} << 24;
-    if (across * down >= most || across * wide * (bwd ? p.split : 1) >= most || down * wide >= most ||
+    if (across * down >= most || across * wide * (bwd ? p.split : 1) + down * wide >= most ||
         ceil_div(p.ld_m, 64) * ceil_div(D, 64) >= most || ceil_div(p.piece, 64) * ceil_div(D, 64) >= most)
         return false;
     bytes = p.bytes;
