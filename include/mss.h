@@ -555,10 +555,8 @@ int mss_gated_norm_backward(const mss_norm_dims* dims, const mss_norm_strides* s
  * shard of the table holds).
  *
  * Row strides in elements, as in mss_gated_strides (NULL: dense rows).  With
- * strides given the tensors need only their element's alignment, except x and
- * weight of the head where a row is a multiple of 16 bytes long: their rows
- * must then start at multiples of 16 bytes (MSS_EALIGN).  Ids, targets and
- * tensors of one value per row need their element's alignment.             */
+ * strides given the tensors need only their element's alignment; ids, targets
+ * and tensors of one value per row always do.                              */
 #define MSS_EMBED_ACCUMULATE 1
 typedef struct mss_embed_dims {
     int32_t struct_size;    /* sizeof(mss_embed_dims) */

@@ -1214,8 +1214,7 @@ def head_loss(x, weight, targets, *, logit_scale=1.0, out=None, workspace=None, 
     """Softmax cross entropy of the logits logit_scale x weight^T, which are not kept.
     Returns (loss, lse), both (M,) float32.
 
-    x (M, D), weight (V, D) float32, bfloat16 or float16, both the same, rows may be strided
-    (starting at multiples of 16 bytes where a row is a multiple of 16 bytes long);
+    x (M, D), weight (V, D) float32, bfloat16 or float16, both the same, rows may be strided;
     targets (M,) int64 or int32.  lse_m is the log of the sum of the exponentials, loss_m = lse_m
     minus the target's logit; a target outside 0 .. V-1 marks a padded row, whose loss is 0.
     ``out``: optional pair of output tensors.  ``workspace``: uint8 GPU tensor of at least

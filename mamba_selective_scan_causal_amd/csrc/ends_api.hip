@@ -90,10 +90,6 @@ void head_inputs(Checks& ck, const mss::HeadArgs& a) {
     ck.in(a.x, a.M, a.D, a.ld_x, e, true);
     ck.in(a.w, a.V, a.D, a.ld_w, e, true);
     ck.in_any(a.targets, a.M, a.wide_ids ? 8 : 4, true);
-    if (mss::head_rows_whole(a.D, e)) {
-        ck.pieces(a.x, a.M, a.ld_x, e);
-        ck.pieces(a.w, a.V, a.ld_w, e);
-    }
 }
 
 // ---- lists of tensors ----------------------------------------------------------------

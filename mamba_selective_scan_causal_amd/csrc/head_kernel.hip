@@ -33,14 +33,14 @@ constexpr int kPadRows = 64;                 // dl^T and x^T have rows of a mult
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The two tile shapes: one workgroup of eight waves on a CU, or two of four.
-template <typename T>
-using Large = RowProduct<T, 256, 256, 4, 2>;
-template <typename T>
-using Small = RowProduct<T, 128, 128, 2, 2>;
+template <typename T, bool DIRECT = true>
+using Large = RowProduct<T, 256, 256, 4, 2, DIRECT>;
+template <typename T, bool DIRECT = true>
+using Small = RowProduct<T, 128, 128, 2, 2, DIRECT>;
 template <typename P>
 struct Shape;
-template <typename T, int BL_, int BR_, int WL_, int WR_>
-struct Shape<RowProduct<T, BL_, BR_, WL_, WR_>> {
+template <typename T, int BL_, int BR_, int WL_, int WR_, bool DIRECT>
+struct Shape<RowProduct<T, BL_, BR_, WL_, WR_, DIRECT>> {
     using type = T;
     static constexpr int BL = BL_, BR = BR_, WL = WL_, WR = WR_;
     static constexpr int kSlab = BR / WR;    // columns of one wave
@@ -196,24 +196,10 @@ __global__ __launch_bounds__(256) void head_join_kernel(JoinArgs h) {
 
 // ---- copies ---------------------------------------------------------------------
 
-// Rows of n values to rows of ld_out values, zeros behind.
-template <typename T>
-__global__ __launch_bounds__(256) void pad_rows_kernel(const T* in, int64_t ld_in, int64_t rows, int64_t n, T* out,
-                                                       int64_t ld_out) {
-    const int64_t row = blockIdx.x * int64_t{4} + threadIdx.x / kWave;
-    if (row >= rows) return;
-    constexpr int V = 16 / sizeof(T);           // ld_out is a multiple
-    for (int64_t c = threadIdx.x % kWave * V; c < ld_out; c += kWave * V) {
-        RowVec<T, V> v;
-        v.load(in + row * ld_in, static_cast<int>(c), static_cast<int>(n));
-        v.template store<false>(out + row * ld_out + c, 0, V);
-    }
-}
-
 // in (rows, n) to out (n, ld_out), ld_out >= rows, zeros behind and in the
 // columns of rows that are off (t < 0).  A tile of 64 x 64 values goes through
-// LDS, read and written in pieces of 16 bytes; in's rows start at multiples of 16
-// bytes (ld_in, a copied row's or the caller's), out's too.
+// LDS, read and written in pieces of 16 bytes (at any element in `in`, whole lines
+// of out, whose rows are a multiple of 64 values long).
 template <typename T>
 __global__ __launch_bounds__(256) void transpose_kernel(const T* in, int64_t ld_in, int64_t rows, int64_t n, T* out,
                                                         int64_t ld_out, const int* t) {
@@ -494,22 +480,18 @@ Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split
 }
 
 struct Plan {
-    bool whole;               // rows are read as they lie
-    int64_t Dk;               // values in a copied row
     int64_t piece;            // vocabulary rows at a time
     int64_t chunk;            // rows at a time (forward)
     int split;                // of dx's K
     bool accumulate;          // dx goes through fp32 partial sums
     int64_t ld_m;             // values in a row of dl^T and x^T
     int64_t ld_acc;           // and of dx's partial sums
-    int64_t x, w, part, at_target, dl, dlt, xt, wt, acc, rows, bytes;
+    int64_t part, at_target, dl, dlt, xt, wt, acc, rows, bytes;
 };
 
 bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p) {
     const int64_t e = dtype == MSS_F32 ? 4 : 2;
     p = Plan{};
-    p.whole = head_rows_whole(D, e);
-    p.Dk = align_up(D, 16 / e);
     p.ld_m = align_up(M, kPadRows);
     bool fits = true;
     const auto take = [&](int64_t a, int64_t b, int64_t c) {
@@ -524,19 +506,13 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
         return here;
     };
     if (!backward) {
-        p.piece = p.whole ? int64_t{1} << 18 : align_up((int64_t{64} << 20) / (p.Dk * e) + 1, 256);
-        if (p.piece > (int64_t{1} << 18)) p.piece = int64_t{1} << 18;
-        if (p.piece > V) p.piece = V;
+        p.piece = V < (int64_t{1} << 18) ? V : int64_t{1} << 18;
         const int64_t slabs = ceil_div(V, 64);
         p.chunk = kPartBytes / (slabs * 8) / 256 * 256;
         if (p.chunk < 256) p.chunk = 256;
         if (p.chunk > M) p.chunk = M;
         p.part = take(slabs, p.chunk, 8);
         p.at_target = take(M, 4, 1);
-        if (!p.whole) {
-            p.x = take(M, p.Dk, e);
-            p.w = take(p.piece, p.Dk, e);
-        }
         return fits;
     }
     // The piece, in steps of 256 vocabulary rows, and the parts of dx's K: what takes the least time
@@ -565,10 +541,6 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
     p.dlt = take(p.piece, p.ld_m, e);
     p.xt = take(D, p.ld_m, e);
     p.wt = take(D, p.piece, e);
-    if (!p.whole) {
-        p.x = take(M, p.Dk, e);
-        p.w = take(p.piece, p.Dk, e);
-    }
     p.ld_acc = align_up(D, 4);
     if (p.accumulate) p.acc = take(M * int64_t{4}, p.ld_acc, p.split);
     p.rows = take(align_up(M, 64) * int64_t{16} + 256, 1, 1);
@@ -587,10 +559,9 @@ ProductArgs product(const void* l, int64_t ld_l, int64_t nl, const void* r, int6
             ceil_div(nr, t)};
 }
 
-template <typename T>
-hipError_t pad_rows(const T* in, int64_t ld, int64_t rows, int64_t n, T* out, int64_t ld_out, hipStream_t st) {
-    pad_rows_kernel<T><<<static_cast<uint32_t>(ceil_div(rows, 4)), 256, 0, st>>>(in, ld, rows, n, out, ld_out);
-    return hipGetLastError();
+// Whether rows of a product's operand can go straight to LDS.
+bool direct(const void* p, int64_t ld, int64_t rows, int64_t n, int64_t e) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && n * e % 16 == 0 && (rows == 1 || ld * e % 16 == 0);
 }
 
 template <typename T>
@@ -605,16 +576,10 @@ template <typename T>
 hipError_t forward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     char* ws = static_cast<char*>(h.ws);
     constexpr int64_t e = sizeof(T);
-    const char* x = static_cast<const char*>(h.x);
-    int64_t ld_x = h.ld_x * e;
+    const T* x = static_cast<const T*>(h.x);
+    const bool straight = direct(x, h.ld_x, h.M, h.D, e) && direct(h.w, h.ld_w, h.V, h.D, e);
     float* at_target = reinterpret_cast<float*>(ws + p.at_target);
     float2* part = reinterpret_cast<float2*>(ws + p.part);
-    if (!p.whole) {
-        T* to = reinterpret_cast<T*>(ws + p.x);
-        if (hipError_t r = pad_rows(static_cast<const T*>(h.x), h.ld_x, h.M, h.D, to, p.Dk, st)) return r;
-        x = ws + p.x;
-        ld_x = p.Dk * e;
-    }
     for (int64_t m0 = 0; m0 < h.M; m0 += p.chunk) {
         const int64_t rows = h.M - m0 < p.chunk ? h.M - m0 : p.chunk;
         const bool large = product_us(e, rows, h.V < p.piece ? h.V : p.piece, h.D).large;
@@ -622,19 +587,14 @@ hipError_t forward(const HeadArgs& h, const Plan& p, hipStream_t st) {
         for (int64_t v0 = 0; v0 < h.V; v0 += p.piece) {
             const int64_t n = h.V - v0 < p.piece ? h.V - v0 : p.piece;
             const T* w = static_cast<const T*>(h.w) + v0 * h.ld_w;
-            int64_t ld_w = h.ld_w * e;
-            if (!p.whole) {
-                T* to = reinterpret_cast<T*>(ws + p.w);
-                if (hipError_t r = pad_rows(w, h.ld_w, n, h.D, to, p.Dk, st)) return r;
-                w = to;
-                ld_w = p.Dk * e;
-            }
-            const ProductArgs a = product(x + m0 * ld_x, ld_x, rows, w, ld_w, n, p.Dk * e, large);
+            const ProductArgs a = product(x + m0 * h.ld_x, h.ld_x * e, rows, w, h.ld_w * e, n, h.D * e, large);
             // a piece is a multiple of 256 rows, or all of them: slabs do not cross pieces
             const LossArgs l{h.logit_scale * kLog2e, v0, m0, h.targets, h.wide_ids, part + v0 / slab * rows, at_target};
             const uint32_t grid = static_cast<uint32_t>(a.tiles_l * a.tiles_r);
-            if (large) head_loss_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, l);
-            else head_loss_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, l);
+            if (large && straight) head_loss_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, l);
+            else if (large) head_loss_kernel<Large<T, false>><<<grid, Large<T>::kThreads, 0, st>>>(a, l);
+            else if (straight) head_loss_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, l);
+            else head_loss_kernel<Small<T, false>><<<grid, Small<T>::kThreads, 0, st>>>(a, l);
             if (hipError_t r = hipGetLastError()) return r;
         }
         const JoinArgs j{part, ceil_div(h.V, slab), rows, m0, h.V, at_target, h.targets, h.wide_ids, h.loss, h.lse};
@@ -660,39 +620,28 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     row_grads_kernel<<<static_cast<uint32_t>(ceil_div(M, 1024)), 1024, 0, st>>>(h, g);
     if (hipError_t r = hipGetLastError()) return r;
     const T* x = static_cast<const T*>(h.x);
-    int64_t ld_x = h.ld_x;
-    if (!p.whole) {
-        T* to = reinterpret_cast<T*>(ws + p.x);
-        if (hipError_t r = pad_rows(x, ld_x, M, D, to, p.Dk, st)) return r;
-        x = to;
-        ld_x = p.Dk;
-    }
+    const bool straight = direct(x, h.ld_x, M, D, e) && direct(h.w, h.ld_w, h.V, D, e);
     T* xt = reinterpret_cast<T*>(ws + p.xt);
     T* wt = reinterpret_cast<T*>(ws + p.wt);
     T* dl = reinterpret_cast<T*>(ws + p.dl);
     T* dlt = reinterpret_cast<T*>(ws + p.dlt);
     if (h.dw)
-        if (hipError_t r = transpose(x, ld_x, M, D, xt, p.ld_m, g.t, st)) return r;
+        if (hipError_t r = transpose(x, h.ld_x, M, D, xt, p.ld_m, g.t, st)) return r;
     for (int64_t v0 = 0; v0 < h.V; v0 += p.piece) {
         const int64_t n = h.V - v0 < p.piece ? h.V - v0 : p.piece;
         const int64_t ld_n = align_up(n, kPadRows);      // at most the piece, a multiple of 256
         const T* w = static_cast<const T*>(h.w) + v0 * h.ld_w;
-        int64_t ld_w = h.ld_w;
-        if (!p.whole) {
-            T* to = reinterpret_cast<T*>(ws + p.w);
-            if (hipError_t r = pad_rows(w, ld_w, n, D, to, p.Dk, st)) return r;
-            w = to;
-            ld_w = p.Dk;
-        }
         bool large = product_us(e, M, n, D).large;
-        const ProductArgs a = product(x, ld_x * e, M, w, ld_w * e, n, p.Dk * e, large);
+        const ProductArgs a = product(x, h.ld_x * e, M, w, h.ld_w * e, n, D * e, large);
         const DlArgs d{h.logit_scale * kLog2e, v0, g, dl, dlt, ld_n, p.ld_m};
         const uint32_t grid = static_cast<uint32_t>(a.tiles_l * a.tiles_r);
-        if (large) head_dl_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, d);
-        else head_dl_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, d);
+        if (large && straight) head_dl_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, d);
+        else if (large) head_dl_kernel<Large<T, false>><<<grid, Large<T>::kThreads, 0, st>>>(a, d);
+        else if (straight) head_dl_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, d);
+        else head_dl_kernel<Small<T, false>><<<grid, Small<T>::kThreads, 0, st>>>(a, d);
         if (hipError_t r = hipGetLastError()) return r;
         if (h.dx)
-            if (hipError_t r = transpose(w, ld_w, n, D, wt, ld_n, static_cast<const int*>(nullptr), st)) return r;
+            if (hipError_t r = transpose(w, h.ld_w, n, D, wt, ld_n, static_cast<const int*>(nullptr), st)) return r;
         large = gradients_us(e, M, n, D, p.split).large;
         const ProductArgs px = product(dl, ld_n * e, M, wt, ld_n * e, D, ld_n * e, large);
         const ProductArgs pw = product(dlt, p.ld_m * e, n, xt, p.ld_m * e, D, p.ld_m * e, large);

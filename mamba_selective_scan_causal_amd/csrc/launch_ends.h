@@ -48,9 +48,6 @@ struct HeadArgs {
     void* ws;
 };
 
-// Whether rows of D elements are read as they lie (16-byte pieces), or copied
-// to rows of such a length first.
-inline bool head_rows_whole(int64_t D, int64_t elem) { return D * elem % 16 == 0; }
 bool head_workspace(int dtype, int64_t M, int64_t V, int64_t D, bool backward, int64_t& bytes);
 hipError_t launch_head(const HeadArgs& a, hipStream_t st);
 hipError_t launch_head_bwd(const HeadArgs& a, hipStream_t st);

@@ -57,11 +57,6 @@ class Checks {
     void out_any(void* p, int64_t elems, int64_t elem, bool required) {
         add(outs_, n_outs_, p, elems > 0 ? 1 : 0, elems, elems, elem, required, elem);
     }
-    // Rows that are read in pieces of 16 bytes.
-    void pieces(const void* p, int64_t rows, int64_t ld, int64_t elem) {
-        if (status_ != MSS_OK || !p || rows == 0) return;
-        if (reinterpret_cast<uintptr_t>(p) % 16 || (rows > 1 && ld * elem % 16)) status_ = MSS_EALIGN;
-    }
     // Bytes of any alignment (the reset flags).
     void in_bytes(const void* p, int64_t n) { add(ins_, n_ins_, p, n > 0 ? 1 : 0, n, n, 1, false, 1); }
     void must(bool ok) {

@@ -4,8 +4,9 @@
 // and both of its gradients are computed.
 //
 // A workgroup computes a BL x BR tile of C.  128 bytes of every row (64 values
-// of two bytes, 32 of four) go to LDS per stage by direct loads, one stage
-// ahead of the matrix instructions.  Chunk c (16 bytes) of row i lies at chunk
+// of two bytes, 32 of four) go to LDS per stage, one stage ahead of the matrix
+// instructions: by direct loads where the rows lie at multiples of 16 bytes,
+// through registers otherwise.  Chunk c (16 bytes) of row i lies at chunk
 // c ^ (i & 7) of the row's 128 bytes: the 16 rows that a fragment reads at one
 // c then fall on different banks.  A lane's 16 bytes are a fragment of one
 // 16x16x32 instruction (two-byte types) or of four 16x16x4 ones (fp32; which k
@@ -13,6 +14,8 @@
 // R is the instruction's row operand, so that a lane ends up with four
 // neighbouring r of one l: runs of C's rows.
 #pragma once
+
+#include <type_traits>
 
 #include "block_math.h"
 
@@ -59,11 +62,11 @@ struct Mma<float> {
 };
 
 struct ProductArgs {
-    const char* l;            // row-strided operands, 16-byte aligned rows
+    const char* l;            // row-strided operands
     const char* r;
     int64_t ld_l, ld_r;       // bytes
     int64_t nl, nr;           // rows of each (at least 1)
-    int64_t kbytes;           // bytes of a row that count, a multiple of 16
+    int64_t kbytes;           // bytes of a row that count
     int64_t tiles_l, tiles_r;
 };
 
@@ -90,7 +93,7 @@ static __device__ const v4i kZeros = {0, 0, 0, 0};
 
 // A stage of ROWS rows of one operand: where this lane's chunks come from.
 template <int ROWS, int WAVES>
-struct Stager {
+struct StageRows {
     static constexpr int kLoads = ROWS / 8 / WAVES;
     const char* p[kLoads];
     int64_t at;               // this lane's byte of the row
@@ -105,21 +108,57 @@ struct Stager {
             p[s] = base + row * ld;
         }
     }
-    // The chunks of the stage that starts at byte k of the rows, to LDS.  Past
-    // the end of a row both operands read zeros.
+    static __device__ __forceinline__ char* place(char* lds, int s, int wave) { return lds + (s * WAVES + wave) * 1024; }
+};
+
+// Rows that start at multiples of 16 bytes and are a multiple of 16 long: straight
+// to LDS, once load() is called.
+template <typename T, int ROWS, int WAVES>
+struct DirectStage : StageRows<ROWS, WAVES> {
+    using Rows = StageRows<ROWS, WAVES>;
+    // The chunks of the stage that starts at byte k of the rows.  Past the end of a
+    // row both operands read zeros.
     __device__ __forceinline__ void load(char* lds, int64_t k, int64_t kbytes, int wave) {
-        const bool in = k + at < kbytes;
+        const bool in = k + this->at < kbytes;
 #pragma unroll
-        for (int s = 0; s < kLoads; s++) {
-            const char* q = in ? p[s] + k + at : reinterpret_cast<const char*>(&kZeros);
-            __builtin_amdgcn_global_load_lds((gmem)q, (lmem)(lds + (s * WAVES + wave) * 1024), 16, 0, 0);
+        for (int s = 0; s < Rows::kLoads; s++) {
+            const char* q = in ? this->p[s] + k + this->at : reinterpret_cast<const char*>(&kZeros);
+            __builtin_amdgcn_global_load_lds((gmem)q, (lmem)Rows::place(lds, s, wave), 16, 0, 0);
         }
+    }
+    __device__ __forceinline__ void keep(char*, int, int) {}
+};
+
+// Rows at any element: to registers when load() is called, to LDS by keep().
+template <typename T, int ROWS, int WAVES>
+struct ThroughStage : StageRows<ROWS, WAVES> {
+    using Rows = StageRows<ROWS, WAVES>;
+    static constexpr int V = 16 / sizeof(T);
+    RowVec<T, V> r[Rows::kLoads];
+    __device__ __forceinline__ void load(char*, int64_t k, int64_t kbytes, int) {
+        const int64_t c = (k + this->at) / static_cast<int>(sizeof(T)), n = kbytes / static_cast<int>(sizeof(T));
+        if (c + V <= n) {
+#pragma unroll
+            for (int s = 0; s < Rows::kLoads; s++)
+                r[s].t = *reinterpret_cast<const typename RowVec<T, V>::type*>(this->p[s] + k + this->at);
+        } else {
+            const int have = c < n ? static_cast<int>(n - c) : 0;
+#pragma unroll
+            for (int s = 0; s < Rows::kLoads; s++)
+                r[s].load(reinterpret_cast<const T*>(this->p[s]) + (have ? c : 0), 0, have);
+        }
+    }
+    __device__ __forceinline__ void keep(char* lds, int wave, int lane) {
+#pragma unroll
+        for (int s = 0; s < Rows::kLoads; s++)
+            *reinterpret_cast<v4i*>(Rows::place(lds, s, wave) + lane * 16) = __builtin_bit_cast(v4i, r[s].t);
     }
 };
 
 // acc[i][j]: the 16 x 16 tile of C at r = 16 i, l = 16 j of the wave's part; a
 // lane holds r = 4 (lane / 16) + 0..3, l = lane % 16 of it.
-template <typename T, int BL, int BR, int WL, int WR>
+// DIRECT: see DirectStage; the products are the same, in the same order.
+template <typename T, int BL, int BR, int WL, int WR, bool DIRECT = true>
 struct RowProduct {
     static constexpr int kWaves = WL * WR, kThreads = kWaves * kWave;
     static constexpr int kTL = BL / WL / 16, kTR = BR / WR / 16;
@@ -157,8 +196,8 @@ struct RowProduct {
         const int lane = threadIdx.x % kWave;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         const int wl = wave % WL, wr = wave / WL;
-        Stager<BL, kWaves> sl;
-        Stager<BR, kWaves> sr;
+        std::conditional_t<DIRECT, DirectStage<T, BL, kWaves>, ThroughStage<T, BL, kWaves>> sl;
+        std::conditional_t<DIRECT, DirectStage<T, BR, kWaves>, ThroughStage<T, BR, kWaves>> sr;
         sl.init(a.l, a.ld_l, l0, a.nl, wave, lane);
         sr.init(a.r, a.ld_r, r0, a.nr, wave, lane);
 #pragma unroll
@@ -168,6 +207,8 @@ struct RowProduct {
         if (kbegin >= kend) return;
         sl.load(lds, kbegin, kend, wave);
         sr.load(lds + BL * kStage, kbegin, kend, wave);
+        sl.keep(lds, wave, lane);
+        sr.keep(lds + BL * kStage, wave, lane);
         int buf = 0;
         const int row = lane % 16, quad = lane / 16;
         for (int64_t k = kbegin; k < kend; k += kStage) {
@@ -200,6 +241,10 @@ struct RowProduct {
                 }
             }
             interleave();
+            if (k + kStage < kend) {
+                sl.keep(next, wave, lane);
+                sr.keep(next + BL * kStage, wave, lane);
+            }
             buf ^= 1;
         }
     }
