@@ -429,13 +429,13 @@ int64_t align_up(int64_t n, int64_t a) { return ceil_div(n, a) * a; }
 
 // What the tile shapes take on this card, in microseconds: a value of K of one
 // tile, with as many workgroups on a CU as fit it (measured at 1210 and 1040
-// TFLOP/s in bf16 and 139 and 132 in fp32), and a tile's start and end.
+// TFLOP/s in bf16 and 211 and 182 in fp32), and a tile's start and end.
 struct TileCost {
     int64_t size, slots;
     double each, fixed;
 };
 TileCost tile_cost(bool large, int64_t elem) {
-    const double wide = elem == 4 ? 8.7 : 1.0;
+    const double wide = elem == 4 ? 5.8 : 1.0;
     return large ? TileCost{256, 256, 0.0277 * wide, 5.0} : TileCost{128, 512, 0.0161 * wide, 4.0};
 }
 

@@ -45,18 +45,19 @@ def embedding_backward(ids, dy, vocab, scale, dtype, before=None):
 def head(x, weight, targets, logit_scale, dloss=None, dlse=None):
     """{name: (value, bound)} of loss and lse, and of dx and dweight where dloss is given.
 
-    Logits: D products (exact in fp32 for 2-byte types, one rounding in fp32) and their sum, the
-    scaling to log2 units and the exponential (2 U of the argument's size each, 4 U relative);
-    the sum over the vocabulary is a sum of V positive terms in runs of at most 64 a lane and
-    a tree or a walk over the runs: fewer than 96 + V / 64 additions deep.  dl is rounded once to
-    the operands' type; its products are summed over V (dx) or M (dweight)."""
+    Logits: D products and their sum; products are exact for 2-byte types, and sums of six partial
+    products in fp32, which leave out three, of less than 2^-22, 2^-22 and 2^-30: 8 U of the
+    product's size in all.  The scaling to log2 units and the exponential (2 U of the argument's
+    size each, 4 U relative); the sum over the vocabulary is a sum of V positive terms in runs of
+    at most 64 a lane and a tree or a walk over the runs: fewer than 96 + V / 64 additions deep.
+    dl is rounded once to the operands' type; its products are summed over V (dx) or M (dweight)."""
     t = x.dtype
     x, w = x.double(), weight.double()
     (M, D), V = x.shape, w.shape[0]
     inside = (targets >= 0) & (targets < V)
     at = targets.clamp(0, V - 1).long()[:, None]
     logits = logit_scale * (x @ w.t())
-    off = (D + 4) * U * abs(logit_scale) * (x.abs() @ w.abs().t()) + 4 * U * logits.abs()
+    off = (D + 12) * U * abs(logit_scale) * (x.abs() @ w.abs().t()) + 4 * U * logits.abs()
     lse = torch.logsumexp(logits, 1)
     p = torch.exp(logits - lse[:, None])
     # a logit's error moves lse by p times it
@@ -81,8 +82,8 @@ def head(x, weight, targets, logit_scale, dloss=None, dlse=None):
     x = torch.where(inside[:, None], x, 0.0)
     dx, dw = logit_scale * (dl @ w), logit_scale * (dl.t() @ x)
     size_x, size_w = abs(logit_scale) * (dl.abs() @ w.abs()), abs(logit_scale) * (dl.abs().t() @ x.abs())
-    off_x = abs(logit_scale) * (e @ w.abs()) + (V + 20) * U * size_x
-    off_w = abs(logit_scale) * (e.t() @ x.abs()) + (M + 4) * U * size_w
+    off_x = abs(logit_scale) * (e @ w.abs()) + (V + 28) * U * size_x
+    off_w = abs(logit_scale) * (e.t() @ x.abs()) + (M + 12) * U * size_w
     return dict(out, dx=(dx, rounded(dx, off_x, t)), dweight=(dw, rounded(dw, off_w, t)))
 
 
