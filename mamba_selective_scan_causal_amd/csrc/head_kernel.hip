@@ -32,11 +32,63 @@ constexpr int kPadRows = 64;                 // dl^T and x^T have rows of a mult
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The two tile shapes: one workgroup of eight waves on a CU, or two of four.
-template <typename T, bool DIRECT = true>
-using Large = RowProduct<T, 256, 256, 4, 2, DIRECT>;
-template <typename T, bool DIRECT = true>
-using Small = RowProduct<T, 128, 128, 2, 2, DIRECT>;
+// The tile shapes, rows of the operand whose rows are C's first.  With 256 x 256
+// and 192 x 320 one workgroup of eight waves fills a CU's LDS, of the others' four
+// waves two do (four of the last, which reads the vocabulary for a few rows: 8 rows
+// of 65536 x 2560 in bf16 take 58 us with it, with 128 x 128 72).
+enum TileShape { kLarge, kTall, kWide, kSmall, kFew };
+template <typename T, int SHAPE, bool DIRECT>
+struct Tile;
+template <typename T, bool DIRECT>
+struct Tile<T, kLarge, DIRECT> {
+    using type = RowProduct<T, 256, 256, 4, 2, DIRECT>;
+};
+template <typename T, bool DIRECT>
+struct Tile<T, kTall, DIRECT> {
+    using type = RowProduct<T, 192, 320, 4, 2, DIRECT>;
+};
+template <typename T, bool DIRECT>
+struct Tile<T, kWide, DIRECT> {
+    using type = RowProduct<T, 128, 160, 2, 2, DIRECT>;
+};
+template <typename T, bool DIRECT>
+struct Tile<T, kSmall, DIRECT> {
+    using type = RowProduct<T, 128, 128, 2, 2, DIRECT>;
+};
+template <typename T, bool DIRECT>
+struct Tile<T, kFew, DIRECT> {
+    using type = RowProduct<T, 32, 128, 1, 4, DIRECT>;
+};
+template <typename P>
+struct Tag {
+    using type = P;
+};
+
+// f(Tag of the shape's RowProduct).  Through registers kTall and kWide are slower than
+// the other shapes, and so is kLarge in fp32 (its registers spill).  FEW: where kFew may
+// be the shape.
+constexpr bool has_tile(int shape, bool direct, int64_t elem) {
+    return direct || shape == kSmall || shape == kFew || (shape == kLarge && elem == 2);
+}
+template <typename T, bool DIRECT, bool FEW, typename F>
+void with_tile(int shape, F&& f) {
+    const auto as = [&](auto s) {
+        if constexpr (has_tile(s, DIRECT, sizeof(T))) f(Tag<typename Tile<T, s, DIRECT>::type>{});
+    };
+    switch (shape) {
+        case kLarge: return as(std::integral_constant<int, kLarge>{});
+        case kTall: return as(std::integral_constant<int, kTall>{});
+        case kWide: return as(std::integral_constant<int, kWide>{});
+        case kSmall: return as(std::integral_constant<int, kSmall>{});
+    }
+    if constexpr (FEW) as(std::integral_constant<int, kFew>{});
+}
+template <typename T, typename F>
+void with_tile(int shape, bool direct, F&& f) {
+    if (direct) with_tile<T, true, true>(shape, f);
+    else with_tile<T, false, true>(shape, f);
+}
+
 template <typename P>
 struct Shape;
 template <typename T, int BL_, int BR_, int WL_, int WR_, bool DIRECT>
@@ -196,6 +248,20 @@ __global__ __launch_bounds__(256) void head_join_kernel(JoinArgs h) {
 
 // ---- copies ---------------------------------------------------------------------
 
+// Rows of n values to rows of ld_out values, zeros behind.
+template <typename T>
+__global__ __launch_bounds__(256) void pad_rows_kernel(const T* in, int64_t ld_in, int64_t rows, int64_t n, T* out,
+                                                       int64_t ld_out) {
+    constexpr int V = 16 / sizeof(T);           // ld_out is a multiple
+    const int64_t row = blockIdx.x * int64_t{4} + threadIdx.x / kWave;
+    if (row >= rows) return;
+    for (int64_t c = threadIdx.x % kWave * V; c < ld_out; c += kWave * V) {
+        RowVec<T, V> v;
+        v.load(in + row * ld_in, static_cast<int>(c), static_cast<int>(n));
+        v.template store<false>(out + row * ld_out + c, 0, V);
+    }
+}
+
 // in (rows, n) to out (n, ld_out), ld_out >= rows, zeros behind and in the
 // columns of rows that are off (t < 0).  A tile of 64 x 64 values goes through
 // LDS, read and written in pieces of 16 bytes (at any element in `in`, whole lines
@@ -294,20 +360,20 @@ struct DlArgs {
     int64_t ld_dl, ld_dlt;
 };
 
-// LDS of a kernel whose waves store T's through it when the product is done.
+// The store of dl^T: the tiles along r that fit the stages' LDS at a time.
 template <typename P>
-constexpr int kStoreLds = P::kWaves * ColStore<typename Shape<P>::type, P::kTR, P::kTL>::kBytes;
-template <typename P>
-constexpr int kLdsWithStore = P::kLds > kStoreLds<P> ? P::kLds : kStoreLds<P>;
+using Transposed = ColStore<typename Shape<P>::type, P::kTR, P::kTL,
+                            P::kTR % 4 == 0 && sizeof(typename Shape<P>::type) == 2 ? 4 : P::kTR % 2 == 0 ? 2 : 1>;
 
 template <typename P>
 __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlArgs h) {
     using T = typename Shape<P>::type;
     using Rows = RowStore<T, P::kTR, P::kTL>;
-    using Cols = ColStore<T, P::kTR, P::kTL>;
+    using Cols = Transposed<P>;
     typedef T quad __attribute__((ext_vector_type(4)));
-    static_assert(Rows::kBytes <= Cols::kBytes, "one region for both");
-    __shared__ __align__(1024) char lds[kLdsWithStore<P>];
+    constexpr int kStore = Rows::kBytes > Cols::kBytes ? Rows::kBytes : Cols::kBytes;
+    static_assert(P::kWaves * kStore <= P::kLds, "stored through the stages' LDS");
+    __shared__ __align__(1024) char lds[P::kLds];
     const Part<P> at(a, blockIdx.x, gridDim.x);
     v4f acc[P::kTR][P::kTL];
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
@@ -335,7 +401,7 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
         return v;
     };
     __syncthreads();          // the last stage is read
-    char* mine = lds + at.wave * Cols::kBytes;
+    char* mine = lds + at.wave * kStore;
     Rows::run(mine, at.lane, static_cast<T*>(h.dl) + at.lw * h.ld_dl + at.rw, h.ld_dl, a.nl - at.lw, h.ld_dl - at.rw, get);
     Cols::run(mine, at.lane, static_cast<T*>(h.dlt) + at.rw * h.ld_dlt + at.lw, h.ld_dlt, h.ld_dlt - at.lw, a.nr - at.rw,
               get);
@@ -428,16 +494,23 @@ constexpr int64_t kDlBytes = int64_t{1} << 30;          // dl and its transpose
 int64_t align_up(int64_t n, int64_t a) { return ceil_div(n, a) * a; }
 
 // What the tile shapes take on this card, in microseconds: a value of K of one
-// tile, with as many workgroups on a CU as fit it (measured at 1210 and 1040
-// TFLOP/s in bf16 and 211 and 182 in fp32), and a tile's start and end.
+// tile, with as many workgroups on a CU as `slots` says for all of them, and a
+// tile's start and end.  Measured in bf16 with 8192 x 32768 x 1536: 1226, 1150, 1095
+// and 1045 TFLOP/s; in fp32 211 in place of 1226 and 182 of 1045.  kFew is bound by
+// what it reads, and is taken by the number of rows.
 struct TileCost {
-    int64_t size, slots;
+    int64_t nl, nr, slots;
     double each, fixed;
 };
-TileCost tile_cost(bool large, int64_t elem) {
-    const double wide = elem == 4 ? 5.8 : 1.0;
-    return large ? TileCost{256, 256, 0.0277 * wide, 5.0} : TileCost{128, 512, 0.0161 * wide, 4.0};
+TileCost tile_cost(int shape, int64_t elem) {
+    constexpr TileCost costs[] = {{256, 256, 256, 0.0274, 5.0}, {192, 320, 256, 0.0274, 5.0},
+                                  {128, 160, 512, 0.0192, 4.0}, {128, 128, 512, 0.0161, 4.0},
+                                  {32, 128, 1024, 0.0161, 4.0}};
+    TileCost c = costs[shape];
+    if (elem == 4) c.each *= 5.8;
+    return c;
 }
+constexpr int64_t kFewRows = 32;
 
 // `n` tiles that take `us` each, on CUs that took `m` tiles of `first` each before.
 double spread(int64_t slots, int64_t m, double first, int64_t n, double us) {
@@ -454,44 +527,57 @@ double spread(int64_t slots, int64_t m, double first, int64_t n, double us) {
 
 struct Choice {
     double us;
-    bool large;
+    int shape;
 };
-Choice product_us(int64_t elem, int64_t nl, int64_t nr, int64_t k) {
-    Choice best{0, false};
-    for (bool large : {true, false}) {
-        const TileCost c = tile_cost(large, elem);
-        const double us = spread(c.slots, 0, 0, ceil_div(nl, c.size) * ceil_div(nr, c.size), c.each * k + c.fixed);
-        if (large || us < best.us) best = {us, large};
+// A product of nl x nr with K = k.
+Choice product_us(int64_t elem, int64_t nl, int64_t nr, int64_t k, bool direct = true) {
+    Choice best{0, -1};
+    for (int shape = 0; shape < kFew; shape++) {
+        if (!has_tile(shape, direct, elem)) continue;
+        const TileCost c = tile_cost(shape, elem);
+        const double us = spread(c.slots, 0, 0, ceil_div(nl, c.nl) * ceil_div(nr, c.nr), c.each * k + c.fixed);
+        if (best.shape < 0 || us < best.us) best = {us, shape};
     }
+    if (nl <= kFewRows) best.shape = kFew;
     return best;
 }
 
 // dx (M, D) with K = n in `split` parts, and dW (n, D) with K = M.
 Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split) {
-    Choice best{0, false};
-    for (bool large : {true, false}) {
-        const TileCost c = tile_cost(large, elem);
-        const int64_t wide = ceil_div(D, c.size), x = ceil_div(M, c.size) * wide * split, w = ceil_div(n, c.size) * wide;
+    Choice best{0, -1};
+    for (int shape = 0; shape < kFew; shape++) {
+        const TileCost c = tile_cost(shape, elem);
+        const int64_t wide = ceil_div(D, c.nr), x = ceil_div(M, c.nl) * wide * split, w = ceil_div(n, c.nl) * wide;
         const double ux = c.each * n / split + c.fixed, uw = c.each * M + c.fixed;
         const double us = ux >= uw ? spread(c.slots, x, ux, w, uw) : spread(c.slots, w, uw, x, ux);
-        if (large || us < best.us) best = {us, large};
+        if (best.shape < 0 || us < best.us) best = {us, shape};
     }
     return best;
 }
 
+// Rows that are not a multiple of 16 bytes long are copied to rows that are where
+// there are so many that the copy of W costs less than reading it through registers
+// (bf16, V32768, forward: M8192 D1535 873 us through registers, 675 + 45 copied;
+// M2048 D769 151 and 120 + 25; fp16 M1551 V10007 D1001 85 and 61 + 13).
+constexpr int64_t kCopyRows = 1024;
+
 struct Plan {
+    bool copied;
+    int64_t Dk;               // values in a row that the products read
     int64_t piece;            // vocabulary rows at a time
     int64_t chunk;            // rows at a time (forward)
     int split;                // of dx's K
     bool accumulate;          // dx goes through fp32 partial sums
     int64_t ld_m;             // values in a row of dl^T and x^T
     int64_t ld_acc;           // and of dx's partial sums
-    int64_t part, at_target, dl, dlt, xt, wt, acc, rows, bytes;
+    int64_t x, w, part, at_target, dl, dlt, xt, wt, acc, rows, bytes;
 };
 
 bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p) {
     const int64_t e = dtype == MSS_F32 ? 4 : 2;
     p = Plan{};
+    p.copied = D * e % 16 != 0 && M >= kCopyRows;
+    p.Dk = p.copied ? align_up(D, 16 / e) : D;
     p.ld_m = align_up(M, kPadRows);
     bool fits = true;
     const auto take = [&](int64_t a, int64_t b, int64_t c) {
@@ -506,13 +592,20 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
         return here;
     };
     if (!backward) {
-        p.piece = V < (int64_t{1} << 18) ? V : int64_t{1} << 18;
-        const int64_t slabs = ceil_div(V, 64);
+        p.piece = p.copied ? align_up((int64_t{64} << 20) / (p.Dk * e) + 1, 256) : int64_t{1} << 18;
+        if (p.piece > (int64_t{1} << 18)) p.piece = int64_t{1} << 18;
+        if (p.piece > V) p.piece = V;
+        // the narrowest slab is 32 columns, of few rows, 64 otherwise; each piece ends in one of its own
+        const int64_t slabs = ceil_div(V, M <= kFewRows ? 32 : 64) + ceil_div(V, p.piece);
         p.chunk = kPartBytes / (slabs * 8) / 256 * 256;
         if (p.chunk < 256) p.chunk = 256;
         if (p.chunk > M) p.chunk = M;
         p.part = take(slabs, p.chunk, 8);
         p.at_target = take(M, 4, 1);
+        if (p.copied) {
+            p.x = take(M, p.Dk, e);
+            p.w = take(p.piece, p.Dk, e);
+        }
         return fits;
     }
     // The piece, in steps of 256 vocabulary rows, and the parts of dx's K: what takes the least time
@@ -541,6 +634,10 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
     p.dlt = take(p.piece, p.ld_m, e);
     p.xt = take(D, p.ld_m, e);
     p.wt = take(D, p.piece, e);
+    if (p.copied) {
+        p.x = take(M, p.Dk, e);
+        p.w = take(p.piece, p.Dk, e);
+    }
     p.ld_acc = align_up(D, 4);
     if (p.accumulate) p.acc = take(M * int64_t{4}, p.ld_acc, p.split);
     p.rows = take(align_up(M, 64) * int64_t{16} + 256, 1, 1);
@@ -553,15 +650,26 @@ hipError_t by_type(int dtype, F&& f) {
 }
 
 ProductArgs product(const void* l, int64_t ld_l, int64_t nl, const void* r, int64_t ld_r, int64_t nr, int64_t kbytes,
-                    bool large) {
-    const int64_t t = large ? 256 : 128;
-    return {static_cast<const char*>(l), static_cast<const char*>(r), ld_l, ld_r, nl, nr, kbytes, ceil_div(nl, t),
-            ceil_div(nr, t)};
+                    int shape) {
+    const TileCost t = tile_cost(shape, 2);
+    return {static_cast<const char*>(l), static_cast<const char*>(r), ld_l, ld_r, nl, nr, kbytes, ceil_div(nl, t.nl),
+            ceil_div(nr, t.nr)};
 }
 
 // Whether rows of a product's operand can go straight to LDS.
 bool direct(const void* p, int64_t ld, int64_t rows, int64_t n, int64_t e) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && n * e % 16 == 0 && (rows == 1 || ld * e % 16 == 0);
+}
+
+// Rows as the products read them: as they lie, or copied to `to`.
+template <typename T>
+hipError_t rows_of(const Plan& p, const T*& in, int64_t& ld, int64_t rows, int64_t n, char* to, hipStream_t st) {
+    if (!p.copied) return hipSuccess;
+    T* out = reinterpret_cast<T*>(to);
+    pad_rows_kernel<T><<<static_cast<uint32_t>(ceil_div(rows, 4)), 256, 0, st>>>(in, ld, rows, n, out, p.Dk);
+    in = out;
+    ld = p.Dk;
+    return hipGetLastError();
 }
 
 template <typename T>
@@ -577,27 +685,30 @@ hipError_t forward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     char* ws = static_cast<char*>(h.ws);
     constexpr int64_t e = sizeof(T);
     const T* x = static_cast<const T*>(h.x);
-    const bool straight = direct(x, h.ld_x, h.M, h.D, e) && direct(h.w, h.ld_w, h.V, h.D, e);
+    int64_t ld_x = h.ld_x;
+    const bool straight = p.copied || (direct(x, ld_x, h.M, h.D, e) && direct(h.w, h.ld_w, h.V, h.D, e));
+    if (hipError_t r = rows_of(p, x, ld_x, h.M, h.D, ws + p.x, st)) return r;
     float* at_target = reinterpret_cast<float*>(ws + p.at_target);
     float2* part = reinterpret_cast<float2*>(ws + p.part);
     for (int64_t m0 = 0; m0 < h.M; m0 += p.chunk) {
         const int64_t rows = h.M - m0 < p.chunk ? h.M - m0 : p.chunk;
-        const bool large = product_us(e, rows, h.V < p.piece ? h.V : p.piece, h.D).large;
-        const int64_t slab = large ? Shape<Large<T>>::kSlab : Shape<Small<T>>::kSlab;
+        const int shape = product_us(e, rows, h.V < p.piece ? h.V : p.piece, h.D, straight).shape;
+        int64_t slabs = 0;
         for (int64_t v0 = 0; v0 < h.V; v0 += p.piece) {
             const int64_t n = h.V - v0 < p.piece ? h.V - v0 : p.piece;
             const T* w = static_cast<const T*>(h.w) + v0 * h.ld_w;
-            const ProductArgs a = product(x + m0 * h.ld_x, h.ld_x * e, rows, w, h.ld_w * e, n, h.D * e, large);
-            // a piece is a multiple of 256 rows, or all of them: slabs do not cross pieces
-            const LossArgs l{h.logit_scale * kLog2e, v0, m0, h.targets, h.wide_ids, part + v0 / slab * rows, at_target};
-            const uint32_t grid = static_cast<uint32_t>(a.tiles_l * a.tiles_r);
-            if (large && straight) head_loss_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, l);
-            else if (large) head_loss_kernel<Large<T, false>><<<grid, Large<T>::kThreads, 0, st>>>(a, l);
-            else if (straight) head_loss_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, l);
-            else head_loss_kernel<Small<T, false>><<<grid, Small<T>::kThreads, 0, st>>>(a, l);
+            int64_t ld_w = h.ld_w;
+            if (hipError_t r = rows_of(p, w, ld_w, n, h.D, ws + p.w, st)) return r;
+            const ProductArgs a = product(x + m0 * ld_x, ld_x * e, rows, w, ld_w * e, n, p.Dk * e, shape);
+            const LossArgs l{h.logit_scale * kLog2e, v0, m0, h.targets, h.wide_ids, part + slabs * rows, at_target};
+            with_tile<T>(shape, straight, [&](auto tag) {
+                using P = typename decltype(tag)::type;
+                head_loss_kernel<P><<<static_cast<uint32_t>(a.tiles_l * a.tiles_r), P::kThreads, 0, st>>>(a, l);
+                slabs += ceil_div(n, Shape<P>::kSlab);
+            });
             if (hipError_t r = hipGetLastError()) return r;
         }
-        const JoinArgs j{part, ceil_div(h.V, slab), rows, m0, h.V, at_target, h.targets, h.wide_ids, h.loss, h.lse};
+        const JoinArgs j{part, slabs, rows, m0, h.V, at_target, h.targets, h.wide_ids, h.loss, h.lse};
         if (rows < 1024) head_join_kernel<1><<<static_cast<uint32_t>(rows), 256, 0, st>>>(j);
         else head_join_kernel<16><<<static_cast<uint32_t>(ceil_div(rows, 16)), 256, 0, st>>>(j);
         if (hipError_t r = hipGetLastError()) return r;
@@ -620,40 +731,45 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     row_grads_kernel<<<static_cast<uint32_t>(ceil_div(M, 1024)), 1024, 0, st>>>(h, g);
     if (hipError_t r = hipGetLastError()) return r;
     const T* x = static_cast<const T*>(h.x);
-    const bool straight = direct(x, h.ld_x, M, D, e) && direct(h.w, h.ld_w, h.V, D, e);
+    int64_t ld_x = h.ld_x;
+    const bool straight = p.copied || (direct(x, ld_x, M, D, e) && direct(h.w, h.ld_w, h.V, D, e));
+    if (hipError_t r = rows_of(p, x, ld_x, M, D, ws + p.x, st)) return r;
     T* xt = reinterpret_cast<T*>(ws + p.xt);
     T* wt = reinterpret_cast<T*>(ws + p.wt);
     T* dl = reinterpret_cast<T*>(ws + p.dl);
     T* dlt = reinterpret_cast<T*>(ws + p.dlt);
     if (h.dw)
-        if (hipError_t r = transpose(x, h.ld_x, M, D, xt, p.ld_m, g.t, st)) return r;
+        if (hipError_t r = transpose(x, ld_x, M, D, xt, p.ld_m, g.t, st)) return r;
     for (int64_t v0 = 0; v0 < h.V; v0 += p.piece) {
         const int64_t n = h.V - v0 < p.piece ? h.V - v0 : p.piece;
         const int64_t ld_n = align_up(n, kPadRows);      // at most the piece, a multiple of 256
         const T* w = static_cast<const T*>(h.w) + v0 * h.ld_w;
-        bool large = product_us(e, M, n, D).large;
-        const ProductArgs a = product(x, h.ld_x * e, M, w, h.ld_w * e, n, D * e, large);
+        int64_t ld_w = h.ld_w;
+        if (hipError_t r = rows_of(p, w, ld_w, n, D, ws + p.w, st)) return r;
+        int shape = product_us(e, M, n, D, straight).shape;
+        const ProductArgs a = product(x, ld_x * e, M, w, ld_w * e, n, p.Dk * e, shape);
         const DlArgs d{h.logit_scale * kLog2e, v0, g, dl, dlt, ld_n, p.ld_m};
-        const uint32_t grid = static_cast<uint32_t>(a.tiles_l * a.tiles_r);
-        if (large && straight) head_dl_kernel<Large<T>><<<grid, Large<T>::kThreads, 0, st>>>(a, d);
-        else if (large) head_dl_kernel<Large<T, false>><<<grid, Large<T>::kThreads, 0, st>>>(a, d);
-        else if (straight) head_dl_kernel<Small<T>><<<grid, Small<T>::kThreads, 0, st>>>(a, d);
-        else head_dl_kernel<Small<T, false>><<<grid, Small<T>::kThreads, 0, st>>>(a, d);
+        with_tile<T>(shape, straight, [&](auto tag) {
+            using P = typename decltype(tag)::type;
+            head_dl_kernel<P><<<static_cast<uint32_t>(a.tiles_l * a.tiles_r), P::kThreads, 0, st>>>(a, d);
+        });
         if (hipError_t r = hipGetLastError()) return r;
         if (h.dx)
-            if (hipError_t r = transpose(w, h.ld_w, n, D, wt, ld_n, static_cast<const int*>(nullptr), st)) return r;
-        large = gradients_us(e, M, n, D, p.split).large;
-        const ProductArgs px = product(dl, ld_n * e, M, wt, ld_n * e, D, ld_n * e, large);
-        const ProductArgs pw = product(dlt, p.ld_m * e, n, xt, p.ld_m * e, D, p.ld_m * e, large);
+            if (hipError_t r = transpose(w, ld_w, n, D, wt, ld_n, static_cast<const int*>(nullptr), st)) return r;
+        shape = gradients_us(e, M, n, D, p.split).shape;
+        // whole 16 bytes of K: head_dl_kernel's tiles reach so far, and write zeros there
+        const ProductArgs px = product(dl, ld_n * e, M, wt, ld_n * e, D, align_up(n * e, 16), shape);
+        const ProductArgs pw = product(dlt, p.ld_m * e, n, xt, p.ld_m * e, D, align_up(M * e, 16), shape);
         const GradArgs gx{g.back, p.accumulate ? nullptr : h.dx, p.accumulate ? p.ld_acc : h.ld_dx,
                           reinterpret_cast<float*>(ws + p.acc), v0 == 0, p.split};
         const GradArgs gw{g.back, h.dw ? static_cast<T*>(h.dw) + v0 * h.ld_dw : nullptr, h.ld_dw, nullptr, false, 1};
         const int64_t nx = h.dx ? px.tiles_l * px.tiles_r * p.split : 0, nw = h.dw ? pw.tiles_l * pw.tiles_r : 0;
         const TwoProducts two =
             n / p.split >= M ? TwoProducts{{px, pw}, {gx, gw}, nx} : TwoProducts{{pw, px}, {gw, gx}, nw};
-        const uint32_t both = static_cast<uint32_t>(nx + nw);
-        if (large) head_grad_kernel<Large<T>><<<both, Large<T>::kThreads, 0, st>>>(two);
-        else head_grad_kernel<Small<T>><<<both, Small<T>::kThreads, 0, st>>>(two);
+        with_tile<T, true, false>(shape, [&](auto tag) {
+            using P = typename decltype(tag)::type;
+            head_grad_kernel<P><<<static_cast<uint32_t>(nx + nw), P::kThreads, 0, st>>>(two);
+        });
         if (hipError_t r = hipGetLastError()) return r;
     }
     if (h.dx && p.accumulate) {
@@ -679,8 +795,8 @@ bool head_workspace(int dtype, int64_t M, int64_t V, int64_t D, bool bwd, int64_
     bytes = 0;
     if (M == 0) return true;
     if (!plan_of(dtype, M, V, D, bwd, p)) return false;
-    // every launch below 2^32 threads: 256 to a small tile, to 64 x 64 values of a transposition and to
-    // four rows (of at most 2^26) of the others
+    // every launch below 2^32 threads: 256 to a tile of 128 x 128 or more (or 32 x 128 of few rows), to
+    // 64 x 64 values of a transposition and to four rows (of at most 2^26) of the others
     const int64_t across = ceil_div(bwd ? M : p.chunk, 128), down = ceil_div(p.piece, 128), wide = ceil_div(D, 128);
     const int64_t most = int64_t{1} << 24;
     if (across * down >= most || across * wide * (bwd ? p.split : 1) + down * wide >= most ||

@@ -330,29 +330,30 @@ struct RowStore {
             }
             wave_lds_fence();
 #pragma unroll
-            for (int k = 0; k < 16 * kPieces / kWave; k++) {
+            for (int k = 0; k < (16 * kPieces + kWave - 1) / kWave; k++) {
                 const int at = k * kWave + lane, row = at / kPieces, c = at % kPieces;
-                const v4i piece = *reinterpret_cast<const v4i*>(lds + row * kRow + c * 16);
                 const int64_t l = 16 * j + row, r = c * (16 / sizeof(T));
-                if (l < nl) store_piece(out + l * ld + r, piece, nr - r);
+                if (row < 16 && l < nl)
+                    store_piece(out + l * ld + r, *reinterpret_cast<const v4i*>(lds + row * kRow + c * 16), nr - r);
             }
             wave_lds_fence();
         }
     }
 };
 
-// Rows of r: out[r * ld + l].  Four tiles along r at a time.
-template <typename T, int TR, int TL>
+// Rows of r: out[r * ld + l], GROUP tiles along r at a time.
+template <typename T, int TR, int TL, int GROUP>
 struct ColStore {
-    static constexpr int kRow = 16 * TL * sizeof(T) + 16;
-    static constexpr int kBytes = 64 * kRow;
+    static_assert(TR % GROUP == 0, "whole groups");
+    static constexpr int kRow = 16 * TL * sizeof(T) + 16, kRows = 16 * GROUP;
+    static constexpr int kBytes = kRows * kRow;
     template <typename F>
     static __device__ __forceinline__ void run(char* lds, int lane, T* out, int64_t ld, int64_t nl, int64_t nr, F get) {
         constexpr int kPieces = TL * sizeof(T);
 #pragma unroll
-        for (int i0 = 0; i0 < TR; i0 += 4) {
+        for (int i0 = 0; i0 < TR; i0 += GROUP) {
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+            for (int i = 0; i < GROUP; i++)
 #pragma unroll
                 for (int j = 0; j < TL; j++) {
                     const auto v = get(i0 + i, j);
@@ -363,11 +364,11 @@ struct ColStore {
                 }
             wave_lds_fence();
 #pragma unroll
-            for (int k = 0; k < 64 * kPieces / kWave; k++) {
+            for (int k = 0; k < (kRows * kPieces + kWave - 1) / kWave; k++) {
                 const int at = k * kWave + lane, row = at / kPieces, c = at % kPieces;
-                const v4i piece = *reinterpret_cast<const v4i*>(lds + row * kRow + c * 16);
                 const int64_t r = 16 * i0 + row, l = c * (16 / sizeof(T));
-                if (r < nr) store_piece(out + r * ld + l, piece, nl - l);
+                if (row < kRows && r < nr)
+                    store_piece(out + r * ld + l, *reinterpret_cast<const v4i*>(lds + row * kRow + c * 16), nl - l);
             }
             wave_lds_fence();
         }
