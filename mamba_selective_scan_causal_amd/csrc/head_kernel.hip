@@ -169,19 +169,19 @@ __global__ __launch_bounds__(P::kThreads) void head_loss_kernel(ProductArgs a, L
     for (int j = 0; j < P::kTL; j++) {
         const int64_t m = at.l + 16 * j;
         const bool in = m < a.nl;
-        const int64_t t = in ? target_of(h.targets, h.wide, h.m0 + m) : -1;
-        const int hit = at.place(t - h.first);
+        const int64_t v = in ? target_of(h.targets, h.wide, h.m0 + m) - h.first : -1;
+        const int hit = at.place(v);
         float top = -INFINITY, own = 0.0f;
 #pragma unroll
         for (int i = 0; i < P::kTR; i++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const float v = whole || 16 * i + e < valid ? acc[i][j][e] * h.c : -INFINITY;
-                acc[i][j][e] = v;
-                top = __builtin_fmaxf(top, v);
-                own = hit == 16 * i + e ? v : own;
+                const float l = whole || 16 * i + e < valid ? acc[i][j][e] * h.c : -INFINITY;
+                acc[i][j][e] = l;
+                top = __builtin_fmaxf(top, l);
+                own = hit == 16 * i + e ? l : own;
             }
-        if (in && at.holds(t - h.first, a.nr)) h.at_target[h.m0 + m] = own;
+        if (at.holds(v, a.nr)) h.at_target[h.m0 + m] = own;
         top = over_quads_max(top);
         float sum = 0.0f;
 #pragma unroll
@@ -375,23 +375,33 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
     static_assert(P::kWaves * kStore <= P::kLds, "stored through the stages' LDS");
     __shared__ __align__(1024) char lds[P::kLds];
     const Part<P> at(a, blockIdx.x, gridDim.x);
-    v4f acc[P::kTR][P::kTL];
-    P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
-    const bool whole = at.rw + 16 * P::kTR <= a.nr;
+    // read ahead of the product
+    int hit[P::kTL];
+    bool on[P::kTL];
+    float up[P::kTL], own[P::kTL], lse2[P::kTL];
 #pragma unroll
     for (int j = 0; j < P::kTL; j++) {
         const int64_t m = at.l + 16 * j;
         const bool in = m < a.nl;
         const int t = in ? h.g.t[m] : -1;
-        const float up = in ? h.g.a[m] : 0.0f, own = in ? h.g.b[m] : 0.0f, lse2 = in ? h.g.lse2[m] : 0.0f;
-        const int hit = at.place(t - h.first);
+        on[j] = t >= 0;
+        hit[j] = at.place(t - h.first);
+        up[j] = in ? h.g.a[m] : 0.0f;
+        own[j] = in ? h.g.b[m] : 0.0f;
+        lse2[j] = in ? h.g.lse2[m] : 0.0f;
+    }
+    v4f acc[P::kTR][P::kTL];
+    P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
+    const bool whole = at.rw + 16 * P::kTR <= a.nr;
+#pragma unroll
+    for (int j = 0; j < P::kTL; j++) {
 #pragma unroll
         for (int i = 0; i < P::kTR; i++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                float p = ex2(__builtin_fmaf(acc[i][j][e], h.c, -lse2)) * up;
-                p = hit == 16 * i + e ? p - own : p;
-                acc[i][j][e] = t >= 0 && (whole || at.r + 16 * i + e < a.nr) ? p : 0.0f;
+                float p = ex2(__builtin_fmaf(acc[i][j][e], h.c, -lse2[j])) * up[j];
+                p = hit[j] == 16 * i + e ? p - own[j] : p;
+                acc[i][j][e] = on[j] && (whole || at.r + 16 * i + e < a.nr) ? p : 0.0f;
             }
     }
     const auto get = [&](int i, int j) {
