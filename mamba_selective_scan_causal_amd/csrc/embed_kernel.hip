@@ -106,6 +106,31 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs& a, int64_t m) {
     return a.ids ? key_of(a.ids, a.wide, m, a.V) : a.key_in[m];
 }
 
+// The lanes of a wave whose keys have the same digit.
+struct Peers {
+    uint64_t same, below;     // of them, those in lower lanes
+    uint32_t digit;
+    bool in;
+    __device__ __forceinline__ Peers(uint32_t digit_, bool in_, int bits, int lane)
+        : same(__builtin_amdgcn_ballot_w64(in_)), digit(digit_), in(in_) {
+        for (int b = 0; b < bits; b++) {
+            const uint64_t ones = __builtin_amdgcn_ballot_w64(digit >> b & 1);
+            same &= digit >> b & 1 ? ones : ~ones;
+        }
+        below = same & ((uint64_t{1} << lane) - 1);
+    }
+    // The key's place: next[digit] says where the digit's next key goes, and moves on by the wave's.
+    // (The lanes of a digit have all read it before the first of them writes: one instruction
+    // after the other for the whole wave.)
+    __device__ __forceinline__ uint32_t place(volatile uint32_t* next) const {
+        const uint32_t first = next[digit];
+        __builtin_amdgcn_wave_barrier();
+        if (below == 0) next[digit] = first + __builtin_popcountll(same);
+        __builtin_amdgcn_wave_barrier();
+        return first + __builtin_popcountll(below);
+    }
+};
+
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
     __shared__ uint32_t bins[kMaxBins];
     const int n = 1 << a.bits;
@@ -185,24 +210,99 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
         const bool in = m < end;
         const uint32_t key = in ? sort_key(a, m) : 0;
         const uint32_t pos = !in ? 0 : a.ids ? static_cast<uint32_t>(m) : a.pos_in[m];
-        const uint32_t digit = key >> a.shift & (n - 1);
-        uint64_t same = __builtin_amdgcn_ballot_w64(in);
-        for (int b = 0; b < a.bits; b++) {
-            const uint64_t ones = __builtin_amdgcn_ballot_w64(digit >> b & 1);
-            same &= digit >> b & 1 ? ones : ~ones;
-        }
-        const uint64_t below = same & ((uint64_t{1} << lane) - 1);
+        const Peers peers(key >> a.shift & (n - 1), in, a.bits, lane);
         if (in) {
-            const uint32_t place = mine[digit];
-            const uint32_t to = place + __builtin_popcountll(below);
-            // the lanes of a digit have all read its place before its first lane moves it on
-            __builtin_amdgcn_wave_barrier();
-            if (below == 0) mine[digit] = place + __builtin_popcountll(same);
+            const uint32_t to = peers.place(mine);
             a.key_out[to] = key;
             a.pos_out[to] = pos;
             if (a.next) atomicAdd(&a.next[to / a.tile * n + (key >> (a.shift + a.bits) & (n - 1))], 1u);
         }
-        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// All passes of few positions in one workgroup and one launch, in LDS: what the
+// launches above take for so few is their start (a gradient added to a table, M 2048
+// V32768 D1536 bf16: 22 us a call in place of 30).  With more, the rounds of one CU take
+// longer than they save (M 16384: 50 us against 23).
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallRounds = 2;
+constexpr int kSmallRows = kSmallThreads * kSmallRounds;
+
+struct SmallSortArgs {
+    const void* ids;
+    bool wide;
+    int M, bits, passes;
+    int64_t V;
+    uint32_t* key_out;
+    uint32_t* pos_out;
+};
+
+__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(SmallSortArgs a) {
+    constexpr int kWaves = kSmallThreads / kWave;
+    static_assert(kMaxBins <= kSmallThreads, "a thread to a digit");
+    __shared__ uint32_t keys[kSmallRows], places[kSmallRows];
+    __shared__ uint32_t at[kWaves][kMaxBins];       // per wave: keys of a digit, then the place of the next one
+    __shared__ uint32_t sums[kWaves];
+    const int n = 1 << a.bits, lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int m0 = wave * kSmallRounds * kWave + lane;          // a wave's positions lie in a row
+    uint32_t key[kSmallRounds], pos[kSmallRounds];
+#pragma unroll
+    for (int i = 0; i < kSmallRounds; i++) {
+        const int m = m0 + i * kWave;
+        key[i] = m < a.M ? key_of(a.ids, a.wide, m, a.V) : 0;
+        pos[i] = m;
+    }
+    for (int p = 0; p < a.passes; p++) {
+        const int shift = p * a.bits;
+        for (int b = threadIdx.x; b < kWaves * n; b += kSmallThreads) at[b / n][b % n] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSmallRounds; i++)
+            if (m0 + i * kWave < a.M) atomicAdd(&at[wave][key[i] >> shift & (n - 1)], 1u);
+        __syncthreads();
+        const int d = threadIdx.x;
+        uint32_t all = 0;
+        if (d < n)
+            for (int w = 0; w < kWaves; w++) all += at[w][d];
+        uint32_t upto = all;
+        for (int k = 1; k < kWave; k *= 2) {
+            const uint32_t below = __shfl_up(upto, k);
+            if (lane >= k) upto += below;
+        }
+        if (lane == kWave - 1) sums[wave] = upto;
+        __syncthreads();
+        if (d < n) {
+            uint32_t to = upto - all;
+            for (int w = 0; w < wave; w++) to += sums[w];
+            for (int w = 0; w < kWaves; w++) {
+                const uint32_t c = at[w][d];
+                at[w][d] = to;
+                to += c;
+            }
+        }
+        __syncthreads();
+        volatile uint32_t* mine = at[wave];
+#pragma unroll
+        for (int i = 0; i < kSmallRounds; i++)
+            if (const Peers peers(key[i] >> shift & (n - 1), m0 + i * kWave < a.M, a.bits, lane); peers.in) {
+                const uint32_t to = peers.place(mine);
+                keys[to] = key[i];
+                places[to] = pos[i];
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSmallRounds; i++) {
+            key[i] = keys[m0 + i * kWave];
+            pos[i] = places[m0 + i * kWave];
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kSmallRounds; i++) {
+        const int m = m0 + i * kWave;
+        if (m >= a.M) break;
+        a.key_out[m] = key[i];
+        a.pos_out[m] = pos[i];
     }
 }
 
@@ -489,7 +589,14 @@ hipError_t launch_embed_bwd(const EmbedArgs& a, hipStream_t st) {
     char* ws = static_cast<char*>(a.ws);
     const auto words = [&](int64_t at) { return reinterpret_cast<uint32_t*>(ws + at); };
     int from = 1;
-    for (int i = 0; i < p.passes && a.M > 0; i++) {
+    const bool small = a.M <= kSmallRows;
+    if (small && a.M > 0) {
+        from = 0;
+        sort_small_kernel<<<1, kSmallThreads, 0, st>>>({a.ids, a.wide_ids, static_cast<int>(a.M), p.bits, p.passes, a.V,
+                                                        words(p.key[0]), words(p.pos[0])});
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    for (int i = 0; i < p.passes && !small; i++) {
         SortArgs s{};
         s.ids = i == 0 ? a.ids : nullptr;
         s.wide = a.wide_ids;
