@@ -37,27 +37,29 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // waves two do (four of the last, which reads the vocabulary for a few rows: 8 rows
 // of 65536 x 2560 in bf16 take 58 us with it, with 128 x 128 72).
 enum TileShape { kLarge, kTall, kWide, kSmall, kFew };
+template <bool DIRECT>
+constexpr Layout kLies = DIRECT ? kDirect : kThrough;
 template <typename T, int SHAPE, bool DIRECT>
 struct Tile;
 template <typename T, bool DIRECT>
 struct Tile<T, kLarge, DIRECT> {
-    using type = RowProduct<T, 256, 256, 4, 2, DIRECT>;
+    using type = RowProduct<T, 256, 256, 4, 2, kLies<DIRECT>, kLies<DIRECT>>;
 };
 template <typename T, bool DIRECT>
 struct Tile<T, kTall, DIRECT> {
-    using type = RowProduct<T, 192, 320, 4, 2, DIRECT>;
+    using type = RowProduct<T, 192, 320, 4, 2, kLies<DIRECT>, kLies<DIRECT>>;
 };
 template <typename T, bool DIRECT>
 struct Tile<T, kWide, DIRECT> {
-    using type = RowProduct<T, 128, 160, 2, 2, DIRECT>;
+    using type = RowProduct<T, 128, 160, 2, 2, kLies<DIRECT>, kLies<DIRECT>>;
 };
 template <typename T, bool DIRECT>
 struct Tile<T, kSmall, DIRECT> {
-    using type = RowProduct<T, 128, 128, 2, 2, DIRECT>;
+    using type = RowProduct<T, 128, 128, 2, 2, kLies<DIRECT>, kLies<DIRECT>>;
 };
 template <typename T, bool DIRECT>
 struct Tile<T, kFew, DIRECT> {
-    using type = RowProduct<T, 32, 128, 1, 4, DIRECT>;
+    using type = RowProduct<T, 32, 128, 1, 4, kLies<DIRECT>, kLies<DIRECT>>;
 };
 template <typename P>
 struct Tag {
@@ -67,6 +69,8 @@ struct Tag {
 // f(Tag of the shape's RowProduct).  Through registers kTall and kWide are slower than
 // the other shapes, and so is kLarge in fp32 (its registers spill).  FEW: where kFew may
 // be the shape.
+// (A column product has the shapes whose columns are groups of 128.)
+constexpr bool has_columns(int shape) { return shape == kLarge || shape == kSmall; }
 constexpr bool has_tile(int shape, bool direct, int64_t elem) {
     return direct || shape == kSmall || shape == kFew || (shape == kLarge && elem == 2);
 }
@@ -91,11 +95,13 @@ void with_tile(int shape, bool direct, F&& f) {
 
 template <typename P>
 struct Shape;
-template <typename T, int BL_, int BR_, int WL_, int WR_, bool DIRECT>
-struct Shape<RowProduct<T, BL_, BR_, WL_, WR_, DIRECT>> {
+template <typename T, int BL_, int BR_, int WL_, int WR_, Layout LL, Layout LR>
+struct Shape<RowProduct<T, BL_, BR_, WL_, WR_, LL, LR>> {
     using type = T;
+    using columns = RowProduct<T, BL_, BR_, WL_, WR_, kDirect, kColumns>;
     static constexpr int BL = BL_, BR = BR_, WL = WL_, WR = WR_;
     static constexpr int kSlab = BR / WR;    // columns of one wave
+    static constexpr int kShape = BL == 256 ? kLarge : BL == 192 ? kTall : BL == 32 ? kFew : BR == 160 ? kWide : kSmall;
 };
 
 // Where a wave's part of the tile lies.
@@ -432,9 +438,11 @@ struct TwoProducts {
     ProductArgs a[2];
     GradArgs g[2];
     int64_t first;            // workgroups of the first
+    bool dx;                  // which of them is dx's
 };
 
-template <typename P>
+// COLUMNS: dx's product reads W as it lies, K down its rows.
+template <typename P, bool COLUMNS>
 __global__ __launch_bounds__(P::kThreads) void head_grad_kernel(TwoProducts two) {
     using T = typename Shape<P>::type;
     using Rows = RowStore<T, P::kTR, P::kTL>;
@@ -452,7 +460,11 @@ __global__ __launch_bounds__(P::kThreads) void head_grad_kernel(TwoProducts two)
     // this workgroup's part of K, whole stages
     const int64_t stages = (a.kbytes + kStage - 1) / kStage;
     const int64_t k0 = stages * part / h.split * kStage, k1 = stages * (part + 1) / h.split * kStage;
-    P::run(a, at.l0, at.r0, k0, k1 < a.kbytes ? k1 : a.kbytes, lds, acc);
+    if (COLUMNS && second == two.dx) {
+        if constexpr (COLUMNS) Shape<P>::columns::run(a, at.l0, at.r0, k0, k1 < a.kbytes ? k1 : a.kbytes, lds, acc);
+    } else {
+        P::run(a, at.l0, at.r0, k0, k1 < a.kbytes ? k1 : a.kbytes, lds, acc);
+    }
     if (!h.out) {
         // fp32 sums: a lane's four are 16 bytes of a row
         float* to = h.acc + (part * a.nl + at.l) * h.ld + at.r;
@@ -553,12 +565,13 @@ Choice product_us(int64_t elem, int64_t nl, int64_t nr, int64_t k, bool direct =
 }
 
 // dx (M, D) with K = n in `split` parts, and dW (n, D) with K = M.
-Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split) {
+Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split, bool columns) {
     Choice best{0, -1};
     for (int shape = 0; shape < kFew; shape++) {
+        if (columns && !has_columns(shape)) continue;
         const TileCost c = tile_cost(shape, elem);
         const int64_t wide = ceil_div(D, c.nr), x = ceil_div(M, c.nl) * wide * split, w = ceil_div(n, c.nl) * wide;
-        const double ux = c.each * n / split + c.fixed, uw = c.each * M + c.fixed;
+        const double ux = (columns ? 1.35 : 1.0) * c.each * n / split + c.fixed, uw = c.each * M + c.fixed;
         const double us = ux >= uw ? spread(c.slots, x, ux, w, uw) : spread(c.slots, w, uw, x, ux);
         if (best.shape < 0 || us < best.us) best = {us, shape};
     }
@@ -570,9 +583,13 @@ Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split
 // (bf16, V32768, forward: M8192 D1535 873 us through registers, 675 + 45 copied;
 // M2048 D769 151 and 120 + 25; fp16 M1551 V10007 D1001 85 and 61 + 13).
 constexpr int64_t kCopyRows = 1024;
+// Below as many rows dx's product reads W as it lies, down its columns, in two-byte
+// types: slower, but W is not transposed first (bf16, both gradients: M16 V65536 D2560
+// 297 us against 424, M517 V50021 D1536 387 and 399, M1000 V32768 D1536 370 and 391).
+constexpr int64_t kColumnRows = 1024;
 
 struct Plan {
-    bool copied;
+    bool copied, columns;     // columns: where W's rows lie at multiples of 16 bytes
     int64_t Dk;               // values in a row that the products read
     int64_t piece;            // vocabulary rows at a time
     int64_t chunk;            // rows at a time (forward)
@@ -588,6 +605,7 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
     p = Plan{};
     p.copied = D * e % 16 != 0 && M >= kCopyRows;
     p.Dk = p.copied ? align_up(D, 16 / e) : D;
+    p.columns = e == 2 && M < kColumnRows && D * e % 16 == 0;
     p.ld_m = align_up(M, kPadRows);
     bool fits = true;
     const auto take = [&](int64_t a, int64_t b, int64_t c) {
@@ -633,9 +651,9 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
         for (int split : {1, 2, 3, 4, 6, 8, 12, 16}) {
             if (split > 1 && 256 * n / split < 512) break;
             const bool sums = split > 1 || pieces > 1;
-            double us = before + full * gradients_us(e, M, 256 * n, D, split).us + (sums ? pass * split * 2 * pieces : 0.0);
+            double us = before + full * gradients_us(e, M, 256 * n, D, split, p.columns).us + (sums ? pass * split * 2 * pieces : 0.0);
             if (best != 0 && us >= best) continue;
-            if (rest) us += gradients_us(e, M, 256 * rest, D, split).us;
+            if (rest) us += gradients_us(e, M, 256 * rest, D, split, p.columns).us;
             if (best == 0 || us < best) best = us, p.piece = 256 * n, p.split = split;
         }
     }
@@ -764,21 +782,26 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
             head_dl_kernel<P><<<static_cast<uint32_t>(a.tiles_l * a.tiles_r), P::kThreads, 0, st>>>(a, d);
         });
         if (hipError_t r = hipGetLastError()) return r;
-        if (h.dx)
+        const bool columns = p.columns && straight;
+        if (h.dx && !columns)
             if (hipError_t r = transpose(w, ld_w, n, D, wt, ld_n, static_cast<const int*>(nullptr), st)) return r;
-        shape = gradients_us(e, M, n, D, p.split).shape;
+        shape = gradients_us(e, M, n, D, p.split, columns).shape;
         // whole 16 bytes of K: head_dl_kernel's tiles reach so far, and write zeros there
-        const ProductArgs px = product(dl, ld_n * e, M, wt, ld_n * e, D, align_up(n * e, 16), shape);
+        const ProductArgs px = columns ? product(dl, ld_n * e, M, w, ld_w * e, D, n * e, shape)
+                                       : product(dl, ld_n * e, M, wt, ld_n * e, D, align_up(n * e, 16), shape);
         const ProductArgs pw = product(dlt, p.ld_m * e, n, xt, p.ld_m * e, D, align_up(M * e, 16), shape);
         const GradArgs gx{g.back, p.accumulate ? nullptr : h.dx, p.accumulate ? p.ld_acc : h.ld_dx,
                           reinterpret_cast<float*>(ws + p.acc), v0 == 0, p.split};
         const GradArgs gw{g.back, h.dw ? static_cast<T*>(h.dw) + v0 * h.ld_dw : nullptr, h.ld_dw, nullptr, false, 1};
         const int64_t nx = h.dx ? px.tiles_l * px.tiles_r * p.split : 0, nw = h.dw ? pw.tiles_l * pw.tiles_r : 0;
         const TwoProducts two =
-            n / p.split >= M ? TwoProducts{{px, pw}, {gx, gw}, nx} : TwoProducts{{pw, px}, {gw, gx}, nw};
+            n / p.split >= M ? TwoProducts{{px, pw}, {gx, gw}, nx, false} : TwoProducts{{pw, px}, {gw, gx}, nw, true};
         with_tile<T, true, false>(shape, [&](auto tag) {
             using P = typename decltype(tag)::type;
-            head_grad_kernel<P><<<static_cast<uint32_t>(nx + nw), P::kThreads, 0, st>>>(two);
+            const uint32_t grid = static_cast<uint32_t>(nx + nw);
+            if constexpr (sizeof(T) == 2 && has_columns(Shape<P>::kShape))
+                if (columns) return head_grad_kernel<P, true><<<grid, P::kThreads, 0, st>>>(two);
+            head_grad_kernel<P, false><<<grid, P::kThreads, 0, st>>>(two);
         });
         if (hipError_t r = hipGetLastError()) return r;
     }

@@ -167,10 +167,108 @@ struct ThroughStage : StageRows<ROWS, WAVES> {
     }
 };
 
+// A stage of COLS columns of an operand that lies with K down its rows (two-byte
+// types): 64 rows of the tile's columns, straight to LDS.  Row k's 32 bytes at
+// columns 16 b lie at block b ^ swap(k): the eight rows that half a wave reads at one b
+// are then on different banks.
+__device__ __forceinline__ int swap_of(int k) { return (k & 3) | (k >> 1 & 4); }
+
+template <typename T, int COLS, int WAVES>
+struct ColumnStage {
+    static_assert(sizeof(T) == 2 && COLS % 128 == 0, "whole groups of eight blocks");
+    static constexpr int kLoads = COLS / 8 / WAVES, kPitch = COLS * 2, kDown = 1024 / kPitch;   // rows of a load
+    const char* p;
+    int64_t ld;
+    int first;                // this lane's row of the wave's first load
+    bool in[kLoads];          // whether its columns are the operand's
+    int64_t at[kLoads];       // bytes from p
+
+    // n columns, a multiple of 8, at multiples of 16 bytes.
+    __device__ __forceinline__ void init(const char* base, int64_t ld_, int64_t col0, int64_t n, int wave, int lane) {
+        p = base + col0 * 2;
+        ld = ld_;
+        const int piece = lane * 16 % kPitch / 16;
+        first = wave * kDown + lane * 16 / kPitch;
+#pragma unroll
+        for (int s = 0; s < kLoads; s++) {
+            const int k = first + s * WAVES * kDown;
+            const int col = ((piece / 2) ^ swap_of(k)) * 16 + piece % 2 * 8;
+            in[s] = col0 + col < n;
+            at[s] = k * ld + col * 2;
+        }
+    }
+    // The 64 rows that start at byte k of what would be a row; zeros past kbytes.
+    __device__ __forceinline__ void load(char* lds, int64_t k, int64_t kbytes, int wave) {
+        const int64_t row = k / 2, rows = kbytes / 2;
+        const char* base = p + row * ld;
+#pragma unroll
+        for (int s = 0; s < kLoads; s++) {
+            const char* q = in[s] && row + first + s * WAVES * kDown < rows ? base + at[s]
+                                                                            : reinterpret_cast<const char*>(&kZeros);
+            __builtin_amdgcn_global_load_lds((gmem)q, (lmem)(lds + (s * WAVES + wave) * 1024), 16, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void keep(char*, int, int) {}
+};
+
+// How an operand lies: K along its rows, at multiples of 16 bytes or anywhere; or
+// down its columns (which takes 1.35 times as long: M16384 N1536 K8192 in bf16 564 us
+// against 418; the transposing load reads half as many bytes at a time).
+enum Layout { kDirect, kThrough, kColumns };
+template <typename T, int ROWS, int WAVES, Layout LAYOUT>
+struct StageOf {
+    using type = DirectStage<T, ROWS, WAVES>;
+};
+template <typename T, int ROWS, int WAVES>
+struct StageOf<T, ROWS, WAVES, kThrough> {
+    using type = ThroughStage<T, ROWS, WAVES>;
+};
+template <typename T, int ROWS, int WAVES>
+struct StageOf<T, ROWS, WAVES, kColumns> {
+    using type = ColumnStage<T, ROWS, WAVES>;
+};
+
+// A lane's fragments of an operand's stage in LDS, in two-byte types: of tile i (16
+// rows of the operand from `first` on) and of half kk of the stage, K = 8 (lane / 16)
+// + 0..7 of its 32.  Columns are read with the transposing load: of 16 lanes, lane
+// l reads 8 bytes of row l / 4, and gets column l of the four rows.
+template <int ROWS, Layout LAYOUT>
+struct Fragments {
+    static constexpr int kReads = 1;
+    const char* p;
+    int c;
+    __device__ __forceinline__ Fragments(const char* stage, int first, int lane)
+        : p(stage + (first + lane % 16) * kStage), c((lane / 16 ^ (lane & 7)) * 16) {}
+    __device__ __forceinline__ v4i at(int i, int kk) const {
+        return *reinterpret_cast<const v4i*>(p + i * 16 * kStage + (c ^ kk * 64));
+    }
+};
+template <int ROWS>
+struct Fragments<ROWS, kColumns> {
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4s* lds4;
+    static constexpr int kReads = 2, kPitch = ROWS * 2;
+    const char* p;
+    int block, swap;
+    __device__ __forceinline__ Fragments(const char* stage, int first, int lane)
+        : p(stage + (lane / 16 * 8 + lane % 16 / 4) * kPitch + lane % 4 * 8),
+          block(first / 16),
+          swap(swap_of(lane / 16 * 8 + lane % 16 / 4)) {}
+    __device__ __forceinline__ v4i at(int i, int kk) const {
+        const char* q = p + ((block + i) ^ swap) * 32 + kk * 32 * kPitch;
+        struct {
+            v4s a, b;
+        } both = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)q),
+                  __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q + 4 * kPitch))};
+        return __builtin_bit_cast(v4i, both);
+    }
+};
+
 // acc[i][j]: the 16 x 16 tile of C at r = 16 i, l = 16 j of the wave's part; a
 // lane holds r = 4 (lane / 16) + 0..3, l = lane % 16 of it.
-// DIRECT: see DirectStage; the products are the same, in the same order.
-template <typename T, int BL, int BR, int WL, int WR, bool DIRECT = true>
+//
+// LL, LR: how L and R lie; the products are the same, in the same order.
+template <typename T, int BL, int BR, int WL, int WR, Layout LL = kDirect, Layout LR = kDirect>
 struct RowProduct {
     static constexpr int kWaves = WL * WR, kThreads = kWaves * kWave;
     static constexpr int kTL = BL / WL / 16, kTR = BR / WR / 16;
@@ -184,16 +282,15 @@ struct RowProduct {
     // first is multiplied.  (Left to the compiler, with a wait after every two
     // reads: 1277 against 1316 TFLOP/s at 8192^3 in bf16; one read for two
     // products, or three for four, 1315 and 1298.)
-    static __device__ __forceinline__ void narrow(const char* pl, const char* pr, int row, int quad,
+    static __device__ __forceinline__ void narrow(const Fragments<BL, LL>& l, const Fragments<BR, LR>& r,
                                                   v4f (&acc)[kTR][kTL]) {
         v4i fl[2][kTL], fr[2][kTR];
 #pragma unroll
         for (int kk = 0; kk < 2; kk++) {
-            const int c = ((kk * 4 + quad) ^ (row & 7)) * 16;
 #pragma unroll
-            for (int j = 0; j < kTL; j++) fl[kk][j] = *reinterpret_cast<const v4i*>(pl + j * 16 * kStage + c);
+            for (int j = 0; j < kTL; j++) fl[kk][j] = l.at(j, kk);
 #pragma unroll
-            for (int i = 0; i < kTR; i++) fr[kk][i] = *reinterpret_cast<const v4i*>(pr + i * 16 * kStage + c);
+            for (int i = 0; i < kTR; i++) fr[kk][i] = r.at(i, kk);
         }
 #pragma unroll
         for (int kk = 0; kk < 2; kk++)
@@ -201,15 +298,15 @@ struct RowProduct {
             for (int i = 0; i < kTR; i++)
 #pragma unroll
                 for (int j = 0; j < kTL; j++) acc[i][j] = Mma<T>::run(fr[kk][i], fl[kk][j], acc[i][j]);
-        constexpr int kRead = 0x100, kMfma = 0x8, kReads = 2 * (kTL + kTR);
-        __builtin_amdgcn_sched_group_barrier(kRead, kTL + 1, 0);
+        constexpr int kRead = 0x100, kMfma = 0x8, nl = Fragments<BL, LL>::kReads, nr = Fragments<BR, LR>::kReads;
+        __builtin_amdgcn_sched_group_barrier(kRead, kTL * nl + nr, 0);
 #pragma unroll
         for (int q = 0; q < kTR - 1; q++) {
             __builtin_amdgcn_sched_group_barrier(kMfma, kTL, 0);
-            __builtin_amdgcn_sched_group_barrier(kRead, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(kRead, 2 * nr, 0);
         }
         __builtin_amdgcn_sched_group_barrier(kMfma, kTL, 0);
-        __builtin_amdgcn_sched_group_barrier(kRead, kReads - (kTL + 1) - 2 * (kTR - 1), 0);
+        __builtin_amdgcn_sched_group_barrier(kRead, kTL * nl + nr, 0);
         __builtin_amdgcn_sched_group_barrier(kMfma, kTR * kTL, 0);
     }
 
@@ -252,8 +349,8 @@ struct RowProduct {
         const int lane = threadIdx.x % kWave;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
         const int wl = wave % WL, wr = wave / WL;
-        std::conditional_t<DIRECT, DirectStage<T, BL, kWaves>, ThroughStage<T, BL, kWaves>> sl;
-        std::conditional_t<DIRECT, DirectStage<T, BR, kWaves>, ThroughStage<T, BR, kWaves>> sr;
+        typename StageOf<T, BL, kWaves, LL>::type sl;
+        typename StageOf<T, BR, kWaves, LR>::type sr;
         sl.init(a.l, a.ld_l, l0, a.nl, wave, lane);
         sr.init(a.r, a.ld_r, r0, a.nr, wave, lane);
 #pragma unroll
@@ -276,12 +373,12 @@ struct RowProduct {
                 sl.load(next, k + kStage, kend, wave);
                 sr.load(next + BL * kStage, k + kStage, kend, wave);
             }
-            const char* pl = lds + buf * (BL + BR) * kStage + (wl * (BL / WL) + row) * kStage;
-            const char* pr = lds + buf * (BL + BR) * kStage + (BL + wr * (BR / WR) + row) * kStage;
+            const char* pl = lds + buf * (BL + BR) * kStage;
+            const char* pr = pl + BL * kStage;
             if constexpr (sizeof(T) == 4)
-                wide(pl, pr, row, quad, acc);
+                wide(pl + (wl * (BL / WL) + row) * kStage, pr + (wr * (BR / WR) + row) * kStage, row, quad, acc);
             else
-                narrow(pl, pr, row, quad, acc);
+                narrow({pl, wl * (BL / WL), lane}, {pr, wr * (BR / WR), lane}, acc);
             if (k + kStage < kend) {
                 sl.keep(next, wave, lane);
                 sr.keep(next + BL * kStage, wave, lane);
