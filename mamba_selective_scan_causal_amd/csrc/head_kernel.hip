@@ -69,8 +69,9 @@ struct Tag {
 // f(Tag of the shape's RowProduct).  Through registers kTall and kWide are slower than
 // the other shapes, and so is kLarge in fp32 (its registers spill).  FEW: where kFew may
 // be the shape.
-// (A column product has the shapes whose columns are groups of 128.)
-constexpr bool has_columns(int shape) { return shape == kLarge || shape == kSmall; }
+// A column product has the shapes whose columns are groups of 128, without kLarge in
+// fp32 (spills too).
+constexpr bool has_columns(int shape, int64_t elem) { return shape == kSmall || (shape == kLarge && elem == 2); }
 constexpr bool has_tile(int shape, bool direct, int64_t elem) {
     return direct || shape == kSmall || shape == kFew || (shape == kLarge && elem == 2);
 }
@@ -101,6 +102,7 @@ struct Shape<RowProduct<T, BL_, BR_, WL_, WR_, LL, LR>> {
     using columns = RowProduct<T, BL_, BR_, WL_, WR_, kDirect, kColumns>;
     static constexpr int BL = BL_, BR = BR_, WL = WL_, WR = WR_;
     static constexpr int kSlab = BR / WR;    // columns of one wave
+    static constexpr bool kDirectRows = LL == kDirect;
     static constexpr int kShape = BL == 256 ? kLarge : BL == 192 ? kTall : BL == 32 ? kFew : BR == 160 ? kWide : kSmall;
 };
 
@@ -381,23 +383,28 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
     static_assert(P::kWaves * kStore <= P::kLds, "stored through the stages' LDS");
     __shared__ __align__(1024) char lds[P::kLds];
     const Part<P> at(a, blockIdx.x, gridDim.x);
-    // read ahead of the product
     int hit[P::kTL];
     bool on[P::kTL];
     float up[P::kTL], own[P::kTL], lse2[P::kTL];
+    const auto read_rows = [&] {
 #pragma unroll
-    for (int j = 0; j < P::kTL; j++) {
-        const int64_t m = at.l + 16 * j;
-        const bool in = m < a.nl;
-        const int t = in ? h.g.t[m] : -1;
-        on[j] = t >= 0;
-        hit[j] = at.place(t - h.first);
-        up[j] = in ? h.g.a[m] : 0.0f;
-        own[j] = in ? h.g.b[m] : 0.0f;
-        lse2[j] = in ? h.g.lse2[m] : 0.0f;
-    }
+        for (int j = 0; j < P::kTL; j++) {
+            const int64_t m = at.l + 16 * j;
+            const bool in = m < a.nl;
+            const int t = in ? h.g.t[m] : -1;
+            on[j] = t >= 0;
+            hit[j] = at.place(t - h.first);
+            up[j] = in ? h.g.a[m] : 0.0f;
+            own[j] = in ? h.g.b[m] : 0.0f;
+            lse2[j] = in ? h.g.lse2[m] : 0.0f;
+        }
+    };
+    // ahead of the product where its registers leave room
+    constexpr bool kAhead = sizeof(T) == 2 && Shape<P>::kDirectRows;
+    if constexpr (kAhead) read_rows();
     v4f acc[P::kTR][P::kTL];
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
+    if constexpr (!kAhead) read_rows();
     const bool whole = at.rw + 16 * P::kTR <= a.nr;
 #pragma unroll
     for (int j = 0; j < P::kTL; j++) {
@@ -568,10 +575,10 @@ Choice product_us(int64_t elem, int64_t nl, int64_t nr, int64_t k, bool direct =
 Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split, bool columns) {
     Choice best{0, -1};
     for (int shape = 0; shape < kFew; shape++) {
-        if (columns && !has_columns(shape)) continue;
+        if (columns && !has_columns(shape, elem)) continue;
         const TileCost c = tile_cost(shape, elem);
         const int64_t wide = ceil_div(D, c.nr), x = ceil_div(M, c.nl) * wide * split, w = ceil_div(n, c.nl) * wide;
-        const double ux = (columns ? 1.35 : 1.0) * c.each * n / split + c.fixed, uw = c.each * M + c.fixed;
+        const double ux = (!columns ? 1.0 : elem == 2 ? 1.35 : 2.3) * c.each * n / split + c.fixed, uw = c.each * M + c.fixed;
         const double us = ux >= uw ? spread(c.slots, x, ux, w, uw) : spread(c.slots, w, uw, x, ux);
         if (best.shape < 0 || us < best.us) best = {us, shape};
     }
@@ -583,10 +590,12 @@ Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split
 // (bf16, V32768, forward: M8192 D1535 873 us through registers, 675 + 45 copied;
 // M2048 D769 151 and 120 + 25; fp16 M1551 V10007 D1001 85 and 61 + 13).
 constexpr int64_t kCopyRows = 1024;
-// Below as many rows dx's product reads W as it lies, down its columns, in two-byte
-// types: slower, but W is not transposed first (bf16, both gradients: M16 V65536 D2560
+// Below as many rows dx's product reads W as it lies, down its columns: slower, but W
+// is not transposed first (bf16, both gradients: M16 V65536 D2560
 // 297 us against 424, M517 V50021 D1536 387 and 399, M1000 V32768 D1536 370 and 391).
-constexpr int64_t kColumnRows = 1024;
+// In fp32 its 4-byte LDS reads take 2.3 times as long: below 256 rows (M128 V65536 D2560
+// 926 us against 1121, M517 V50021 D1536 1784 and 1598).
+constexpr int64_t kColumnRows = 1024, kColumnRowsWide = 256;
 
 struct Plan {
     bool copied, columns;     // columns: where W's rows lie at multiples of 16 bytes
@@ -605,7 +614,7 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
     p = Plan{};
     p.copied = D * e % 16 != 0 && M >= kCopyRows;
     p.Dk = p.copied ? align_up(D, 16 / e) : D;
-    p.columns = e == 2 && M < kColumnRows && D * e % 16 == 0;
+    p.columns = M < (e == 2 ? kColumnRows : kColumnRowsWide) && D * e % 16 == 0;
     p.ld_m = align_up(M, kPadRows);
     bool fits = true;
     const auto take = [&](int64_t a, int64_t b, int64_t c) {
@@ -799,7 +808,7 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
         with_tile<T, true, false>(shape, [&](auto tag) {
             using P = typename decltype(tag)::type;
             const uint32_t grid = static_cast<uint32_t>(nx + nw);
-            if constexpr (sizeof(T) == 2 && has_columns(Shape<P>::kShape))
+            if constexpr (has_columns(Shape<P>::kShape, sizeof(T)))
                 if (columns) return head_grad_kernel<P, true><<<grid, P::kThreads, 0, st>>>(two);
             head_grad_kernel<P, false><<<grid, P::kThreads, 0, st>>>(two);
         });

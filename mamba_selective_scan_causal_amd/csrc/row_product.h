@@ -55,7 +55,8 @@ struct Mma<f16> {
 // splitting (M2048 V32768 D768: 211 TFLOP/s against 139 with the fp32 instruction).
 struct Parts {
     v4i p[3];
-    __device__ __forceinline__ void of(v4f a, v4f b) {
+    __device__ __forceinline__ void of(v4i a_, v4i b_) {
+        const v4f a = __builtin_bit_cast(v4f, a_), b = __builtin_bit_cast(v4f, b_);
         float v[8];
 #pragma unroll
         for (int e = 0; e < 4; e++) v[e] = a[e], v[4 + e] = b[e];
@@ -167,39 +168,44 @@ struct ThroughStage : StageRows<ROWS, WAVES> {
     }
 };
 
-// A stage of COLS columns of an operand that lies with K down its rows (two-byte
-// types): 64 rows of the tile's columns, straight to LDS.  Row k's 32 bytes at
-// columns 16 b lie at block b ^ swap(k): the eight rows that half a wave reads at one b
-// are then on different banks.
-__device__ __forceinline__ int swap_of(int k) { return (k & 3) | (k >> 1 & 4); }
+// A stage of COLS columns of an operand that lies with K down its rows: 128 bytes'
+// worth of rows of the tile's columns, straight to LDS.  Row k's values at columns
+// 16 b .. 16 b + 15 lie at block b ^ swap(k): the rows that are read at one b at one
+// time (eight by half a wave in two-byte types, four by a wave in fp32) are then on
+// different banks.
+template <typename T>
+__device__ __forceinline__ int swap_of(int k) {
+    return sizeof(T) == 2 ? (k & 3) | (k >> 1 & 4) : k >> 2 & 3;
+}
 
 template <typename T, int COLS, int WAVES>
 struct ColumnStage {
-    static_assert(sizeof(T) == 2 && COLS % 128 == 0, "whole groups of eight blocks");
-    static constexpr int kLoads = COLS / 8 / WAVES, kPitch = COLS * 2, kDown = 1024 / kPitch;   // rows of a load
+    static_assert(COLS % 128 == 0, "whole groups of blocks");
+    static constexpr int kSize = sizeof(T), kLoads = COLS / 8 / WAVES, kPitch = COLS * kSize;
+    static constexpr int kDown = 1024 / kPitch;                 // rows of a load
     const char* p;
     int64_t ld;
     int first;                // this lane's row of the wave's first load
     bool in[kLoads];          // whether its columns are the operand's
     int64_t at[kLoads];       // bytes from p
 
-    // n columns, a multiple of 8, at multiples of 16 bytes.
+    // n columns, whole pieces of 16 bytes, at multiples of 16 bytes.
     __device__ __forceinline__ void init(const char* base, int64_t ld_, int64_t col0, int64_t n, int wave, int lane) {
-        p = base + col0 * 2;
+        p = base + col0 * kSize;
         ld = ld_;
         const int piece = lane * 16 % kPitch / 16;
         first = wave * kDown + lane * 16 / kPitch;
 #pragma unroll
         for (int s = 0; s < kLoads; s++) {
             const int k = first + s * WAVES * kDown;
-            const int col = ((piece / 2) ^ swap_of(k)) * 16 + piece % 2 * 8;
+            const int col = ((piece / kSize) ^ swap_of<T>(k)) * 16 + piece % kSize * (16 / kSize);
             in[s] = col0 + col < n;
-            at[s] = k * ld + col * 2;
+            at[s] = k * ld + col * kSize;
         }
     }
-    // The 64 rows that start at byte k of what would be a row; zeros past kbytes.
+    // The rows that start at byte k of what would be a row; zeros past kbytes.
     __device__ __forceinline__ void load(char* lds, int64_t k, int64_t kbytes, int wave) {
-        const int64_t row = k / 2, rows = kbytes / 2;
+        const int64_t row = k / kSize, rows = kbytes / kSize;
         const char* base = p + row * ld;
 #pragma unroll
         for (int s = 0; s < kLoads; s++) {
@@ -228,11 +234,10 @@ struct StageOf<T, ROWS, WAVES, kColumns> {
     using type = ColumnStage<T, ROWS, WAVES>;
 };
 
-// A lane's fragments of an operand's stage in LDS, in two-byte types: of tile i (16
-// rows of the operand from `first` on) and of half kk of the stage, K = 8 (lane / 16)
-// + 0..7 of its 32.  Columns are read with the transposing load: of 16 lanes, lane
-// l reads 8 bytes of row l / 4, and gets column l of the four rows.
-template <int ROWS, Layout LAYOUT>
+// A lane's part of an operand's stage in LDS: of tile i (16 rows of the operand
+// from `first` on), 16 bytes of the row lane % 16.  In two-byte types those are K =
+// 8 (lane / 16) + 0..7 of half kk of the stage, in fp32 4 (lane / 16) + 0..3.
+template <typename T, int ROWS, Layout LAYOUT>
 struct Fragments {
     static constexpr int kReads = 1;
     const char* p;
@@ -243,8 +248,10 @@ struct Fragments {
         return *reinterpret_cast<const v4i*>(p + i * 16 * kStage + (c ^ kk * 64));
     }
 };
-template <int ROWS>
-struct Fragments<ROWS, kColumns> {
+// Columns of two-byte types are read with the transposing load: of 16 lanes, lane l
+// reads 8 bytes of row l / 4, and gets column l of the four rows.
+template <typename T, int ROWS>
+struct Fragments<T, ROWS, kColumns> {
     typedef short v4s __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) v4s* lds4;
     static constexpr int kReads = 2, kPitch = ROWS * 2;
@@ -253,7 +260,7 @@ struct Fragments<ROWS, kColumns> {
     __device__ __forceinline__ Fragments(const char* stage, int first, int lane)
         : p(stage + (lane / 16 * 8 + lane % 16 / 4) * kPitch + lane % 4 * 8),
           block(first / 16),
-          swap(swap_of(lane / 16 * 8 + lane % 16 / 4)) {}
+          swap(swap_of<T>(lane / 16 * 8 + lane % 16 / 4)) {}
     __device__ __forceinline__ v4i at(int i, int kk) const {
         const char* q = p + ((block + i) ^ swap) * 32 + kk * 32 * kPitch;
         struct {
@@ -261,6 +268,21 @@ struct Fragments<ROWS, kColumns> {
         } both = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)q),
                   __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(q + 4 * kPitch))};
         return __builtin_bit_cast(v4i, both);
+    }
+};
+template <int ROWS>
+struct Fragments<float, ROWS, kColumns> {
+    static constexpr int kPitch = ROWS * 4;
+    const char* p;
+    int block, swap;
+    __device__ __forceinline__ Fragments(const char* stage, int first, int lane)
+        : p(stage + lane / 16 * 4 * kPitch + lane % 16 * 4), block(first / 16), swap(lane / 16) {}
+    __device__ __forceinline__ v4i at(int i, int kk) const {
+        const char* q = p + ((block + i) ^ swap) * 64 + kk * 16 * kPitch;
+        v4i v;
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = *reinterpret_cast<const int*>(q + e * kPitch);
+        return v;
     }
 };
 
@@ -282,7 +304,7 @@ struct RowProduct {
     // first is multiplied.  (Left to the compiler, with a wait after every two
     // reads: 1277 against 1316 TFLOP/s at 8192^3 in bf16; one read for two
     // products, or three for four, 1315 and 1298.)
-    static __device__ __forceinline__ void narrow(const Fragments<BL, LL>& l, const Fragments<BR, LR>& r,
+    static __device__ __forceinline__ void narrow(const Fragments<T, BL, LL>& l, const Fragments<T, BR, LR>& r,
                                                   v4f (&acc)[kTR][kTL]) {
         v4i fl[2][kTL], fr[2][kTR];
 #pragma unroll
@@ -298,7 +320,8 @@ struct RowProduct {
             for (int i = 0; i < kTR; i++)
 #pragma unroll
                 for (int j = 0; j < kTL; j++) acc[i][j] = Mma<T>::run(fr[kk][i], fl[kk][j], acc[i][j]);
-        constexpr int kRead = 0x100, kMfma = 0x8, nl = Fragments<BL, LL>::kReads, nr = Fragments<BR, LR>::kReads;
+        constexpr int kRead = 0x100, kMfma = 0x8, nl = Fragments<T, BL, LL>::kReads;
+        constexpr int nr = Fragments<T, BR, LR>::kReads;
         __builtin_amdgcn_sched_group_barrier(kRead, kTL * nl + nr, 0);
 #pragma unroll
         for (int q = 0; q < kTR - 1; q++) {
@@ -312,22 +335,16 @@ struct RowProduct {
 
     // The same in fp32: L's fragments are split once for the stage, R's one by one,
     // ahead of the products of the one before.
-    static __device__ __forceinline__ void wide(const char* pl, const char* pr, int row, int quad,
+    static __device__ __forceinline__ void wide(const Fragments<T, BL, LL>& l, const Fragments<T, BR, LR>& r,
                                                 v4f (&acc)[kTR][kTL]) {
-        const int c0 = (quad ^ (row & 7)) * 16, c1 = c0 ^ 64;
-        const auto part = [&](const char* p) {
-            Parts f;
-            f.of(*reinterpret_cast<const v4f*>(p + c0), *reinterpret_cast<const v4f*>(p + c1));
-            return f;
-        };
-        Parts fl[kTL];
+        Parts fl[kTL], fr;
 #pragma unroll
-        for (int j = 0; j < kTL; j++) fl[j] = part(pl + j * 16 * kStage);
-        Parts fr = part(pr);
+        for (int j = 0; j < kTL; j++) fl[j].of(l.at(j, 0), l.at(j, 1));
+        fr.of(r.at(0, 0), r.at(0, 1));
 #pragma unroll
         for (int i = 0; i < kTR; i++) {
             Parts next;
-            if (i + 1 < kTR) next = part(pr + (i + 1) * 16 * kStage);
+            if (i + 1 < kTR) next.of(r.at(i + 1, 0), r.at(i + 1, 1));
             // small products first; the sum of 32 values of K is rounded to acc's size once
             v4f sums[kTL];
 #pragma unroll
@@ -363,7 +380,6 @@ struct RowProduct {
         sl.keep(lds, wave, lane);
         sr.keep(lds + BL * kStage, wave, lane);
         int buf = 0;
-        const int row = lane % 16, quad = lane / 16;
         for (int64_t k = kbegin; k < kend; k += kStage) {
             // this stage has landed for every wave, and every wave has read the other one
             __builtin_amdgcn_s_waitcnt(kNoLoads);
@@ -376,7 +392,7 @@ struct RowProduct {
             const char* pl = lds + buf * (BL + BR) * kStage;
             const char* pr = pl + BL * kStage;
             if constexpr (sizeof(T) == 4)
-                wide(pl + (wl * (BL / WL) + row) * kStage, pr + (wr * (BR / WR) + row) * kStage, row, quad, acc);
+                wide({pl, wl * (BL / WL), lane}, {pr, wr * (BR / WR), lane}, acc);
             else
                 narrow({pl, wl * (BL / WL), lane}, {pr, wr * (BR / WR), lane}, acc);
             if (k + kStage < kend) {
