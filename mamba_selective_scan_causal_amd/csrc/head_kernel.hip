@@ -172,30 +172,44 @@ __global__ __launch_bounds__(P::kThreads) void head_loss_kernel(ProductArgs a, L
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
     if (at.rw >= a.nr) return;
     const bool whole = at.rw + S::kSlab <= a.nr;
-    const int valid = static_cast<int>(a.nr - at.rw) - (at.r - at.rw);       // from the lane's r on, where not whole
+    float c = h.c;
+    // c > 0 below, and every value counts: the few waves that are not so make it so
+    if (!whole || c <= 0.0f) {
+        const int valid = whole ? S::kSlab : static_cast<int>(a.nr - at.r);       // from the lane's r on
+#pragma unroll
+        for (int j = 0; j < P::kTL; j++)
+#pragma unroll
+            for (int i = 0; i < P::kTR; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[i][j][e] = 16 * i + e < valid ? acc[i][j][e] * c : -INFINITY;
+        c = 1.0f;
+    }
 #pragma unroll
     for (int j = 0; j < P::kTL; j++) {
         const int64_t m = at.l + 16 * j;
         const bool in = m < a.nl;
         const int64_t v = in ? target_of(h.targets, h.wide, h.m0 + m) - h.first : -1;
-        const int hit = at.place(v);
-        float top = -INFINITY, own = 0.0f;
+        float top = acc[0][j][0];
 #pragma unroll
         for (int i = 0; i < P::kTR; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float l = whole || 16 * i + e < valid ? acc[i][j][e] * h.c : -INFINITY;
-                acc[i][j][e] = l;
-                top = __builtin_fmaxf(top, l);
-                own = hit == 16 * i + e ? l : own;
-            }
-        if (at.holds(v, a.nr)) h.at_target[h.m0 + m] = own;
-        top = over_quads_max(top);
+            for (int e = 0; e < 4; e++) top = __builtin_fmaxf(top, acc[i][j][e]);
+        top = over_quads_max(top) * c;
+        // one wave in V / kSlab has a row's target
+        if (const bool here = at.holds(v, a.nr); wave_any(here)) {
+            const int hit = at.place(v);
+            float own = 0.0f;
+#pragma unroll
+            for (int i = 0; i < P::kTR; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) own = hit == 16 * i + e ? acc[i][j][e] : own;
+            if (here) h.at_target[h.m0 + m] = own * c;
+        }
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < P::kTR; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) sum += ex2(acc[i][j][e] - top);
+            for (int e = 0; e < 4; e++) sum += ex2(__builtin_fmaf(acc[i][j][e], c, -top));
         sum = over_quads_sum(sum);
         if (at.lane < 16 && in) h.part[at.rw / S::kSlab * a.nl + m] = make_float2(top, sum);
     }
@@ -384,16 +398,13 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
     __shared__ __align__(1024) char lds[P::kLds];
     const Part<P> at(a, blockIdx.x, gridDim.x);
     int hit[P::kTL];
-    bool on[P::kTL];
     float up[P::kTL], own[P::kTL], lse2[P::kTL];
     const auto read_rows = [&] {
 #pragma unroll
         for (int j = 0; j < P::kTL; j++) {
             const int64_t m = at.l + 16 * j;
             const bool in = m < a.nl;
-            const int t = in ? h.g.t[m] : -1;
-            on[j] = t >= 0;
-            hit[j] = at.place(t - h.first);
+            hit[j] = at.place((in ? h.g.t[m] : -1) - h.first);
             up[j] = in ? h.g.a[m] : 0.0f;
             own[j] = in ? h.g.b[m] : 0.0f;
             lse2[j] = in ? h.g.lse2[m] : 0.0f;
@@ -405,17 +416,29 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
     v4f acc[P::kTR][P::kTL];
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
     if constexpr (!kAhead) read_rows();
-    const bool whole = at.rw + 16 * P::kTR <= a.nr;
+    // a padded row's x counts as zeros (ProductArgs::off) and its up is 0: so is its dl
 #pragma unroll
     for (int j = 0; j < P::kTL; j++) {
 #pragma unroll
         for (int i = 0; i < P::kTR; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                float p = ex2(__builtin_fmaf(acc[i][j][e], h.c, -lse2[j])) * up[j];
-                p = hit[j] == 16 * i + e ? p - own[j] : p;
-                acc[i][j][e] = on[j] && (whole || at.r + 16 * i + e < a.nr) ? p : 0.0f;
-            }
+            for (int e = 0; e < 4; e++) acc[i][j][e] = ex2(__builtin_fmaf(acc[i][j][e], h.c, -lse2[j])) * up[j];
+        if (wave_any(hit[j] >= 0)) {
+#pragma unroll
+            for (int i = 0; i < P::kTR; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[i][j][e] -= hit[j] == 16 * i + e ? own[j] : 0.0f;
+        }
+    }
+    if (at.rw + 16 * P::kTR > a.nr || at.lw + 16 * P::kTL > a.nl) {
+        // zeros past the piece and past the rows, where the last ones were read again
+#pragma unroll
+        for (int j = 0; j < P::kTL; j++)
+#pragma unroll
+            for (int i = 0; i < P::kTR; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (at.r + 16 * i + e >= a.nr || at.l + 16 * j >= a.nl) acc[i][j][e] = 0.0f;
     }
     const auto get = [&](int i, int j) {
         quad v;
@@ -687,10 +710,10 @@ hipError_t by_type(int dtype, F&& f) {
 }
 
 ProductArgs product(const void* l, int64_t ld_l, int64_t nl, const void* r, int64_t ld_r, int64_t nr, int64_t kbytes,
-                    int shape) {
+                    int shape, const int* off = nullptr) {
     const TileCost t = tile_cost(shape, 2);
-    return {static_cast<const char*>(l), static_cast<const char*>(r), ld_l, ld_r, nl, nr, kbytes, ceil_div(nl, t.nl),
-            ceil_div(nr, t.nr)};
+    return {static_cast<const char*>(l), static_cast<const char*>(r), ld_l, ld_r, nl, nr, kbytes, off,
+            ceil_div(nl, t.nl), ceil_div(nr, t.nr)};
 }
 
 // Whether rows of a product's operand can go straight to LDS.
@@ -784,7 +807,7 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
         int64_t ld_w = h.ld_w;
         if (hipError_t r = rows_of(p, w, ld_w, n, D, ws + p.w, st)) return r;
         int shape = product_us(e, M, n, D, straight).shape;
-        const ProductArgs a = product(x, ld_x * e, M, w, ld_w * e, n, p.Dk * e, shape);
+        const ProductArgs a = product(x, ld_x * e, M, w, ld_w * e, n, p.Dk * e, shape, g.t);
         const DlArgs d{h.logit_scale * kLog2e, v0, g, dl, dlt, ld_n, p.ld_m};
         with_tile<T>(shape, straight, [&](auto tag) {
             using P = typename decltype(tag)::type;

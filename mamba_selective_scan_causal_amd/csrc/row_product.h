@@ -80,6 +80,7 @@ struct ProductArgs {
     int64_t ld_l, ld_r;       // bytes
     int64_t nl, nr;           // rows of each (at least 1)
     int64_t kbytes;           // bytes of a row that count
+    const int* off;           // rows of l that count as zeros: off[row] < 0 (null: none)
     int64_t tiles_l, tiles_r;
 };
 
@@ -110,8 +111,10 @@ struct StageRows {
     static constexpr int kLoads = ROWS / 8 / WAVES;
     const char* p[kLoads];
     int64_t at;               // this lane's byte of the row
+    bool on[kLoads];          // whether the row counts
 
-    __device__ __forceinline__ void init(const char* base, int64_t ld, int64_t row0, int64_t n, int wave, int lane) {
+    __device__ __forceinline__ void init(const char* base, int64_t ld, int64_t row0, int64_t n, int wave, int lane,
+                                         const int* off) {
         at = ((lane & 7) ^ (lane >> 3)) * 16;
 #pragma unroll
         for (int s = 0; s < kLoads; s++) {
@@ -119,6 +122,7 @@ struct StageRows {
             int64_t row = row0 + (s * WAVES + wave) * 8 + (lane >> 3);
             row = row < n ? row : n - 1;
             p[s] = base + row * ld;
+            on[s] = !off || off[row] >= 0;
         }
     }
     static __device__ __forceinline__ char* place(char* lds, int s, int wave) { return lds + (s * WAVES + wave) * 1024; }
@@ -135,7 +139,7 @@ struct DirectStage : StageRows<ROWS, WAVES> {
         const bool in = k + this->at < kbytes;
 #pragma unroll
         for (int s = 0; s < Rows::kLoads; s++) {
-            const char* q = in ? this->p[s] + k + this->at : reinterpret_cast<const char*>(&kZeros);
+            const char* q = in && this->on[s] ? this->p[s] + k + this->at : reinterpret_cast<const char*>(&kZeros);
             __builtin_amdgcn_global_load_lds((gmem)q, (lmem)Rows::place(lds, s, wave), 16, 0, 0);
         }
     }
@@ -164,7 +168,8 @@ struct ThroughStage : StageRows<ROWS, WAVES> {
     __device__ __forceinline__ void keep(char* lds, int wave, int lane) {
 #pragma unroll
         for (int s = 0; s < Rows::kLoads; s++)
-            *reinterpret_cast<v4i*>(Rows::place(lds, s, wave) + lane * 16) = __builtin_bit_cast(v4i, r[s].t);
+            *reinterpret_cast<v4i*>(Rows::place(lds, s, wave) + lane * 16) =
+                this->on[s] ? __builtin_bit_cast(v4i, r[s].t) : v4i{0, 0, 0, 0};
     }
 };
 
@@ -190,7 +195,8 @@ struct ColumnStage {
     int64_t at[kLoads];       // bytes from p
 
     // n columns, whole pieces of 16 bytes, at multiples of 16 bytes.
-    __device__ __forceinline__ void init(const char* base, int64_t ld_, int64_t col0, int64_t n, int wave, int lane) {
+    __device__ __forceinline__ void init(const char* base, int64_t ld_, int64_t col0, int64_t n, int wave, int lane,
+                                         const int*) {
         p = base + col0 * kSize;
         ld = ld_;
         const int piece = lane * 16 % kPitch / 16;
@@ -368,8 +374,8 @@ struct RowProduct {
         const int wl = wave % WL, wr = wave / WL;
         typename StageOf<T, BL, kWaves, LL>::type sl;
         typename StageOf<T, BR, kWaves, LR>::type sr;
-        sl.init(a.l, a.ld_l, l0, a.nl, wave, lane);
-        sr.init(a.r, a.ld_r, r0, a.nr, wave, lane);
+        sl.init(a.l, a.ld_l, l0, a.nl, wave, lane, a.off);
+        sr.init(a.r, a.ld_r, r0, a.nr, wave, lane, nullptr);
 #pragma unroll
         for (int i = 0; i < kTR; i++)
 #pragma unroll
