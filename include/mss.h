@@ -603,7 +603,7 @@ typedef struct mss_head_dims {
     int32_t flags;          /* must be 0 */
     int32_t dtype;          /* of x, weight and their gradients */
     int32_t id_bytes;       /* of the targets: 4 or 8 */
-    int64_t rows;           /* M, below 2^26 */
+    int64_t rows;           /* M, below 2^26; backward: M D below about 2^36 as well */
     int64_t vocab;          /* V, 1 .. 2^26 - 1 */
     int64_t width;          /* D, 1 .. MSS_MAX_WIDTH */
     float logit_scale;      /* finite */
@@ -627,7 +627,9 @@ int mss_head_workspace_bytes(const mss_head_dims* dims, int op, size_t* bytes);
  *   lse_m  = log sum_v exp(l_mv)
  *   loss_m = lse_m - l_{m, t_m}; 0 where t_m marks a padded place
  *   x (M, D), weight (V, D) dtype;  targets (M);  loss, lse (M) fp32
- * Logits are sums of exact products in fp32.                               */
+ * Logits are fp32 sums of exact products of 2-byte operands.  fp32 operands
+ * are split in three parts of 8 bits each, and of their nine products the six
+ * largest are summed: what is left out is below 2^-21 of each product.      */
 int mss_head_loss(const mss_head_dims* dims, const mss_head_strides* strides, const void* x,
                   const void* weight, const void* targets, float* loss, float* lse,
                   void* workspace, size_t workspace_bytes, hipStream_t stream);
@@ -638,9 +640,10 @@ int mss_head_loss(const mss_head_dims* dims, const mss_head_strides* strides, co
  *   dx = logit_scale dl weight,  dweight = logit_scale dl^T x
  * A padded row takes no part: its dx is 0, and its x, dloss and dlse are not
  * used (they may be NaN).  dl is computed a piece of the vocabulary at a time
- * and held in dtype for the two products, times a power of two that brings
- * the largest |dloss| + |dlse| near 2^13 (so that fp16 does not lose the
- * small ones): in 2-byte types each of its values is rounded once.
+ * and held in dtype for the two products, times a factor that brings the
+ * largest |dloss| + |dlse| to just below 2^13 (fp16 would lose the small
+ * ones, and bf16 rounds least there): in 2-byte types each of its values is
+ * rounded once.  dx and dweight are summed in fp32.
  *   dx (M, D), dweight (V, D) dtype: each computed where given.            */
 int mss_head_loss_backward(const mss_head_dims* dims, const mss_head_strides* strides,
                            const void* x, const void* weight, const void* targets,

@@ -270,18 +270,24 @@ __global__ __launch_bounds__(256) void head_join_kernel(JoinArgs h) {
 
 // ---- copies ---------------------------------------------------------------------
 
+// A wave to a row, four waves to a workgroup, workgroups in turn where there are more rows.
+__device__ __forceinline__ int64_t first_row() { return blockIdx.x * int64_t{4} + threadIdx.x / kWave; }
+__device__ __forceinline__ int64_t rows_apart() { return gridDim.x * int64_t{4}; }
+uint32_t row_groups(int64_t rows) {
+    return static_cast<uint32_t>(rows < (int64_t{1} << 22) ? ceil_div(rows, 4) : int64_t{1} << 20);
+}
+
 // Rows of n values to rows of ld_out values, zeros behind.
 template <typename T>
 __global__ __launch_bounds__(256) void pad_rows_kernel(const T* in, int64_t ld_in, int64_t rows, int64_t n, T* out,
                                                        int64_t ld_out) {
     constexpr int V = 16 / sizeof(T);           // ld_out is a multiple
-    const int64_t row = blockIdx.x * int64_t{4} + threadIdx.x / kWave;
-    if (row >= rows) return;
-    for (int64_t c = threadIdx.x % kWave * V; c < ld_out; c += kWave * V) {
-        RowVec<T, V> v;
-        v.load(in + row * ld_in, static_cast<int>(c), static_cast<int>(n));
-        v.template store<false>(out + row * ld_out + c, 0, V);
-    }
+    for (int64_t row = first_row(); row < rows; row += rows_apart())
+        for (int64_t c = threadIdx.x % kWave * V; c < ld_out; c += kWave * V) {
+            RowVec<T, V> v;
+            v.load(in + row * ld_in, static_cast<int>(c), static_cast<int>(n));
+            v.template store<false>(out + row * ld_out + c, 0, V);
+        }
 }
 
 // in (rows, n) to out (n, ld_out), ld_out >= rows, zeros behind and in the
@@ -332,18 +338,30 @@ struct RowGrads {
 
 constexpr float kMostDl = 8190.0f;       // rounds to less than 2^13 in every type
 
-// Each workgroup finds the largest factor of all rows for itself (12 to 16 bytes
-// a row, from L2) and writes 1024 rows: one launch, and no wait between workgroups.
-__global__ __launch_bounds__(1024) void row_grads_kernel(HeadArgs h, RowGrads g) {
+constexpr int kTops = 256;
+constexpr int64_t kRowsEach = 16384;
+
+// Of a workgroup's 1024 threads.
+__device__ __forceinline__ float largest_of_all(float top, float* most) {
+    for (int d = 32; d > 0; d /= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    if (threadIdx.x % kWave == 0) most[threadIdx.x / kWave] = top;
+    __syncthreads();
+    for (int w = 0; w < 16; w++) top = __builtin_fmaxf(top, most[w]);
+    return top;
+}
+
+// The largest |dloss| + |dlse| of the rows that count, for all threads of the workgroup:
+// the `first` 1024 rows and every `apart` times 1024 behind them.
+__device__ __forceinline__ float largest(const HeadArgs& h, int64_t first, int64_t apart) {
     constexpr int kAhead = 8;
     __shared__ float most[16];
     float top = 0.0f;
-    for (int64_t m0 = threadIdx.x; m0 < h.M; m0 += 1024 * kAhead) {
+    for (int64_t m0 = first * 1024 + threadIdx.x; m0 < h.M; m0 += 1024 * kAhead * apart) {
         int64_t t[kAhead];
         float up[kAhead], more[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; i++) {
-            const int64_t m = m0 + 1024 * i;
+            const int64_t m = m0 + 1024 * apart * i;
             const bool in = m < h.M;
             t[i] = in ? target_of(h.targets, h.wide_ids, m) : -1;
             up[i] = in ? h.dloss[m] : 0.0f;
@@ -354,10 +372,22 @@ __global__ __launch_bounds__(1024) void row_grads_kernel(HeadArgs h, RowGrads g)
             if (t[i] >= 0 && t[i] < h.V)
                 top = __builtin_fmaxf(top, __builtin_fabsf(up[i]) + __builtin_fabsf(more[i]));
     }
-    for (int d = 32; d > 0; d /= 2) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-    if (threadIdx.x % kWave == 0) most[threadIdx.x / kWave] = top;
-    __syncthreads();
-    for (int w = 0; w < 16; w++) top = __builtin_fmaxf(top, most[w]);
+    return largest_of_all(top, most);
+}
+
+// Of many rows, for row_grads_kernel: kTops workgroups leave a value each.
+__global__ __launch_bounds__(1024) void row_tops_kernel(HeadArgs h, float* tops) {
+    const float top = largest(h, blockIdx.x, kTops);
+    if (threadIdx.x == 0) tops[blockIdx.x] = top;
+}
+
+// 1024 rows to a workgroup.  Up to kRowsEach rows each workgroup finds the largest factor
+// of all for itself (12 to 16 bytes a row, from L2): one launch, and no wait between
+// workgroups.  With more it takes it from `tops` (8192 rows: 5.2 us against 3.6 + 3.2 and
+// the launch; 32768: 10.9 and 3.6 + 3.4).
+__global__ __launch_bounds__(1024) void row_grads_kernel(HeadArgs h, RowGrads g, const float* tops) {
+    __shared__ float most[16];
+    const float top = tops ? largest_of_all(threadIdx.x < kTops ? tops[threadIdx.x] : 0.0f, most) : largest(h, 0, 1);
     // 1 where nothing or not a number would come of it; bounded, so that 1 / s is a normal number
     float s = 1.0f;
     if (top > 0.0f && top < INFINITY) s = __builtin_fminf(kMostDl / top, 0x1p120f);
@@ -525,17 +555,16 @@ __global__ __launch_bounds__(P::kThreads) void head_grad_kernel(TwoProducts two)
 template <typename T>
 __global__ __launch_bounds__(256) void head_finish_kernel(const float* acc, int64_t ld_acc, int split, int64_t rows,
                                                           int64_t n, const float* back, T* out, int64_t ld) {
-    const int64_t row = blockIdx.x * int64_t{4} + threadIdx.x / kWave;
-    if (row >= rows) return;
     const float s = back[0];
-    for (int64_t c = threadIdx.x % kWave * 4; c < n; c += kWave * 4) {
-        v4f v = {0, 0, 0, 0};
-        for (int k = 0; k < split; k++) v += *reinterpret_cast<const v4f*>(acc + (k * rows + row) * ld_acc + c);
-        RowVec<T, 4> o;
+    for (int64_t row = first_row(); row < rows; row += rows_apart())
+        for (int64_t c = threadIdx.x % kWave * 4; c < n; c += kWave * 4) {
+            v4f v = {0, 0, 0, 0};
+            for (int k = 0; k < split; k++) v += *reinterpret_cast<const v4f*>(acc + (k * rows + row) * ld_acc + c);
+            RowVec<T, 4> o;
 #pragma unroll
-        for (int e = 0; e < 4; e++) o.set(e, v[e] * s);
-        o.template store<false>(out + row * ld, static_cast<int>(c), static_cast<int>(n));
-    }
+            for (int e = 0; e < 4; e++) o.set(e, v[e] * s);
+            o.template store<false>(out + row * ld, static_cast<int>(c), static_cast<int>(n));
+        }
 }
 
 // ---- plans -------------------------------------------------------------------------
@@ -594,14 +623,16 @@ Choice product_us(int64_t elem, int64_t nl, int64_t nr, int64_t k, bool direct =
     return best;
 }
 
-// dx (M, D) with K = n in `split` parts, and dW (n, D) with K = M.
-Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split, bool columns) {
+// dx (M, D) with K = n in `split` parts, and dW (n, D) with K = M in split_w.
+Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split, int64_t split_w, bool columns) {
     Choice best{0, -1};
     for (int shape = 0; shape < kFew; shape++) {
         if (columns && !has_columns(shape, elem)) continue;
         const TileCost c = tile_cost(shape, elem);
-        const int64_t wide = ceil_div(D, c.nr), x = ceil_div(M, c.nl) * wide * split, w = ceil_div(n, c.nl) * wide;
-        const double ux = (!columns ? 1.0 : elem == 2 ? 1.35 : 2.3) * c.each * n / split + c.fixed, uw = c.each * M + c.fixed;
+        const int64_t wide = ceil_div(D, c.nr), x = ceil_div(M, c.nl) * wide * split,
+                      w = ceil_div(n, c.nl) * wide * split_w;
+        const double ux = (!columns ? 1.0 : elem == 2 ? 1.35 : 2.3) * c.each * n / split + c.fixed,
+                     uw = c.each * M / split_w + c.fixed;
         const double us = ux >= uw ? spread(c.slots, x, ux, w, uw) : spread(c.slots, w, uw, x, ux);
         if (best.shape < 0 || us < best.us) best = {us, shape};
     }
@@ -625,11 +656,11 @@ struct Plan {
     int64_t Dk;               // values in a row that the products read
     int64_t piece;            // vocabulary rows at a time
     int64_t chunk;            // rows at a time (forward)
-    int split;                // of dx's K
-    bool accumulate;          // dx goes through fp32 partial sums
+    int split, split_w;       // parts of dx's K and of dW's
+    bool accumulate;          // dx goes through fp32 partial sums (and dW where split_w > 1)
     int64_t ld_m;             // values in a row of dl^T and x^T
-    int64_t ld_acc;           // and of dx's partial sums
-    int64_t x, w, part, at_target, dl, dlt, xt, wt, acc, rows, bytes;
+    int64_t ld_acc;           // and of the partial sums
+    int64_t x, w, part, at_target, dl, dlt, xt, wt, acc, acc_w, rows, bytes;
 };
 
 bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p) {
@@ -668,26 +699,34 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
         }
         return fits;
     }
-    // The piece, in steps of 256 vocabulary rows, and the parts of dx's K: what takes the least time
-    // by the costs above, the traffic of dx's partial sums (5 TB/s) and launches counted in
+    // The piece, in steps of 256 vocabulary rows, and the parts of both K: what takes the least
+    // time by the costs above, the traffic of the partial sums (5 TB/s) and launches counted in.
+    // dW's K is split where a small vocabulary leaves it few tiles (bf16, M65536 V256 D1024: both
+    // gradients 288 us, with K whole 1085; M4096 V1000 D512 50 and 74).
     const int64_t steps = ceil_div(V, 256);
     int64_t most = kDlBytes / (2 * 256 * e * p.ld_m);
-    most = most < 1 ? 1 : most > 1024 ? 1024 : most > steps ? steps : most;
-    const double pass = 4.0 * M * D / 5e6;          // of dx's sums, one part
+    for (int64_t bound : {int64_t{1024}, steps})
+        if (most > bound) most = bound;
+    if (most < 1) most = 1;
+    const double pass = 4.0 * D / 5e6;              // of a row of sums, one part
     double best = 0;
     const int64_t stride = ceil_div(most, 32);
     for (int64_t n = most; n > 0 && n > most / 3; n -= stride) {
         const int64_t full = steps / n, rest = steps % n, pieces = full + (rest > 0);
+        const int64_t tiles_w = ceil_div(256 * n, 128) * ceil_div(D, 128);
         const double before = full * product_us(e, M, 256 * n, D).us + 10.0 * pieces +
                               (rest ? product_us(e, M, 256 * rest, D).us : 0.0);
-        for (int split : {1, 2, 3, 4, 6, 8, 12, 16}) {
-            if (split > 1 && 256 * n / split < 512) break;
-            const bool sums = split > 1 || pieces > 1;
-            double us = before + full * gradients_us(e, M, 256 * n, D, split, p.columns).us + (sums ? pass * split * 2 * pieces : 0.0);
-            if (best != 0 && us >= best) continue;
-            if (rest) us += gradients_us(e, M, 256 * rest, D, split, p.columns).us;
-            if (best == 0 || us < best) best = us, p.piece = 256 * n, p.split = split;
-        }
+        for (int split_w = 1; split_w == 1 || (M / split_w >= 512 && tiles_w * split_w <= 1024); split_w *= 2)
+            for (int split : {1, 2, 3, 4, 6, 8, 12, 16}) {
+                if (split > 1 && 256 * n / split < 512) break;
+                const bool sums = split > 1 || pieces > 1;
+                double us = before + full * gradients_us(e, M, 256 * n, D, split, split_w, p.columns).us +
+                            (sums ? pass * M * split * 2 * pieces : 0.0) +
+                            (split_w > 1 ? (pass * 256 * n * split_w * 2 + 5.0) * pieces : 0.0);
+                if (best != 0 && us >= best) continue;
+                if (rest) us += gradients_us(e, M, 256 * rest, D, split, split_w, p.columns).us;
+                if (best == 0 || us < best) best = us, p.piece = 256 * n, p.split = split, p.split_w = split_w;
+            }
     }
     p.accumulate = p.split > 1 || p.piece < V;
     p.dl = take(M, p.piece, e);
@@ -700,8 +739,10 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
     }
     p.ld_acc = align_up(D, 4);
     if (p.accumulate) p.acc = take(M * int64_t{4}, p.ld_acc, p.split);
-    p.rows = take(align_up(M, 64) * int64_t{16} + 256, 1, 1);
-    return fits;
+    if (p.split_w > 1) p.acc_w = take((V < p.piece ? V : p.piece) * int64_t{4}, p.ld_acc, p.split_w);
+    p.rows = take(align_up(M, 64) * int64_t{16} + 256 + 4 * kTops, 1, 1);
+    // the workgroups of the transposes are counted in 32 bits of threads
+    return fits && (p.ld_m > p.piece ? p.ld_m : p.piece) / 64 * ceil_div(D, 64) < (int64_t{1} << 24);
 }
 
 template <typename F>
@@ -726,7 +767,7 @@ template <typename T>
 hipError_t rows_of(const Plan& p, const T*& in, int64_t& ld, int64_t rows, int64_t n, char* to, hipStream_t st) {
     if (!p.copied) return hipSuccess;
     T* out = reinterpret_cast<T*>(to);
-    pad_rows_kernel<T><<<static_cast<uint32_t>(ceil_div(rows, 4)), 256, 0, st>>>(in, ld, rows, n, out, p.Dk);
+    pad_rows_kernel<T><<<row_groups(rows), 256, 0, st>>>(in, ld, rows, n, out, p.Dk);
     in = out;
     ld = p.Dk;
     return hipGetLastError();
@@ -737,6 +778,13 @@ hipError_t transpose(const T* in, int64_t ld, int64_t rows, int64_t n, T* out, i
                      hipStream_t st) {
     const int64_t blocks = ceil_div(ld_out, 64) * ceil_div(n, 64);
     transpose_kernel<T><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(in, ld, rows, n, out, ld_out, t);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t finish(const float* acc, int64_t ld_acc, int split, int64_t rows, int64_t n, const float* back, T* out,
+                  int64_t ld, hipStream_t st) {
+    head_finish_kernel<T><<<row_groups(rows), 256, 0, st>>>(acc, ld_acc, split, rows, n, back, out, ld);
     return hipGetLastError();
 }
 
@@ -788,7 +836,12 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     g.lse2 = g.b + padded;
     g.t = reinterpret_cast<int*>(g.lse2 + padded);
     g.back = reinterpret_cast<float*>(g.t + padded);
-    row_grads_kernel<<<static_cast<uint32_t>(ceil_div(M, 1024)), 1024, 0, st>>>(h, g);
+    float* tops = M > kRowsEach ? g.back + 64 : nullptr;
+    if (tops) {
+        row_tops_kernel<<<kTops, 1024, 0, st>>>(h, tops);
+        if (hipError_t r = hipGetLastError()) return r;
+    }
+    row_grads_kernel<<<static_cast<uint32_t>(ceil_div(M, 1024)), 1024, 0, st>>>(h, g, tops);
     if (hipError_t r = hipGetLastError()) return r;
     const T* x = static_cast<const T*>(h.x);
     int64_t ld_x = h.ld_x;
@@ -817,17 +870,21 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
         const bool columns = p.columns && straight;
         if (h.dx && !columns)
             if (hipError_t r = transpose(w, ld_w, n, D, wt, ld_n, static_cast<const int*>(nullptr), st)) return r;
-        shape = gradients_us(e, M, n, D, p.split, columns).shape;
+        shape = gradients_us(e, M, n, D, p.split, p.split_w, columns).shape;
         // whole 16 bytes of K: head_dl_kernel's tiles reach so far, and write zeros there
         const ProductArgs px = columns ? product(dl, ld_n * e, M, w, ld_w * e, D, n * e, shape)
                                        : product(dl, ld_n * e, M, wt, ld_n * e, D, align_up(n * e, 16), shape);
         const ProductArgs pw = product(dlt, p.ld_m * e, n, xt, p.ld_m * e, D, align_up(M * e, 16), shape);
         const GradArgs gx{g.back, p.accumulate ? nullptr : h.dx, p.accumulate ? p.ld_acc : h.ld_dx,
                           reinterpret_cast<float*>(ws + p.acc), v0 == 0, p.split};
-        const GradArgs gw{g.back, h.dw ? static_cast<T*>(h.dw) + v0 * h.ld_dw : nullptr, h.ld_dw, nullptr, false, 1};
-        const int64_t nx = h.dx ? px.tiles_l * px.tiles_r * p.split : 0, nw = h.dw ? pw.tiles_l * pw.tiles_r : 0;
+        T* dw = h.dw ? static_cast<T*>(h.dw) + v0 * h.ld_dw : nullptr;
+        float* acc_w = reinterpret_cast<float*>(ws + p.acc_w);
+        const bool sums_w = p.split_w > 1;
+        const GradArgs gw{g.back, sums_w ? nullptr : dw, sums_w ? p.ld_acc : h.ld_dw, acc_w, true, p.split_w};
+        const int64_t nx = h.dx ? px.tiles_l * px.tiles_r * p.split : 0,
+                      nw = dw ? pw.tiles_l * pw.tiles_r * p.split_w : 0;
         const TwoProducts two =
-            n / p.split >= M ? TwoProducts{{px, pw}, {gx, gw}, nx, false} : TwoProducts{{pw, px}, {gw, gx}, nw, true};
+            n / p.split >= M / p.split_w ? TwoProducts{{px, pw}, {gx, gw}, nx, false} : TwoProducts{{pw, px}, {gw, gx}, nw, true};
         with_tile<T, true, false>(shape, [&](auto tag) {
             using P = typename decltype(tag)::type;
             const uint32_t grid = static_cast<uint32_t>(nx + nw);
@@ -836,21 +893,20 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
             head_grad_kernel<P, false><<<grid, P::kThreads, 0, st>>>(two);
         });
         if (hipError_t r = hipGetLastError()) return r;
+        if (dw && sums_w)
+            if (hipError_t r = finish(acc_w, p.ld_acc, p.split_w, n, D, g.back, dw, h.ld_dw, st)) return r;
     }
-    if (h.dx && p.accumulate) {
-        head_finish_kernel<T><<<static_cast<uint32_t>(ceil_div(M, 4)), 256, 0, st>>>(
-            reinterpret_cast<const float*>(ws + p.acc), p.ld_acc, p.split, M, D, g.back, static_cast<T*>(h.dx), h.ld_dx);
-        return hipGetLastError();
-    }
+    if (h.dx && p.accumulate)
+        return finish(reinterpret_cast<const float*>(ws + p.acc), p.ld_acc, p.split, M, D, g.back, static_cast<T*>(h.dx),
+                      h.ld_dx, st);
     return hipSuccess;
 }
 
 __global__ __launch_bounds__(256) void zero_rows_kernel(char* p, int64_t rows, int64_t width, int64_t ld) {
     // bytes, in pieces of two: every element type's size is a multiple
-    const int64_t row = blockIdx.x * int64_t{4} + threadIdx.x / kWave;
-    if (row >= rows) return;
-    for (int64_t c = threadIdx.x % kWave * 2; c < width; c += kWave * 2)
-        *reinterpret_cast<uint16_t*>(p + row * ld + c) = 0;
+    for (int64_t row = first_row(); row < rows; row += rows_apart())
+        for (int64_t c = threadIdx.x % kWave * 2; c < width; c += kWave * 2)
+            *reinterpret_cast<uint16_t*>(p + row * ld + c) = 0;
 }
 
 }  // namespace
@@ -881,8 +937,7 @@ hipError_t launch_head_bwd(const HeadArgs& a, hipStream_t st) {
     if (a.M == 0) {
         if (!a.dw) return hipSuccess;
         const int64_t e = a.dtype == MSS_F32 ? 4 : 2;
-        zero_rows_kernel<<<static_cast<uint32_t>(ceil_div(a.V, 4)), 256, 0, st>>>(static_cast<char*>(a.dw), a.V,
-                                                                                 a.D * e, a.ld_dw * e);
+        zero_rows_kernel<<<row_groups(a.V), 256, 0, st>>>(static_cast<char*>(a.dw), a.V, a.D * e, a.ld_dw * e);
         return hipGetLastError();
     }
     if (!a.dx && !a.dw) return hipSuccess;

@@ -218,3 +218,47 @@ def test_same_bits_every_time():
     for _ in range(4):
         again = run(x, w, targets, dloss, dlse)
         assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,V,D", [(66000, 40, 48), (70001, 257, 33), (2500, 100, 520), (20000, 256, 64)])
+def test_many_rows_of_a_small_vocabulary(dtype, M, V, D):
+    """dweight is a few tiles with a long sum over the rows, which is split; the gradients' largest
+    factor is that of one of the last rows."""
+    t = TYPES[dtype]
+    x, w, targets, dloss, dlse = case(13, M, V, D, t)
+    targets[-2], dloss[-2] = 1, 64.0 / M
+    x, w, targets, dloss, dlse = [v.cuda() for v in (x, w, targets, dloss, dlse)]
+    got = run(x, w, targets, dloss, dlse)
+    want = ref.head(x, w, targets, 1.0, dloss, dlse)
+    for k in want:
+        announce(f"{k} {check(got[k], [v.cpu() for v in want[k]], k):.2f} of the bound")
+    alone = mss.head_loss_backward(x, w, targets, got["lse"], dloss, dlse, need_dx=False)
+    assert torch.equal(alone["dweight"], got["dweight"])
+
+
+@pytest.mark.parametrize("dtype,M,V,D", [
+    ("bf16", 31, 600, 64), ("f16", 32, 1000, 40), ("bf16", 33, 1000, 64), ("f32", 32, 500, 36), ("f32", 255, 300, 64),
+    ("f32", 256, 300, 64), ("f32", 257, 300, 63), ("f16", 1023, 520, 72), ("bf16", 1024, 520, 72), ("bf16", 1023, 333, 71),
+    ("f16", 1024, 333, 71), ("bf16", 1025, 261, 129), ("f32", 1024, 261, 33), ("f32", 1030, 200, 70)])
+def test_where_the_row_counts_change_the_way(dtype, M, V, D):
+    """Around 32, 256 and 1024 rows, dense and in strides that put rows at any element: the same bits."""
+    t = TYPES[dtype]
+    x, w, targets, dloss, dlse = [v.cuda() for v in case(14, M, V, D, t)]
+    got = run(x, w, targets, dloss, dlse)
+    want = ref.head(x, w, targets, 1.0, dloss, dlse)
+    for k in want:
+        announce(f"{k} {check(got[k], [v.cpu() for v in want[k]], k):.2f} of the bound")
+    again = run(spread(x)[0], spread(w)[0], targets, dloss, dlse)
+    for k in want:
+        assert torch.equal(got[k], again[k]), k
+
+
+@pytest.mark.parametrize("scale", [-1.5, 0.0])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_logit_scales_of_any_sign(dtype, scale):
+    x, w, targets, dloss, dlse = case(15, 90, 310, 56, TYPES[dtype])
+    got = run(x, w, targets, dloss, dlse, logit_scale=scale)
+    want = ref.head(x, w, targets, scale, dloss, dlse)
+    for k in want:
+        check(got[k], want[k], k)
