@@ -90,8 +90,9 @@ __global__ __launch_bounds__(kThreads) void square_kernel(List l, double* part) 
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-// The factor as part 2^exponent, 1/2 <= part < 1, so that it keeps its digits where
-// it is subnormal in fp32 (a norm near the end of the range).
+// The factor, part 2^exponent: exponent 0 where it is a normal fp32 number (a value is then
+// multiplied by it and rounded once, also a subnormal one: 1 leaves it as it is), else
+// 1/2 <= part < 1, so that it keeps its digits (a norm near the end of the range).
 struct Factor {
     float part;
     int exponent;
@@ -116,7 +117,8 @@ __device__ __forceinline__ Factor factor_of(const Clip& c, double norm) {
     const bool finite = norm < INFINITY;        // false for NaN too
     int exponent;
     const double part = frexp(!finite ? 1.0 : c.scale * (norm > c.max_norm ? c.max_norm / norm : 1.0), &exponent);
-    return {static_cast<float>(part), exponent};
+    if (exponent < -125) return {static_cast<float>(part), exponent};
+    return {static_cast<float>(ldexp(part, exponent)), 0};
 }
 
 __global__ __launch_bounds__(kThreads) void norm_kernel(Clip c) {
@@ -168,7 +170,7 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(List l, Clip c) {
     int64_t chunk = blockIdx.x + (l.chunks - 1 - blockIdx.x) / gridDim.x * gridDim.x;
     for (int i = tensor_of(l, static_cast<uint32_t>(chunk)); chunk >= 0; chunk -= gridDim.x) {
         while (l.first[i] > chunk) i--;
-        if (f.part == 0.5f && f.exponent == 1 && l.in[i] == l.out[i] && l.dtype[i] == l.out_dtype[i]) continue;     // as it is
+        if (f.part == 1.0f && f.exponent == 0 && l.in[i] == l.out[i] && l.dtype[i] == l.out_dtype[i]) continue;     // as it is
         const int64_t from = (chunk - l.first[i]) * l.chunk;
         const int64_t n = l.numel[i] - from < l.chunk ? l.numel[i] - from : l.chunk;
         const bool wide = l.out_dtype[i] == MSS_F32;

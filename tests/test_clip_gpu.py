@@ -139,3 +139,15 @@ def test_refusals():
             mss.clip_grads([g], max_norm, scale=scale)
         assert err.value.status == -1
     assert (g == 1).all()
+
+
+def test_a_factor_of_one_changes_no_value():
+    """Out of place too, down to the smallest subnormal; and one of a power of two rounds once."""
+    g = torch.tensor([1.4e-45, -4.2e-45, 1e-39, -0.0, 1.5, -3e38], device="cuda")
+    b = (torch.arange(1, 200).float() * 2.0 ** -133).bfloat16().cuda()
+    for grads in ([g], [b], [g, b]):
+        same = [torch.empty_like(v) for v in grads]
+        mss.clip_grads(grads, 3.4e38, out=same)
+        assert all(torch.equal(s.view(torch.uint8), v.view(torch.uint8)) for s, v in zip(same, grads))
+    twice, _ = mss.clip_grads([g[:5]], 1e6, scale=2.0, out=[torch.empty(5, device="cuda")])
+    assert torch.equal(twice[0].cpu(), g[:5].cpu() * 2)
