@@ -575,11 +575,18 @@ bool embed_bwd_workspace(int64_t M, int64_t V, int64_t D, int64_t& bytes) {
     return true;
 }
 
-hipError_t launch_embed(const EmbedArgs& a, hipStream_t st) {
-    const int64_t blocks = ceil_div(a.M, 4);
-    return by_types(a.dtype, a.out_dtype, [&](auto w, auto y) {
-        embed_kernel<decltype(w), decltype(y)><<<static_cast<uint32_t>(blocks), 256, 0, st>>>(a);
-        return hipGetLastError();
+hipError_t launch_embed(const EmbedArgs& all, hipStream_t st) {
+    constexpr int64_t kMost = int64_t{1} << 25;      // rows of a launch, below 2^32 threads
+    return by_types(all.dtype, all.out_dtype, [&](auto w, auto y) {
+        for (int64_t m0 = 0; m0 < all.M; m0 += kMost) {
+            EmbedArgs a = all;
+            a.M = all.M - m0 < kMost ? all.M - m0 : kMost;
+            a.ids = static_cast<const char*>(all.ids) + m0 * (all.wide_ids ? 8 : 4);
+            a.y = static_cast<decltype(y)*>(all.y) + m0 * all.ld_y;
+            embed_kernel<decltype(w), decltype(y)><<<static_cast<uint32_t>(ceil_div(a.M, 4)), 256, 0, st>>>(a);
+            if (hipError_t e = hipGetLastError()) return e;
+        }
+        return hipSuccess;
     });
 }
 

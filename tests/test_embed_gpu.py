@@ -138,3 +138,15 @@ def test_the_gradient_of_the_lookup():
     left, right = (dy.double() * y).sum(), (dw * d.double()).sum()
     # 700 x 48 products, each off by at most (n + 4) U with n < 400 places of a token
     assert abs(left - right) <= 404 * ref.U * (dy.double() * y).abs().sum()
+
+
+def test_as_many_positions_as_there_may_be():
+    """2^26 - 1 of them, in rows of one value: sums of ones, exact in fp32."""
+    M, V = 2 ** 26 - 1, 5
+    ids = (torch.arange(M, dtype=torch.int32, device="cuda") * 7 % 11)
+    w = torch.arange(1, V + 1, device="cuda").float().view(V, 1).half()
+    y = mss.embedding(ids, w)
+    assert torch.equal(y[:, 0], torch.where(ids < V, ids + 1, 0).half())
+    dw = mss.embedding_backward(ids, torch.ones(M, 1, device="cuda"), vocab=V)
+    want = torch.tensor([float((ids == v).sum()) for v in range(V)], device="cuda")
+    assert torch.equal(dw[:, 0], want)

@@ -262,3 +262,29 @@ def test_logit_scales_of_any_sign(dtype, scale):
     want = ref.head(x, w, targets, scale, dloss, dlse)
     for k in want:
         check(got[k], want[k], k)
+
+
+def test_a_vocabulary_in_pieces_of_the_forward():
+    x, w, targets, dloss, dlse = [v.cuda() for v in case(16, 37, 270001, 24, torch.bfloat16)]
+    got = run(x, w, targets, dloss, dlse)
+    want = ref.head(x, w, targets, 1.0, dloss, dlse)
+    for k in want:
+        check(got[k], [v.cpu() for v in want[k]], k)
+
+
+@pytest.mark.parametrize("M", [30484, 33001])
+def test_rows_in_pieces_of_the_forward(M):
+    """More partial sums than are held at a time; the last piece has a few rows, or thousands."""
+    V = 70001
+    x, w, targets, _, _ = [v.cuda() for v in case(17, M, V, 8, torch.bfloat16)]
+    need = mss.head_workspace_bytes(mss.OP_HEAD_LOSS, rows=M, vocab=V, width=8, dtype=torch.bfloat16)
+    assert need < (V // 64 + 2) * M * 8 + 4 * M        # of all rows at once
+    loss, lse = mss.head_loss(x, w, targets)
+    rows = torch.cat([torch.arange(40), torch.arange(30400, 30484), torch.arange(M - 40, M)])
+    want = ref.head(x[rows], w, targets[rows], 1.0)
+    check(loss[rows], [v.cpu() for v in want["loss"]], "loss")
+    check(lse[rows], [v.cpu() for v in want["lse"]], "lse")
+    # and the rest by their own sums in fp32, in which a logit and its exponential are off by little
+    for r in range(0, M, 4000):
+        l = x[r:r + 4000].float() @ w.float().t()
+        assert torch.allclose(lse[r:r + 4000], torch.logsumexp(l, 1), rtol=1e-5, atol=1e-5)
