@@ -9,10 +9,17 @@
 // Backward, a piece of the vocabulary at a time:
 //   dl = (dloss + dlse) p - dloss [v = t],  p = 2^(l - lse),  recomputed from
 // the logits' tiles, in the operands' type, as dl (rows, piece) and its
-// transpose; then dx += dl W and dW = dl^T x.  All three are products of rows
-// (row_product.h), for which x and the piece of W are transposed first: that
-// reads and writes each once, against products that take hundreds of
-// operations for each of their values.
+// transpose; then dx += dl W and dW = dl^T x, in one launch.  All three are
+// products of rows (row_product.h), for which x and the piece of W are transposed
+// first: that reads and writes each once, against products that take hundreds of
+// operations for each of their values.  With few rows dx's product reads W down
+// its columns instead (kColumnRows).
+//
+// What bounds it, by a trace: M8192 V32768 D1536 bf16 takes 755 us forward (1092
+// TFLOP/s, a library product of the size 583 us; 677 us and 1218 TFLOP/s in a run of
+// forwards alone), 898 for dl with its two stores of 537 MB, 1411 for both gradients (1169
+// TFLOP/s): matrix instructions, with 10 to 15 % in the start and end of tiles.
+// M8 V65536 D2560 reads W at 5.9 TB/s (57 us).
 //
 // dl is held times a factor that brings the largest |dloss| + |dlse| to just
 // below 2^13: fp16 would lose what a mean over many rows leaves of it, and right
@@ -35,7 +42,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // The tile shapes, rows of the operand whose rows are C's first.  With 256 x 256
 // and 192 x 320 one workgroup of eight waves fills a CU's LDS, of the others' four
 // waves two do (four of the last, which reads the vocabulary for a few rows: 8 rows
-// of 65536 x 2560 in bf16 take 58 us with it, with 128 x 128 72).
+// of 65536 x 2560 in bf16 take 63.0 us a call with it, 64.5 with 128 x 128 and 86 with
+// 256 x 256).
 enum TileShape { kLarge, kTall, kWide, kSmall, kFew };
 template <bool DIRECT>
 constexpr Layout kLies = DIRECT ? kDirect : kThrough;
@@ -576,9 +584,10 @@ int64_t align_up(int64_t n, int64_t a) { return ceil_div(n, a) * a; }
 
 // What the tile shapes take on this card, in microseconds: a value of K of one
 // tile, with as many workgroups on a CU as `slots` says for all of them, and a
-// tile's start and end.  Measured in bf16 with 8192 x 32768 x 1536: 1226, 1150, 1095
-// and 1045 TFLOP/s; in fp32 211 in place of 1226 and 182 of 1045.  kFew is bound by
-// what it reads, and is taken by the number of rows.
+// tile's start and end.  Measured in bf16 with 8192 x 32768 x 1536: 1218, 1123, 1063
+// and 1006 TFLOP/s; in fp32 (4096 x 32768 x 1024) 213, 200, 189 and 181.  The best shape
+// changes with the size: fp16, 1551 x 10007 x 1001 take 76, 78, 66 and 75 us.  kFew is
+// bound by what it reads, and is taken by the number of rows.
 struct TileCost {
     int64_t nl, nr, slots;
     double each, fixed;
@@ -641,14 +650,15 @@ Choice gradients_us(int64_t elem, int64_t M, int64_t n, int64_t D, int64_t split
 
 // Rows that are not a multiple of 16 bytes long are copied to rows that are where
 // there are so many that the copy of W costs less than reading it through registers
-// (bf16, V32768, forward: M8192 D1535 873 us through registers, 675 + 45 copied;
-// M2048 D769 151 and 120 + 25; fp16 M1551 V10007 D1001 85 and 61 + 13).
+// (bf16, V32768, forward: M8192 D1535 880 us through registers, 741 copied; M2048 D769
+// 130 and 131; fp16 M1551 V10007 D1001 85 and 66).
 constexpr int64_t kCopyRows = 1024;
 // Below as many rows dx's product reads W as it lies, down its columns: slower, but W
-// is not transposed first (bf16, both gradients: M16 V65536 D2560
-// 297 us against 424, M517 V50021 D1536 387 and 399, M1000 V32768 D1536 370 and 391).
-// In fp32 its 4-byte LDS reads take 2.3 times as long: below 256 rows (M128 V65536 D2560
-// 926 us against 1121, M517 V50021 D1536 1784 and 1598).
+// is not transposed first (bf16, both gradients: M16 V65536 D2560 292 us against 428, M517
+// V50021 D1536 380 and 399, M1000 V32768 D1536 359 and 387, M1100 441 and 461, M1536 540
+// and 535, M2048 719 and 681; M1280 V50304 D768 420 and 396).  In fp32 its 4-byte LDS reads
+// take 2.3 times as long: below 256 rows (M128 V65536 D2560 949 us against 1158, M250 V50021
+// D1536 782 and 876, M517 1623 and 1611).
 constexpr int64_t kColumnRows = 1024, kColumnRowsWide = 256;
 
 struct Plan {
