@@ -28,6 +28,8 @@
 // there (bf16, M8192 V32768 D1536: dx is off by 0.0020 of its norm, of which 0.0017
 // is its own rounding; with the same dl right above a power of two, 0.0028).  dx and
 // dW are scaled back in fp32.
+#include <algorithm>
+
 #include "launch_ends.h"
 #include "row_product.h"
 
@@ -578,7 +580,10 @@ __global__ __launch_bounds__(256) void head_finish_kernel(const float* acc, int6
 // ---- plans -------------------------------------------------------------------------
 
 constexpr int64_t kPartBytes = int64_t{256} << 20;      // partial sums of the forward at a time
-constexpr int64_t kDlBytes = int64_t{1} << 30;          // dl and its transpose
+// dl and its transpose take 1 GiB, with many rows what 3328 vocabulary rows take, up to 8:
+// every piece reads and writes dx's sums (both gradients, M262144 V32768 D1536 bf16: 79 ms,
+// with 1 GiB 96; M400000 V10000 D768 fp16 22 and 32).
+constexpr int64_t kDlBytes = int64_t{1} << 30, kMostDlBytes = int64_t{8} << 30, kDlColumns = 3328;
 
 int64_t align_up(int64_t n, int64_t a) { return ceil_div(n, a) * a; }
 
@@ -714,7 +719,7 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
     // dW's K is split where a small vocabulary leaves it few tiles (bf16, M65536 V256 D1024: both
     // gradients 288 us, with K whole 1085; M4096 V1000 D512 50 and 74).
     const int64_t steps = ceil_div(V, 256);
-    int64_t most = kDlBytes / (2 * 256 * e * p.ld_m);
+    int64_t most = std::clamp(2 * e * p.ld_m * kDlColumns, kDlBytes, kMostDlBytes) / (2 * 256 * e * p.ld_m);
     for (int64_t bound : {int64_t{1024}, steps})
         if (most > bound) most = bound;
     if (most < 1) most = 1;

@@ -288,3 +288,14 @@ def test_rows_in_pieces_of_the_forward(M):
     for r in range(0, M, 4000):
         l = x[r:r + 4000].float() @ w.float().t()
         assert torch.allclose(lse[r:r + 4000], torch.logsumexp(l, 1), rtol=1e-5, atol=1e-5)
+
+
+def test_more_rows_than_a_gibibyte_of_gradients():
+    M, V, D = 90000, 4900, 16
+    x, w, targets, dloss, dlse = [v.cuda() for v in case(18, M, V, D, torch.float16)]
+    need = mss.head_workspace_bytes(mss.OP_HEAD_LOSS_BACKWARD, rows=M, vocab=V, width=D, dtype=torch.float16)
+    assert 2 ** 30 < need < 2 * 2 * M * V            # dl and its transpose, a piece of the vocabulary at a time
+    got = run(x, w, targets, dloss, dlse)
+    want = ref.head(x, w, targets, 1.0, dloss, dlse)
+    for k in want:
+        check(got[k], [v.cpu() for v in want[k]], k)
