@@ -1333,8 +1333,8 @@ def clip_grads(grads, max_norm, *, scale=1.0, out=None, norm=None, workspace=Non
     number of micro-batches in them).  The tensors are updated in place, or written to ``out``, a
     list of tensors of their types or float32 (each may be its input).  Where a value is infinite or
     NaN they are left as they are (``out``: copied), so that the caller can look at the norm, which
-    is not finite then, and pass over the step.  ``norm``: optional output tensor without dimensions.  ``workspace`` as in
-    ``grad_norm``."""
+    is not finite then, and pass over the step.  A tensor may stand in the list once.  ``norm``:
+    optional output tensor without dimensions.  ``workspace`` as in ``grad_norm``."""
     grads = list(grads)
     c, scale, max_norm = _list_call(grads, stream), float(scale), float(max_norm)
     out = grads if out is None else list(out)

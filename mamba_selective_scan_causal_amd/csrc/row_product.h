@@ -8,8 +8,8 @@
 // instructions: by direct loads where the rows lie at multiples of 16 bytes,
 // through registers otherwise.  Chunk c (16 bytes) of row i lies at chunk
 // c ^ (i & 7) of the row's 128 bytes: the 16 rows that a fragment reads at one
-// c then fall on different banks.  R is the instruction's row operand, so that a lane ends up with four
-// neighbouring r of one l: runs of C's rows.
+// c then fall on different banks.  R is the instruction's row operand, so that a
+// lane ends up with four neighbouring r of one l: runs of C's rows.
 #pragma once
 
 #include <type_traits>
