@@ -1,13 +1,14 @@
 // head_kernel.hip -- softmax cross entropy of x W^T over a large vocabulary, and
 // its gradients, without keeping the logits.
 //
-// Forward, with l = c x W^T in units of log2 (c = logit_scale log2 e): each
-// tile of logits leaves, for each of its rows, the largest logit and the sum of
-// 2^(l - largest) of the columns of one wave; a second kernel joins those of a
-// row and takes the target's logit, which the tile that has it wrote.
+// Forward: each tile of logits l leaves, for each of its rows, the largest logit
+// and the sum of e^(l - largest) of the columns of one wave; a second kernel joins
+// those of a row and takes the target's logit, which the tile that has it wrote.
+// The exponentials are powers of 2 whose argument is one fused multiply-add of the
+// product; where its rounding could matter (kFar) logits are subtracted first.
 //
 // Backward, a piece of the vocabulary at a time:
-//   dl = (dloss + dlse) p - dloss [v = t],  p = 2^(l - lse),  recomputed from
+//   dl = (dloss + dlse) p - dloss [v = t],  p = e^(l - lse),  recomputed from
 // the logits' tiles, in the operands' type, as dl (rows, piece) and its
 // transpose; then dx += dl W and dW = dl^T x, in one launch.  All three are
 // products of rows (row_product.h), for which x and the piece of W are transposed
@@ -153,8 +154,15 @@ struct Part {
 
 // ---- forward -----------------------------------------------------------------
 
+// With |l| in units of log2 below this, fma(product, c, -l') is off by 2^-5 at most where l' is l
+// rounded. Beyond, that error grows until the power overflows (from 2^31 on, where half a step is
+// 2^7), and c times a product may overflow where the logit does not: there logits are subtracted
+// before they are scaled.
+constexpr float kFar = 0x1p20f;
+__device__ __forceinline__ bool is_far(float l) { return !(__builtin_fabsf(l) < kFar); }      // NaN too
+
 struct LossArgs {
-    float c;                  // logit_scale log2(e)
+    float s, c;               // logit_scale, and times log2(e)
     int64_t first;            // vocabulary row of the piece's first
     int64_t m0;               // row of the rows' first
     const void* targets;
@@ -185,29 +193,30 @@ __global__ __launch_bounds__(P::kThreads) void head_loss_kernel(ProductArgs a, L
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
     if (at.rw >= a.nr) return;
     const bool whole = at.rw + S::kSlab <= a.nr;
-    float c = h.c;
-    // c > 0 below, and every value counts: the few waves that are not so make it so
-    if (!whole || c <= 0.0f) {
+    float s = h.s, c = h.c;
+    // s > 0 below, and every value counts: the few waves that are not so make it so
+    if (!whole || !(s > 0.0f)) {
         const int valid = whole ? S::kSlab : static_cast<int>(a.nr - at.r);       // from the lane's r on
 #pragma unroll
         for (int j = 0; j < P::kTL; j++)
 #pragma unroll
             for (int i = 0; i < P::kTR; i++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) acc[i][j][e] = 16 * i + e < valid ? acc[i][j][e] * c : -INFINITY;
-        c = 1.0f;
+                for (int e = 0; e < 4; e++) acc[i][j][e] = 16 * i + e < valid ? acc[i][j][e] * s : -INFINITY;
+        s = 1.0f;
+        c = kLog2e;
     }
 #pragma unroll
     for (int j = 0; j < P::kTL; j++) {
         const int64_t m = at.l + 16 * j;
         const bool in = m < a.nl;
         const int64_t v = in ? target_of(h.targets, h.wide, h.m0 + m) - h.first : -1;
-        float top = acc[0][j][0];
+        float most = acc[0][j][0];
 #pragma unroll
         for (int i = 0; i < P::kTR; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) top = __builtin_fmaxf(top, acc[i][j][e]);
-        top = over_quads_max(top) * c;
+            for (int e = 0; e < 4; e++) most = __builtin_fmaxf(most, acc[i][j][e]);
+        most = over_quads_max(most);
         // one wave in V / kSlab has a row's target
         if (const bool here = at.holds(v, a.nr); wave_any(here)) {
             const int hit = at.place(v);
@@ -216,13 +225,27 @@ __global__ __launch_bounds__(P::kThreads) void head_loss_kernel(ProductArgs a, L
             for (int i = 0; i < P::kTR; i++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) own = hit == 16 * i + e ? acc[i][j][e] : own;
-            if (here) h.at_target[h.m0 + m] = own * c;
+            if (here) h.at_target[h.m0 + m] = own * s;
         }
+        const float top = most * s, top2 = most * c;
         float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < P::kTR; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) sum += ex2(__builtin_fmaf(acc[i][j][e], c, -top));
+            for (int e = 0; e < 4; e++) sum += ex2(__builtin_fmaf(acc[i][j][e], c, -top2));
+        // from the roundings of top2 to those of top
+        sum *= ex2(__builtin_fmaf(__builtin_fmaf(most, s, -top), kLog2e, -__builtin_fmaf(most, c, -top2)));
+        if (const bool far = is_far(top2); wave_any(far)) {
+            // equal ones count 1, infinite ones too: a slab of logits -inf leaves (-inf, their number),
+            // which the join takes as nothing beside a finite one
+            float apart = 0.0f;
+#pragma unroll
+            for (int i = 0; i < P::kTR; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    apart += ex2(acc[i][j][e] == most ? 0.0f : (acc[i][j][e] - most) * c);
+            sum = far ? apart : sum;
+        }
         sum = over_quads_sum(sum);
         if (at.lane < 16 && in) h.part[at.rw / S::kSlab * a.nl + m] = make_float2(top, sum);
     }
@@ -240,9 +263,9 @@ struct JoinArgs {
 
 __device__ __forceinline__ void join(float& top, float& sum, float2 p) {
     const float t = __builtin_fmaxf(top, p.x);
-    // equal infinities would give NaN here: a slab without a finite logit adds 2^(l - top) as it is
-    const float from = top == t ? sum : sum * ex2(top - t);
-    const float add = p.x == t ? p.y : p.y * ex2(p.x - t);
+    // equal infinities, whose difference is NaN, are taken as they are
+    const float from = top == t ? sum : sum * ex2((top - t) * kLog2e);
+    const float add = p.x == t ? p.y : p.y * ex2((p.x - t) * kLog2e);
     sum = from + add;
     top = t;
 }
@@ -275,10 +298,10 @@ __global__ __launch_bounds__(256) void head_join_kernel(JoinArgs h) {
         }
     }
     if (member != 0 || m >= h.rows) return;
-    const float lse2 = top + log2f(sum);
+    const float lse = __builtin_fmaf(log2f(sum), kLn2, top);
     const int64_t at = h.m0 + m, t = target_of(h.targets, h.wide, at);
-    h.lse[at] = lse2 * kLn2;
-    h.loss[at] = t >= 0 && t < h.V ? (lse2 - h.at_target[at]) * kLn2 : 0.0f;
+    h.lse[at] = lse;
+    h.loss[at] = t >= 0 && t < h.V ? lse - h.at_target[at] : 0.0f;
 }
 
 // ---- copies ---------------------------------------------------------------------
@@ -339,12 +362,12 @@ __global__ __launch_bounds__(256) void transpose_kernel(const T* in, int64_t ld_
 
 // ---- backward --------------------------------------------------------------------
 
-// What a row brings to dl: a = (dloss + dlse) s, b = dloss s, its lse in units
-// of log2 and its target (-1: a padded row, all zeros).
+// What a row brings to dl: a = (dloss + dlse) s, b = dloss s, its lse and its
+// target (-1: a padded row, all zeros).
 struct RowGrads {
     float* a;
     float* b;
-    float* lse2;
+    float* lse;
     int* t;
     float* back;              // [0]: logit_scale / s
 };
@@ -412,12 +435,12 @@ __global__ __launch_bounds__(1024) void row_grads_kernel(HeadArgs h, RowGrads g,
     const float up = on ? h.dloss[m] : 0.0f;
     g.a[m] = on ? (up + (h.dlse ? h.dlse[m] : 0.0f)) * s : 0.0f;
     g.b[m] = up * s;
-    g.lse2[m] = on ? h.lse[m] * kLog2e : 0.0f;
+    g.lse[m] = on ? h.lse[m] : 0.0f;
     g.t[m] = on ? static_cast<int>(t) : -1;
 }
 
 struct DlArgs {
-    float c;
+    float s, c;               // logit_scale, and times log2(e)
     int64_t first;
     RowGrads g;
     void* dl;                 // (M, ld_dl)
@@ -441,7 +464,7 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
     __shared__ __align__(1024) char lds[P::kLds];
     const Part<P> at(a, blockIdx.x, gridDim.x);
     int hit[P::kTL];
-    float up[P::kTL], own[P::kTL], lse2[P::kTL];
+    float up[P::kTL], own[P::kTL], lse[P::kTL];
     const auto read_rows = [&] {
 #pragma unroll
         for (int j = 0; j < P::kTL; j++) {
@@ -450,7 +473,7 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
             hit[j] = at.place((in ? h.g.t[m] : -1) - h.first);
             up[j] = in ? h.g.a[m] : 0.0f;
             own[j] = in ? h.g.b[m] : 0.0f;
-            lse2[j] = in ? h.g.lse2[m] : 0.0f;
+            lse[j] = in ? h.g.lse[m] : 0.0f;
         }
     };
     // ahead of the product where its registers leave room
@@ -462,10 +485,24 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
     // a padded row's x counts as zeros (ProductArgs::off) and its up is 0: so is its dl
 #pragma unroll
     for (int j = 0; j < P::kTL; j++) {
+        if (const bool far = is_far(lse[j]); wave_any(far)) {
+            // the logit is rounded as the forward rounds it, and not into the difference
+#pragma clang fp contract(off)
 #pragma unroll
-        for (int i = 0; i < P::kTR; i++)
+            for (int i = 0; i < P::kTR; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) acc[i][j][e] = ex2(__builtin_fmaf(acc[i][j][e], h.c, -lse2[j])) * up[j];
+                for (int e = 0; e < 4; e++) {
+                    const float l = acc[i][j][e] * h.s;
+                    const float x = far ? (l - lse[j]) * kLog2e : __builtin_fmaf(acc[i][j][e], h.c, -lse[j] * kLog2e);
+                    acc[i][j][e] = ex2(x) * up[j];
+                }
+        } else {
+            const float lse2 = lse[j] * kLog2e;
+#pragma unroll
+            for (int i = 0; i < P::kTR; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[i][j][e] = ex2(__builtin_fmaf(acc[i][j][e], h.c, -lse2)) * up[j];
+        }
         if (wave_any(hit[j] >= 0)) {
 #pragma unroll
             for (int i = 0; i < P::kTR; i++)
@@ -826,7 +863,7 @@ hipError_t forward(const HeadArgs& h, const Plan& p, hipStream_t st) {
             int64_t ld_w = h.ld_w;
             if (hipError_t r = rows_of(p, w, ld_w, n, h.D, ws + p.w, st)) return r;
             const ProductArgs a = product(x + m0 * ld_x, ld_x * e, rows, w, ld_w * e, n, p.Dk * e, shape);
-            const LossArgs l{h.logit_scale * kLog2e, v0, m0, h.targets, h.wide_ids, part + slabs * rows, at_target};
+            const LossArgs l{h.logit_scale, h.logit_scale * kLog2e, v0, m0, h.targets, h.wide_ids, part + slabs * rows, at_target};
             with_tile<T>(shape, straight, [&](auto tag) {
                 using P = typename decltype(tag)::type;
                 head_loss_kernel<P><<<static_cast<uint32_t>(a.tiles_l * a.tiles_r), P::kThreads, 0, st>>>(a, l);
@@ -851,8 +888,8 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     const int64_t padded = align_up(M, 64);
     g.a = reinterpret_cast<float*>(ws + p.rows);
     g.b = g.a + padded;
-    g.lse2 = g.b + padded;
-    g.t = reinterpret_cast<int*>(g.lse2 + padded);
+    g.lse = g.b + padded;
+    g.t = reinterpret_cast<int*>(g.lse + padded);
     g.back = reinterpret_cast<float*>(g.t + padded);
     float* tops = M > kRowsEach ? g.back + 64 : nullptr;
     if (tops) {
@@ -879,7 +916,7 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
         if (hipError_t r = rows_of(p, w, ld_w, n, D, ws + p.w, st)) return r;
         int shape = product_us(e, M, n, D, straight).shape;
         const ProductArgs a = product(x, ld_x * e, M, w, ld_w * e, n, p.Dk * e, shape, g.t);
-        const DlArgs d{h.logit_scale * kLog2e, v0, g, dl, dlt, ld_n, p.ld_m};
+        const DlArgs d{h.logit_scale, h.logit_scale * kLog2e, v0, g, dl, dlt, ld_n, p.ld_m};
         with_tile<T>(shape, straight, [&](auto tag) {
             using P = typename decltype(tag)::type;
             head_dl_kernel<P><<<static_cast<uint32_t>(a.tiles_l * a.tiles_r), P::kThreads, 0, st>>>(a, d);
