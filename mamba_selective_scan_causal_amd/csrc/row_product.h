@@ -53,6 +53,8 @@ struct Mma<f16> {
 // A product is the six of the nine partial products that are not below 2^-22 of it:
 // six instructions at a sixteenth of the fp32 instruction's time each, and the
 // splitting (M2048 V32768 D768: 211 TFLOP/s against 139 with the fp32 instruction).
+// An infinity has no such parts (inf - inf is NaN, and so is inf times the other operand's
+// empty lower parts): sums that are not finite are computed again (RowProduct::mend).
 struct Parts {
     v4i p[3];
     __device__ __forceinline__ void of(v4i a_, v4i b_) {
@@ -367,6 +369,84 @@ struct RowProduct {
         }
     }
 
+    // The 16 x 16 tiles of the wave at l, l + 16, .. (where asked for) and r with the fp32
+    // instruction, straight from memory: this lane's rows of L and its row of R at value k0 + lane / 16
+    // of K, in steps of four.
+    static __device__ __forceinline__ void exact(const ProductArgs& a, int64_t l, int64_t r, int64_t kbegin,
+                                                 int64_t kend, int lane, const bool (&asked)[kTL], v4f (&sum)[kTL]) {
+        constexpr int kAhead = 4;
+        const int64_t down_l = LL == kColumns ? a.ld_l : 4, down_r = LR == kColumns ? a.ld_r : 4;
+        r = r < a.nr ? r : a.nr - 1;
+        const char* pr = a.r + r * (LR == kColumns ? 4 : a.ld_r);
+        const char* pl[kTL];
+        bool on[kTL];
+#pragma unroll
+        for (int j = 0; j < kTL; j++) {
+            const int64_t row = l + 16 * j < a.nl ? l + 16 * j : a.nl - 1;
+            pl[j] = a.l + row * (LL == kColumns ? 4 : a.ld_l);
+            on[j] = !a.off || a.off[row] >= 0;
+            sum[j] = v4f{0, 0, 0, 0};
+        }
+        for (int64_t k0 = kbegin / 4; k0 < kend / 4; k0 += 4 * kAhead) {
+            float x[kTL][kAhead], y[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; i++) {
+                const int64_t k = k0 + 4 * i + lane / 16;
+                y[i] = k < kend / 4 ? *reinterpret_cast<const float*>(pr + k * down_r) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < kTL; j++)
+                if (asked[j])
+#pragma unroll
+                    for (int i = 0; i < kAhead; i++) {
+                        const int64_t k = k0 + 4 * i + lane / 16;
+                        x[j][i] = on[j] && k < kend / 4 ? *reinterpret_cast<const float*>(pl[j] + k * down_l) : 0.0f;
+                    }
+#pragma unroll
+            for (int j = 0; j < kTL; j++)
+                if (asked[j])
+#pragma unroll
+                    for (int i = 0; i < kAhead; i++)
+                        sum[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(y[i], x[j][i], sum[j], 0, 0, 0);
+        }
+    }
+
+    // fp32: the sums that are infinite or NaN, as the fp32 instruction has them. The others stay as they
+    // are, so that no sum depends on what else is in its tile. Slow, and rare: an infinity is a mask or
+    // the end of a run that has diverged (M2048 V32768 D768: forward 0.59 ms, with 100 tokens masked by
+    // -inf 1.23, all of it NaN 7.0; looking for them costs 0.5 to 1 %).
+    static __device__ __forceinline__ void mend(const ProductArgs& a, int64_t l0, int64_t r0, int64_t kbegin,
+                                                int64_t kend, int lane, v4f (&acc)[kTR][kTL]) {
+        float zero = 0.0f;            // 0 times each sum: NaN where one is not finite
+#pragma unroll
+        for (int i = 0; i < kTR; i++)
+#pragma unroll
+            for (int j = 0; j < kTL; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) zero = __builtin_fmaf(acc[i][j][e], 0.0f, zero);
+        if (!wave_any(!(zero == 0.0f))) return;
+        const auto finite = [](float v) { return __builtin_fabsf(v) < INFINITY; };
+#pragma unroll
+        for (int i = 0; i < kTR; i++) {
+            bool asked[kTL], some = false;
+#pragma unroll
+            for (int j = 0; j < kTL; j++) {
+                bool all = true;
+#pragma unroll
+                for (int e = 0; e < 4; e++) all &= finite(acc[i][j][e]);
+                asked[j] = wave_any(!all);
+                some |= asked[j];
+            }
+            if (!some) continue;
+            v4f sum[kTL];
+            exact(a, l0 + lane % 16, r0 + 16 * i + lane % 16, kbegin, kend, lane, asked, sum);
+#pragma unroll
+            for (int j = 0; j < kTL; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[i][j][e] = finite(acc[i][j][e]) ? acc[i][j][e] : sum[j][e];
+        }
+    }
+
     static __device__ __forceinline__ void run(const ProductArgs& a, int64_t l0, int64_t r0, int64_t kbegin,
                                                int64_t kend, char* lds, v4f (&acc)[kTR][kTL]) {
         const int lane = threadIdx.x % kWave;
@@ -407,6 +487,7 @@ struct RowProduct {
             }
             buf ^= 1;
         }
+        if constexpr (sizeof(T) == 4) mend(a, l0 + wl * (BL / WL), r0 + wr * (BR / WR), kbegin, kend, lane, acc);
     }
 };
 

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import ends_ref as ref
-from ends_util import TYPES, check, generator, normal
+from ends_util import TYPES, check, generator, normal, spread
 from gpu_util import announce
 from test_head_gpu import run
 
@@ -121,3 +121,59 @@ def test_infinite_logits(dtype):
     w[:, 0] = -INF
     got = run(x, w, targets, dloss, None)
     assert (got["lse"] == -INF).all()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("D", [72, 33])
+@pytest.mark.parametrize("M", [5, 40, 300])
+def test_tokens_masked_by_an_infinity_in_fp32(M, D, layout):
+    """Operands of the products are three parts each, which an infinity has not."""
+    V, off = LAYOUTS[layout]
+    x, w, keep, targets, dloss = masked(M + V, M, V, D, "f32", off(torch.arange(V)), -INF)
+    got = run(x, w, targets, dloss, None)
+    check_masked(x, w, keep, targets, dloss, got, slice(1, None))
+    got = run(spread(x)[0], spread(w)[0], targets, dloss, None)
+    check_masked(x, w, keep, targets, dloss, got, slice(1, None))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,D", [(5, 72), (40, 33), (300, 64), (1500, 31)])
+def test_infinities_here_and_there(dtype, M, D):
+    """Infinities of either sign and NaN as the sums of products have them, and in no other row."""
+    V, t = 700, TYPES[dtype]
+    g = generator(M)
+    x, w = normal(g, M, D, std=2.0), normal(g, V, D, std=D ** -0.5)
+    targets, dloss = torch.randint(20, V, (M,), generator=g), normal(g, M, std=0.1 / M)
+    x, w = x.to(t), w.to(t)
+    w[11, 3] = w[12, 3] = INF
+    x[1, 3] = 0.0
+    x[2, 7] = INF
+    x[3, 5] = float("nan")
+    x[4, 3] = -1.0
+    got = run(x, w, targets, dloss, None)
+    logits = torch.stack([(r * w.double()).sum(1) for r in x.double()])
+    lse = torch.logsumexp(logits, 1)
+    far = logits.max(1).values == INF
+    lse[far & ~logits.isnan().any(1)] = INF
+    here = got["lse"].double().cpu()
+    assert here[1].isnan() and here[3].isnan() and torch.equal(here.isnan(), logits.isnan().any(1))
+    assert torch.equal(here == INF, lse == INF) and ((lse == INF).any() or M == 5)
+    rest = torch.isfinite(lse)
+    assert rest[4]
+    keep = torch.tensor([v for v in range(V) if v not in (11, 12)])
+    want = ref.head(x[rest], w[keep], torch.where(targets > 12, targets - 2, targets)[rest], 1.0, dloss[rest])
+    for k in ("loss", "lse"):
+        check(got[k][rest.cuda()], want[k], k)
+    columns = [d for d in range(D) if d != 3]
+    value, bound = want["dx"]
+    check(got["dx"][rest.cuda()][:, columns], (value[:, columns], bound[:, columns]), "dx")
+    # a row that has none of it keeps its bits
+    w[11:13, 3] = 0.0
+    x[1, 3] = 1.0
+    a = run(x, w, targets, dloss, None)
+    x[2, 7] = x[3, 5] = 1.0
+    b = run(x, w, targets, dloss, None)
+    same = torch.ones(M, dtype=torch.bool, device="cuda")
+    same[2:4] = False
+    for k in ("loss", "lse", "dx"):
+        assert torch.equal(a[k][same], b[k][same]), k
