@@ -463,6 +463,7 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
     static_assert(P::kWaves * kStore <= P::kLds, "stored through the stages' LDS");
     __shared__ __align__(1024) char lds[P::kLds];
     const Part<P> at(a, blockIdx.x, gridDim.x);
+    constexpr int kPadded = -2;
     int hit[P::kTL];
     float up[P::kTL], own[P::kTL], lse[P::kTL];
     const auto read_rows = [&] {
@@ -470,7 +471,8 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
         for (int j = 0; j < P::kTL; j++) {
             const int64_t m = at.l + 16 * j;
             const bool in = m < a.nl;
-            hit[j] = at.place((in ? h.g.t[m] : -1) - h.first);
+            const int t = in ? h.g.t[m] : -1;
+            hit[j] = t < 0 ? kPadded : at.place(t - h.first);
             up[j] = in ? h.g.a[m] : 0.0f;
             own[j] = in ? h.g.b[m] : 0.0f;
             lse[j] = in ? h.g.lse[m] : 0.0f;
@@ -482,7 +484,6 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
     v4f acc[P::kTR][P::kTL];
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
     if constexpr (!kAhead) read_rows();
-    // a padded row's x counts as zeros (ProductArgs::off) and its up is 0: so is its dl
 #pragma unroll
     for (int j = 0; j < P::kTL; j++) {
         if (const bool far = is_far(lse[j]); wave_any(far)) {
@@ -508,6 +509,14 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
             for (int i = 0; i < P::kTR; i++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) acc[i][j][e] -= hit[j] == 16 * i + e ? own[j] : 0.0f;
+        }
+        // a padded row's x counts as zeros (ProductArgs::off) and its up is 0, but 0 times an infinite
+        // weight is NaN
+        if (wave_any(hit[j] == kPadded)) {
+#pragma unroll
+            for (int i = 0; i < P::kTR; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[i][j][e] = hit[j] == kPadded ? 0.0f : acc[i][j][e];
         }
     }
     if (at.rw + 16 * P::kTR > a.nr || at.lw + 16 * P::kTL > a.nl) {
@@ -540,6 +549,7 @@ struct GradArgs {
     float* acc;               // [split][nl][ld] fp32, ld a multiple of 4; added to unless it is the first piece
     bool first;
     int split;                // of K
+    const int* t;             // rows of out with t < 0 are zeros, whatever the weight (null: none)
 };
 
 // The products of a piece, dx's and dW's, in one launch, the tiles of the longer K
@@ -591,30 +601,36 @@ __global__ __launch_bounds__(P::kThreads) void head_grad_kernel(TwoProducts two)
         return;
     }
     const float back = h.back[0];
+    bool on[P::kTL];
+#pragma unroll
+    for (int j = 0; j < P::kTL; j++) on[j] = !h.t || (at.l + 16 * j < a.nl && h.t[at.l + 16 * j] >= 0);
     __syncthreads();          // the last stage is read
     Rows::run(lds + at.wave * Rows::kBytes, at.lane, static_cast<T*>(h.out) + at.lw * h.ld + at.rw, h.ld, a.nl - at.lw,
               a.nr - at.rw, [&](int i, int j) {
                   quad v;
 #pragma unroll
-                  for (int e = 0; e < 4; e++) v[e] = static_cast<T>(acc[i][j][e] * back);
+                  for (int e = 0; e < 4; e++) v[e] = static_cast<T>(on[j] ? acc[i][j][e] * back : 0.0f);
                   return v;
               });
 }
 
-// out = back * the sum of the parts of K, 16 bytes of them to a lane.
+// out = back * the sum of the parts of K, 16 bytes of them to a lane; zeros in rows with t < 0.
 template <typename T>
 __global__ __launch_bounds__(256) void head_finish_kernel(const float* acc, int64_t ld_acc, int split, int64_t rows,
-                                                          int64_t n, const float* back, T* out, int64_t ld) {
+                                                          int64_t n, const float* back, const int* t, T* out,
+                                                          int64_t ld) {
     const float s = back[0];
-    for (int64_t row = first_row(); row < rows; row += rows_apart())
+    for (int64_t row = first_row(); row < rows; row += rows_apart()) {
+        const bool on = !t || t[row] >= 0;
         for (int64_t c = threadIdx.x % kWave * 4; c < n; c += kWave * 4) {
             v4f v = {0, 0, 0, 0};
             for (int k = 0; k < split; k++) v += *reinterpret_cast<const v4f*>(acc + (k * rows + row) * ld_acc + c);
             RowVec<T, 4> o;
 #pragma unroll
-            for (int e = 0; e < 4; e++) o.set(e, v[e] * s);
+            for (int e = 0; e < 4; e++) o.set(e, on ? v[e] * s : 0.0f);
             o.template store<false>(out + row * ld, static_cast<int>(c), static_cast<int>(n));
         }
+    }
 }
 
 // ---- plans -------------------------------------------------------------------------
@@ -837,9 +853,9 @@ hipError_t transpose(const T* in, int64_t ld, int64_t rows, int64_t n, T* out, i
 }
 
 template <typename T>
-hipError_t finish(const float* acc, int64_t ld_acc, int split, int64_t rows, int64_t n, const float* back, T* out,
-                  int64_t ld, hipStream_t st) {
-    head_finish_kernel<T><<<row_groups(rows), 256, 0, st>>>(acc, ld_acc, split, rows, n, back, out, ld);
+hipError_t finish(const float* acc, int64_t ld_acc, int split, int64_t rows, int64_t n, const float* back,
+                  const int* t, T* out, int64_t ld, hipStream_t st) {
+    head_finish_kernel<T><<<row_groups(rows), 256, 0, st>>>(acc, ld_acc, split, rows, n, back, t, out, ld);
     return hipGetLastError();
 }
 
@@ -931,11 +947,11 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
                                        : product(dl, ld_n * e, M, wt, ld_n * e, D, align_up(n * e, 16), shape);
         const ProductArgs pw = product(dlt, p.ld_m * e, n, xt, p.ld_m * e, D, align_up(M * e, 16), shape);
         const GradArgs gx{g.back, p.accumulate ? nullptr : h.dx, p.accumulate ? p.ld_acc : h.ld_dx,
-                          reinterpret_cast<float*>(ws + p.acc), v0 == 0, p.split};
+                          reinterpret_cast<float*>(ws + p.acc), v0 == 0, p.split, g.t};
         T* dw = h.dw ? static_cast<T*>(h.dw) + v0 * h.ld_dw : nullptr;
         float* acc_w = reinterpret_cast<float*>(ws + p.acc_w);
         const bool sums_w = p.split_w > 1;
-        const GradArgs gw{g.back, sums_w ? nullptr : dw, sums_w ? p.ld_acc : h.ld_dw, acc_w, true, p.split_w};
+        const GradArgs gw{g.back, sums_w ? nullptr : dw, sums_w ? p.ld_acc : h.ld_dw, acc_w, true, p.split_w, nullptr};
         const int64_t nx = h.dx ? px.tiles_l * px.tiles_r * p.split : 0,
                       nw = dw ? pw.tiles_l * pw.tiles_r * p.split_w : 0;
         const TwoProducts two =
@@ -949,11 +965,11 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
         });
         if (hipError_t r = hipGetLastError()) return r;
         if (dw && sums_w)
-            if (hipError_t r = finish(acc_w, p.ld_acc, p.split_w, n, D, g.back, dw, h.ld_dw, st)) return r;
+            if (hipError_t r = finish(acc_w, p.ld_acc, p.split_w, n, D, g.back, nullptr, dw, h.ld_dw, st)) return r;
     }
     if (h.dx && p.accumulate)
-        return finish(reinterpret_cast<const float*>(ws + p.acc), p.ld_acc, p.split, M, D, g.back, static_cast<T*>(h.dx),
-                      h.ld_dx, st);
+        return finish(reinterpret_cast<const float*>(ws + p.acc), p.ld_acc, p.split, M, D, g.back, g.t,
+                      static_cast<T*>(h.dx), h.ld_dx, st);
     return hipSuccess;
 }
 

@@ -177,3 +177,33 @@ def test_infinities_here_and_there(dtype, M, D):
     same[2:4] = False
     for k in ("loss", "lse", "dx"):
         assert torch.equal(a[k][same], b[k][same]), k
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,V,D", [(40, 700, 72), (300, 5000, 33), (5, 20000, 64), (1100, 900, 40), (9000, 130, 24)])
+def test_padded_rows_beside_an_infinite_weight(dtype, M, V, D):
+    """A token masked by -inf leaves the others' gradients as they are, and padded rows take no part: 0 times
+    it is none of theirs."""
+    x, w, keep, targets, dloss = masked(M, M, V, D, dtype, torch.arange(V) % 100 == 99, -INF)
+    padded = torch.arange(M) % 3 == 1
+    targets = torch.where(padded, torch.where(torch.arange(M) % 2 == 1, -1, V), targets)
+    x[padded] = float("nan")
+    got = run(x, w, targets, dloss, None)
+    x[padded] = 0.0
+    on = ~padded.cuda()
+    assert (got["dx"][~on] == 0).all()
+    got["lse"][~on] = 0.0
+    where = torch.full((V,), -100)
+    where[keep] = torch.arange(len(keep))
+    want = ref.head(x[~padded], w[keep], where[targets[~padded]], 1.0, dloss[~padded])
+    for k in ("loss", "lse"):
+        check(got[k][on], want[k], k)
+    check(got["dx"][on][:, 1:], [v[:, 1:] for v in want["dx"]], "dx")
+    check(got["dweight"][keep.cuda()], want["dweight"], "dweight")
+    hidden = torch.ones(V, dtype=torch.bool, device="cuda")
+    hidden[keep] = False
+    assert (got["dweight"][hidden] == 0).all()
+    # a weight of NaN makes every other row NaN
+    w[0] = float("nan")
+    got = run(x, w, targets, dloss, None)
+    assert (got["dx"][~on] == 0).all() and (got["loss"][~on] == 0).all() and got["dx"][on].isnan().all()
