@@ -555,8 +555,9 @@ int mss_gated_norm_backward(const mss_norm_dims* dims, const mss_norm_strides* s
  * sum runs in a fixed order), gradients are written once and rounded once.
  *
  * Token ids and targets are int32 or int64 (id_bytes 4 or 8).  One outside
- * 0 .. vocab-1 is no error: it marks a padded place (or a token that another
- * shard of the table holds).
+ * 0 .. vocab-1 is no error: it marks a padded place (for the embedding also a
+ * token that another shard of the table holds; for the head see
+ * mss_head_loss_backward).
  *
  * Row strides in elements, as in mss_gated_strides (NULL: dense rows).  With
  * strides given the tensors need only their element's alignment; ids, targets
@@ -652,7 +653,14 @@ int mss_head_loss(const mss_head_dims* dims, const mss_head_strides* strides, co
  * largest |dloss| + |dlse| to just below 2^13 (fp16 would lose the small
  * ones, and bf16 rounds least there): in 2-byte types each of its values is
  * rounded once.  dx and dweight are summed in fp32.
- *   dx (M, D), dweight (V, D) dtype: each computed where given.            */
+ *   dx (M, D), dweight (V, D) dtype: each computed where given.
+ * A vocabulary in shards: with LSE, the log of the sum of the shards' exp(lse),
+ * the loss is LSE - (lse - loss) with lse and loss of the shard that has the
+ * target.  Backwards every shard is given LSE as lse.  A row whose target is in
+ * another shard takes part in this one by dlse: any token of the shard as its
+ * target, dloss 0 and dlse the row's dloss + dlse.  (Left as a padded row it
+ * would lose the shard's part of its gradients.)  dx is the sum over the
+ * shards.                                                                   */
 int mss_head_loss_backward(const mss_head_dims* dims, const mss_head_strides* strides,
                            const void* x, const void* weight, const void* targets,
                            const float* lse, const float* dloss, const float* dlse, void* dx,

@@ -1216,7 +1216,8 @@ def head_loss(x, weight, targets, *, logit_scale=1.0, out=None, workspace=None, 
 
     x (M, D), weight (V, D) float32, bfloat16 or float16, both the same, rows may be strided;
     targets (M,) int64 or int32.  lse_m is the log of the sum of the exponentials, loss_m = lse_m
-    minus the target's logit; a target outside 0 .. V-1 marks a padded row, whose loss is 0.
+    minus the target's logit; a target outside 0 .. V-1 marks a padded row, whose loss is 0 (its lse
+    is that of its logits).
     ``out``: optional pair of output tensors.  ``workspace``: uint8 GPU tensor of at least
     ``head_workspace_bytes(OP_HEAD_LOSS, ...)`` + 256 bytes (allocated here when omitted)."""
     c, logit_scale = _Call(x, "x", stream), float(logit_scale) + 0.0
@@ -1240,6 +1241,9 @@ def head_loss_backward(x, weight, targets, lse, dloss, dlse=None, *, logit_scale
 
     ``lse``: the forward's.  Returns a dict: dx (M, D) and dweight (V, D) in x's type, None where
     not needed.  A padded row takes no part: its dx is 0, and its x, dloss and dlse are not used.
+    A vocabulary in shards: ``lse`` is the log sum over all shards; a row whose target is in another
+    shard is given any token of this one, dloss 0 and dlse its dloss + dlse (as a padded row it would
+    lose this shard's part); dx is the sum over the shards.
     In 2-byte types the gradient of each logit is rounded once before the products that make
     dx and dweight.  ``out`` and ``workspace`` as in gated_scan_backward
     (``head_workspace_bytes(OP_HEAD_LOSS_BACKWARD, ...)``)."""
