@@ -652,7 +652,9 @@ int mss_head_loss(const mss_head_dims* dims, const mss_head_strides* strides, co
  * and held in dtype for the two products, times a factor that brings the
  * largest |dloss| + |dlse| to just below 2^13 (fp16 would lose the small
  * ones, and bf16 rounds least there): in 2-byte types each of its values is
- * rounded once.  dx and dweight are summed in fp32.
+ * rounded once.  In fp16 a row of dl has for dx a further power of 2 of its own,
+ * so that its dx does not depend on the others' size; to dweight what is below
+ * 2^-38 of the largest is lost.  dx and dweight are summed in fp32.
  *   dx (M, D), dweight (V, D) dtype: each computed where given.
  * A vocabulary in shards: with LSE, the log of the sum of the shards' exp(lse),
  * the loss is LSE - (lse - loss) with lse and loss of the shard that has the

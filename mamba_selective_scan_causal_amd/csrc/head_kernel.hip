@@ -28,7 +28,11 @@
 // gives all rows one factor, the dl of unlikely targets, which weigh most, all lie
 // there (bf16, M8192 V32768 D1536: dx is off by 0.0020 of its norm, of which 0.0017
 // is its own rounding; with the same dl right above a power of two, 0.0028).  dx and
-// dW are scaled back in fp32.
+// dW are scaled back in fp32.  In fp16 the rows of dl, which make dx, have each a
+// further power of 2 (RowGrads::lift), so that a row's digits do not depend on how
+// large the others' dloss is (V32768 D256, a row of 2^-26 of the largest: its dx
+// off by 0.1 % of its norm in place of 3 %).  dl^T, which sums over the rows, has
+// none: what lies below 2^-38 of the largest is lost to dW.
 #include <algorithm>
 
 #include "launch_ends.h"
@@ -363,12 +367,14 @@ __global__ __launch_bounds__(256) void transpose_kernel(const T* in, int64_t ld_
 // ---- backward --------------------------------------------------------------------
 
 // What a row brings to dl: a = (dloss + dlse) s, b = dloss s, its lse and its
-// target (-1: a padded row, all zeros).
+// target (-1: a padded row, all zeros); and the power of 2 that brings its own
+// |dloss| + |dlse| times s to 2^12 .. 2^13 (1 for the largest).
 struct RowGrads {
     float* a;
     float* b;
     float* lse;
     int* t;
+    float* lift;
     float* back;              // [0]: logit_scale / s
 };
 
@@ -435,9 +441,16 @@ __global__ __launch_bounds__(1024) void row_grads_kernel(HeadArgs h, RowGrads g,
     const float up = on ? h.dloss[m] : 0.0f;
     g.a[m] = on ? (up + (h.dlse ? h.dlse[m] : 0.0f)) * s : 0.0f;
     g.b[m] = up * s;
+    const float size = on ? (__builtin_fabsf(up) + (h.dlse ? __builtin_fabsf(h.dlse[m]) : 0.0f)) * s : 0.0f;
+    int e = 12;
+    if (size > 0.0f && size < INFINITY) e = ilogbf(size);
+    g.lift[m] = ldexpf(1.0f, e < -88 ? 100 : 12 - e);
     g.lse[m] = on ? h.lse[m] : 0.0f;
     g.t[m] = on ? static_cast<int>(t) : -1;
 }
+
+template <typename T>
+constexpr bool kLifted = std::is_same_v<T, f16>;      // the others have fp32's exponents
 
 struct DlArgs {
     float s, c;               // logit_scale, and times log2(e)
@@ -465,7 +478,9 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
     const Part<P> at(a, blockIdx.x, gridDim.x);
     constexpr int kPadded = -2;
     int hit[P::kTL];
-    float up[P::kTL], own[P::kTL], lse[P::kTL];
+    float up[P::kTL], own[P::kTL], lse[P::kTL], lift[P::kTL];
+    // ahead of the product where its registers leave room
+    constexpr bool kAhead = sizeof(T) == 2 && Shape<P>::kDirectRows;
     const auto read_rows = [&] {
 #pragma unroll
         for (int j = 0; j < P::kTL; j++) {
@@ -478,9 +493,12 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
             lse[j] = in ? h.g.lse[m] : 0.0f;
         }
     };
-    // ahead of the product where its registers leave room
-    constexpr bool kAhead = sizeof(T) == 2 && Shape<P>::kDirectRows;
+    const auto read_lift = [&] {
+#pragma unroll
+        for (int j = 0; j < P::kTL; j++) lift[j] = at.l + 16 * j < a.nl ? h.g.lift[at.l + 16 * j] : 0.0f;
+    };
     if constexpr (kAhead) read_rows();
+    if constexpr (kAhead && kLifted<T>) read_lift();
     v4f acc[P::kTR][P::kTL];
     P::run(a, at.l0, at.r0, 0, a.kbytes, lds, acc);
     if constexpr (!kAhead) read_rows();
@@ -535,9 +553,17 @@ __global__ __launch_bounds__(P::kThreads) void head_dl_kernel(ProductArgs a, DlA
         for (int e = 0; e < 4; e++) v[e] = static_cast<T>(acc[i][j][e]);
         return v;
     };
+    if constexpr (!kAhead && kLifted<T>) read_lift();
     __syncthreads();          // the last stage is read
     char* mine = lds + at.wave * kStore;
-    Rows::run(mine, at.lane, static_cast<T*>(h.dl) + at.lw * h.ld_dl + at.rw, h.ld_dl, a.nl - at.lw, h.ld_dl - at.rw, get);
+    Rows::run(mine, at.lane, static_cast<T*>(h.dl) + at.lw * h.ld_dl + at.rw, h.ld_dl, a.nl - at.lw, h.ld_dl - at.rw,
+              [&](int i, int j) {
+                  if constexpr (!kLifted<T>) return get(i, j);
+                  quad v;
+#pragma unroll
+                  for (int e = 0; e < 4; e++) v[e] = static_cast<T>(acc[i][j][e] * lift[j]);
+                  return v;
+              });
     Cols::run(mine, at.lane, static_cast<T*>(h.dlt) + at.rw * h.ld_dlt + at.lw, h.ld_dlt, h.ld_dlt - at.lw, a.nr - at.rw,
               get);
 }
@@ -550,6 +576,7 @@ struct GradArgs {
     bool first;
     int split;                // of K
     const int* t;             // rows of out with t < 0 are zeros, whatever the weight (null: none)
+    const float* lift;        // out's rows are to be divided by (null: 1)
 };
 
 // The products of a piece, dx's and dW's, in one launch, the tiles of the longer K
@@ -600,28 +627,34 @@ __global__ __launch_bounds__(P::kThreads) void head_grad_kernel(TwoProducts two)
         }
         return;
     }
-    const float back = h.back[0];
+    float back[P::kTL];
     bool on[P::kTL];
 #pragma unroll
-    for (int j = 0; j < P::kTL; j++) on[j] = !h.t || (at.l + 16 * j < a.nl && h.t[at.l + 16 * j] >= 0);
+    for (int j = 0; j < P::kTL; j++) {
+        const int64_t l = at.l + 16 * j;
+        on[j] = !h.t || (l < a.nl && h.t[l] >= 0);
+        back[j] = h.back[0];
+        if constexpr (kLifted<T>) back[j] /= h.lift && l < a.nl ? h.lift[l] : 1.0f;
+    }
     __syncthreads();          // the last stage is read
     Rows::run(lds + at.wave * Rows::kBytes, at.lane, static_cast<T*>(h.out) + at.lw * h.ld + at.rw, h.ld, a.nl - at.lw,
               a.nr - at.rw, [&](int i, int j) {
                   quad v;
 #pragma unroll
-                  for (int e = 0; e < 4; e++) v[e] = static_cast<T>(on[j] ? acc[i][j][e] * back : 0.0f);
+                  for (int e = 0; e < 4; e++) v[e] = static_cast<T>(on[j] ? acc[i][j][e] * back[j] : 0.0f);
                   return v;
               });
 }
 
-// out = back * the sum of the parts of K, 16 bytes of them to a lane; zeros in rows with t < 0.
+// out = back * the sum of the parts of K, 16 bytes of them to a lane; zeros in rows with t < 0,
+// other rows divided by their lift.
 template <typename T>
 __global__ __launch_bounds__(256) void head_finish_kernel(const float* acc, int64_t ld_acc, int split, int64_t rows,
-                                                          int64_t n, const float* back, const int* t, T* out,
-                                                          int64_t ld) {
-    const float s = back[0];
+                                                          int64_t n, const float* back, const int* t,
+                                                          const float* lift, T* out, int64_t ld) {
     for (int64_t row = first_row(); row < rows; row += rows_apart()) {
         const bool on = !t || t[row] >= 0;
+        const float s = lift ? back[0] / lift[row] : back[0];
         for (int64_t c = threadIdx.x % kWave * 4; c < n; c += kWave * 4) {
             v4f v = {0, 0, 0, 0};
             for (int k = 0; k < split; k++) v += *reinterpret_cast<const v4f*>(acc + (k * rows + row) * ld_acc + c);
@@ -811,7 +844,7 @@ bool plan_of(int dtype, int64_t M, int64_t V, int64_t D, bool backward, Plan& p)
     p.ld_acc = align_up(D, 4);
     if (p.accumulate) p.acc = take(M * int64_t{4}, p.ld_acc, p.split);
     if (p.split_w > 1) p.acc_w = take((V < p.piece ? V : p.piece) * int64_t{4}, p.ld_acc, p.split_w);
-    p.rows = take(align_up(M, 64) * int64_t{16} + 256 + 4 * kTops, 1, 1);
+    p.rows = take(align_up(M, 64) * int64_t{20} + 256 + 4 * kTops, 1, 1);
     // the workgroups of the transposes are counted in 32 bits of threads
     return fits && (p.ld_m > p.piece ? p.ld_m : p.piece) / 64 * ceil_div(D, 64) < (int64_t{1} << 24);
 }
@@ -854,8 +887,8 @@ hipError_t transpose(const T* in, int64_t ld, int64_t rows, int64_t n, T* out, i
 
 template <typename T>
 hipError_t finish(const float* acc, int64_t ld_acc, int split, int64_t rows, int64_t n, const float* back,
-                  const int* t, T* out, int64_t ld, hipStream_t st) {
-    head_finish_kernel<T><<<row_groups(rows), 256, 0, st>>>(acc, ld_acc, split, rows, n, back, t, out, ld);
+                  const int* t, const float* lift, T* out, int64_t ld, hipStream_t st) {
+    head_finish_kernel<T><<<row_groups(rows), 256, 0, st>>>(acc, ld_acc, split, rows, n, back, t, lift, out, ld);
     return hipGetLastError();
 }
 
@@ -906,7 +939,9 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
     g.b = g.a + padded;
     g.lse = g.b + padded;
     g.t = reinterpret_cast<int*>(g.lse + padded);
-    g.back = reinterpret_cast<float*>(g.t + padded);
+    g.lift = reinterpret_cast<float*>(g.t + padded);
+    g.back = g.lift + padded;
+    const float* lift = kLifted<T> ? g.lift : nullptr;
     float* tops = M > kRowsEach ? g.back + 64 : nullptr;
     if (tops) {
         row_tops_kernel<<<kTops, 1024, 0, st>>>(h, tops);
@@ -947,11 +982,11 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
                                        : product(dl, ld_n * e, M, wt, ld_n * e, D, align_up(n * e, 16), shape);
         const ProductArgs pw = product(dlt, p.ld_m * e, n, xt, p.ld_m * e, D, align_up(M * e, 16), shape);
         const GradArgs gx{g.back, p.accumulate ? nullptr : h.dx, p.accumulate ? p.ld_acc : h.ld_dx,
-                          reinterpret_cast<float*>(ws + p.acc), v0 == 0, p.split, g.t};
+                          reinterpret_cast<float*>(ws + p.acc), v0 == 0, p.split, g.t, lift};
         T* dw = h.dw ? static_cast<T*>(h.dw) + v0 * h.ld_dw : nullptr;
         float* acc_w = reinterpret_cast<float*>(ws + p.acc_w);
         const bool sums_w = p.split_w > 1;
-        const GradArgs gw{g.back, sums_w ? nullptr : dw, sums_w ? p.ld_acc : h.ld_dw, acc_w, true, p.split_w, nullptr};
+        const GradArgs gw{g.back, sums_w ? nullptr : dw, sums_w ? p.ld_acc : h.ld_dw, acc_w, true, p.split_w, nullptr, nullptr};
         const int64_t nx = h.dx ? px.tiles_l * px.tiles_r * p.split : 0,
                       nw = dw ? pw.tiles_l * pw.tiles_r * p.split_w : 0;
         const TwoProducts two =
@@ -965,10 +1000,10 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
         });
         if (hipError_t r = hipGetLastError()) return r;
         if (dw && sums_w)
-            if (hipError_t r = finish(acc_w, p.ld_acc, p.split_w, n, D, g.back, nullptr, dw, h.ld_dw, st)) return r;
+            if (hipError_t r = finish(acc_w, p.ld_acc, p.split_w, n, D, g.back, nullptr, nullptr, dw, h.ld_dw, st)) return r;
     }
     if (h.dx && p.accumulate)
-        return finish(reinterpret_cast<const float*>(ws + p.acc), p.ld_acc, p.split, M, D, g.back, g.t,
+        return finish(reinterpret_cast<const float*>(ws + p.acc), p.ld_acc, p.split, M, D, g.back, g.t, lift,
                       static_cast<T*>(h.dx), h.ld_dx, st);
     return hipSuccess;
 }
