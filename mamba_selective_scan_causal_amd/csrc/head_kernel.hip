@@ -16,9 +16,9 @@
 // operations for each of their values.  With few rows dx's product reads W down
 // its columns instead (kColumnRows).
 //
-// What bounds it, by a trace: M8192 V32768 D1536 bf16 takes 752 us forward (1097
+// What bounds it, by a trace: M8192 V32768 D1536 bf16 takes 751 us forward (1099
 // TFLOP/s, a library product of the size 583 us; 669 us and 1232 TFLOP/s in a run of
-// forwards alone), 878 for dl with its two stores of 537 MB, 1388 for both gradients (1188
+// forwards alone), 883 for dl with its two stores of 537 MB, 1384 for both gradients (1192
 // TFLOP/s): matrix instructions, with 10 to 15 % in the start and end of tiles.
 // M8 V65536 D2560 reads W at 5.9 TB/s (57 us).
 //
