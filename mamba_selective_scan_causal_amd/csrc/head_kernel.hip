@@ -912,7 +912,8 @@ hipError_t forward(const HeadArgs& h, const Plan& p, hipStream_t st) {
             int64_t ld_w = h.ld_w;
             if (hipError_t r = rows_of(p, w, ld_w, n, h.D, ws + p.w, st)) return r;
             const ProductArgs a = product(x + m0 * ld_x, ld_x * e, rows, w, ld_w * e, n, p.Dk * e, shape);
-            const LossArgs l{h.logit_scale, h.logit_scale * kLog2e, v0, m0, h.targets, h.wide_ids, part + slabs * rows, at_target};
+            const LossArgs l{h.logit_scale, h.logit_scale * kLog2e, v0, m0, h.targets, h.wide_ids,
+                             part + slabs * rows, at_target};
             with_tile<T>(shape, straight, [&](auto tag) {
                 using P = typename decltype(tag)::type;
                 head_loss_kernel<P><<<static_cast<uint32_t>(a.tiles_l * a.tiles_r), P::kThreads, 0, st>>>(a, l);
@@ -986,7 +987,8 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
         T* dw = h.dw ? static_cast<T*>(h.dw) + v0 * h.ld_dw : nullptr;
         float* acc_w = reinterpret_cast<float*>(ws + p.acc_w);
         const bool sums_w = p.split_w > 1;
-        const GradArgs gw{g.back, sums_w ? nullptr : dw, sums_w ? p.ld_acc : h.ld_dw, acc_w, true, p.split_w, nullptr, nullptr};
+        const GradArgs gw{g.back, sums_w ? nullptr : dw, sums_w ? p.ld_acc : h.ld_dw, acc_w, true, p.split_w,
+                          nullptr, nullptr};
         const int64_t nx = h.dx ? px.tiles_l * px.tiles_r * p.split : 0,
                       nw = dw ? pw.tiles_l * pw.tiles_r * p.split_w : 0;
         const TwoProducts two =
@@ -1000,7 +1002,8 @@ hipError_t backward(const HeadArgs& h, const Plan& p, hipStream_t st) {
         });
         if (hipError_t r = hipGetLastError()) return r;
         if (dw && sums_w)
-            if (hipError_t r = finish(acc_w, p.ld_acc, p.split_w, n, D, g.back, nullptr, nullptr, dw, h.ld_dw, st)) return r;
+            if (hipError_t r = finish(acc_w, p.ld_acc, p.split_w, n, D, g.back, nullptr, nullptr, dw, h.ld_dw, st))
+                return r;
     }
     if (h.dx && p.accumulate)
         return finish(reinterpret_cast<const float*>(ws + p.acc), p.ld_acc, p.split, M, D, g.back, g.t, lift,
