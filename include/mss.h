@@ -634,8 +634,9 @@ int mss_head_workspace_bytes(const mss_head_dims* dims, int op, size_t* bytes);
  *   x (M, D), weight (V, D) dtype;  targets (M);  loss, lse (M) fp32
  * Logits are fp32 sums of exact products of 2-byte operands.  fp32 operands
  * are split in three parts of 8 bits each, and of their nine products the six
- * largest are summed: what is left out is below 2^-21 of each product; a sum
- * with an infinite or NaN operand is that of the fp32 products.
+ * largest are summed: what is left out is below 2^-21 of each product (of
+ * operands of 2^-100 and more, whose last part is no subnormal); a sum with an
+ * infinite or NaN operand is that of the fp32 products.
  * A logit may have any value of fp32: one far below a row's largest, down to
  * -inf, adds 0 to the sum (masked tokens).  lse is inf where a logit is, and
  * -inf (and the loss NaN) where every logit is.                             */
